@@ -87,9 +87,24 @@ class MaskDesc(ctypes.Structure):
     ]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("n_axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 3),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("inv_freq", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("token_stride", ctypes.c_int64 * 3),
+        ("batch_stride", ctypes.c_int64 * 3),
+    ]
+
+
 EXPORTS = (
     "mattn_fwd", "mattn_fwd_gqa", "mattn_fwd_host", "mattn_fwd_noalloc", "mattn_decode", "mattn_rr_select",
-    "mattn_received",
+    "mattn_received", "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
+    "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks", "mattn_decode_blocks_workspace",
     "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles", "mattn_plan_tiles_device",
     "mattn_device_status", "mattn_debug_checks", "mattn_set_wait_timeout_ns", "mattn_status_string",
     "mattn_last_error", "mattn_version",
@@ -134,6 +149,15 @@ def lib() -> ctypes.CDLL:
     L.mattn_rr_select.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, ctypes.c_uint32,
                                   vp, vp, vp]
     L.mattn_received.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, dp, vp]
+    sz, szp, f32 = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), ctypes.c_float
+    L.mattn_qk_rope.argtypes = [vp] * 9 + [i32] * 7 + [ctypes.POINTER(RopeDesc), vp]
+    L.mattn_decode_shared.argtypes = [vp] * 8 + [i32] * 8 + [vp, f32, vp, sz, vp]
+    L.mattn_decode_shared_workspace.argtypes = [i32] * 6 + [szp]
+    L.mattn_block_means.argtypes = [vp] * 4 + [i32] * 7 + [vp]
+    L.mattn_decode_select.argtypes = [vp] * 4 + [i32] * 10 + [vp, sz, vp]
+    L.mattn_decode_select_workspace.argtypes = [i32] * 5 + [szp]
+    L.mattn_decode_blocks.argtypes = [vp] * 7 + [i32] * 8 + [vp, f32, vp, sz, vp]
+    L.mattn_decode_blocks_workspace.argtypes = [i32] * 6 + [szp]
     L.mattn_count_pairs.argtypes = [dp, i32, i32, i32, u64p]
     L.mattn_plan_schedule.argtypes = [dp, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_uint32)]
     L.mattn_plan_tiles.argtypes = [dp, i32, i32, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
@@ -147,6 +171,9 @@ def lib() -> ctypes.CDLL:
     L.mattn_last_error.argtypes = []
     L.mattn_version.argtypes = []
     for name in ("mattn_fwd", "mattn_fwd_gqa", "mattn_fwd_host", "mattn_fwd_noalloc", "mattn_decode", "mattn_rr_select", "mattn_received",
+                 "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
+                 "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
+                 "mattn_decode_blocks_workspace",
                  "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles",
                  "mattn_plan_tiles_device", "mattn_device_status", "mattn_debug_checks",
                  "mattn_set_wait_timeout_ns", "mattn_version"):
@@ -343,6 +370,355 @@ def decode(q, k_cache, v_cache, mask: PreparedMask, seq_lens=None, out=None, lse
                             lse.data_ptr() if lse is not None else None,
                             seq_lens.data_ptr() if seq_lens is not None else None,
                             B, H, H_kv, L, d, _dtype_code(q), ctypes.byref(mask.desc), stream)
+    _check(rc)
+    return out, lse
+
+
+class _Launch:
+    """The device and stream of one call, and its workspace.  The library
+    launches on the current device, so the call runs with the tensors' device
+    current; a workspace made here belongs to torch's allocator and is kept
+    from reuse until a stream other than the current one is done with it."""
+
+    def __init__(self, device, stream):
+        import torch
+
+        self.device = device
+        self.raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+        self.other = stream is not None
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def own(self, t):
+        """A tensor made for this call: another stream than the current one uses it."""
+        import torch
+
+        if self.other:
+            t.record_stream(torch.cuda.ExternalStream(self.raw, device=self.device))
+        return t
+
+
+def _on(device, dtype, **tensors):
+    """Every given tensor (None is skipped) is a contiguous one of `device` and `dtype`."""
+    for name, t in tensors.items():
+        if t is not None and (t.device != device or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _size(fn, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(nbytes: int, device):
+    import torch
+
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+class RopePlan:
+    """Frequencies, axes and norm weights of ``qk_rope``, checked once.
+
+    inv_freq: CUDA fp32 [R], pair p turns by position * inv_freq[p] radians;
+    sections: rotated pairs of each position axis (1 to 3 axes, sum R, a
+    multiple of 8 of at most d / 2; None = one axis); q_weight, k_weight: CUDA
+    fp32 [d] or None (no norm); interleaved: pairs (2p, 2p + 1) instead of
+    (p, p + R).  The tensors are kept and read at every call."""
+
+    def __init__(self, inv_freq, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+        import torch
+
+        if not inv_freq.is_cuda or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a CUDA fp32 tensor [R]")
+        sections = [inv_freq.shape[0]] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
+            raise ValueError("sections must be 1 to 3 pair counts that add up to inv_freq's length")
+        _on(inv_freq.device, torch.float32, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
+        for w in (q_weight, k_weight):
+            if w is not None and w.dim() != 1:
+                raise ValueError("norm weights must be [d]")
+        self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
+        self.sections, self.eps, self.interleaved = sections, float(eps), bool(interleaved)
+
+    def desc(self) -> RopeDesc:
+        """The descriptor without the call's strides."""
+        d = RopeDesc()
+        d.n_axes = len(self.sections)
+        for a, n in enumerate(self.sections):
+            d.sections[a] = n
+        d.interleaved = int(self.interleaved)
+        d.eps = self.eps
+        d.inv_freq = self.inv_freq.data_ptr()
+        d.q_weight = _ptr(self.q_weight)
+        d.k_weight = _ptr(self.k_weight)
+        return d
+
+
+def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positions=None, starts=None, lens=None,
+            stream=None):
+    """Norms of queries and keys per head with the position rotation in one
+    pass (``mattn_qk_rope``), from the projection's layout into the
+    attention's.
+
+    q: CUDA bf16 or fp32 [B, N, H, d], k, v: [B, N, H_kv, d] (v may be None),
+    heads side by side (any strides over B and N, e.g. views of one
+    projection output); q_out: [B, H, N, d]; k_out, v_out: [B, H_kv, L, d],
+    outputs or caches: token n of sequence b goes to row starts[b] + n (rows
+    outside the cache are not written); positions: int32 [axes, B, N] or None
+    (starts[b] + n); starts, lens: int32 [B] or None (0 and N; tokens past
+    lens[b] are padding and leave the outputs as they are).
+    Returns (q_out, k_out, v_out)."""
+    import torch
+
+    B, N, H, d = q.shape
+    H_kv, dev = k.shape[2], q.device
+    if not q.is_cuda:
+        raise ValueError("q, k and v must be CUDA tensors")
+    made = []
+
+    def out(given, heads, rows):
+        if given is None:
+            given = torch.empty((B, heads, N if rows is None else rows, d), dtype=q.dtype, device=dev)
+            made.append(given)
+        return given
+
+    q_out, k_out = out(q_out, H, N), out(k_out, H_kv, N)
+    L = k_out.shape[2]
+    v_out = out(v_out, H_kv, L) if v is not None else None
+    code = _dtype_code(q)
+    _on(dev, q.dtype, q_out=q_out, k_out=k_out, v_out=v_out)
+    _on(dev, torch.int32, positions=positions, starts=starts, lens=lens)
+    if (q_out.shape != (B, H, N, d) or k_out.shape != (B, H_kv, L, d)
+            or (v_out is not None and v_out.shape != (B, H_kv, L, d))):
+        raise ValueError("q_out must be [B, H, N, d], k_out and v_out [B, H_kv, L, d]")
+    if positions is not None and positions.shape != (len(plan.sections), B, N):
+        raise ValueError("positions must be [axes, B, N]")
+    if (starts is not None and starts.shape != (B,)) or (lens is not None and lens.shape != (B,)):
+        raise ValueError("starts and lens must be [B]")
+    if plan.inv_freq.device != dev or any(w is not None and w.shape[0] != d for w in (plan.q_weight, plan.k_weight)):
+        raise ValueError("the plan's tensors must be on q's device and its weights [d]")
+    desc = plan.desc()
+    for i, t in enumerate((q, k, v)):
+        if t is None:
+            continue
+        if t.device != dev or t.dtype != q.dtype or t.shape != (B, N, H if i == 0 else H_kv, d):
+            raise ValueError("q must be [B, N, H, d] and k, v [B, N, H_kv, d] of one type and device")
+        s = t.stride()
+        if (s[3] != 1 and d > 1) or (s[2] != d and t.shape[2] > 1):
+            raise ValueError("the heads of a token must lie side by side")
+        # (the stride of a dimension of one entry says nothing)
+        desc.token_stride[i] = s[1] if N > 1 else 0
+        desc.batch_stride[i] = s[0] if B > 1 else 0
+    with _Launch(dev, stream) as on:
+        rc = lib().mattn_qk_rope(q.data_ptr(), k.data_ptr(), _ptr(v), q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out),
+                                 _ptr(positions), _ptr(starts), _ptr(lens), B, H, H_kv, N, L, d, code,
+                                 ctypes.byref(desc), on.raw)
+        for t in made:
+            on.own(t)
+    _check(rc)
+    return q_out, k_out, v_out
+
+
+def _decode_outputs(q, out, lse, want_lse, made):
+    import torch
+
+    B, H, d = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    if want_lse and lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    if out.shape != q.shape or (lse is not None and lse.shape != (B, H)):
+        raise ValueError("out must be [B, H, d] and lse [B, H]")
+    _on(q.device, q.dtype, out=out)
+    _on(q.device, torch.float32, lse=lse)
+    return out, lse
+
+
+def _decode_inputs(q, k, seq_lens, sink):
+    """Sizes of a decode call on the cache k [B, H_kv, L, d]; its small tensors checked."""
+    import torch
+
+    if not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [B, H, d]")
+    B, H, d = q.shape
+    if k.dim() != 4 or k.shape[0] != B or k.shape[3] != d:
+        raise ValueError("the cache must be [B, H_kv, L, d]")
+    _on(q.device, q.dtype, q=q, cache=k)
+    _on(q.device, torch.int32, seq_lens=seq_lens)
+    _on(q.device, torch.float32, sink=sink)
+    if (seq_lens is not None and seq_lens.shape != (B,)) or (sink is not None and sink.shape != (H,)):
+        raise ValueError("seq_lens must be [B] and sink [H]")
+    return B, H, k.shape[1], k.shape[2], d
+
+
+def decode_shared_workspace(B: int, H: int, H_kv: int, P: int, L: int, d: int, device="cuda"):
+    """A workspace for ``decode_shared`` calls of these sizes that do not overlap."""
+    return _workspace(_size(lib().mattn_decode_shared_workspace, B, H, H_kv, P, L, d), device)
+
+
+def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens=None, prefix_len=None, sink=None, scale=None,
+                  out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Decode attention of a batch that shares a prefix (``mattn_decode_shared``):
+    one query per sequence against the shared keys and then its own.
+
+    q: CUDA bf16 [B, H, d]; k_prefix, v_prefix: [H_kv, P, d], of which the
+    first ``prefix_len`` (None = all) are read, once for the whole batch;
+    k_cache, v_cache: [B, H_kv, L, d] (L may be 0); seq_lens: CUDA int32 [B]
+    own keys of each sequence (None = L); sink: fp32 [H] or None.
+    Returns (o [B, H, d], lse [B, H] fp32 or None)."""
+    B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
+    if (k_prefix.dim() != 3 or k_prefix.shape[0] != H_kv or k_prefix.shape[2] != d
+            or v_prefix.shape != k_prefix.shape or v_cache.shape != k_cache.shape):
+        raise ValueError("k_prefix, v_prefix must be [H_kv, P, d] and k_cache, v_cache [B, H_kv, L, d]")
+    _on(q.device, q.dtype, k_prefix=k_prefix, v_prefix=v_prefix, v_cache=v_cache)
+    cap = k_prefix.shape[1]
+    P = cap if prefix_len is None else int(prefix_len)
+    made = []
+    out, lse = _decode_outputs(q, out, lse, want_lse, made)
+    with _Launch(q.device, stream) as on:
+        if workspace is None:
+            workspace = decode_shared_workspace(B, H, H_kv, P, L, d, q.device)
+            made.append(workspace)
+        rc = lib().mattn_decode_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
+                                       v_cache.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(seq_lens), B, H, H_kv, P,
+                                       cap, L, d, _dtype_code(q), _ptr(sink), 0.0 if scale is None else float(scale),
+                                       workspace.data_ptr(), _bytes(workspace, q.device), on.raw)
+        for t in made:
+            on.own(t)
+    _check(rc)
+    return out, lse
+
+
+def _bytes(workspace, device) -> int:
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
+def block_means(k_cache, block: int, seq_lens=None, first=None, max_new=None, out=None, stream=None):
+    """The mean key of every block of ``block`` cached keys (``mattn_block_means``).
+
+    k_cache: CUDA bf16 [B, H_kv, L, d]; seq_lens: int32 [B] or None (L).
+    Without ``first`` every block is formed; with first (int32 [B]) and
+    ``max_new`` only those that hold one of the positions first[b] ..
+    first[b] + max_new - 1 that are cached, and the others stay as they are in
+    ``out``.  Returns out [B, H_kv, ceil(L / block), d] (bf16)."""
+    import torch
+
+    if not k_cache.is_cuda or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a CUDA tensor [B, H_kv, L, d]")
+    B, H_kv, L, d = k_cache.shape
+    if block < 1:
+        raise ValueError("block must be >= 1")
+    made = []
+    shape = (B, H_kv, -(-L // block), d)
+    if out is None:
+        if first is not None:
+            raise ValueError("an update of means (first) needs the means to update (out)")
+        out = torch.zeros(shape, dtype=k_cache.dtype, device=k_cache.device)  # blocks past a sequence's end: zeros
+        made.append(out)
+    _on(k_cache.device, k_cache.dtype, k_cache=k_cache, out=out)
+    _on(k_cache.device, torch.int32, seq_lens=seq_lens, first=first)
+    if out.shape != shape or any(t is not None and t.shape != (B,) for t in (seq_lens, first)):
+        raise ValueError("out must be [B, H_kv, ceil(L / block), d]; seq_lens and first [B]")
+    with _Launch(k_cache.device, stream) as on:
+        rc = lib().mattn_block_means(k_cache.data_ptr(), out.data_ptr(), _ptr(seq_lens), _ptr(first), B, H_kv, L, d,
+                                     _dtype_code(k_cache), block, L if max_new is None else int(max_new), on.raw)
+        for t in made:
+            on.own(t)
+    _check(rc)
+    return out
+
+
+def decode_select_workspace(B: int, H: int, H_kv: int, n_blocks: int, d: int, device="cuda"):
+    """A workspace for ``decode_select`` calls of these sizes that do not overlap."""
+    return _workspace(_size(lib().mattn_decode_select_workspace, B, H, H_kv, n_blocks, d), device)
+
+
+def decode_select(q, means, block: int, top_k: int, seq_lens=None, keep_first: int = 1, keep_recent: int = 1, out=None,
+                  workspace=None, stream=None):
+    """The blocks each sequence's new token attends (``mattn_decode_select``):
+    per key/value head the first ``keep_first``, the newest ``keep_recent``
+    and then those whose mean key its query heads score highest, ``top_k`` in
+    all.
+
+    q: CUDA bf16 [B, H, d]; means: [B, H_kv, n_blocks, d] (``block_means``);
+    seq_lens: int32 [B] or None (n_blocks * block).  Returns block ids int32
+    [B, H_kv, top_k], ascending, -1 behind the last one."""
+    import torch
+
+    B, H, H_kv, n, d = _decode_inputs(q, means, seq_lens, None)
+    made = []
+    if out is None:
+        out = torch.empty((B, H_kv, top_k), dtype=torch.int32, device=q.device)
+        made.append(out)
+    _on(q.device, torch.int32, out=out)
+    if out.shape != (B, H_kv, top_k):
+        raise ValueError("out must be [B, H_kv, top_k]")
+    with _Launch(q.device, stream) as on:
+        if workspace is None:
+            workspace = decode_select_workspace(B, H, H_kv, n, d, q.device)
+            made.append(workspace)
+        rc = lib().mattn_decode_select(q.data_ptr(), means.data_ptr(), _ptr(seq_lens), out.data_ptr(), B, H, H_kv, n,
+                                       d, _dtype_code(q), block, top_k, keep_first, keep_recent,
+                                       workspace.data_ptr(), _bytes(workspace, q.device), on.raw)
+        for t in made:
+            on.own(t)
+    _check(rc)
+    return out
+
+
+def decode_blocks_workspace(B: int, H: int, H_kv: int, top_k: int, block: int, d: int, device="cuda"):
+    """A workspace for ``decode_blocks`` calls of these sizes that do not overlap."""
+    return _workspace(_size(lib().mattn_decode_blocks_workspace, B, H, H_kv, top_k, block, d), device)
+
+
+def decode_blocks(q, k_cache, v_cache, block_ids, block: int, seq_lens=None, sink=None, scale=None, out=None,
+                  lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Decode attention over the listed blocks of each cache (``mattn_decode_blocks``).
+
+    q: CUDA bf16 [B, H, d]; k_cache, v_cache: [B, H_kv, L, d]; block_ids:
+    int32 [B, H_kv, top_k] (``decode_select``; entries without a cached key
+    are skipped); seq_lens: int32 [B] or None (L); sink: fp32 [H] or None.
+    Returns (o [B, H, d], lse [B, H] fp32 or None)."""
+    import torch
+
+    B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
+    if v_cache.shape != k_cache.shape or block_ids.dim() != 3 or block_ids.shape[:2] != (B, H_kv):
+        raise ValueError("k_cache and v_cache must be [B, H_kv, L, d] and block_ids [B, H_kv, top_k]")
+    _on(q.device, q.dtype, v_cache=v_cache)
+    _on(q.device, torch.int32, block_ids=block_ids)
+    top_k = block_ids.shape[2]
+    made = []
+    out, lse = _decode_outputs(q, out, lse, want_lse, made)
+    with _Launch(q.device, stream) as on:
+        if workspace is None:
+            workspace = decode_blocks_workspace(B, H, H_kv, top_k, block, d, q.device)
+            made.append(workspace)
+        rc = lib().mattn_decode_blocks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+                                       _ptr(lse), _ptr(seq_lens), block_ids.data_ptr(), B, H, H_kv, L, d,
+                                       _dtype_code(q), block, top_k, _ptr(sink),
+                                       0.0 if scale is None else float(scale), workspace.data_ptr(),
+                                       _bytes(workspace, q.device), on.raw)
+        for t in made:
+            on.own(t)
     _check(rc)
     return out, lse
 

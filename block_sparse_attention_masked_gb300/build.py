@@ -26,7 +26,8 @@ DEBUG_LIB = os.path.join(PKG, "libmattn_debug.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["attention_fwd.cu", "attention_persist.cu", "attention_sp.cu", "rr_select.cu", "received.cu", "decode.cu", "mattn_api.cpp",
-           "mattn_noalloc.cu"]
+           "mattn_noalloc.cu", "qk_rope.cu", "decode_shared.cu", "decode_rows.cu", "block_select.cu",
+           "decode_ops_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,127 @@
+// Launch parameters and host-side plans of the decode step's operators: the
+// head norms with the position rotation (qk_rope.cu), attention over a
+// shared prefix (decode_shared.cu), attention over a sequence's own keys or
+// its selected blocks (decode_rows.cu), block means and block selection
+// (block_select.cu).  Their C entry points are in decode_ops_api.cpp.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mattn {
+
+// Every plan below is a function of the sizes alone, so that the workspace
+// queries need no device: this is the SM count of the one target (GB300).
+constexpr int kPlanSms = 152;
+
+// ------------------------------------------------------------ qk_rope.cu
+struct RopeParams {
+  const void* src[3];       // q, k, v rows: element (b, n, head, c) at b * batch_stride + n * token_stride + head * d + c
+  void* dst[3];             // q: [B][H][N][d]; k, v: [B][H_kv][L][d] (v may be null)
+  int64_t batch_stride[3];  // in elements
+  int64_t token_stride[3];
+  const int32_t* positions; // [axes][B][N] or null: start + n on every axis
+  const int32_t* starts;    // [B] cache row of token 0, or null: 0
+  const int32_t* lens;      // [B] tokens of each sequence, or null: N
+  const float* inv_freq;    // [rot]
+  const float* weight[2];   // [d] norm weights of q and k, or null: no norm
+  int B, H, H_kv, N, L, d;
+  int axes, axis_end[3];    // pairs [axis_end[a - 1], axis_end[a]) turn with axis a
+  int rot;                  // rotated pairs
+  int interleaved;          // pairs (2p, 2p + 1) instead of (p, p + rot)
+  int segs;                 // warps that share one token's rows
+  float eps;
+};
+cudaError_t launch_qk_rope(const RopeParams& p, bool f32, cudaStream_t stream);
+
+// ------------------------------------------------------------ decode_rows.cu
+// Keys per tile of the row kernel (one tile is 16 KB of K and V at d >= 128).
+constexpr int decode_rows_tile(int d) { return d == 256 ? 16 : 32; }
+
+struct DecodeRowsParams {
+  CUtensorMap tk, tv;       // [B*H_kv][L][d] bf16 views, boxes of 64 columns x box_rows keys (128-byte swizzle)
+  const void* q;            // [B][H][d] bf16
+  const int32_t* seq_lens;  // [B] or null: L
+  const int32_t* ids;       // [B*H_kv][top_k] selected blocks, or null: every key in order
+  const float* sink;        // [H] or null (read only when the kernel writes o itself)
+  float* part_o;            // [B*H][n_split][d] states, unnormalised (null: write o)
+  float* part_ml;           // [B*H][n_split][2]
+  void* o;                  // [B][H][d] bf16
+  float* lse;               // [B][H] or null
+  uint32_t* err;
+  unsigned long long timeout_ns;
+  int B, H, H_kv, L;
+  int top_k, block, box_rows;
+  int n_split;
+  float scale_log2;
+};
+// `after`: launched as a programmatic dependent of the stream's previous
+// grid, whose results it does not read; it completes only after that grid.
+cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cudaStream_t stream);
+// Splits of each (sequence, key/value head)'s `keys` list entries.
+int decode_rows_splits(int64_t groups, int64_t keys, int d);
+
+// ------------------------------------------------------------ decode_shared.cu
+struct SharedPlan {
+  int sub;      // 128-row query tiles per CTA (1 or 2)
+  int row_tiles;
+  int n_split;  // key splits
+  int tiles;    // key tiles of the prefix
+  int per_split;
+};
+constexpr int shared_key_tile(int d) { return d == 256 ? 64 : 128; }
+SharedPlan shared_plan(int B, int H, int H_kv, int P, int d);
+
+struct SharedParams {
+  CUtensorMap tk, tv;       // [H_kv][P][d] bf16 views, boxes of 64 columns x shared_key_tile(d) keys
+  const void* q;            // [B][H][d] bf16
+  float* part_o;            // [H_kv * B * G][n_split][d]
+  float* part_ml;           // [H_kv * B * G][n_split][2]
+  uint32_t* err;
+  unsigned long long timeout_ns;
+  int B, H, H_kv, P;
+  int rows;                 // B * G
+  SharedPlan plan;
+  float scale_log2;
+};
+cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stream);
+
+// One merge for all: row (b, h)'s states of the prefix and of its own keys,
+// with the sink logit, into o and the log-sum-exp.
+struct MergeParams {
+  const float *a_o, *a_ml;  // prefix states [H_kv * B * G][na][..]
+  const float *b_o, *b_ml;  // own states [B * H][nb][..]
+  int na, nb;
+  const float* sink;
+  void* o;
+  float* lse;
+  int B, H, H_kv;
+};
+cudaError_t launch_decode_merge(const MergeParams& p, int d, bool after, cudaStream_t stream);
+
+// ------------------------------------------------------------ block_select.cu
+struct BlockMeansParams {
+  const void* k;            // [B*H_kv][L][d] bf16
+  void* means;              // [B*H_kv][n_blocks][d] bf16
+  const int32_t* seq_lens;  // [B] or null: L
+  const int32_t* first;     // [B] or null: 0
+  int B, H_kv, L, n_blocks, block;
+  int max_new, span;        // new keys of a sequence at most, and the blocks they can lie in
+};
+cudaError_t launch_block_means(const BlockMeansParams& p, int d, cudaStream_t stream);
+
+constexpr int kSelectMaxBlocks = 32768;
+
+struct DecodeSelectParams {
+  const void* q;            // [B][H][d] bf16
+  const void* means;        // [B*H_kv][n_blocks][d] bf16
+  const int32_t* seq_lens;  // [B] or null: n_blocks * block
+  float2* scores;           // [B*H_kv][n_blocks] score and bound of its error
+  double* again;            // [B*H_kv][n_blocks] scores formed again in 64 bits
+  int32_t* ids;             // out [B*H_kv][top_k]
+  int B, H, H_kv, n_blocks, block, top_k, keep_first, keep_recent;
+};
+cudaError_t launch_decode_select(const DecodeSelectParams& p, int d, cudaStream_t stream);
+
+}  // namespace mattn

@@ -40,4 +40,17 @@ int prepare_in_place_launch(const void* q, const void* k, const void* v, void* o
 // returns code.
 int report_error(int code, const char* fmt, ...);
 
+// The current device's error word, made on the device's first use; refused
+// (MATTN_ERR_UNSUPPORTED) where that first use is a call under stream capture.
+int device_error_word(cudaStream_t stream, uint32_t** err);
+
+// Limit of a device-side wait (mattn_set_wait_timeout_ns).
+unsigned long long device_wait_timeout_ns();
+
+// View of `heads` bf16 matrices of `rows` x d values, `head_rows` rows apart:
+// boxes of 64 columns x box_rows rows, 128-byte swizzle.  Rows at or past
+// `rows` read as zeros.
+int make_rows_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
+                  int box_rows);
+
 }  // namespace mattn

@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -967,6 +968,37 @@ int report_error(int code, const char* fmt, ...) {
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
   return code;
+}
+
+int device_error_word(cudaStream_t stream, uint32_t** err) try {
+  std::lock_guard<std::mutex> lk(g_mutex);
+  int dev = -1;
+  MATTN_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (g_devices.find(dev) == g_devices.end()) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    MATTN_CUDA(cudaStreamIsCapturing(stream, &cap), "capture status");
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(MATTN_ERR_UNSUPPORTED, "the first call on a device allocates: make one before capturing");
+  }
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc) return rc;
+  *err = st->err;
+  return MATTN_OK;
+} catch (const std::exception& e) {  // no exception leaves a C entry point
+  return fail(MATTN_ERR_CUDA, "device state: %s", e.what());
+}
+
+unsigned long long device_wait_timeout_ns() { return wait_timeout_ns(); }
+
+int make_rows_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
+                  int box_rows) {
+  const int rc = get_encoder();
+  if (rc) return rc;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)head_rows * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  return encode(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int prepare_in_place_launch(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N,

@@ -370,6 +370,140 @@ int mattn_rr_select(const void* q, const void* k, int B, int H, int N, int d, in
                     uint64_t* block_bits, float* block_scores, void* stream);
 
 /*
+ * The decode step's operators: mattn_qk_rope makes a step's queries, keys
+ * and values from the projection's output and appends to the cache;
+ * mattn_decode_shared attends a prefix that all sequences share and each
+ * one's own keys; mattn_block_means, mattn_decode_select and
+ * mattn_decode_blocks attend the blocks of a long cache that each query
+ * scores highest (the decode-time counterpart of mattn_rr_select and
+ * MATTN_BLOCK_SPARSE).  The pages have no counterpart of the first two.
+ *
+ * They take their workspace from the caller and keep nothing between
+ * calls: `workspace` is DEVICE memory, 256-byte aligned, of at least the
+ * bytes that the operator's _workspace function reports for the same sizes
+ * (host only, no device needed; 0 = may be NULL).  Calls that may overlap on
+ * the GPU need workspaces of their own; a captured graph keeps its own
+ * alive.  A first call on a device makes the library's error word and must
+ * not be under stream capture (MATTN_ERR_UNSUPPORTED); every other call can
+ * be captured.  All are asynchronous on `stream`; errors as for mattn_fwd,
+ * MATTN_ERR_CAPACITY for a workspace that is too small.
+ */
+
+/* Norms and rotation of mattn_qk_rope. */
+typedef struct {
+  int32_t n_axes;            /* position axes, 1..3 (text; row and column; time, row, column) */
+  int32_t sections[3];       /* rotated pairs of each axis, in order; their sum R <= d/2 must  */
+                             /* be a multiple of 8; R = 0: no rotation                         */
+  int32_t interleaved;       /* 0: pair p is (x[p], x[p + R]); 1: (x[2p], x[2p + 1])           */
+  float eps;                 /* of the norm; finite, >= 0                                      */
+  const float* inv_freq;     /* DEVICE fp32 [R], finite: pair p turns by position * inv_freq[p] */
+                             /* radians, exact in the position (any int32)                     */
+  const float* q_weight;     /* DEVICE fp32 [d] norm weights, NULL: no norm of the queries     */
+  const float* k_weight;     /* DEVICE fp32 [d], NULL: no norm of the keys                     */
+  int64_t token_stride[3];   /* of q, k, v, in elements: head h of token n of sequence b is at  */
+  int64_t batch_stride[3];   /* b * batch_stride + n * token_stride + h * d; multiples of 16    */
+                             /* bytes, >= 0                                                    */
+} mattn_rope_desc;
+
+/*
+ * mattn_qk_rope -- norms of queries and keys per head with the position
+ * rotation in the same pass, from the projection's layout into the
+ * attention's.  Per row x (one head of one token):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight                (with weights)
+ *   (a, b) <- (a cos t - b sin t, b cos t + a sin t) for each rotated pair
+ * in fp32, rounded once; dims past 2 R are normed but not rotated.  Values
+ * are copied as they are.
+ *   q, k, v    DEVICE [B][N][H or H_kv][d] with the descriptor's strides,
+ *              bf16 or fp32, 16-byte aligned; v may be NULL (with v_out).
+ *   q_out      DEVICE [B][H][N][d].
+ *   k_out, v_out  DEVICE [B][H_kv][L][d]: token n of sequence b goes to row
+ *              starts_b + n (a prefill's outputs have L = N; a cache's L is
+ *              its capacity).  Rows outside 0..L-1 are not written.
+ *   positions  DEVICE int32 [n_axes][B][N], or NULL: starts_b + n on every axis.
+ *   starts     DEVICE int32 [B] or NULL (0).
+ *   lens       DEVICE int32 [B] or NULL (N): tokens n >= lens_b are padding;
+ *              nothing of theirs is read or written.
+ *   d in {32, 64, 80, 96, 128, 256}.  Outputs must not overlap inputs.
+ */
+int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+                  const int32_t* positions, const int32_t* starts, const int32_t* lens, int B, int H, int H_kv, int N,
+                  int L, int d, int dtype, const mattn_rope_desc* desc, void* stream);
+
+/*
+ * mattn_decode_shared -- mattn_decode (MATTN_FULL) for a batch whose
+ * sequences share their first P keys, kept once and read once for the whole
+ * batch: sequence b's query sees the P prefix keys and its own
+ * 0 .. seq_lens_b - 1.
+ *   q, o               DEVICE bf16 [B][H][d];   lse  DEVICE fp32 [B][H] or NULL
+ *   k_prefix, v_prefix DEVICE bf16 [H_kv][P_cap][d], rows 0..P-1 read (P >= 0;
+ *                      P = 0: may be NULL)
+ *   k, v               DEVICE bf16 [B][H_kv][L][d], own keys (L = 0: may be NULL)
+ *   seq_lens           DEVICE int32 [B] or NULL (L); values outside 0..L are
+ *                      clamped.  Rows past a sequence's length are not used.
+ *   sink               DEVICE fp32 [H] sink logits or NULL
+ *   softmax_scale      0 => 1/sqrt(d)
+ *   d in {64, 128, 256}, H / H_kv <= 16, B * H_kv <= 65535.
+ * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).
+ */
+int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                        void* o, float* lse, const int32_t* seq_lens, int B, int H, int H_kv, int P, int P_cap, int L,
+                        int d, int dtype, const float* sink, float softmax_scale, void* workspace,
+                        size_t workspace_bytes, void* stream);
+int mattn_decode_shared_workspace(int B, int H, int H_kv, int P, int L, int d, size_t* bytes_out);
+
+/*
+ * mattn_block_means -- the mean key of each block of `block` keys of a cache,
+ * rounded to bf16 (fp32 sums): block n's mean is over its cached keys
+ * [n * block, min((n + 1) * block, seq_lens_b)).
+ *   k         DEVICE bf16 [B][H_kv][L][d];  seq_lens  DEVICE int32 [B] or NULL (L)
+ *   means     DEVICE bf16 [B][H_kv][ceil(L / block)][d], updated in place:
+ *             the blocks that hold a new key, i.e. one of positions
+ *             first_b .. min(first_b + max_new, seq_lens_b) - 1, are formed
+ *             again from all their keys; every other block is left as it is.
+ *   first     DEVICE int32 [B] or NULL (0; negative values count as 0).
+ *   max_new   new keys of a sequence at most (L: whole caches; 1: a decode step).
+ *   block     a multiple of 16;  d in {64, 128, 256}.
+ */
+int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const int32_t* first, int B, int H_kv,
+                      int L, int d, int dtype, int block, int max_new, void* stream);
+
+/*
+ * mattn_decode_select -- per sequence and key/value head, the blocks its new
+ * token's queries score highest: score_n = max over the group's query heads
+ * g of q_g . means_n.  Of the sequence's ceil(seq_lens_b / block) blocks (at
+ * most n_blocks) the first keep_first and the newest keep_recent are taken,
+ * then those of highest score (lowest index first on equal scores), top_k in
+ * all.  The choice is that of exact arithmetic on the bf16 inputs: scores
+ * next to the border are compared in 64 bits.  A NaN score counts as -inf.
+ *   q          DEVICE bf16 [B][H][d];  means  DEVICE bf16 [B][H_kv][n_blocks][d]
+ *   seq_lens   DEVICE int32 [B] or NULL (n_blocks * block)
+ *   block_ids  DEVICE int32 [B][H_kv][top_k]: block indices, ascending, -1
+ *              behind the last one.
+ *   keep_first + keep_recent <= top_k; n_blocks <= 32768; d, H / H_kv and
+ *   B * H_kv as for mattn_decode_shared.
+ */
+int mattn_decode_select(const void* q, const void* means, const int32_t* seq_lens, int32_t* block_ids, int B, int H,
+                        int H_kv, int n_blocks, int d, int dtype, int block, int top_k, int keep_first,
+                        int keep_recent, void* workspace, size_t workspace_bytes, void* stream);
+int mattn_decode_select_workspace(int B, int H, int H_kv, int n_blocks, int d, size_t* bytes_out);
+
+/*
+ * mattn_decode_blocks -- decode attention over the listed blocks of each
+ * sequence's cache: the query of sequence b, head h sees the cached keys
+ * (positions < seq_lens_b) of the blocks block_ids[b][h / (H / H_kv)][..].
+ * Entries that name no cached key (negative, or at or past the sequence's
+ * end) are skipped; a block listed twice counts twice.
+ *   q, o, lse, sink, softmax_scale, d, H / H_kv, B * H_kv: as for
+ *   mattn_decode_shared;  k, v  DEVICE bf16 [B][H_kv][L][d];
+ *   block_ids  DEVICE int32 [B][H_kv][top_k];  block  a multiple of 16.
+ */
+int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* seq_lens,
+                        const int32_t* block_ids, int B, int H, int H_kv, int L, int d, int dtype, int block,
+                        int top_k, const float* sink, float softmax_scale, void* workspace, size_t workspace_bytes,
+                        void* stream);
+int mattn_decode_blocks_workspace(int B, int H, int H_kv, int top_k, int block, int d, size_t* bytes_out);
+
+/*
  * mattn_plan_schedule -- the schedule mattn_fwd would run for these
  * arguments: one of the MATTN_FLAG_SCHEDULE_* flags (PAIRED, SPLIT, SINGLE,
  * PERSISTENT), the descriptor's own flag if it sets one, else the
