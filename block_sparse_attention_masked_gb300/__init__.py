@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -374,44 +375,58 @@ def decode(q, k_cache, v_cache, mask: PreparedMask, seq_lens=None, out=None, lse
     return out, lse
 
 
-class _Launch:
-    """The device and stream of one call, and its workspace.  The library
-    launches on the current device, so the call runs with the tensors' device
-    current; a workspace made here belongs to torch's allocator and is kept
-    from reuse until a stream other than the current one is done with it."""
+class _Runtime:
+    """What the calls below ask of torch, looked up once: a decode step's
+    calls are short, and the host side of each is a share of its time."""
 
-    def __init__(self, device, stream):
+    def __init__(self):
         import torch
 
-        self.device = device
-        self.raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-        self.other = stream is not None
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def own(self, t):
-        """A tensor made for this call: another stream than the current one uses it."""
-        import torch
-
-        if self.other:
-            t.record_stream(torch.cuda.ExternalStream(self.raw, device=self.device))
-        return t
+        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        self.empty, self.zeros = torch.empty, torch.zeros
+        self.current_device = torch.cuda.current_device
+        # the current stream's handle without a Stream object around it (2 us less a call)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.device_guard = torch.cuda.device
 
 
-def _on(device, dtype, **tensors):
-    """Every given tensor (None is skipped) is a contiguous one of `device` and `dtype`."""
+_runtime = None
+
+
+def _rt() -> _Runtime:
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
+
+
+def _launch(fn, device: int, *args):
+    """Calls fn(*args, stream) with `device` current, on its current stream."""
+    rt = _rt()
+    if rt.current_device() == device:
+        rc = fn(*args, rt.raw_stream(device))
+    else:
+        with rt.device_guard(device):
+            rc = fn(*args, rt.raw_stream(device))
+    if rc:
+        _check(rc)
+
+
+def _on_stream(stream, call, first, *args):
+    """call(first, *args) with the stream of that handle as the current one, so
+    that what the call allocates belongs to it too."""
+    import torch
+
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=first.device)):
+        return call(first, *args)
+
+
+def _on(device: int, dtype, **tensors):
+    """Every given tensor (None is skipped) is a contiguous one of `dtype` on CUDA device `device`."""
     for name, t in tensors.items():
-        if t is not None and (t.device != device or t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+        if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
 
 
 def _ptr(t):
@@ -425,9 +440,11 @@ def _size(fn, *args) -> int:
 
 
 def _workspace(nbytes: int, device):
-    import torch
+    rt = _rt()
+    return rt.empty(max(nbytes, 16), dtype=rt.u8, device=device)
 
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+_STRIDES = struct.Struct("=6q")
 
 
 class RopePlan:
@@ -441,32 +458,30 @@ class RopePlan:
 
     def __init__(self, inv_freq, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False):
-        import torch
-
         if not inv_freq.is_cuda or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be a CUDA fp32 tensor [R]")
         sections = [inv_freq.shape[0]] if sections is None else [int(n) for n in sections]
         if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
             raise ValueError("sections must be 1 to 3 pair counts that add up to inv_freq's length")
-        _on(inv_freq.device, torch.float32, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
+        self.device = inv_freq.get_device()
+        _on(self.device, _rt().f32, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
         for w in (q_weight, k_weight):
-            if w is not None and w.dim() != 1:
+            if w is not None and (w.dim() != 1 or w.shape != (q_weight if q_weight is not None else w).shape):
                 raise ValueError("norm weights must be [d]")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         self.sections, self.eps, self.interleaved = sections, float(eps), bool(interleaved)
-
-    def desc(self) -> RopeDesc:
-        """The descriptor without the call's strides."""
+        w = q_weight if q_weight is not None else k_weight
+        self.width = None if w is None else w.shape[0]
         d = RopeDesc()
-        d.n_axes = len(self.sections)
-        for a, n in enumerate(self.sections):
+        d.n_axes = len(sections)
+        for a, n in enumerate(sections):
             d.sections[a] = n
         d.interleaved = int(self.interleaved)
         d.eps = self.eps
-        d.inv_freq = self.inv_freq.data_ptr()
-        d.q_weight = _ptr(self.q_weight)
-        d.k_weight = _ptr(self.k_weight)
-        return d
+        d.inv_freq = inv_freq.data_ptr()
+        d.q_weight = _ptr(q_weight)
+        d.k_weight = _ptr(k_weight)
+        self._head = bytes(d)[:RopeDesc.token_stride.offset]  # all but a call's strides
 
 
 def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positions=None, starts=None, lens=None,
@@ -483,89 +498,91 @@ def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positio
     (starts[b] + n); starts, lens: int32 [B] or None (0 and N; tokens past
     lens[b] are padding and leave the outputs as they are).
     Returns (q_out, k_out, v_out)."""
-    import torch
-
+    if stream is not None:
+        return _on_stream(stream, qk_rope, q, k, v, plan, q_out, k_out, v_out, positions, starts, lens)
+    rt = _rt()
     B, N, H, d = q.shape
-    H_kv, dev = k.shape[2], q.device
-    if not q.is_cuda:
+    H_kv, dev, t = k.shape[2], q.get_device(), q.dtype
+    if dev < 0:
         raise ValueError("q, k and v must be CUDA tensors")
-    made = []
-
-    def out(given, heads, rows):
-        if given is None:
-            given = torch.empty((B, heads, N if rows is None else rows, d), dtype=q.dtype, device=dev)
-            made.append(given)
-        return given
-
-    q_out, k_out = out(q_out, H, N), out(k_out, H_kv, N)
+    if plan.device != dev or (plan.width is not None and plan.width != d):
+        raise ValueError("the plan's tensors must be on q's device and its weights [d]")
+    strides = []
+    for x, heads in ((q, H), (k, H_kv), (v, H_kv)):
+        if x is None:
+            strides.append((0, 0, 0, 0))
+            continue
+        s = x.stride()
+        if x.dtype is not t or x.get_device() != dev or x.shape != (B, N, heads, d):
+            raise ValueError("q must be [B, N, H, d] and k, v [B, N, H_kv, d] of one type and device")
+        if s[3] != 1 or (s[2] != d and heads > 1):
+            raise ValueError("the heads of a token must lie side by side")
+        strides.append(s)
+    if q_out is None:
+        q_out = rt.empty((B, H, N, d), dtype=t, device=q.device)
+    if k_out is None:
+        k_out = rt.empty((B, H_kv, N, d), dtype=t, device=q.device)
     L = k_out.shape[2]
-    v_out = out(v_out, H_kv, L) if v is not None else None
-    code = _dtype_code(q)
-    _on(dev, q.dtype, q_out=q_out, k_out=k_out, v_out=v_out)
-    _on(dev, torch.int32, positions=positions, starts=starts, lens=lens)
+    if v is None:
+        v_out = None
+    elif v_out is None:
+        v_out = rt.empty((B, H_kv, L, d), dtype=t, device=q.device)
+    _on(dev, t, q_out=q_out, k_out=k_out, v_out=v_out)
+    _on(dev, rt.i32, positions=positions, starts=starts, lens=lens)
     if (q_out.shape != (B, H, N, d) or k_out.shape != (B, H_kv, L, d)
-            or (v_out is not None and v_out.shape != (B, H_kv, L, d))):
+            or (v_out is not None and v_out.shape != k_out.shape)):
         raise ValueError("q_out must be [B, H, N, d], k_out and v_out [B, H_kv, L, d]")
     if positions is not None and positions.shape != (len(plan.sections), B, N):
         raise ValueError("positions must be [axes, B, N]")
     if (starts is not None and starts.shape != (B,)) or (lens is not None and lens.shape != (B,)):
         raise ValueError("starts and lens must be [B]")
-    if plan.inv_freq.device != dev or any(w is not None and w.shape[0] != d for w in (plan.q_weight, plan.k_weight)):
-        raise ValueError("the plan's tensors must be on q's device and its weights [d]")
-    desc = plan.desc()
-    for i, t in enumerate((q, k, v)):
-        if t is None:
-            continue
-        if t.device != dev or t.dtype != q.dtype or t.shape != (B, N, H if i == 0 else H_kv, d):
-            raise ValueError("q must be [B, N, H, d] and k, v [B, N, H_kv, d] of one type and device")
-        s = t.stride()
-        if (s[3] != 1 and d > 1) or (s[2] != d and t.shape[2] > 1):
-            raise ValueError("the heads of a token must lie side by side")
-        # (the stride of a dimension of one entry says nothing)
-        desc.token_stride[i] = s[1] if N > 1 else 0
-        desc.batch_stride[i] = s[0] if B > 1 else 0
-    with _Launch(dev, stream) as on:
-        rc = lib().mattn_qk_rope(q.data_ptr(), k.data_ptr(), _ptr(v), q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out),
-                                 _ptr(positions), _ptr(starts), _ptr(lens), B, H, H_kv, N, L, d, code,
-                                 ctypes.byref(desc), on.raw)
-        for t in made:
-            on.own(t)
-    _check(rc)
+    (qb, qt, _, _), (kb, kt, _, _), (vb, vt, _, _) = strides
+    if N == 1:  # the stride of a dimension of one entry says nothing
+        qt = kt = vt = 0
+    if B == 1:
+        qb = kb = vb = 0
+    desc = RopeDesc.from_buffer_copy(plan._head + _STRIDES.pack(qt, kt, vt, qb, kb, vb))
+    _launch(lib().mattn_qk_rope, dev, q.data_ptr(), k.data_ptr(), _ptr(v), q_out.data_ptr(),
+            k_out.data_ptr(), _ptr(v_out), _ptr(positions), _ptr(starts), _ptr(lens), B, H, H_kv, N, L, d,
+            _dtype_code(q), ctypes.byref(desc))
     return q_out, k_out, v_out
 
 
-def _decode_outputs(q, out, lse, want_lse, made):
-    import torch
-
-    B, H, d = q.shape
+def _decode_outputs(q, out, lse, want_lse):
+    rt = _rt()
+    shape = q.shape
     if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
-    if want_lse and lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        made.append(lse)
-    if out.shape != q.shape or (lse is not None and lse.shape != (B, H)):
-        raise ValueError("out must be [B, H, d] and lse [B, H]")
-    _on(q.device, q.dtype, out=out)
-    _on(q.device, torch.float32, lse=lse)
+        out = rt.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape:
+        raise ValueError("out must be [B, H, d]")
+    if lse is not None:
+        if lse.shape != shape[:2]:
+            raise ValueError("lse must be [B, H]")
+    elif want_lse:
+        lse = rt.empty(shape[:2], dtype=rt.f32, device=q.device)
     return out, lse
 
 
 def _decode_inputs(q, k, seq_lens, sink):
-    """Sizes of a decode call on the cache k [B, H_kv, L, d]; its small tensors checked."""
-    import torch
-
-    if not q.is_cuda or q.dim() != 3:
+    """Device and sizes of a decode call on the cache k [B, H_kv, L, d]."""
+    dev = q.get_device()
+    if dev < 0 or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [B, H, d]")
     B, H, d = q.shape
-    if k.dim() != 4 or k.shape[0] != B or k.shape[3] != d:
+    if k.dim() != 4:
         raise ValueError("the cache must be [B, H_kv, L, d]")
-    _on(q.device, q.dtype, q=q, cache=k)
-    _on(q.device, torch.int32, seq_lens=seq_lens)
-    _on(q.device, torch.float32, sink=sink)
+    Bk, H_kv, L, dk = k.shape
+    if Bk != B or dk != d:
+        raise ValueError("the cache must be [B, H_kv, L, d]")
     if (seq_lens is not None and seq_lens.shape != (B,)) or (sink is not None and sink.shape != (H,)):
         raise ValueError("seq_lens must be [B] and sink [H]")
-    return B, H, k.shape[1], k.shape[2], d
+    return dev, B, H, H_kv, L, d
+
+
+def _bytes(workspace, device: int) -> int:
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{device}")
+    return workspace.numel() * workspace.element_size()
 
 
 def decode_shared_workspace(B: int, H: int, H_kv: int, P: int, L: int, d: int, device="cuda"):
@@ -583,33 +600,26 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens=None, prefix
     k_cache, v_cache: [B, H_kv, L, d] (L may be 0); seq_lens: CUDA int32 [B]
     own keys of each sequence (None = L); sink: fp32 [H] or None.
     Returns (o [B, H, d], lse [B, H] fp32 or None)."""
-    B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
-    if (k_prefix.dim() != 3 or k_prefix.shape[0] != H_kv or k_prefix.shape[2] != d
+    if stream is not None:
+        return _on_stream(stream, decode_shared, q, k_prefix, v_prefix, k_cache, v_cache, seq_lens, prefix_len, sink, scale,
+                          out, lse, want_lse, workspace)
+    rt = _rt()
+    dev, B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
+    if (k_prefix.dim() != 3 or k_prefix.shape != (H_kv, cap := k_prefix.shape[1], d)
             or v_prefix.shape != k_prefix.shape or v_cache.shape != k_cache.shape):
         raise ValueError("k_prefix, v_prefix must be [H_kv, P, d] and k_cache, v_cache [B, H_kv, L, d]")
-    _on(q.device, q.dtype, k_prefix=k_prefix, v_prefix=v_prefix, v_cache=v_cache)
-    cap = k_prefix.shape[1]
     P = cap if prefix_len is None else int(prefix_len)
-    made = []
-    out, lse = _decode_outputs(q, out, lse, want_lse, made)
-    with _Launch(q.device, stream) as on:
-        if workspace is None:
-            workspace = decode_shared_workspace(B, H, H_kv, P, L, d, q.device)
-            made.append(workspace)
-        rc = lib().mattn_decode_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
-                                       v_cache.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(seq_lens), B, H, H_kv, P,
-                                       cap, L, d, _dtype_code(q), _ptr(sink), 0.0 if scale is None else float(scale),
-                                       workspace.data_ptr(), _bytes(workspace, q.device), on.raw)
-        for t in made:
-            on.own(t)
-    _check(rc)
+    out, lse = _decode_outputs(q, out, lse, want_lse)
+    _on(dev, q.dtype, q=q, k_prefix=k_prefix, v_prefix=v_prefix, k_cache=k_cache, v_cache=v_cache, out=out)
+    _on(dev, rt.f32, lse=lse, sink=sink)
+    _on(dev, rt.i32, seq_lens=seq_lens)
+    if workspace is None:
+        workspace = decode_shared_workspace(B, H, H_kv, P, L, d, q.device)
+    _launch(lib().mattn_decode_shared, dev, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(seq_lens), B, H, H_kv, P, cap, L, d,
+            _dtype_code(q), _ptr(sink), 0.0 if scale is None else float(scale), workspace.data_ptr(),
+            _bytes(workspace, dev))
     return out, lse
-
-
-def _bytes(workspace, device) -> int:
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
-    return workspace.numel() * workspace.element_size()
 
 
 def block_means(k_cache, block: int, seq_lens=None, first=None, max_new=None, out=None, stream=None):
@@ -620,30 +630,28 @@ def block_means(k_cache, block: int, seq_lens=None, first=None, max_new=None, ou
     ``max_new`` only those that hold one of the positions first[b] ..
     first[b] + max_new - 1 that are cached, and the others stay as they are in
     ``out``.  Returns out [B, H_kv, ceil(L / block), d] (bf16)."""
-    import torch
-
-    if not k_cache.is_cuda or k_cache.dim() != 4:
+    if stream is not None:
+        return _on_stream(stream, block_means, k_cache, block, seq_lens, first, max_new, out)
+    rt = _rt()
+    dev = k_cache.get_device()
+    if dev < 0 or k_cache.dim() != 4:
         raise ValueError("k_cache must be a CUDA tensor [B, H_kv, L, d]")
     B, H_kv, L, d = k_cache.shape
     if block < 1:
         raise ValueError("block must be >= 1")
-    made = []
     shape = (B, H_kv, -(-L // block), d)
     if out is None:
         if first is not None:
             raise ValueError("an update of means (first) needs the means to update (out)")
-        out = torch.zeros(shape, dtype=k_cache.dtype, device=k_cache.device)  # blocks past a sequence's end: zeros
-        made.append(out)
-    _on(k_cache.device, k_cache.dtype, k_cache=k_cache, out=out)
-    _on(k_cache.device, torch.int32, seq_lens=seq_lens, first=first)
-    if out.shape != shape or any(t is not None and t.shape != (B,) for t in (seq_lens, first)):
+        # blocks past a sequence's end: zeros
+        out = rt.zeros(shape, dtype=k_cache.dtype, device=k_cache.device)
+    _on(dev, k_cache.dtype, k_cache=k_cache, out=out)
+    _on(dev, rt.i32, seq_lens=seq_lens, first=first)
+    if (out.shape != shape or (seq_lens is not None and seq_lens.shape != (B,))
+            or (first is not None and first.shape != (B,))):
         raise ValueError("out must be [B, H_kv, ceil(L / block), d]; seq_lens and first [B]")
-    with _Launch(k_cache.device, stream) as on:
-        rc = lib().mattn_block_means(k_cache.data_ptr(), out.data_ptr(), _ptr(seq_lens), _ptr(first), B, H_kv, L, d,
-                                     _dtype_code(k_cache), block, L if max_new is None else int(max_new), on.raw)
-        for t in made:
-            on.own(t)
-    _check(rc)
+    _launch(lib().mattn_block_means, dev, k_cache.data_ptr(), out.data_ptr(), _ptr(seq_lens), _ptr(first),
+            B, H_kv, L, d, _dtype_code(k_cache), block, L if max_new is None else int(max_new))
     return out
 
 
@@ -662,26 +670,21 @@ def decode_select(q, means, block: int, top_k: int, seq_lens=None, keep_first: i
     q: CUDA bf16 [B, H, d]; means: [B, H_kv, n_blocks, d] (``block_means``);
     seq_lens: int32 [B] or None (n_blocks * block).  Returns block ids int32
     [B, H_kv, top_k], ascending, -1 behind the last one."""
-    import torch
-
-    B, H, H_kv, n, d = _decode_inputs(q, means, seq_lens, None)
-    made = []
+    if stream is not None:
+        return _on_stream(stream, decode_select, q, means, block, top_k, seq_lens, keep_first, keep_recent, out, workspace)
+    rt = _rt()
+    dev, B, H, H_kv, n, d = _decode_inputs(q, means, seq_lens, None)
     if out is None:
-        out = torch.empty((B, H_kv, top_k), dtype=torch.int32, device=q.device)
-        made.append(out)
-    _on(q.device, torch.int32, out=out)
+        out = rt.empty((B, H_kv, max(top_k, 0)), dtype=rt.i32, device=q.device)
+    _on(dev, q.dtype, q=q, means=means)
+    _on(dev, rt.i32, seq_lens=seq_lens, out=out)
     if out.shape != (B, H_kv, top_k):
         raise ValueError("out must be [B, H_kv, top_k]")
-    with _Launch(q.device, stream) as on:
-        if workspace is None:
-            workspace = decode_select_workspace(B, H, H_kv, n, d, q.device)
-            made.append(workspace)
-        rc = lib().mattn_decode_select(q.data_ptr(), means.data_ptr(), _ptr(seq_lens), out.data_ptr(), B, H, H_kv, n,
-                                       d, _dtype_code(q), block, top_k, keep_first, keep_recent,
-                                       workspace.data_ptr(), _bytes(workspace, q.device), on.raw)
-        for t in made:
-            on.own(t)
-    _check(rc)
+    if workspace is None:
+        workspace = decode_select_workspace(B, H, H_kv, n, d, q.device)
+    _launch(lib().mattn_decode_select, dev, q.data_ptr(), means.data_ptr(), _ptr(seq_lens),
+            out.data_ptr(), B, H, H_kv, n, d, _dtype_code(q), block, top_k, keep_first, keep_recent,
+            workspace.data_ptr(), _bytes(workspace, dev))
     return out
 
 
@@ -698,28 +701,22 @@ def decode_blocks(q, k_cache, v_cache, block_ids, block: int, seq_lens=None, sin
     int32 [B, H_kv, top_k] (``decode_select``; entries without a cached key
     are skipped); seq_lens: int32 [B] or None (L); sink: fp32 [H] or None.
     Returns (o [B, H, d], lse [B, H] fp32 or None)."""
-    import torch
-
-    B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
-    if v_cache.shape != k_cache.shape or block_ids.dim() != 3 or block_ids.shape[:2] != (B, H_kv):
+    if stream is not None:
+        return _on_stream(stream, decode_blocks, q, k_cache, v_cache, block_ids, block, seq_lens, sink, scale, out, lse, want_lse,
+                          workspace)
+    rt = _rt()
+    dev, B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
+    if block_ids.dim() != 3 or block_ids.shape != (B, H_kv, top_k := block_ids.shape[2]) or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must be [B, H_kv, L, d] and block_ids [B, H_kv, top_k]")
-    _on(q.device, q.dtype, v_cache=v_cache)
-    _on(q.device, torch.int32, block_ids=block_ids)
-    top_k = block_ids.shape[2]
-    made = []
-    out, lse = _decode_outputs(q, out, lse, want_lse, made)
-    with _Launch(q.device, stream) as on:
-        if workspace is None:
-            workspace = decode_blocks_workspace(B, H, H_kv, top_k, block, d, q.device)
-            made.append(workspace)
-        rc = lib().mattn_decode_blocks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-                                       _ptr(lse), _ptr(seq_lens), block_ids.data_ptr(), B, H, H_kv, L, d,
-                                       _dtype_code(q), block, top_k, _ptr(sink),
-                                       0.0 if scale is None else float(scale), workspace.data_ptr(),
-                                       _bytes(workspace, q.device), on.raw)
-        for t in made:
-            on.own(t)
-    _check(rc)
+    out, lse = _decode_outputs(q, out, lse, want_lse)
+    _on(dev, q.dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    _on(dev, rt.f32, lse=lse, sink=sink)
+    _on(dev, rt.i32, seq_lens=seq_lens, block_ids=block_ids)
+    if workspace is None:
+        workspace = decode_blocks_workspace(B, H, H_kv, top_k, block, d, q.device)
+    _launch(lib().mattn_decode_blocks, dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            out.data_ptr(), _ptr(lse), _ptr(seq_lens), block_ids.data_ptr(), B, H, H_kv, L, d, _dtype_code(q), block,
+            top_k, _ptr(sink), 0.0 if scale is None else float(scale), workspace.data_ptr(), _bytes(workspace, dev))
     return out, lse
 
 

@@ -9,11 +9,28 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mattn {
 
 // Every plan below is a function of the sizes alone, so that the workspace
 // queries need no device: this is the SM count of the one target (GB300).
 constexpr int kPlanSms = 152;
+
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device
+// (the attribute call costs as much as a tenth of a launch).  `done`: the
+// kernel's own bit set, one bit per device; devices past 64 ask every time.
+template <class Kernel>
+cudaError_t allow_shared(Kernel kern, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ------------------------------------------------------------ qk_rope.cu
 struct RopeParams {

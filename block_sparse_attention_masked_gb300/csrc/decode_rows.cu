@@ -400,7 +400,8 @@ cudaError_t launch_nt(const DecodeRowsParams& p, bool after, cudaStream_t stream
   static_assert(kRowWarps * 8 * NT * D * 4 <= Geo::kRing, "the warps' O must fit in the ring");
   const size_t smem = 1024 + Geo::kRing + sizeof(RowBar) + kRowWarps * 8 * NT * 2 * sizeof(float);
   auto kern = decode_rows_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_split, p.B * p.H_kv);

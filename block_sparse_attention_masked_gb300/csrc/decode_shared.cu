@@ -387,7 +387,8 @@ cudaError_t launch_sub(const SharedParams& p, cudaStream_t stream) {
   const size_t smem = 1024 + (size_t)SUB * Geo::kQTile + (size_t)Geo::kSlots * Geo::kSlot + sizeof(ShBar);
   static_assert(1024 + SUB * Geo::kQTile + Geo::kSlots * Geo::kSlot + sizeof(ShBar) <= 227 * 1024, "shared memory");
   auto kern = decode_shared_kernel<D, SUB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
   kern<<<p.plan.row_tiles * p.plan.n_split * p.H_kv, Geo::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
