@@ -53,46 +53,49 @@ struct RopeParams {
 cudaError_t launch_qk_rope(const RopeParams& p, bool f32, cudaStream_t stream);
 
 // ------------------------------------------------------------ decode_rows.cu
-// Keys per tile of the row kernel (one tile is 16 KB of K and V at d >= 128).
-constexpr int decode_rows_tile(int d) { return d == 256 ? 16 : 32; }
+// Keys per tile (8 KB of K and V, 16 KB at d = 256) and warps per SM of the row
+// kernel: each warp has two tiles in flight, 192 KB per SM.
+constexpr int decode_rows_tile(int d) { return d == 64 ? 32 : 16; }
+constexpr int decode_rows_warps(int d) { return d == 256 ? 6 : 12; }
 
 struct DecodeRowsParams {
-  CUtensorMap tk, tv;       // [B*H_kv][L][d] bf16 views, boxes of 64 columns x box_rows keys (128-byte swizzle)
+  CUtensorMap tk, tv;       // [B*H_kv][L][d] bf16 views, boxes of 64 columns x 16 keys (128-byte swizzle)
   const void* q;            // [B][H][d] bf16
   const int32_t* seq_lens;  // [B] or null: L
   const int32_t* ids;       // [B*H_kv][top_k] selected blocks, or null: every key in order
-  const float* sink;        // [H] or null (read only when the kernel writes o itself)
-  float* part_o;            // [B*H][n_split][d] states, unnormalised (null: write o)
-  float* part_ml;           // [B*H][n_split][2]
-  void* o;                  // [B][H][d] bf16
-  float* lse;               // [B][H] or null
+  float* part_o;            // [warps + B*H_kv][G][d] states, unnormalised (decode_rows.cuh)
+  float* part_ml;           // [warps + B*H_kv][G][2]
+  int* group_start;         // [B*H_kv] number of each list's first tile, then the tiles of a warp's share
   uint32_t* err;
   unsigned long long timeout_ns;
   int B, H, H_kv, L;
-  int top_k, block, box_rows;
-  int n_split;
+  int top_k, block, box16;  // block = 16 box16 keys
+  int list_tiles;           // tiles of a list of top_k blocks (0: by the sequence's length)
+  int min_tiles;            // of a warp's share
+  int ctas;                 // of the grid
   float scale_log2;
 };
 // `after`: launched as a programmatic dependent of the stream's previous
 // grid, whose results it does not read; it completes only after that grid.
 cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cudaStream_t stream);
-// Splits of each (sequence, key/value head)'s `keys` list entries.
-int decode_rows_splits(int64_t groups, int64_t keys, int d);
 
 // ------------------------------------------------------------ decode_shared.cu
 struct SharedPlan {
-  int sub;      // 128-row query tiles per CTA (1 or 2)
+  int sub;      // query tiles per CTA (1 or 2)
+  int seqs;     // sequences of a query tile, 128 / G: seqs * G of its 128 rows are used
   int row_tiles;
   int n_split;  // key splits
   int tiles;    // key tiles of the prefix
   int per_split;
+  int own_ctas; // CTAs of the own keys' grid
 };
 constexpr int shared_key_tile(int d) { return d == 256 ? 64 : 128; }
-SharedPlan shared_plan(int B, int H, int H_kv, int P, int d);
+SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d);
 
 struct SharedParams {
   CUtensorMap tk, tv;       // [H_kv][P][d] bf16 views, boxes of 64 columns x shared_key_tile(d) keys
-  const void* q;            // [B][H][d] bf16
+  CUtensorMap tq;           // [B][H][d] bf16 view, boxes of 64 columns x G heads x plan.seqs sequences
+  CUtensorMap to;           // part_o as [H_kv][B * G][n_split][d]: boxes of 32 columns (128 bytes) x 32 rows
   float* part_o;            // [H_kv * B * G][n_split][d]
   float* part_ml;           // [H_kv * B * G][n_split][2]
   uint32_t* err;
@@ -104,12 +107,15 @@ struct SharedParams {
 };
 cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stream);
 
-// One merge for all: row (b, h)'s states of the prefix and of its own keys,
+// One merge for all: row (b, h)'s states of the prefix and of its own list,
 // with the sink logit, into o and the log-sum-exp.
 struct MergeParams {
-  const float *a_o, *a_ml;  // prefix states [H_kv * B * G][na][..]
-  const float *b_o, *b_ml;  // own states [B * H][nb][..]
-  int na, nb;
+  const float *a_o, *a_ml;   // prefix states [H_kv * B * G][na][..]
+  const float *b_o, *b_ml;   // own states (DecodeRowsParams)
+  const int* group_start;    // DecodeRowsParams'; null: no own lists
+  const int32_t* seq_lens;
+  int na;
+  int L, list_tiles;
   const float* sink;
   void* o;
   float* lse;

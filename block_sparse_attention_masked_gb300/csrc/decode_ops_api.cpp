@@ -72,18 +72,41 @@ size_t state_bytes(int64_t rows, int n, int d) {
   return round256((size_t)rows * n * d * 4) + round256((size_t)rows * n * 8);
 }
 
+// States of the own lists: a slot for each (warp, group) piece, then the
+// lists' starts (DecodeRowsParams).
+struct RowsLayout {
+  int warps;
+  size_t o_bytes, ml_bytes, start_bytes;
+  size_t all() const { return o_bytes + ml_bytes + start_bytes; }
+};
+
+RowsLayout rows_layout(int64_t groups, int G, int warps, int d) {
+  RowsLayout r;
+  r.warps = warps;
+  r.o_bytes = round256((size_t)(warps + groups) * G * d * 4);
+  r.ml_bytes = round256((size_t)(warps + groups) * G * 8);
+  r.start_bytes = round256((size_t)(groups + 1) * 4);
+  return r;
+}
+
+void place_rows(DecodeRowsParams* p, const RowsLayout& r, char* ws) {
+  p->part_o = reinterpret_cast<float*>(ws);
+  p->part_ml = reinterpret_cast<float*>(ws + r.o_bytes);
+  p->group_start = reinterpret_cast<int*>(ws + r.o_bytes + r.ml_bytes);
+}
+
 struct SharedLayout {
   SharedPlan prefix;
-  int own_splits;
+  RowsLayout own;
   size_t prefix_bytes, own_bytes;
 };
 
 SharedLayout shared_layout(int B, int H, int H_kv, int P, int L, int d) {
   SharedLayout s;
-  s.prefix = shared_plan(B, H, H_kv, P, d);
-  s.own_splits = L > 0 ? decode_rows_splits((int64_t)B * H_kv, L, d) : 0;
+  s.prefix = shared_plan(B, H, H_kv, P, L, d);
   s.prefix_bytes = P > 0 ? state_bytes((int64_t)B * H, s.prefix.n_split, d) : 0;
-  s.own_bytes = L > 0 ? state_bytes((int64_t)B * H, s.own_splits, d) : 0;
+  s.own = rows_layout((int64_t)B * H_kv, H / H_kv, s.prefix.own_ctas * decode_rows_warps(d), d);
+  s.own_bytes = L > 0 ? s.own.all() : 0;
   return s;
 }
 
@@ -95,6 +118,11 @@ int check_shared(int B, int H, int H_kv, int P, int L, int d, int dtype) {
   return MATTN_OK;
 }
 
+int list_tiles(int top_k, int block, int d) {
+  const int tk = decode_rows_tile(d);
+  return (int)(((int64_t)top_k * block + tk - 1) / tk);
+}
+
 int check_blocks(int B, int H, int H_kv, int top_k, int block, int d, int dtype) {
   int rc = check_heads("decode_blocks", B, H, H_kv, d, dtype);
   if (rc) return rc;
@@ -103,6 +131,9 @@ int check_blocks(int B, int H, int H_kv, int top_k, int block, int d, int dtype)
   if (top_k < 1) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: top_k must be >= 1");
   if ((int64_t)top_k * block > kMaxRows)
     return report_error(MATTN_ERR_UNSUPPORTED, "decode_blocks: top_k * block exceeds 2^30");
+  // the tiles of all lists are numbered in 32 bits
+  if ((int64_t)B * H_kv * list_tiles(top_k, block, d) > INT32_MAX)
+    return report_error(MATTN_ERR_UNSUPPORTED, "decode_blocks: more than 2^31 - 1 key tiles in all lists");
   return MATTN_OK;
 }
 
@@ -235,9 +266,10 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     memset(&sp, 0, sizeof(sp));
     if ((rc = make_rows_map(&sp.tk, k_prefix, d, P, P_cap, H_kv, shared_key_tile(d)))) return rc;
     if ((rc = make_rows_map(&sp.tv, v_prefix, d, P, P_cap, H_kv, shared_key_tile(d)))) return rc;
-    sp.q = q;
+    if ((rc = make_box_map(&sp.tq, q, d, H, H, B, H / H_kv, s.prefix.seqs))) return rc;
     sp.part_o = reinterpret_cast<float*>(ws);
     sp.part_ml = reinterpret_cast<float*>(ws + round256((size_t)rows * s.prefix.n_split * d * 4));
+    if ((rc = make_state_map(&sp.to, sp.part_o, d, s.prefix.n_split, rows / H_kv, H_kv))) return rc;
     sp.err = err;
     sp.timeout_ns = device_wait_timeout_ns();
     sp.B = B; sp.H = H; sp.H_kv = H_kv; sp.P = P;
@@ -249,24 +281,25 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     m.na = s.prefix.n_split;
   }
   if (L > 0) {
-    char* own = ws + s.prefix_bytes;
     memset(&rp, 0, sizeof(rp));
-    rp.box_rows = decode_rows_tile(d);
-    if ((rc = make_rows_map(&rp.tk, k, d, L, L, (int64_t)B * H_kv, rp.box_rows))) return rc;
-    if ((rc = make_rows_map(&rp.tv, v, d, L, L, (int64_t)B * H_kv, rp.box_rows))) return rc;
+    if ((rc = make_rows_map(&rp.tk, k, d, L, L, (int64_t)B * H_kv, 16))) return rc;
+    if ((rc = make_rows_map(&rp.tv, v, d, L, L, (int64_t)B * H_kv, 16))) return rc;
     rp.q = q;
     rp.seq_lens = seq_lens;
-    rp.part_o = reinterpret_cast<float*>(own);
-    rp.part_ml = reinterpret_cast<float*>(own + round256((size_t)rows * s.own_splits * d * 4));
+    place_rows(&rp, s.own, ws + s.prefix_bytes);
     rp.err = err;
     rp.timeout_ns = device_wait_timeout_ns();
     rp.B = B; rp.H = H; rp.H_kv = H_kv; rp.L = L;
-    rp.block = 1;
-    rp.n_split = s.own_splits;
+    rp.block = 16;
+    rp.box16 = 1;
+    rp.min_tiles = 1;
+    rp.ctas = s.prefix.own_ctas;
     rp.scale_log2 = scale_log2(softmax_scale, d);
     m.b_o = rp.part_o;
     m.b_ml = rp.part_ml;
-    m.nb = s.own_splits;
+    m.group_start = rp.group_start;
+    m.seq_lens = seq_lens;
+    m.L = L;
   }
   m.sink = sink;
   m.o = o;
@@ -357,8 +390,7 @@ int mattn_decode_blocks_workspace(int B, int H, int H_kv, int top_k, int block, 
   if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: bytes_out is NULL");
   const int rc = check_blocks(B, H, H_kv, top_k, block, d, MATTN_BF16);
   if (rc) return rc;
-  const int ns = decode_rows_splits((int64_t)B * H_kv, (int64_t)top_k * block, d);
-  *bytes_out = ns > 1 ? state_bytes((int64_t)B * H, ns, d) : 0;
+  *bytes_out = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d).all();
   return MATTN_OK;
 }
 
@@ -377,41 +409,37 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   if ((rc = check_small("decode_blocks", lse, seq_lens, sink))) return rc;
   if (!aligned(block_ids, 4)) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: block_ids must be 4-byte aligned");
   if ((rc = check_scale("decode_blocks", softmax_scale))) return rc;
-  const int64_t rows = (int64_t)B * H;
-  const int ns = decode_rows_splits((int64_t)B * H_kv, (int64_t)top_k * block, d);
-  const size_t need = ns > 1 ? state_bytes(rows, ns, d) : 0;
-  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, need))) return rc;
+  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d);
+  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, lay.all()))) return rc;
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   DecodeRowsParams p;
   memset(&p, 0, sizeof(p));
-  p.box_rows = block % decode_rows_tile(d) == 0 ? decode_rows_tile(d) : 16;
-  if ((rc = make_rows_map(&p.tk, k, d, L, L, (int64_t)B * H_kv, p.box_rows))) return rc;
-  if ((rc = make_rows_map(&p.tv, v, d, L, L, (int64_t)B * H_kv, p.box_rows))) return rc;
+  if ((rc = make_rows_map(&p.tk, k, d, L, L, (int64_t)B * H_kv, 16))) return rc;
+  if ((rc = make_rows_map(&p.tv, v, d, L, L, (int64_t)B * H_kv, 16))) return rc;
   p.q = q;
   p.seq_lens = seq_lens;
   p.ids = block_ids;
-  p.sink = sink;
-  p.o = o;
-  p.lse = lse;
+  place_rows(&p, lay, static_cast<char*>(workspace));
   p.err = err;
   p.timeout_ns = device_wait_timeout_ns();
   p.B = B; p.H = H; p.H_kv = H_kv; p.L = L;
   p.top_k = top_k;
   p.block = block;
-  p.n_split = ns;
+  p.box16 = block / 16;
+  p.list_tiles = list_tiles(top_k, block, d);
+  p.min_tiles = 1;
+  p.ctas = kPlanSms;
   p.scale_log2 = scale_log2(softmax_scale, d);
-  if (ns > 1) {
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256((size_t)rows * ns * d * 4));
-  }
   if ((rc = launched(launch_decode_rows(p, d, false, stream), "block launch"))) return rc;
-  if (ns == 1) return MATTN_OK;
   MergeParams m;
   memset(&m, 0, sizeof(m));
   m.b_o = p.part_o;
   m.b_ml = p.part_ml;
-  m.nb = ns;
+  m.group_start = p.group_start;
+  m.seq_lens = seq_lens;
+  m.L = L;
+  m.list_tiles = p.list_tiles;
   m.sink = sink;
   m.o = o;
   m.lse = lse;

@@ -55,10 +55,13 @@ struct ShGeo {
   static constexpr int kThreads = 128 + 128 * SUB;
   static constexpr int kOcol = 2 * KT > 256 ? 2 * KT : 256;  // first tensor-memory column of O
   static_assert(kOcol + SUB * D <= 512, "tensor memory");
+  static_assert(SUB * 128 * D * 4 <= kSlots * kSlot, "the staged O must fit in the ring");
+  static constexpr size_t kSmem = 1024 + (size_t)SUB * kQTile + (size_t)kSlots * kSlot;
 };
 
 struct ShBar {
   uint64_t full[12], empty[12];
+  uint64_t q_full;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t o_final;
   uint64_t drain;
@@ -91,28 +94,16 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   const int split = (blockIdx.x / p.plan.row_tiles) % p.plan.n_split;
   const int kvh = blockIdx.x / (p.plan.row_tiles * p.plan.n_split);
   const int G = p.H / p.H_kv;
-  const int row0 = rt * 128 * SUB;
   const int t_lo = split * p.plan.per_split;
   const int t_hi = t_lo + p.plan.per_split < p.plan.tiles ? t_lo + p.plan.per_split : p.plan.tiles;
   const int nt = t_hi - t_lo;       // key tiles of this CTA (>= 1: shared_plan)
+  // One row tile: the tensor cores idle for half of the time, and P goes to
+  // them as the sum of two bf16 values (the rest of the rounding to one in the
+  // other half of S's columns).  It would cost half as much again with more
+  // row tiles, where P is rounded to bf16 as in the forward kernels.
+  const bool two_part = SUB == 1 && p.plan.row_tiles == 1;
   const int n_steps = nt * SUB;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NSL; ++i) {
-      ptx::mbar_init(&bar->full[i], 1);
-      ptx::mbar_init(&bar->empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&bar->s_full[i], 1);
-      ptx::mbar_init(&bar->p_full[i], 128);
-      ptx::mbar_init(&bar->pv_done[i], 1);
-    }
-    ptx::mbar_init(&bar->o_final, 1);
-    ptx::mbar_init(&bar->drain, 1);
-    bar->abort_flag = 0;
-    ptx::fence_barrier_init();
-    ptx::fence_proxy_async_shared();
-  }
   // Load order = the order the products take the tiles.  SUB 1: K0 K1 V0 K2 V1
   // ... ; SUB 2: K0 V0 K1 V1 ...  Load i of 2 nt: its tile and whether it is V.
   auto load_tile_of = [&](int i, int* t) -> bool {
@@ -146,26 +137,51 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
       ptx::tma_load_3d(ring + slot * Geo::kSlot + c * Geo::kKVChunk, v ? &p.tv : &p.tk, &bar->full[slot], c * 64, k0,
                        kvh);
   };
-  // the first copies fly while the queries are gathered
-  if (threadIdx.x == 0)
-    for (int i = 0; i < NSL && i < 2 * nt; ++i) issue_load(i);
-  // queries: row r is query head g of sequence b, b * G + g = r; rows past the last are zero
-  for (int i = threadIdx.x; i < SUB * 128 * (D / 8); i += Geo::kThreads) {
-    const int r = i / (D / 8), u = i % (D / 8);
-    const int row = row0 + r;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (row < p.rows) {
-      const int b = row / G, g = row - b * G;
-      x = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                               ((int64_t)b * p.H + kvh * G + g) * D) + u);
+  // Set-up, side by side: warp 0 makes the barriers and starts the copies of the
+  // queries and the first keys, warp 1 takes the tensor memory.  Queries: row r
+  // of a query tile is head r % G of the tile's sequence r / G, whole sequences
+  // only, so that a tile is one box of q as [B][H][d]; the rows left over
+  // (128 mod G) are zeros.
+  constexpr int kAhead = SUB == 2 ? 1 : 2;  // tiles started before the CTA's first barrier
+  if (warp == 0) {
+    if (lane < NSL) {
+      ptx::mbar_init(&bar->full[lane], 1);
+      ptx::mbar_init(&bar->empty[lane], 1);
     }
-    uint8_t* dst = sq + (r >> 7) * Geo::kQTile + (u >> 3) * Geo::kQChunk + (r & 127) * 128 + (((u & 7) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4*>(dst) = x;
-  }
-  ptx::fence_proxy_async_shared();
-  if (warp == 1) {
+    if (lane < 2) {
+      ptx::mbar_init(&bar->s_full[lane], 1);
+      ptx::mbar_init(&bar->p_full[lane], 128);
+      ptx::mbar_init(&bar->pv_done[lane], 1);
+    }
+    if (lane == 31) {
+      ptx::mbar_init(&bar->q_full, 1);
+      ptx::mbar_init(&bar->o_final, 1);
+      ptx::mbar_init(&bar->drain, 1);
+      bar->abort_flag = 0;
+    }
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(&bar->q_full, (uint32_t)(SUB * (D / 64) * p.plan.seqs * G * 128));
+#pragma unroll
+      for (int x = 0; x < SUB; ++x)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          ptx::tma_load_3d(sq + x * Geo::kQTile + c * Geo::kQChunk, &p.tq, &bar->q_full, c * 64, kvh * G,
+                           (rt * SUB + x) * p.plan.seqs);
+      for (int i = 0; i < kAhead && i < 2 * nt; ++i) issue_load(i);
+    }
+  } else if (warp == 1) {
     ptx::tmem_alloc(&bar->tmem_base, 512);
     ptx::tmem_relinquish();
+  } else if (p.plan.seqs * G < 128) {
+    const int used = p.plan.seqs * G;
+    for (int i = threadIdx.x - 64; i < SUB * (D / 64) * (128 - used) * 8; i += Geo::kThreads - 64) {
+      const int r = used + (i >> 3) % (128 - used), xc = (i >> 3) / (128 - used);  // xc: query tile and chunk
+      *reinterpret_cast<uint4*>(sq + xc * Geo::kQChunk + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    ptx::fence_proxy_async_shared();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -175,8 +191,8 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      for (int i = NSL; i < 2 * nt; ++i) {
-        if (!ptx::mbar_wait(&bar->empty[i % NSL], ((i / NSL) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+      for (int i = kAhead; i < 2 * nt; ++i) {
+        if (i >= NSL && !ptx::mbar_wait(&bar->empty[i % NSL], ((i / NSL) & 1) ^ 1, p.timeout_ns, abort_flag)) {
           fail_sh(p, bar, kErrProducer);
           break;
         }
@@ -219,7 +235,7 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
       if (sub == SUB - 1) ptx::mma_commit_elect(&bar->empty[slot]);
       return true;
     };
-    bool ok = true, issued = false;
+    bool ok = wait_all(&bar->q_full, 0), issued = false;
     for (int u = 0; ok && u < 2 && u < n_steps; ++u) {
       ok = issue_s(u);
       issued = issued || ok;
@@ -240,6 +256,13 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
           const uint32_t vo = (uint32_t)((slot * Geo::kSlot + k * 16 * 128) >> 4) + lbo_v;
           ptx::mma_ts(o_tm, p_tm + k * 8, desc64(r4 + vo, hi128), idesc_pv, t > 0 || k > 0);
         }
+        if (two_part) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k) {
+            const uint32_t vo = (uint32_t)((slot * Geo::kSlot + k * 16 * 128) >> 4) + lbo_v;
+            ptx::mma_ts(o_tm, p_tm + KT / 2 + k * 8, desc64(r4 + vo, hi128), idesc_pv, 1);
+          }
+        }
       }
       __syncwarp();
       ptx::mma_commit_elect(&bar->pv_done[sub]);
@@ -259,7 +282,8 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     // ------------------------------------------------------------ softmax + state output
     const int sub = (warp - 4) >> 2;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int row = row0 + sub * 128 + (warp & 3) * 32 + lane;
+    const int local = (warp & 3) * 32 + lane, used = p.plan.seqs * G;
+    const int row = (rt * SUB + sub) * used + local;  // of the key/value head's B * G rows
     const uint32_t o_tmem = tmem + lane_off + Geo::kOcol + sub * D;
     const float sl2 = p.scale_log2;
     float m = -INFINITY, l = 0.f;
@@ -287,15 +311,18 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c0 = 0; c0 < KT; c0 += 64) {
-          uint32_t pk[32];
+          uint32_t pk[32], lo[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 tt = ptx::ffma2(make_float2(x[c0 + 2 * i], x[c0 + 2 * i + 1]), sl2v, negm);
             const float2 pp = make_float2(ptx::ex2(tt.x), ptx::ex2(tt.y));
             pk[i] = ptx::pack_bf16x2(pp.x, pp.y);
+            if (SUB == 1)
+              lo[i] = ptx::pack_bf16x2(pp.x - __uint_as_float(pk[i] << 16), pp.y - __uint_as_float(pk[i] & 0xffff0000u));
             acc[i & 1] = ptx::fadd2(acc[i & 1], pp);
           }
           ptx::tmem_st32(s_tmem + c0 / 2, pk);
+          if (two_part) ptx::tmem_st32(s_tmem + KT / 2 + c0 / 2, lo);
         }
         const float2 a = ptx::fadd2(acc[0], acc[1]);
         sum = a.x + a.y;
@@ -356,20 +383,40 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     if (!ok) {
       if (lane == 0) fail_sh(p, bar, kErrSoftmax);
     } else {
-      const bool valid = row < p.rows;
+      // O leaves through shared memory (the ring is idle by now: every tile was
+      // consumed), as boxes of 32 rows x 32 columns in the 128-byte swizzle,
+      // whose rows the threads write without bank conflicts.  (16-byte stores
+      // from the registers touch 32 rows each, and a copy per row costs the
+      // copy engine 8 ns: 2 us for 256 rows.)
+      const bool valid = local < used && row < p.rows;
       const int64_t at = ((int64_t)kvh * p.rows + (valid ? row : 0)) * p.plan.n_split + split;
-#pragma unroll 1
+      uint8_t* stage = ring + (warp - 4) * (32 * D * 4);
+#pragma unroll 2
       for (int c0 = 0; c0 < D; c0 += 32) {
         float ov[32];
         ptx::tmem_ld32(o_tmem + c0, ov);
         ptx::tmem_wait_ld();
-        if (valid) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + c0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-        }
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(stage + c0 * 128 + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+      }
+      ptx::fence_proxy_async_shared();
+      __syncwarp();
+      const int first = row - lane;  // the warp's first row; a box ends at the head's last row by itself
+      if (((warp & 3) + 1) * 32 <= used) {
+        if (lane == 0 && first < p.rows)
+          for (int c = 0; c < D / 32; ++c)
+            ptx::tma_store_4d(&p.to, stage + c * 4096, c * 64, split, first, kvh);
+      } else if (valid) {
+        // rows past the tile's last sequence belong to the next tile: row by row
+        for (int c = 0; c < D / 4; ++c)
+          *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = *reinterpret_cast<const float4*>(
+              stage + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4));
       }
       if (valid) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+      ptx::bulk_commit_group();
+      ptx::bulk_wait_all();
     }
   }
 
@@ -384,8 +431,8 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
 template <int D, int SUB>
 cudaError_t launch_sub(const SharedParams& p, cudaStream_t stream) {
   using Geo = ShGeo<D, SUB>;
-  const size_t smem = 1024 + (size_t)SUB * Geo::kQTile + (size_t)Geo::kSlots * Geo::kSlot + sizeof(ShBar);
-  static_assert(1024 + SUB * Geo::kQTile + Geo::kSlots * Geo::kSlot + sizeof(ShBar) <= 227 * 1024, "shared memory");
+  const size_t smem = Geo::kSmem + sizeof(ShBar);
+  static_assert(Geo::kSmem + sizeof(ShBar) <= 227 * 1024, "shared memory");
   auto kern = decode_shared_kernel<D, SUB>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
@@ -407,32 +454,69 @@ cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stre
   }
 }
 
-// The prefix's split: a CTA holds its SM, so the launch runs in waves; the
-// number of key splits is the one whose waves cost least, a wave costing its
-// key tiles and a start-up and state output of about three.
-SharedPlan shared_plan(int B, int H, int H_kv, int P, int d) {
+// The prefix's split over `sms` SMs: a CTA holds its SM, so the launch runs in
+// waves; of the splits that fill one to four waves (and of none) the one whose
+// waves cost least, a wave costing its key tiles and a start-up and state output
+// of about six steps.
+static double split_over(SharedPlan* s, int H_kv, int sms) {
+  const int64_t units = (int64_t)s->row_tiles * H_kv;
+  double best = 1e300;
+  for (int64_t w = 0; w <= 4; ++w) {
+    int64_t ns = w * sms / units;
+    ns = ns < 1 ? 1 : (ns > s->tiles ? s->tiles : ns);
+    const int64_t per = (s->tiles + ns - 1) / ns;
+    ns = (s->tiles + per - 1) / per;  // no split without tiles
+    const int64_t waves = (units * ns + sms - 1) / sms;
+    const double cost = (double)waves * ((double)per * s->sub + 6.0) + 0.02 * (double)ns;
+    if (cost < best - 1e-9) {
+      best = cost;
+      s->n_split = (int)ns;
+      s->per_split = (int)per;
+    }
+  }
+  return best;
+}
+
+// The own keys' grid runs beside the prefix's on SMs of its own (it is launched
+// as soon as that one's CTAs have all started), as many as make both end
+// together if the sequences hold half of their capacity: the prefix is bound by
+// the tensor cores or the memory, the own keys by the memory's latency, and one
+// after the other they take their sum.  Measured beside each other: own keys 60
+// GB/s an SM and 6 us of start-up, a prefix step (128 rows x a key tile) 0.95
+// us, at most 6.5 TB/s; own keys on all SMs 4.5 TB/s and 8 us.  (64 sequences,
+// 32 / 8 heads of 128, 32K prefix, 256 own keys on average: 60.2 us one after the
+// other, 52.5 with 32 SMs for the own keys; 128 over 8K: 55.0 and 35.0.)
+SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d) {
   SharedPlan s = {};
-  const int64_t rows = (int64_t)B * (H / H_kv);
-  s.sub = rows > 128 && d <= 128 ? 2 : 1;
-  s.row_tiles = (int)((rows + 128 * s.sub - 1) / (128 * s.sub));
+  s.seqs = 128 / (H / H_kv);
+  s.sub = B > s.seqs && d <= 128 ? 2 : 1;
+  s.row_tiles = (B + s.seqs * s.sub - 1) / (s.seqs * s.sub);
   const int kt = shared_key_tile(d);
   s.tiles = (P + kt - 1) / kt;
   s.n_split = 1;
   s.per_split = s.tiles;
+  s.own_ctas = kPlanSms;
   if (s.tiles == 0) return s;
-  const int64_t units = (int64_t)s.row_tiles * H_kv;
+  const double own_bytes = 2.0 * d * H_kv * (double)B * L;
+  const double stream_us = 4.0 * d * H_kv * (double)P / 6.5e6;
   double best = 1e300;
-  for (int64_t ns = 1; ns <= s.tiles && ns <= 256; ++ns) {
-    const int64_t per = (s.tiles + ns - 1) / ns;
-    if ((s.tiles + per - 1) / per != ns) continue;  // a split without tiles
-    const int64_t waves = (units * ns + kPlanSms - 1) / kPlanSms;
-    const double cost = (double)waves * ((double)per * s.sub + 3.0) + 0.02 * (double)ns;
-    if (cost < best - 1e-9) {
-      best = cost;
-      s.n_split = (int)ns;
-      s.per_split = (int)per;
+  int take = 0;
+  for (int r = 0; r <= kPlanSms / 2; r += 8) {
+    SharedPlan t = s;
+    const double steps = split_over(&t, H_kv, kPlanSms - r);
+    const double prefix = steps * 0.95 > stream_us ? steps * 0.95 : stream_us;
+    const double own = own_bytes <= 0.0 ? 0.0 : r > 0 ? 6.0 + own_bytes / (r * 60e3) : 8.0 + own_bytes / 4.5e6;
+    const double total = r == 0 ? prefix + own : (prefix > own ? prefix : own);
+    if (total < best - 1e-9) {
+      best = total;
+      take = r;
     }
+    if (L <= 0) break;
   }
+  split_over(&s, H_kv, kPlanSms - take);
+  // SMs that the prefix leaves free are the own keys' too
+  const int64_t ctas = (int64_t)s.row_tiles * s.n_split * H_kv;
+  if (ctas <= kPlanSms - 8) s.own_ctas = kPlanSms - (int)ctas;
   return s;
 }
 

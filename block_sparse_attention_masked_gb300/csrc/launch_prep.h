@@ -52,5 +52,12 @@ unsigned long long device_wait_timeout_ns();
 // `rows` read as zeros.
 int make_rows_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
                   int box_rows);
+// The same with boxes that take box_rows rows of box_heads matrices.
+int make_box_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
+                 int box_rows, int box_heads);
+// View of fp32 states [heads][rows][splits][d] for stores of 32 rows x 32
+// columns (as 64 16-bit columns: a copy does not look at the type), 128-byte
+// swizzle.
+int make_state_map(CUtensorMap* map, const void* base, int d, int64_t splits, int64_t rows, int64_t heads);
 
 }  // namespace mattn

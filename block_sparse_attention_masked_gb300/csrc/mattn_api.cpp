@@ -993,12 +993,27 @@ unsigned long long device_wait_timeout_ns() { return wait_timeout_ns(); }
 
 int make_rows_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
                   int box_rows) {
+  return make_box_map(map, base, d, rows, head_rows, heads, box_rows, 1);
+}
+
+int make_box_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t head_rows, int64_t heads,
+                 int box_rows, int box_heads) {
   const int rc = get_encoder();
   if (rc) return rc;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)head_rows * d * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads};
   return encode(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int make_state_map(CUtensorMap* map, const void* base, int d, int64_t splits, int64_t rows, int64_t heads) {
+  const int rc = get_encoder();
+  if (rc) return rc;
+  const cuuint64_t row = (cuuint64_t)splits * d * 4;
+  cuuint64_t dims[4] = {(cuuint64_t)d * 2, (cuuint64_t)splits, (cuuint64_t)rows, (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)d * 4, row, row * (cuuint64_t)rows};
+  cuuint32_t box[4] = {64, 1, 32, 1};
+  return encode(map, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int prepare_in_place_launch(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N,
