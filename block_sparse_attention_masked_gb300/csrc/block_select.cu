@@ -13,22 +13,27 @@
 //
 // Selection.  The choice is that of exact arithmetic on the bf16 means and
 // queries, so that it does not depend on how a product was summed:
-//   1. decode_scores_kernel: score_n by matrix instructions with fp32 sums, and
-//      e_n, a bound of its error: |sum of d rounded products - exact| <= u d'
-//      sum |q_c k_c| <= u d' |q| |k_n|; with d / 16 <= 16 sums of 16 products
-//      each, u d' <= 2^-17 even if each of them loses 2^-21 of its terms'
-//      magnitudes, and 2^-15 is used.  Lanes load 16 bytes of a mean's row
-//      straight into operand registers: the order of the dims inside a product
-//      is free as long as the queries use the same one, so no shared memory.
+//   1. Scores by matrix instructions with fp32 sums, and e_n, a bound of each
+//      one's error: |sum of d rounded products - exact| <= u d' sum |q_c k_c| <=
+//      u d' |q| |k_n|; with d / 16 <= 16 sums of 16 products each, u d' <= 2^-17
+//      even if each of them loses 2^-21 of its terms' magnitudes, and 2^-15 is
+//      used.  Lanes load 16 bytes of a mean's row straight into operand
+//      registers: the order of the dims inside a product is free as long as the
+//      queries use the same one, so the means pass through no shared memory.
 //      One pass over the means: HBM-bound.
-//   2. decode_select_kernel, one CTA per (sequence, key/value head): the k-th
-//      largest score by digits (22 bits: T lies in [t0, t1)).  Every set of k
-//      scores bounds the exact k-th score from below by the least of its
-//      members' score - e, and every set of n - k + 1 from above by the most of
-//      score + e; applied to {score >= t0} and {score < t1} this gives
-//      lo <= exact k-th <= hi.  A block is in if score - e > hi, out if
-//      score + e < lo; the few between are formed again in 64 bits (products of
-//      two bf16 are exact there) and ranked.
+//   2. The k-th largest score T: the scores' range is cut into 512 even bins,
+//      counted, and the bin that holds T ranked by one warp (or cut again, where
+//      it holds more than 32).  Every set of k scores bounds the exact k-th score
+//      from below by the least of its members' score - e, and every set of
+//      n - k + 1 from above by the most of score + e; applied to {score >= T} and
+//      {score <= T} this gives lo <= exact k-th <= hi.  A block is in if
+//      score - e > hi, out if score + e < lo; the few between are formed again in
+//      64 bits (products of two bf16 are exact there) and ranked.
+// One launch: a cluster of up to eight CTAs scores one (sequence, key/value
+// head)'s blocks, and its first CTA, after the cluster's barrier, selects with
+// the scores in shared memory (up to 6,144 blocks; more are read from L2).  The
+// selection's stages are short and end in a sum over the threads, so that its
+// time is what each warp issues once: eight of the sixteen warps go on to it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -99,8 +104,18 @@ __global__ void __launch_bounds__(32 * kMeanWarps) block_means_kernel(const __gr
   }
 }
 
-// ------------------------------------------------------------ scores
-constexpr int kScoreWarps = 4;
+// ------------------------------------------------------------ selection
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kPick = 256;       // threads that select
+constexpr int kPickWarps = kPick / 32;
+constexpr int kSelKept = 6144;   // scores kept in shared memory
+constexpr int kBatch = 8;        // scores a thread works on at once
+constexpr int kCutBins = 2 * kPick;
+constexpr int kCuts = 8;         // at most: what is left then goes to the 64-bit scores
+constexpr int kDigit = 11;
+constexpr int kBins = 1 << kDigit;
+constexpr int kSmallBand = 256;  // candidates ranked in shared memory; more go through the digits again
 constexpr float kScoreErr = 3.0517578125e-05f;  // 2^-15 (see above)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -110,9 +125,28 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// 32 bytes of a mean's row (a whole 128-byte line by four lanes).
+__device__ __forceinline__ void ld32(const uint4* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
 __device__ __forceinline__ float sq2(uint32_t x, float s) { return fmaf(bfl(x), bfl(x), fmaf(bfh(x), bfh(x), s)); }
 __device__ __forceinline__ float sq8(const uint4& x, float s) {
   return sq2(x.x, sq2(x.y, sq2(x.z, sq2(x.w, s))));
+}
+
+// Keys that order like the floats; NaN is taken as -inf.
+__device__ __forceinline__ uint32_t key32(float x) {
+  if (x != x) x = -INFINITY;
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 as 0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unkey32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
+__device__ __forceinline__ unsigned long long key64(double x) {
+  if (x != x) x = -INFINITY;
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
 __device__ __forceinline__ int blocks_of(const DecodeSelectParams& p, int b) {
@@ -122,28 +156,108 @@ __device__ __forceinline__ int blocks_of(const DecodeSelectParams& p, int b) {
   return n < p.n_blocks ? (int)n : p.n_blocks;
 }
 
-// A warp scores 16 blocks at a time: block rows are the tall operand, the
+constexpr uint32_t kKeyMin = 0x00800000u, kKeyMax = 0xff7fffffu;  // keys of the least and largest finite float
+
+struct SelShared {
+  uint4 q[2][8][32];                       // the group's queries as operands: [group of 8 heads][32 dims][lane]
+  uint32_t hist[kBins];
+  uint32_t member[kSelectMaxBlocks / 32];  // blocks chosen
+  uint32_t band[kSelectMaxBlocks / 32];    // blocks between lo and hi
+  double val[kSmallBand];
+  int idx[kSmallBand];
+  uint32_t wsum[kPickWarps];
+  uint2 bound[kPickWarps];
+  uint4 range[kPickWarps];
+  uint32_t list[32];
+  int n_list;
+  uint32_t digit, above;
+  int n_in, n_band;
+  uint2 kept[kSelKept];                    // Score
+};
+
+// Barrier of the threads that select.
+__device__ __forceinline__ void pick_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPick) : "memory"); }
+
+// Exclusive prefix sum over the selecting threads; *total gets the sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint32_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  pick_sync();
+  if (lane == 31) wsum[warp] = x;
+  pick_sync();
+  const uint32_t w = lane < kPickWarps ? wsum[lane] : 0u;
+  *total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + x - v;
+}
+
+// The bin of the histogram's BINS, from the top, at which the count from above
+// reaches `want` (1-based): sh->digit = the bin, sh->above = entries in higher ones.
+template <int BINS>
+__device__ __forceinline__ void pick_digit(SelShared* sh, uint32_t want) {
+  constexpr int PER = BINS / kPick;
+  // thread t holds the bins of descending order t * PER ...
+  uint32_t c[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = sh->hist[BINS - 1 - (threadIdx.x * PER + i)];
+    sum += c[i];
+  }
+  uint32_t total;
+  uint32_t before = block_scan(sum, sh->wsum, &total);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (before < want && before + c[i] >= want) {
+      sh->digit = BINS - 1 - (threadIdx.x * PER + i);
+      sh->above = before;
+    }
+    before += c[i];
+  }
+  pick_sync();
+}
+
+// Scores of the blocks [0, n) of one group, shared by the `ctas` CTAs of a
+// cluster: a warp takes 16 blocks at a time, block rows the tall operand, the
 // group's heads (NT groups of eight) the other.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kScoreWarps) decode_scores_kernel(const __grid_constant__ DecodeSelectParams p) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bkv = blockIdx.y, b = bkv / p.H_kv, kvh = bkv % p.H_kv, G = p.H / p.H_kv;
-  const int n = blocks_of(p, b);
+__device__ __forceinline__ void score_blocks(const DecodeSelectParams& p, SelShared* sh, int b, int kvh, int rank,
+                                             int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.H / p.H_kv;
   const int r = lane >> 2, j = lane & 3;
-  const uint4* mean = reinterpret_cast<const uint4*>(p.means) + (int64_t)bkv * p.n_blocks * (D / 8) + j;
-  uint4 q[NT][D / 32];
-  float qq = 0.f;
+  const int64_t row = (int64_t)b * p.H_kv + kvh;
+  // operand i, lane j of a row: 16-byte pieces 8 (i / 2) + 2 j + i % 2
+  const uint4* mean = reinterpret_cast<const uint4*>(p.means) + row * p.n_blocks * (D / 8) + 2 * j;
+  uint4 x[D / 32], y[D / 32];
+  auto load = [&](int t, int n) {
+    const int r0 = t * 16 + r, r1 = r0 + 8;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) x[i] = y[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2) {
+      if (r0 < n) ld32(mean + (int64_t)r0 * (D / 8) + i * 4, x[i], x[i + 1]);
+      if (r1 < n) ld32(mean + (int64_t)r1 * (D / 8) + i * 4, y[i], y[i + 1]);
+    }
+  };
+  int t = rank * kSelWarps + warp;
+  load(t, p.n_blocks);  // in flight while the sequence's length and the queries arrive
+  for (int k = threadIdx.x; k < NT * (D / 32) * 32; k += kSelThreads) {
+    const int l = k & 31, i = (k >> 5) % (D / 32), nt = (k >> 5) / (D / 32), g = nt * 8 + (l >> 2);
+    sh->q[nt][i][l] = g < G ? __ldg(reinterpret_cast<const uint4*>(p.q) + ((int64_t)b * p.H + kvh * G + g) * (D / 8) +
+                                    (i >> 1) * 8 + (l & 3) * 2 + (i & 1))
+                            : make_uint4(0, 0, 0, 0);
+  }
+  const int n = blocks_of(p, b);
+  __syncthreads();
+  float qq = 0.f;  // the longest query's squared length
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int g = nt * 8 + r;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q) + ((int64_t)b * p.H + kvh * G + (g < G ? g : 0)) * (D / 8) + j;
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      q[nt][i] = g < G ? __ldg(src + i * 4) : make_uint4(0, 0, 0, 0);
-      s = sq8(q[nt][i], s);
-    }
+    for (int i = 0; i < D / 32; ++i) s = sq8(sh->q[nt][i][lane], s);
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     qq = fmaxf(qq, s);
@@ -151,14 +265,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) decode_scores_kernel(const _
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) qq = fmaxf(qq, __shfl_xor_sync(0xffffffffu, qq, off));
   const float err = kScoreErr * sqrtf(qq + 1e-40f);
-  for (int t = blockIdx.x * kScoreWarps + warp; t * 16 < n; t += gridDim.x * kScoreWarps) {
+  for (; t * 16 < n; t += ctas * kSelWarps, load(t, n)) {
     const int r0 = t * 16 + r, r1 = r0 + 8;
-    uint4 x[D / 32], y[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      x[i] = r0 < n ? __ldg(mean + (int64_t)r0 * (D / 8) + i * 4) : make_uint4(0, 0, 0, 0);
-      y[i] = r1 < n ? __ldg(mean + (int64_t)r1 * (D / 8) + i * 4) : make_uint4(0, 0, 0, 0);
-    }
     float acc[NT][2][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -171,13 +279,15 @@ __global__ void __launch_bounds__(32 * kScoreWarps) decode_scores_kernel(const _
     for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_bf16(acc[nt][0], x[i].x, y[i].x, x[i].y, y[i].y, q[nt][i].x, q[nt][i].y);
-        mma_bf16(acc[nt][1], x[i].z, y[i].z, x[i].w, y[i].w, q[nt][i].z, q[nt][i].w);
+        const uint4 q = sh->q[nt][i][lane];
+        mma_bf16(acc[nt][0], x[i].x, y[i].x, x[i].y, y[i].y, q.x, q.y);
+        mma_bf16(acc[nt][1], x[i].z, y[i].z, x[i].w, y[i].w, q.z, q.w);
       }
       sx = sq8(x[i], sx);
       sy = sq8(y[i], sy);
     }
     // heads of this lane: 2 j, 2 j + 1 (of each eight); rows r0 and r1
+    const float nan = __int_as_float(0x7fffffff);
     float s0 = -INFINITY, s1 = -INFINITY;
     bool nan0 = false, nan1 = false;
 #pragma unroll
@@ -191,109 +301,36 @@ __global__ void __launch_bounds__(32 * kScoreWarps) decode_scores_kernel(const _
           s0 = fmaxf(s0, u);
           s1 = fmaxf(s1, v);
         }
-    if (nan0) s0 = __int_as_float(0x7fffffff);
-    if (nan1) s1 = __int_as_float(0x7fffffff);
+    if (nan0) s0 = nan;
+    if (nan1) s1 = nan;
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
       const float u = __shfl_xor_sync(0xffffffffu, s0, off), v = __shfl_xor_sync(0xffffffffu, s1, off);
-      s0 = u != u || s0 != s0 ? __int_as_float(0x7fffffff) : fmaxf(s0, u);
-      s1 = v != v || s1 != s1 ? __int_as_float(0x7fffffff) : fmaxf(s1, v);
+      s0 = u != u || s0 != s0 ? nan : fmaxf(s0, u);
+      s1 = v != v || s1 != s1 ? nan : fmaxf(s1, v);
       sx += __shfl_xor_sync(0xffffffffu, sx, off);
       sy += __shfl_xor_sync(0xffffffffu, sy, off);
     }
     if (j == 0) {
       // (the small terms cover squares and products that underflow)
-      float2* dst = p.scores + (int64_t)bkv * p.n_blocks;
-      if (r0 < n) dst[r0] = make_float2(s0, fmaf(err, sqrtf(sx + 1e-40f), 1e-36f));
-      if (r1 < n) dst[r1] = make_float2(s1, fmaf(err, sqrtf(sy + 1e-40f), 1e-36f));
+      Score* dst = p.scores + row * p.n_blocks;
+      if (r0 < n) dst[r0] = Score{key32(s0), fmaf(err, sqrtf(sx + 1e-40f), 1e-36f)};
+      if (r1 < n) dst[r1] = Score{key32(s1), fmaf(err, sqrtf(sy + 1e-40f), 1e-36f)};
     }
   }
 }
 
-// ------------------------------------------------------------ selection
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kDigit = 11;
-constexpr int kBins = 1 << kDigit;
-constexpr int kSmallBand = 256;  // candidates ranked in shared memory; more go through the digits again
-
-// Keys that order like the floats; NaN is taken as -inf.
-__device__ __forceinline__ uint32_t key32(float x) {
-  if (x != x) x = -INFINITY;
-  const uint32_t u = __float_as_uint(x + 0.f);  // -0 as 0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ unsigned long long key64(double x) {
-  if (x != x) x = -INFINITY;
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-}
-
-struct SelShared {
-  uint32_t hist[kBins];
-  uint32_t member[kSelectMaxBlocks / 32];  // blocks chosen
-  uint32_t band[kSelectMaxBlocks / 32];    // blocks between lo and hi
-  double val[kSmallBand];
-  int idx[kSmallBand];
-  uint32_t wsum[kSelWarps];
-  float wlo[kSelWarps], whi[kSelWarps];
-  uint32_t digit, above;
-  int n_in, n_band;
-};
-
-// Exclusive prefix sum over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint32_t* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t x = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) wsum[warp] = x;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const uint32_t s = wsum[w];
-    before += w < warp ? s : 0u;
-    all += s;
-  }
-  *total = all;
-  return before + x - v;
-}
-
-// The digit d of the histogram, from the top, at which the count from above
-// reaches `want` (1-based): sh->digit = d, sh->above = entries in digits > d.
-__device__ __forceinline__ void pick_digit(SelShared* sh, uint32_t want) {
-  constexpr int PER = kBins / kSelThreads;
-  // thread t holds the bins of descending order t * PER ...
-  uint32_t c[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    c[i] = sh->hist[kBins - 1 - (threadIdx.x * PER + i)];
-    sum += c[i];
-  }
-  uint32_t total;
-  uint32_t before = block_scan(sum, sh->wsum, &total);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (before < want && before + c[i] >= want) {
-      sh->digit = kBins - 1 - (threadIdx.x * PER + i);
-      sh->above = before;
-    }
-    before += c[i];
-  }
-  __syncthreads();
-}
-
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) decode_select_kernel(const __grid_constant__ DecodeSelectParams p) {
+// A cluster per (sequence, key/value head).
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
+    decode_select_kernel(const __grid_constant__ DecodeSelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelShared* sh = reinterpret_cast<SelShared*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bkv = blockIdx.x, b = bkv / p.H_kv, kvh = bkv % p.H_kv, G = p.H / p.H_kv;
+  const int rank = blockIdx.x % p.ctas, bkv = blockIdx.x / p.ctas;
+  const int b = bkv / p.H_kv, kvh = bkv % p.H_kv, G = p.H / p.H_kv;
+  // (before the length is known: where every block fits, the scores go unread)
+  if (p.n_blocks > p.top_k) score_blocks<D, NT>(p, sh, b, kvh, rank, p.ctas);
   const int n = blocks_of(p, b);
   const int words = (n + 31) / 32;
   // blocks kept whatever their score: [0, f0) and [f1, n)
@@ -301,104 +338,237 @@ __global__ void __launch_bounds__(kSelThreads) decode_select_kernel(const __grid
   const int f1 = n - p.keep_recent > f0 ? n - p.keep_recent : f0;
   const int rest = f1 - f0;                          // blocks that compete
   const int want = p.top_k - f0 - (n - f1);          // places left for them (>= 0: checked on the host)
-  for (int w = tid; w < words; w += kSelThreads) {
-    // the kept blocks' bits; all of them when every block fits
-    uint32_t bits = 0;
-    for (int i = 0; i < 32; ++i) {
-      const int x = w * 32 + i;
-      if (x < n && (x < f0 || x >= f1 || rest <= want)) bits |= 1u << i;
+  const bool choose = want > 0 && rest > want;       // the same in all CTAs of the cluster
+  if (rank == 0) {
+    for (int w = tid; w < words; w += kSelThreads) {
+      // the kept blocks' bits; all of them when every block fits
+      uint32_t bits = 0;
+      if (rest <= want) {
+        bits = n - w * 32 >= 32 ? 0xffffffffu : (1u << (n - w * 32)) - 1u;
+      } else {
+        for (int i = w * 32; i < f0 && i < w * 32 + 32; ++i) bits |= 1u << (i & 31);
+        for (int i = f1 > w * 32 ? f1 : w * 32; i < n && i < w * 32 + 32; ++i) bits |= 1u << (i & 31);
+      }
+      sh->member[w] = bits;
+      sh->band[w] = 0;
     }
-    sh->member[w] = bits;
-    sh->band[w] = 0;
+    if (tid == 0) sh->n_in = sh->n_band = 0;
   }
-  for (int i = tid; i < kBins; i += kSelThreads) sh->hist[i] = 0;
-  if (tid == 0) sh->n_in = sh->n_band = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncthreads();
-  const float2* sc = p.scores + (int64_t)bkv * p.n_blocks;
-  if (want > 0 && rest > want) {
-    // T: two digits of 11 bits of the want-th largest score
-    for (int i = f0 + tid; i < f1; i += kSelThreads) atomicAdd(&sh->hist[key32(sc[i].x) >> 21], 1u);
+  if (choose && p.ctas > 1) {
+    // every CTA's scores before the first one's selection
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
     __syncthreads();
-    pick_digit(sh, (uint32_t)want);
-    const uint32_t d1 = sh->digit, left = (uint32_t)want - sh->above;
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kSelThreads) sh->hist[i] = 0;
-    __syncthreads();
-    for (int i = f0 + tid; i < f1; i += kSelThreads) {
-      const uint32_t k = key32(sc[i].x);
-      if ((k >> 21) == d1) atomicAdd(&sh->hist[(k >> 10) & (kBins - 1)], 1u);
-    }
-    __syncthreads();
-    pick_digit(sh, left);
-    const uint32_t prefix = (d1 << 11) | sh->digit;  // the want-th largest score's top 22 bits
-    // bounds of the exact want-th score
-    float lo = INFINITY, hi = -INFINITY;
-    for (int i = f0 + tid; i < f1; i += kSelThreads) {
-      const float2 s = sc[i];
-      const uint32_t k = key32(s.x) >> 10;
-      const bool fine = fabsf(s.x) < INFINITY && s.y < INFINITY;  // else nothing is known of it
-      if (k >= prefix) lo = fminf(lo, fine ? s.x - s.y : -INFINITY);
-      if (k <= prefix) hi = fmaxf(hi, fine ? s.x + s.y : INFINITY);
-    }
+  }
+  if (rank || tid >= kPick) return;
+  if (choose) {
+    const uint2* far = reinterpret_cast<const uint2*>(p.scores + (int64_t)bkv * p.n_blocks + f0);
+    const bool kept = rest <= kSelKept;
+    // fn(place, its score, whether there is one) over this thread's places, eight
+    // loaded at once: fn has no branch that its lanes take apart, so that the
+    // eight overlap
+    auto each = [&](bool near, auto&& fn) {
+#pragma unroll 1
+      for (int base = tid; base < rest; base += kPick * kBatch) {
+        uint2 u[kBatch];
+        if (near) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    }
-    if (lane == 0) {
-      sh->wlo[warp] = lo;
-      sh->whi[warp] = hi;
-    }
-    __syncthreads();
+          for (int j = 0; j < kBatch; ++j) {
+            const int i = base + j * kPick;
+            u[j] = sh->kept[i < rest ? i : 0];
+          }
+        } else {
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      lo = fminf(lo, sh->wlo[w]);
-      hi = fmaxf(hi, sh->whi[w]);
+          for (int j = 0; j < kBatch; ++j) {
+            const int i = base + j * kPick;
+            u[j] = __ldcg(far + (i < rest ? i : 0));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) fn(base + j * kPick, u[j].x, __uint_as_float(u[j].y), base + j * kPick < rest);
+      }
+    };
+    // the interval of the want-th largest score: keys [from, to]
+    uint32_t from = 0, to = 0xffffffffu, above = 0;  // above: scores past `to`
+    int left = rest;
+    float emax = 0.f;  // the largest bound of an error
+    float bin_width = 0.f;
+    bool unknown = false;  // some score or error is not finite
+#pragma unroll 1
+    for (int cut = 0; cut < kCuts && left > 1; ++cut) {
+      // the finite scores' range inside the interval (and the scores to shared memory)
+      const uint32_t first = from > kKeyMin ? from : kKeyMin, span = (to < kKeyMax ? to : kKeyMax) - first;
+      const bool some = to >= kKeyMin && from <= kKeyMax;
+      uint32_t kmin = 0xffffffffu, kmax = 0;
+      each(kept && cut > 0, [&](int i, uint32_t k, float err, bool there) {
+        if (kept && cut == 0 && there) sh->kept[i] = make_uint2(k, __float_as_uint(err));
+        const bool in = some && there && k - first <= span;
+        kmin = min(kmin, in ? k : 0xffffffffu);
+        kmax = max(kmax, in ? k : 0u);
+        const bool fine = k - kKeyMin <= kKeyMax - kKeyMin && err < INFINITY;
+        emax = fmaxf(emax, there && fine ? err : 0.f);
+        unknown = unknown || (there && !fine);
+      });
+      kmin = __reduce_min_sync(0xffffffffu, kmin);
+      kmax = __reduce_max_sync(0xffffffffu, kmax);
+      const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(emax));  // (>= 0: ordered as it is)
+      const uint32_t u = __any_sync(0xffffffffu, unknown);
+      if (lane == 0) sh->range[warp] = make_uint4(kmin, kmax, e, u);
+      sh->hist[tid] = sh->hist[tid + kPick] = 0;
+      if (tid == 0) sh->n_list = 0;
+      pick_sync();
+      const uint4 range = lane < kPickWarps ? sh->range[lane] : make_uint4(0xffffffffu, 0u, 0u, 0u);
+      kmin = __reduce_min_sync(0xffffffffu, range.x);
+      kmax = __reduce_max_sync(0xffffffffu, range.y);
+      emax = __uint_as_float(__reduce_max_sync(0xffffffffu, range.z));
+      unknown = __any_sync(0xffffffffu, range.w != 0u);
+      if (kmin >= kmax) break;  // equal scores, or none finite
+      const float s0 = unkey32(kmin), width = unkey32(kmax) - s0, per = __fdividef((float)(kCutBins - 2), width);
+      if (!(width < INFINITY) || !(per < INFINITY) || !(per > 0.f)) break;
+      bin_width = width / (float)(kCutBins - 2);
+      // a bin of each score, growing with it (infinities at the ends)
+      auto bin_of = [&](uint32_t k) {
+        return (int)fminf(fmaxf((unkey32(k) - s0) * per, -1.f), (float)(kCutBins - 2)) + 1;
+      };
+      each(kept, [&](int, uint32_t k, float, bool there) {
+        const int bin = bin_of(k);
+        if (there && k - from <= to - from) atomicAdd(&sh->hist[bin], 1u);
+      });
+      pick_sync();
+      pick_digit<kCutBins>(sh, (uint32_t)want - above);
+      const int bin = (int)sh->digit;
+      above += sh->above;
+      left = (int)sh->hist[bin];
+      // the bin's keys: listed and ranked where they are few, else an interval again
+      uint32_t f = 0xffffffffu, t = 0;
+      each(kept, [&](int, uint32_t k, float, bool there) {
+        const bool in = there && k - from <= to - from && bin_of(k) == bin;
+        f = min(f, in ? k : 0xffffffffu);
+        t = max(t, in ? k : 0u);
+        if (in && left <= 32) sh->list[atomicAdd(&sh->n_list, 1)] = k;
+      });
+      f = __reduce_min_sync(0xffffffffu, f);
+      t = __reduce_max_sync(0xffffffffu, t);
+      if (lane == 0) sh->bound[warp] = make_uint2(f, t);
+      pick_sync();
+      if (left <= 32) {
+        // every warp: the key that fewer than want - above and, with its equals, at least that many pass
+        const uint32_t k = lane < left ? sh->list[lane] : 0u;
+        int more = 0, same = 0;
+        for (int j = 0; j < left; ++j) {
+          const uint32_t o = __shfl_sync(0xffffffffu, k, j);
+          more += o > k;
+          same += o == k;
+        }
+        const int rank_ = want - (int)above;
+        const uint32_t hit = __ballot_sync(0xffffffffu, lane < left && more < rank_ && more + same >= rank_);
+        from = to = __shfl_sync(0xffffffffu, k, __ffs(hit) - 1);
+        break;
+      }
+      const uint2 now = lane < kPickWarps ? sh->bound[lane] : make_uint2(0xffffffffu, 0u);
+      from = __reduce_min_sync(0xffffffffu, now.x);
+      to = __reduce_max_sync(0xffffffffu, now.y);
+      pick_sync();  // (the next cut writes the same words)
+    }
+    // Bounds of the exact want-th score.  One border score (from == to) and errors
+    // well below the scores' spacing: itself, give or take the largest error.  Else
+    // from the scores' own errors (of a score that is not finite nothing is known).
+    float lo, hi;
+    const float border = unkey32(from);
+    if (from == to && emax <= bin_width && !unknown) {
+      lo = border - emax;
+      hi = border + emax;
+    } else {
+      uint32_t klo = 0xffffffffu, khi = 0;
+      each(kept, [&](int, uint32_t k, float err, bool there) {
+        const float s = unkey32(k);
+        const bool fine = fabsf(s) < INFINITY && err < INFINITY;
+        const uint32_t down = key32(fine ? s - err : -INFINITY), up = key32(fine ? s + err : INFINITY);
+        klo = min(klo, there && k >= from ? down : 0xffffffffu);
+        khi = max(khi, there && k <= to ? up : 0u);
+      });
+      klo = __reduce_min_sync(0xffffffffu, klo);
+      khi = __reduce_max_sync(0xffffffffu, khi);
+      pick_sync();
+      if (lane == 0) sh->bound[warp] = make_uint2(klo, khi);
+      pick_sync();
+      const uint2 bound = lane < kPickWarps ? sh->bound[lane] : make_uint2(0xffffffffu, 0u);
+      lo = unkey32(__reduce_min_sync(0xffffffffu, bound.x));
+      hi = unkey32(__reduce_max_sync(0xffffffffu, bound.y));
     }
     int in = 0;
-    for (int i = f0 + tid; i < f1; i += kSelThreads) {
-      const float2 s = sc[i];
-      const bool fine = fabsf(s.x) < INFINITY && s.y < INFINITY;
-      if (fine && s.x - s.y > hi) {
-        atomicOr(&sh->member[i >> 5], 1u << (i & 31));
-        ++in;
-      } else if (!fine || s.x + s.y >= lo) {
-        atomicOr(&sh->band[i >> 5], 1u << (i & 31));
-        const int at = atomicAdd(&sh->n_band, 1);
-        if (at < kSmallBand) sh->idx[at] = i;
+    each(kept, [&](int i, uint32_t k, float err, bool there) {
+      const float s = unkey32(k);
+      const bool fine = fabsf(s) < INFINITY && err < INFINITY;
+      const bool sure = there && fine && s - err > hi, maybe = there && !sure && (!fine || s + err >= lo);
+      in += sure;
+      if (sure || maybe) {
+        const int x = f0 + i;
+        atomicOr(sure ? &sh->member[x >> 5] : &sh->band[x >> 5], 1u << (x & 31));
+        if (maybe) {
+          const int at = atomicAdd(&sh->n_band, 1);
+          if (at < kSmallBand) sh->idx[at] = x;
+        }
       }
-    }
-    if (in) atomicAdd(&sh->n_in, in);
-    __syncthreads();
+    });
+    in = __reduce_add_sync(0xffffffffu, in);
+    if (lane == 0 && in) atomicAdd(&sh->n_in, in);
+    pick_sync();
     const int band = sh->n_band, need = want - sh->n_in;  // 0 < need <= band
     double* again = p.again + (int64_t)bkv * p.n_blocks;
-    const __nv_bfloat16* q0 = reinterpret_cast<const __nv_bfloat16*>(p.q) + ((int64_t)b * p.H + kvh * G) * D;
-    const __nv_bfloat16* m0 = reinterpret_cast<const __nv_bfloat16*>(p.means) + (int64_t)bkv * p.n_blocks * D;
-    // one warp: the score of block i in 64 bits (NaN ranks below everything)
+    // one warp: the score of block i in 64 bits (NaN ranks below everything); a
+    // lane takes D / 32 dims, the queries' from the operands in shared memory
+    constexpr int VPL = D / 32;
+    const int piece = lane * VPL / 8, at = lane * VPL % 8;
     auto score64 = [&](int i) -> double {
-      double best = -INFINITY;
-      for (int g = 0; g < G; ++g) {
-        double s = 0.0;
+      const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p.means) +
+                                 ((int64_t)bkv * p.n_blocks + i) * D + lane * VPL;
+      float m[VPL];
 #pragma unroll
-        for (int c = lane; c < D; c += 32)
-          s = fma((double)__bfloat162float(q0[g * D + c]), (double)__bfloat162float(m0[(int64_t)i * D + c]), s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (s != s) return -INFINITY;
-        best = s > best ? s : best;
+      for (int c = 0; c < VPL; c += 2) {
+        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + c));
+        m[c] = bfl(u);
+        m[c + 1] = bfh(u);
       }
-      return best;
+      double best = -INFINITY;
+      bool bad = false;
+#pragma unroll 1
+      for (int g0 = 0; g0 < G; g0 += 4) {
+        double s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int g = g0 + k < G ? g0 + k : g0;
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(
+                                  &sh->q[g >> 3][(piece >> 3) * 2 + (piece & 1)][(g & 7) * 4 + ((piece & 7) >> 1)]) + at / 2;
+          s[k] = 0.0;
+#pragma unroll
+          for (int c = 0; c < VPL; c += 2) {
+            s[k] = fma((double)bfl(q[c / 2]), (double)m[c], s[k]);
+            s[k] = fma((double)bfh(q[c / 2]), (double)m[c + 1], s[k]);
+          }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          bad = bad || s[k] != s[k];
+          best = s[k] > best ? s[k] : best;
+        }
+      }
+      return bad ? -INFINITY : best;
     };
     if (need >= band) {
-      for (int w = tid; w < words; w += kSelThreads) sh->member[w] |= sh->band[w];
+      for (int w = tid; w < words; w += kPick) sh->member[w] |= sh->band[w];
     } else if (band <= kSmallBand) {
-      for (int x = warp; x < band; x += kSelWarps) {
+      for (int x = warp; x < band; x += kPickWarps) {
         const double s = score64(sh->idx[x]);
         if (lane == 0) sh->val[x] = s;
       }
-      __syncthreads();
-      for (int x = tid; x < band; x += kSelThreads) {
+      pick_sync();
+      for (int x = tid; x < band; x += kPick) {
         const double s = sh->val[x];
         const int i = sh->idx[x];
         int rank = 0;
@@ -408,7 +578,7 @@ __global__ void __launch_bounds__(kSelThreads) decode_select_kernel(const __grid
     } else {
       // many near-equal scores: the digits of the 64-bit scores, then the
       // lowest indices among those equal to the last one in
-      for (int i = f0 + warp; i < f1; i += kSelWarps)
+      for (int i = f0 + warp; i < f1; i += kPickWarps)
         if ((sh->band[i >> 5] >> (i & 31)) & 1u) {
           const double s = score64(i);
           if (lane == 0) again[i] = s;
@@ -419,24 +589,24 @@ __global__ void __launch_bounds__(kSelThreads) decode_select_kernel(const __grid
       for (int shift = 55; ; shift -= kDigit) {
         const int sft = shift > 0 ? shift : 0;
         const int bits = shift >= 0 ? kDigit : kDigit + shift;  // the last digit is what is left
-        __syncthreads();
-        for (int i = tid; i < kBins; i += kSelThreads) sh->hist[i] = 0;
-        __syncthreads();
-        for (int i = f0 + tid; i < f1; i += kSelThreads)
+        pick_sync();
+        for (int i = tid; i < kBins; i += kPick) sh->hist[i] = 0;
+        pick_sync();
+        for (int i = f0 + tid; i < f1; i += kPick)
           if ((sh->band[i >> 5] >> (i & 31)) & 1u) {
             const unsigned long long k = key64(again[i]);
             // (a shift by 64 or more is undefined: the first digit has no prefix)
             if (sft + bits >= 64 || (k >> (sft + bits)) == pre)
               atomicAdd(&sh->hist[(uint32_t)(k >> sft) & ((1u << bits) - 1u)], 1u);
           }
-        __syncthreads();
-        pick_digit(sh, todo);
+        pick_sync();
+        pick_digit<kBins>(sh, todo);
         pre = (pre << bits) | sh->digit;
         todo -= sh->above;
         if (sft == 0) break;
       }
       // pre: the last score in; todo of those equal to it belong
-      const int per = (rest + kSelThreads - 1) / kSelThreads;
+      const int per = (rest + kPick - 1) / kPick;
       const int i0 = f0 + tid * per, i1 = i0 + per < f1 ? i0 + per : f1;
       uint32_t equal = 0;
       for (int i = i0; i < i1; ++i)
@@ -454,50 +624,60 @@ __global__ void __launch_bounds__(kSelThreads) decode_select_kernel(const __grid
         }
     }
   }
-  __syncthreads();
-  // the chosen blocks in ascending order, -1 behind them
+  pick_sync();
+  // the chosen blocks in ascending order, -1 behind them: one warp
+  if (warp) return;
   int32_t* out = p.ids + (int64_t)bkv * p.top_k;
-  const int wper = (words + kSelThreads - 1) / kSelThreads;
-  uint32_t cnt = 0;
-  for (int w = tid * wper; w < words && w < (tid + 1) * wper; ++w) cnt += __popc(sh->member[w]);
-  uint32_t total;
-  uint32_t at = block_scan(cnt, sh->wsum, &total);
-  for (int w = tid * wper; w < words && w < (tid + 1) * wper; ++w)
+  const int wper = (words + 31) / 32, w0 = lane * wper, w1 = w0 + wper < words ? w0 + wper : words;
+  int cnt = 0;
+  for (int w = w0; w < w1; ++w) cnt += __popc(sh->member[w]);
+  int at = cnt;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, at, off);
+    if (lane >= off) at += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, at, 31);
+  at -= cnt;
+  for (int w = w0; w < w1; ++w)
     for (uint32_t u = sh->member[w]; u; u &= u - 1) {
-      if (at < (uint32_t)p.top_k) out[at] = w * 32 + __ffs(u) - 1;
+      if (at < p.top_k) out[at] = w * 32 + __ffs(u) - 1;
       ++at;
     }
-  for (int i = (int)total + tid; i < p.top_k; i += kSelThreads) out[i] = -1;
+  for (int i = total + lane; i < p.top_k; i += 32) out[i] = -1;
 }
 
 template <int D, int NT>
-cudaError_t launch_select_nt(const DecodeSelectParams& p, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.B * p.H_kv;
-  const int tiles = (p.n_blocks + 15) / 16;  // 16 blocks per warp step
-  // enough CTAs for about eight per SM, each warp at least one step
-  int64_t gx = (8 * kPlanSms + rows - 1) / rows;
-  const int64_t most = (tiles + kScoreWarps - 1) / kScoreWarps;
-  gx = gx < 1 ? 1 : (gx > most ? most : gx);
-  decode_scores_kernel<D, NT><<<dim3((unsigned)gx, (unsigned)rows), 32 * kScoreWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_select_nt(const DecodeSelectParams& p0, cudaStream_t stream) {
+  DecodeSelectParams p = p0;
+  // CTAs per cluster: enough to fill the SMs (two CTAs each; one where the
+  // registers allow no more), each warp with at least one step of 16 blocks
+  const int rows = p.B * p.H_kv, slots = kPlanSms * (D == 256 || NT == 2 ? 1 : 2);
+  const int steps = (p.n_blocks + 16 * kSelWarps - 1) / (16 * kSelWarps);
+  p.ctas = 1;
+  while (p.ctas < 8 && rows * p.ctas * 2 <= slots && p.ctas * 2 <= steps) p.ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * p.ctas));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = sizeof(SelShared);
+  cfg.stream = stream;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(decode_select_kernel<D, NT>, sizeof(SelShared), &done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static_assert(2 * (sizeof(SelShared) + 1024) <= 228 * 1024, "two CTAs per SM");
+  return cudaLaunchKernelEx(&cfg, decode_select_kernel<D, NT>, p);
 }
 
 template <int D>
 cudaError_t launch_select_d(const DecodeSelectParams& p, cudaStream_t stream) {
-  cudaError_t e = (p.H / p.H_kv) <= 8 ? launch_select_nt<D, 1>(p, stream) : launch_select_nt<D, 2>(p, stream);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.B * p.H_kv);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelShared);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  static_assert(sizeof(SelShared) <= 48 * 1024, "static shared-memory limit");
-  return cudaLaunchKernelEx(&cfg, decode_select_kernel<D>, p);
+  return (p.H / p.H_kv) <= 8 ? launch_select_nt<D, 1>(p, stream) : launch_select_nt<D, 2>(p, stream);
 }
 
 template <int D>

@@ -136,14 +136,21 @@ cudaError_t launch_block_means(const BlockMeansParams& p, int d, cudaStream_t st
 
 constexpr int kSelectMaxBlocks = 32768;
 
+// A block's score as an ordered key, and a bound of its error.
+struct __align__(8) Score {
+  uint32_t key;
+  float err;
+};
+
 struct DecodeSelectParams {
   const void* q;            // [B][H][d] bf16
   const void* means;        // [B*H_kv][n_blocks][d] bf16
   const int32_t* seq_lens;  // [B] or null: n_blocks * block
-  float2* scores;           // [B*H_kv][n_blocks] score and bound of its error
+  Score* scores;            // [B*H_kv][n_blocks]
   double* again;            // [B*H_kv][n_blocks] scores formed again in 64 bits
   int32_t* ids;             // out [B*H_kv][top_k]
   int B, H, H_kv, n_blocks, block, top_k, keep_first, keep_recent;
+  int ctas;                 // of a (sequence, key/value head)'s cluster (set by the launch)
 };
 cudaError_t launch_decode_select(const DecodeSelectParams& p, int d, cudaStream_t stream);
 

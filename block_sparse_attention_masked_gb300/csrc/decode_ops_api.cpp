@@ -363,8 +363,8 @@ int mattn_decode_select(const void* q, const void* means, const int32_t* seq_len
                         "decode_select: top_k >= 1 and keep_first + keep_recent <= top_k (got %d, %d, %d)", top_k,
                         keep_first, keep_recent);
   if ((int64_t)B * H_kv * top_k > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "decode_select: top_k too large");
-  if (!aligned(q, 16) || !aligned(means, 16))
-    return report_error(MATTN_ERR_UNSUPPORTED, "decode_select: q and means must be 16-byte aligned");
+  if (!aligned(q, 16) || !aligned(means, 32))
+    return report_error(MATTN_ERR_UNSUPPORTED, "decode_select: q must be 16-byte and means 32-byte aligned");
   if ((rc = check_small("decode_select", block_ids, seq_lens, nullptr))) return rc;
   const size_t need = select_bytes(B, H_kv, n_blocks);
   if ((rc = check_workspace("decode_select", workspace, workspace_bytes, need))) return rc;
@@ -374,7 +374,7 @@ int mattn_decode_select(const void* q, const void* means, const int32_t* seq_len
   p.q = q;
   p.means = means;
   p.seq_lens = seq_lens;
-  p.scores = static_cast<float2*>(workspace);
+  p.scores = static_cast<Score*>(workspace);
   p.again = reinterpret_cast<double*>(static_cast<char*>(workspace) + need / 2);
   p.ids = block_ids;
   p.B = B; p.H = H; p.H_kv = H_kv;
