@@ -21,8 +21,8 @@ k and v may have fewer heads than q (grouped-query attention).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional
 
 import numpy as np
@@ -33,6 +33,7 @@ LIB_PATH = os.path.join(_PKG, "libmattn.so")
 # loaded instead of LIB_PATH when the environment sets MATTN_DEBUG=1, or
 # after use_debug_library(True).
 DEBUG_LIB_PATH = os.path.join(_PKG, "libmattn_debug.so")
+TORCH_CALLS_PATH = os.path.join(_PKG, "_torch_calls.so")
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -375,42 +376,40 @@ def decode(q, k_cache, v_cache, mask: PreparedMask, seq_lens=None, out=None, lse
     return out, lse
 
 
-class _Runtime:
-    """What the calls below ask of torch, looked up once: a decode step's
-    calls are short, and the host side of each is a share of its time."""
-
-    def __init__(self):
-        import torch
-
-        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-        self.empty, self.zeros = torch.empty, torch.zeros
-        self.current_device = torch.cuda.current_device
-        # the current stream's handle without a Stream object around it (2 us less a call)
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
-        self.device_guard = torch.cuda.device
+# The decode step's operators: the tensors are checked, and what is missing
+# made, in csrc/torch_calls.cpp (a decode step makes many of these calls, each
+# of a few microseconds, and the checks alone take as long from Python).
+_CALLS = ("mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
+          "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
+          "mattn_decode_blocks_workspace")
+_calls = None
+_calls_lib = None
 
 
-_runtime = None
+def _torch_calls():
+    """The module built from torch_calls.cpp, set to the library in use."""
+    global _calls, _calls_lib
+    L = _lib if _lib is not None else lib()
+    if _calls_lib is not L:
+        if _calls is None:
+            import torch  # noqa: F401  (its libraries are the module's)
+
+            if not os.path.exists(TORCH_CALLS_PATH):
+                raise RuntimeError(f"{os.path.basename(TORCH_CALLS_PATH)} is not built ({TORCH_CALLS_PATH}); run "
+                                   "python -m block_sparse_attention_masked_gb300.build")
+            spec = importlib.util.spec_from_file_location("_torch_calls", TORCH_CALLS_PATH)
+            _calls = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_calls)
+        _calls.set_functions(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _CALLS))
+        _calls_lib = L
+    return _calls
 
 
-def _rt() -> _Runtime:
-    global _runtime
-    if _runtime is None:
-        _runtime = _Runtime()
-    return _runtime
-
-
-def _launch(fn, device: int, *args):
-    """Calls fn(*args, stream) with `device` current, on its current stream."""
-    rt = _rt()
-    if rt.current_device() == device:
-        rc = fn(*args, rt.raw_stream(device))
-    else:
-        with rt.device_guard(device):
-            rc = fn(*args, rt.raw_stream(device))
-    if rc:
-        _check(rc)
+def _result(r):
+    """A call's outputs; where the library refused it, an int came back."""
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def _on_stream(stream, call, first, *args):
@@ -422,29 +421,16 @@ def _on_stream(stream, call, first, *args):
         return call(first, *args)
 
 
-def _on(device: int, dtype, **tensors):
-    """Every given tensor (None is skipped) is a contiguous one of `dtype` on CUDA device `device`."""
-    for name, t in tensors.items():
-        if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _size(fn, *args) -> int:
+def _workspace(fn, device, *sizes):
+    import torch
+
     n = ctypes.c_size_t(0)
-    _check(fn(*args, ctypes.byref(n)))
-    return n.value
-
-
-def _workspace(nbytes: int, device):
-    rt = _rt()
-    return rt.empty(max(nbytes, 16), dtype=rt.u8, device=device)
-
-
-_STRIDES = struct.Struct("=6q")
+    _check(fn(*sizes, ctypes.byref(n)))
+    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=device)
 
 
 class RopePlan:
@@ -458,20 +444,24 @@ class RopePlan:
 
     def __init__(self, inv_freq, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False):
+        import torch
+
         if not inv_freq.is_cuda or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be a CUDA fp32 tensor [R]")
         sections = [inv_freq.shape[0]] if sections is None else [int(n) for n in sections]
         if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
             raise ValueError("sections must be 1 to 3 pair counts that add up to inv_freq's length")
         self.device = inv_freq.get_device()
-        _on(self.device, _rt().f32, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
+        for t in (inv_freq, q_weight, k_weight):
+            if t is not None and (t.dtype != torch.float32 or t.get_device() != self.device or not t.is_contiguous()):
+                raise ValueError("inv_freq and the norm weights must be contiguous fp32 tensors on one CUDA device")
         for w in (q_weight, k_weight):
             if w is not None and (w.dim() != 1 or w.shape != (q_weight if q_weight is not None else w).shape):
                 raise ValueError("norm weights must be [d]")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         self.sections, self.eps, self.interleaved = sections, float(eps), bool(interleaved)
         w = q_weight if q_weight is not None else k_weight
-        self.width = None if w is None else w.shape[0]
+        self.width = 0 if w is None else w.shape[0]
         d = RopeDesc()
         d.n_axes = len(sections)
         for a, n in enumerate(sections):
@@ -500,94 +490,13 @@ def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positio
     Returns (q_out, k_out, v_out)."""
     if stream is not None:
         return _on_stream(stream, qk_rope, q, k, v, plan, q_out, k_out, v_out, positions, starts, lens)
-    rt = _rt()
-    B, N, H, d = q.shape
-    H_kv, dev, t = k.shape[2], q.get_device(), q.dtype
-    if dev < 0:
-        raise ValueError("q, k and v must be CUDA tensors")
-    if plan.device != dev or (plan.width is not None and plan.width != d):
-        raise ValueError("the plan's tensors must be on q's device and its weights [d]")
-    strides = []
-    for x, heads in ((q, H), (k, H_kv), (v, H_kv)):
-        if x is None:
-            strides.append((0, 0, 0, 0))
-            continue
-        s = x.stride()
-        if x.dtype is not t or x.get_device() != dev or x.shape != (B, N, heads, d):
-            raise ValueError("q must be [B, N, H, d] and k, v [B, N, H_kv, d] of one type and device")
-        if s[3] != 1 or (s[2] != d and heads > 1):
-            raise ValueError("the heads of a token must lie side by side")
-        strides.append(s)
-    if q_out is None:
-        q_out = rt.empty((B, H, N, d), dtype=t, device=q.device)
-    if k_out is None:
-        k_out = rt.empty((B, H_kv, N, d), dtype=t, device=q.device)
-    L = k_out.shape[2]
-    if v is None:
-        v_out = None
-    elif v_out is None:
-        v_out = rt.empty((B, H_kv, L, d), dtype=t, device=q.device)
-    _on(dev, t, q_out=q_out, k_out=k_out, v_out=v_out)
-    _on(dev, rt.i32, positions=positions, starts=starts, lens=lens)
-    if (q_out.shape != (B, H, N, d) or k_out.shape != (B, H_kv, L, d)
-            or (v_out is not None and v_out.shape != k_out.shape)):
-        raise ValueError("q_out must be [B, H, N, d], k_out and v_out [B, H_kv, L, d]")
-    if positions is not None and positions.shape != (len(plan.sections), B, N):
-        raise ValueError("positions must be [axes, B, N]")
-    if (starts is not None and starts.shape != (B,)) or (lens is not None and lens.shape != (B,)):
-        raise ValueError("starts and lens must be [B]")
-    (qb, qt, _, _), (kb, kt, _, _), (vb, vt, _, _) = strides
-    if N == 1:  # the stride of a dimension of one entry says nothing
-        qt = kt = vt = 0
-    if B == 1:
-        qb = kb = vb = 0
-    desc = RopeDesc.from_buffer_copy(plan._head + _STRIDES.pack(qt, kt, vt, qb, kb, vb))
-    _launch(lib().mattn_qk_rope, dev, q.data_ptr(), k.data_ptr(), _ptr(v), q_out.data_ptr(),
-            k_out.data_ptr(), _ptr(v_out), _ptr(positions), _ptr(starts), _ptr(lens), B, H, H_kv, N, L, d,
-            _dtype_code(q), ctypes.byref(desc))
-    return q_out, k_out, v_out
-
-
-def _decode_outputs(q, out, lse, want_lse):
-    rt = _rt()
-    shape = q.shape
-    if out is None:
-        out = rt.empty(shape, dtype=q.dtype, device=q.device)
-    elif out.shape != shape:
-        raise ValueError("out must be [B, H, d]")
-    if lse is not None:
-        if lse.shape != shape[:2]:
-            raise ValueError("lse must be [B, H]")
-    elif want_lse:
-        lse = rt.empty(shape[:2], dtype=rt.f32, device=q.device)
-    return out, lse
-
-
-def _decode_inputs(q, k, seq_lens, sink):
-    """Device and sizes of a decode call on the cache k [B, H_kv, L, d]."""
-    dev = q.get_device()
-    if dev < 0 or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor [B, H, d]")
-    B, H, d = q.shape
-    if k.dim() != 4:
-        raise ValueError("the cache must be [B, H_kv, L, d]")
-    Bk, H_kv, L, dk = k.shape
-    if Bk != B or dk != d:
-        raise ValueError("the cache must be [B, H_kv, L, d]")
-    if (seq_lens is not None and seq_lens.shape != (B,)) or (sink is not None and sink.shape != (H,)):
-        raise ValueError("seq_lens must be [B] and sink [H]")
-    return dev, B, H, H_kv, L, d
-
-
-def _bytes(workspace, device: int) -> int:
-    if workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{device}")
-    return workspace.numel() * workspace.element_size()
+    return _result(_torch_calls().qk_rope(q, k, v, plan._head, plan.device, plan.width, len(plan.sections), q_out, k_out,
+                                          v_out, positions, starts, lens))
 
 
 def decode_shared_workspace(B: int, H: int, H_kv: int, P: int, L: int, d: int, device="cuda"):
     """A workspace for ``decode_shared`` calls of these sizes that do not overlap."""
-    return _workspace(_size(lib().mattn_decode_shared_workspace, B, H, H_kv, P, L, d), device)
+    return _workspace(lib().mattn_decode_shared_workspace, device, B, H, H_kv, P, L, d)
 
 
 def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens=None, prefix_len=None, sink=None, scale=None,
@@ -603,23 +512,8 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens=None, prefix
     if stream is not None:
         return _on_stream(stream, decode_shared, q, k_prefix, v_prefix, k_cache, v_cache, seq_lens, prefix_len, sink, scale,
                           out, lse, want_lse, workspace)
-    rt = _rt()
-    dev, B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
-    if (k_prefix.dim() != 3 or k_prefix.shape != (H_kv, cap := k_prefix.shape[1], d)
-            or v_prefix.shape != k_prefix.shape or v_cache.shape != k_cache.shape):
-        raise ValueError("k_prefix, v_prefix must be [H_kv, P, d] and k_cache, v_cache [B, H_kv, L, d]")
-    P = cap if prefix_len is None else int(prefix_len)
-    out, lse = _decode_outputs(q, out, lse, want_lse)
-    _on(dev, q.dtype, q=q, k_prefix=k_prefix, v_prefix=v_prefix, k_cache=k_cache, v_cache=v_cache, out=out)
-    _on(dev, rt.f32, lse=lse, sink=sink)
-    _on(dev, rt.i32, seq_lens=seq_lens)
-    if workspace is None:
-        workspace = decode_shared_workspace(B, H, H_kv, P, L, d, q.device)
-    _launch(lib().mattn_decode_shared, dev, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(seq_lens), B, H, H_kv, P, cap, L, d,
-            _dtype_code(q), _ptr(sink), 0.0 if scale is None else float(scale), workspace.data_ptr(),
-            _bytes(workspace, dev))
-    return out, lse
+    return _result(_torch_calls().decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens, prefix_len, sink, scale,
+                                                out, lse, want_lse, workspace))
 
 
 def block_means(k_cache, block: int, seq_lens=None, first=None, max_new=None, out=None, stream=None):
@@ -632,32 +526,12 @@ def block_means(k_cache, block: int, seq_lens=None, first=None, max_new=None, ou
     ``out``.  Returns out [B, H_kv, ceil(L / block), d] (bf16)."""
     if stream is not None:
         return _on_stream(stream, block_means, k_cache, block, seq_lens, first, max_new, out)
-    rt = _rt()
-    dev = k_cache.get_device()
-    if dev < 0 or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a CUDA tensor [B, H_kv, L, d]")
-    B, H_kv, L, d = k_cache.shape
-    if block < 1:
-        raise ValueError("block must be >= 1")
-    shape = (B, H_kv, -(-L // block), d)
-    if out is None:
-        if first is not None:
-            raise ValueError("an update of means (first) needs the means to update (out)")
-        # blocks past a sequence's end: zeros
-        out = rt.zeros(shape, dtype=k_cache.dtype, device=k_cache.device)
-    _on(dev, k_cache.dtype, k_cache=k_cache, out=out)
-    _on(dev, rt.i32, seq_lens=seq_lens, first=first)
-    if (out.shape != shape or (seq_lens is not None and seq_lens.shape != (B,))
-            or (first is not None and first.shape != (B,))):
-        raise ValueError("out must be [B, H_kv, ceil(L / block), d]; seq_lens and first [B]")
-    _launch(lib().mattn_block_means, dev, k_cache.data_ptr(), out.data_ptr(), _ptr(seq_lens), _ptr(first),
-            B, H_kv, L, d, _dtype_code(k_cache), block, L if max_new is None else int(max_new))
-    return out
+    return _result(_torch_calls().block_means(k_cache, block, seq_lens, first, max_new, out))
 
 
 def decode_select_workspace(B: int, H: int, H_kv: int, n_blocks: int, d: int, device="cuda"):
     """A workspace for ``decode_select`` calls of these sizes that do not overlap."""
-    return _workspace(_size(lib().mattn_decode_select_workspace, B, H, H_kv, n_blocks, d), device)
+    return _workspace(lib().mattn_decode_select_workspace, device, B, H, H_kv, n_blocks, d)
 
 
 def decode_select(q, means, block: int, top_k: int, seq_lens=None, keep_first: int = 1, keep_recent: int = 1, out=None,
@@ -672,25 +546,12 @@ def decode_select(q, means, block: int, top_k: int, seq_lens=None, keep_first: i
     [B, H_kv, top_k], ascending, -1 behind the last one."""
     if stream is not None:
         return _on_stream(stream, decode_select, q, means, block, top_k, seq_lens, keep_first, keep_recent, out, workspace)
-    rt = _rt()
-    dev, B, H, H_kv, n, d = _decode_inputs(q, means, seq_lens, None)
-    if out is None:
-        out = rt.empty((B, H_kv, max(top_k, 0)), dtype=rt.i32, device=q.device)
-    _on(dev, q.dtype, q=q, means=means)
-    _on(dev, rt.i32, seq_lens=seq_lens, out=out)
-    if out.shape != (B, H_kv, top_k):
-        raise ValueError("out must be [B, H_kv, top_k]")
-    if workspace is None:
-        workspace = decode_select_workspace(B, H, H_kv, n, d, q.device)
-    _launch(lib().mattn_decode_select, dev, q.data_ptr(), means.data_ptr(), _ptr(seq_lens),
-            out.data_ptr(), B, H, H_kv, n, d, _dtype_code(q), block, top_k, keep_first, keep_recent,
-            workspace.data_ptr(), _bytes(workspace, dev))
-    return out
+    return _result(_torch_calls().decode_select(q, means, block, top_k, seq_lens, keep_first, keep_recent, out, workspace))
 
 
 def decode_blocks_workspace(B: int, H: int, H_kv: int, top_k: int, block: int, d: int, device="cuda"):
     """A workspace for ``decode_blocks`` calls of these sizes that do not overlap."""
-    return _workspace(_size(lib().mattn_decode_blocks_workspace, B, H, H_kv, top_k, block, d), device)
+    return _workspace(lib().mattn_decode_blocks_workspace, device, B, H, H_kv, top_k, block, d)
 
 
 def decode_blocks(q, k_cache, v_cache, block_ids, block: int, seq_lens=None, sink=None, scale=None, out=None,
@@ -704,20 +565,8 @@ def decode_blocks(q, k_cache, v_cache, block_ids, block: int, seq_lens=None, sin
     if stream is not None:
         return _on_stream(stream, decode_blocks, q, k_cache, v_cache, block_ids, block, seq_lens, sink, scale, out, lse, want_lse,
                           workspace)
-    rt = _rt()
-    dev, B, H, H_kv, L, d = _decode_inputs(q, k_cache, seq_lens, sink)
-    if block_ids.dim() != 3 or block_ids.shape != (B, H_kv, top_k := block_ids.shape[2]) or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must be [B, H_kv, L, d] and block_ids [B, H_kv, top_k]")
-    out, lse = _decode_outputs(q, out, lse, want_lse)
-    _on(dev, q.dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
-    _on(dev, rt.f32, lse=lse, sink=sink)
-    _on(dev, rt.i32, seq_lens=seq_lens, block_ids=block_ids)
-    if workspace is None:
-        workspace = decode_blocks_workspace(B, H, H_kv, top_k, block, d, q.device)
-    _launch(lib().mattn_decode_blocks, dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            out.data_ptr(), _ptr(lse), _ptr(seq_lens), block_ids.data_ptr(), B, H, H_kv, L, d, _dtype_code(q), block,
-            top_k, _ptr(sink), 0.0 if scale is None else float(scale), workspace.data_ptr(), _bytes(workspace, dev))
-    return out, lse
+    return _result(_torch_calls().decode_blocks(q, k_cache, v_cache, block_ids, block, seq_lens, sink, scale, out, lse,
+                                                want_lse, workspace))
 
 
 def attention_noalloc(q, k, v, mask: PreparedMask, out, lse=None, stream=None, check_wait: bool = True):

@@ -1,4 +1,5 @@
-"""Build libmattn.so (and libmattn_debug.so) in-tree with nvcc for sm_103a.
+"""Build libmattn.so (and libmattn_debug.so) in-tree with nvcc for sm_103a, and
+the binding's torch calls (_torch_calls.so) with the host compiler.
 
 Usage: python -m block_sparse_attention_masked_gb300.build [--verbose] [--no-debug]
 The libraries land next to this file; they are git-ignored and rebuilt on
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmattn.so")
 DEBUG_LIB = os.path.join(PKG, "libmattn_debug.so")
+TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["attention_fwd.cu", "attention_persist.cu", "attention_sp.cu", "rr_select.cu", "received.cu", "decode.cu", "mattn_api.cpp",
@@ -63,13 +66,40 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _build_torch_calls(verbose: bool = False) -> str:
+    """csrc/torch_calls.cpp against this machine's torch and Python."""
+    import torch
+
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = TORCH_CALLS + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-shared", "-fPIC", "-std=c++17", "-O2",
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem" if d != INCLUDE else "-I", d]
+    cmd += ["-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the compiler failed on torch_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    if verbose and (res.stdout or res.stderr):
+        print(res.stdout + res.stderr, file=sys.stderr)
+    os.replace(tmp, TORCH_CALLS)
+    return TORCH_CALLS
+
+
 def build(verbose: bool = False, debug: bool = True) -> str:
     """Compiles every source (twice with `debug`: product and debug objects,
-    all in parallel) and links libmattn.so and libmattn_debug.so."""
+    all in parallel), links libmattn.so and libmattn_debug.so, and builds
+    _torch_calls.so beside them."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = [(s, False) for s in SOURCES] + ([(s, True) for s in SOURCES] if debug else [])
-    with ThreadPoolExecutor(max_workers=min(len(jobs), max(4, os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, max(4, os.cpu_count() or 4))) as ex:
+        calls = ex.submit(_build_torch_calls, verbose)
         objs = list(ex.map(lambda j: _compile(j[0], verbose, j[1]), jobs))
+        calls.result()
     _link(objs[:len(SOURCES)], LIB)
     if debug:
         _link(objs[len(SOURCES):], DEBUG_LIB)

@@ -8,8 +8,12 @@
 // caller keeps) and then those of highest score, lowest index first on equal
 // scores, top_k in all, in ascending order.
 //
-// block_means_kernel: one warp per block, 16 bytes per lane, 32-bit sums: it
-// reads every new key once and is HBM-bound.
+// block_means_kernel: 16 bytes per lane, 32-bit sums; it reads every key of a
+// block that holds new ones once and is HBM-bound.  A warp per block where there
+// are blocks for all SMs (8 caches of 32K keys, 403 MB: 64 us, 81 with four
+// warps per block and their meeting), four where there are few: a quarter of a
+// 64-key block is one batch of loads, so that a decode step's update waits for
+// the memory once and not four times (64 requests: 4.2 us, 5.2 with one).
 //
 // Selection.  The choice is that of exact arithmetic on the bf16 means and
 // queries, so that it does not depend on how a product was summed:
@@ -50,58 +54,83 @@ __device__ __forceinline__ float bfh(uint32_t x) { return __uint_as_float(x & 0x
 // ------------------------------------------------------------ block means
 constexpr int kMeanWarps = 8;
 
-template <int D>
+// PARTS: warps per block.
+template <int D, int PARTS>
 __global__ void __launch_bounds__(32 * kMeanWarps) block_means_kernel(const __grid_constant__ BlockMeansParams p) {
   constexpr int LPR = D / 8;          // lanes of a key row
   constexpr int RPI = 32 / LPR;       // keys per warp load
   constexpr int U = 8;                // loads in flight per lane
+  constexpr int kMeanBlocks = kMeanWarps / PARTS;
+  __shared__ float sums[PARTS > 1 ? kMeanWarps : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kMeanWarps + warp;
+  const int slot = warp / PARTS, part = warp % PARTS;
+  const int64_t w = (int64_t)blockIdx.x * kMeanBlocks + slot;
   const int64_t row = w / p.span;     // (sequence, key/value head)
-  if (row >= (int64_t)p.B * p.H_kv) return;
-  const int b = (int)(row / p.H_kv);
-  int len = p.seq_lens ? p.seq_lens[b] : p.L;
-  len = len < 0 ? 0 : (len > p.L ? p.L : len);
-  int first = p.first ? p.first[b] : 0;
-  first = first < 0 ? 0 : first;
-  const int64_t end64 = (int64_t)first + p.max_new;
-  const int end = end64 < len ? (int)end64 : len;  // new keys: [first, end)
-  const int64_t blk = first / p.block + w % p.span;
-  const int64_t k0 = blk * p.block;
-  if (first >= end || k0 >= end || blk >= p.n_blocks) return;
-  const int n = len - k0 < p.block ? (int)(len - k0) : p.block;
+  int n = 0;                          // cached keys of the block, 0: not one to form
+  int64_t blk = 0;
+  if (row < (int64_t)p.B * p.H_kv) {
+    const int b = (int)(row / p.H_kv);
+    int len = p.seq_lens ? p.seq_lens[b] : p.L;
+    len = len < 0 ? 0 : (len > p.L ? p.L : len);
+    int first = p.first ? p.first[b] : 0;
+    first = first < 0 ? 0 : first;
+    const int64_t end64 = (int64_t)first + p.max_new;
+    const int end = end64 < len ? (int)end64 : len;  // new keys: [first, end)
+    blk = first / p.block + w % p.span;
+    const int64_t k0 = blk * p.block;
+    if (first < end && k0 < end && blk < p.n_blocks) n = len - k0 < p.block ? (int)(len - k0) : p.block;
+  }
   const int sub = lane % LPR, r0 = lane / LPR;
-  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k) +
-                                                    (row * p.L + k0) * D) + sub;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int r = r0; r < n; r += RPI * U) {
-    uint4 x[U];
+  const int share = p.block / PARTS, lo = part * share, hi = lo + share < n ? lo + share : n;
+  if (lo < hi) {
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k) +
+                                                      (row * p.L + blk * p.block) * D) + sub;
+    for (int r = lo + r0; r < hi; r += RPI * U) {
+      uint4 x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      x[u] = r + u * RPI < n ? __ldg(src + (int64_t)(r + u * RPI) * LPR) : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; ++u)
+        x[u] = r + u * RPI < hi ? __ldg(src + (int64_t)(r + u * RPI) * LPR) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      acc[0] += bfl(x[u].x); acc[1] += bfh(x[u].x);
-      acc[2] += bfl(x[u].y); acc[3] += bfh(x[u].y);
-      acc[4] += bfl(x[u].z); acc[5] += bfh(x[u].z);
-      acc[6] += bfl(x[u].w); acc[7] += bfh(x[u].w);
+      for (int u = 0; u < U; ++u) {
+        acc[0] += bfl(x[u].x); acc[1] += bfh(x[u].x);
+        acc[2] += bfl(x[u].y); acc[3] += bfh(x[u].y);
+        acc[4] += bfl(x[u].z); acc[5] += bfh(x[u].z);
+        acc[6] += bfl(x[u].w); acc[7] += bfh(x[u].w);
+      }
     }
   }
 #pragma unroll
   for (int off = LPR; off < 32; off <<= 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-  if (lane < LPR) {
-    const float c = (float)n;
-    uint4 y;
-    y.x = ptx::pack_bf16x2(acc[0] / c, acc[1] / c);
-    y.y = ptx::pack_bf16x2(acc[2] / c, acc[3] / c);
-    y.z = ptx::pack_bf16x2(acc[4] / c, acc[5] / c);
-    y.w = ptx::pack_bf16x2(acc[6] / c, acc[7] / c);
-    reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.means) + (row * p.n_blocks + blk) * D)[sub] = y;
+  const float c = (float)n;
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.means) + (row * p.n_blocks + blk) * D;
+  if constexpr (PARTS == 1) {
+    if (lane < LPR && n > 0)
+      reinterpret_cast<uint4*>(dst)[sub] =
+          make_uint4(ptx::pack_bf16x2(acc[0] / c, acc[1] / c), ptx::pack_bf16x2(acc[2] / c, acc[3] / c),
+                     ptx::pack_bf16x2(acc[4] / c, acc[5] / c), ptx::pack_bf16x2(acc[6] / c, acc[7] / c));
+    return;
   }
+  if (lane < LPR) {
+    *reinterpret_cast<float4*>(&sums[warp][sub * 8]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *reinterpret_cast<float4*>(&sums[warp][sub * 8 + 4]) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+  __syncthreads();
+  // the block's dims over its warps, two values per lane
+  if (n > 0)
+    for (int d = (part * 32 + lane) * 2; d < D; d += PARTS * 64) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        x += sums[slot * PARTS + k][d];
+        y += sums[slot * PARTS + k][d + 1];
+      }
+      reinterpret_cast<uint32_t*>(dst)[d / 2] = ptx::pack_bf16x2(x / c, y / c);
+    }
 }
 
 // ------------------------------------------------------------ selection
@@ -680,11 +709,18 @@ cudaError_t launch_select_d(const DecodeSelectParams& p, cudaStream_t stream) {
   return (p.H / p.H_kv) <= 8 ? launch_select_nt<D, 1>(p, stream) : launch_select_nt<D, 2>(p, stream);
 }
 
+template <int D, int PARTS>
+cudaError_t launch_means_parts(const BlockMeansParams& p, cudaStream_t stream) {
+  const int64_t warps = (int64_t)p.B * p.H_kv * p.span * PARTS;
+  block_means_kernel<D, PARTS><<<(unsigned)((warps + kMeanWarps - 1) / kMeanWarps), 32 * kMeanWarps, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_means_d(const BlockMeansParams& p, cudaStream_t stream) {
-  const int64_t warps = (int64_t)p.B * p.H_kv * p.span;
-  block_means_kernel<D><<<(unsigned)((warps + kMeanWarps - 1) / kMeanWarps), 32 * kMeanWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  // four warps per block while those fill no more than the SMs' 64 warps
+  return (int64_t)p.B * p.H_kv * p.span <= kPlanSms * 16 ? launch_means_parts<D, 4>(p, stream)
+                                                         : launch_means_parts<D, 1>(p, stream);
 }
 
 }  // namespace

@@ -336,8 +336,8 @@ int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const
   // new keys that start anywhere in a block reach into one block more
   const int64_t span = ((int64_t)max_new - 1) / block + 2;
   p.span = (int)(span < p.n_blocks ? span : p.n_blocks);
-  if ((int64_t)B * H_kv * p.span > (int64_t)1 << 33)
-    return report_error(MATTN_ERR_UNSUPPORTED, "block_means: more than 2^33 blocks");
+  if ((int64_t)B * H_kv * p.span > (int64_t)1 << 31)
+    return report_error(MATTN_ERR_UNSUPPORTED, "block_means: more than 2^31 blocks");
   return launched(launch_block_means(p, d, static_cast<cudaStream_t>(stream)), "block_means launch");
 }
 
