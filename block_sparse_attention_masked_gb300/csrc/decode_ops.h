@@ -47,6 +47,7 @@ struct RopeParams {
   int axes, axis_end[3];    // pairs [axis_end[a - 1], axis_end[a]) turn with axis a
   int rot;                  // rotated pairs
   int interleaved;          // pairs (2p, 2p + 1) instead of (p, p + rot)
+  bool wide;                // fp32: every row starts on a 32-byte boundary
   int segs;                 // warps that share one token's rows
   float eps;
 };

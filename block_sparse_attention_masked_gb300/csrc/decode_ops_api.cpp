@@ -194,11 +194,13 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
   const void* in[3] = {q, k, v};
   void* out[3] = {q_out, k_out, v_out};
   const int es = dtype == MATTN_F32 ? 4 : 2;
+  p.wide = true;
   for (int t = 0; t < (v ? 3 : 2); ++t) {
     const int64_t ts = desc->token_stride[t], bs = desc->batch_stride[t];
     if (!aligned(in[t], 16) || !aligned(out[t], 16) || (ts * es) % 16 || (bs * es) % 16)
       return report_error(MATTN_ERR_UNSUPPORTED, "qk_rope: rows must start on 16-byte boundaries");
     if (ts < 0 || bs < 0) return report_error(MATTN_ERR_INVALID_ARG, "qk_rope: strides must be >= 0");
+    p.wide = p.wide && aligned(in[t], 32) && aligned(out[t], 32) && (ts * es) % 32 == 0 && (bs * es) % 32 == 0;
     p.src[t] = in[t];
     p.dst[t] = out[t];
     p.token_stride[t] = ts;

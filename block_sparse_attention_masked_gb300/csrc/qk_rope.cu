@@ -8,10 +8,14 @@
 // in 32 bits with one rounding at the store; queries go to [B][H][N][d],
 // keys and (unchanged) values to row start + n of their caches.  Each value
 // is read once and written once, so the pass is HBM-bound: a warp takes one
-// token's rows (d / 16 lanes per row, each two 16-byte pieces that hold whole
-// pairs, so no lane needs another's values but for the row's mean square),
-// four rows per lane group in flight, and forms the token's cosines and
-// sines once for all its heads.
+// token's rows (d / 16 lanes per row, each two pieces of 8 values that hold whole
+// pairs, so no lane needs another's values but for the row's mean square) and
+// forms the token's cosines and sines once for all its heads.  What counts is
+// loads in flight: with the angles and weights in shared memory and two rows a
+// lane group at a time the kernel keeps 64 registers and 32 warps an SM (805 MB
+// in bf16: 136 us, 5.9 TB/s; 156 us with both in registers, four rows and 16
+// warps); fp32 rows move 32 bytes an access (503 MB: 83 us, 100 with 16).
+// Where tokens are few, warps share a token's rows.
 //
 // Angles: inv_freq / 2 pi is held as a 64-bit fraction of a turn (rounded
 // once, below 2^-53 of itself), so position times it modulo a whole turn is
@@ -28,15 +32,16 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeMaxPairs = 128;
-constexpr int kRopeBatch = 4;  // rows in flight per lane group
+constexpr int kRopeBatch = 2;  // rows in flight per lane group
 
-// 8 values of a row: 16 bytes of bf16, or two 16-byte pieces of fp32.
+// 8 values of a row: 16 bytes of bf16, or 32 of fp32 (`wide`: as one access,
+// where every row starts on a 32-byte boundary).
 template <bool F32>
 struct Piece;
 template <>
 struct Piece<false> {
   uint4 u;
-  __device__ __forceinline__ void load(const void* base, int64_t e) {
+  __device__ __forceinline__ void load(const void* base, int64_t e, bool) {
     u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + e));
   }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
@@ -57,17 +62,23 @@ struct Piece<false> {
     }
     u = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void store(void* base, int64_t e) const {
+  __device__ __forceinline__ void store(void* base, int64_t e, bool) const {
     *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + e) = u;
   }
 };
 template <>
 struct Piece<true> {
   float4 a, b;
-  __device__ __forceinline__ void load(const void* base, int64_t e) {
+  __device__ __forceinline__ void load(const void* base, int64_t e, bool wide) {
     const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + e);
-    a = __ldg(s);
-    b = __ldg(s + 1);
+    if (wide) {
+      asm volatile("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                   : "l"(s));
+    } else {
+      a = __ldg(s);
+      b = __ldg(s + 1);
+    }
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -78,12 +89,24 @@ struct Piece<true> {
     a = make_float4(x[0], x[1], x[2], x[3]);
     b = make_float4(x[4], x[5], x[6], x[7]);
   }
-  __device__ __forceinline__ void store(void* base, int64_t e) const {
+  __device__ __forceinline__ void store(void* base, int64_t e, bool wide) const {
     float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + e);
-    d[0] = a;
-    d[1] = b;
+    if (wide) {
+      asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d), "f"(a.x), "f"(a.y), "f"(a.z),
+                   "f"(a.w), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+                   : "memory");
+    } else {
+      d[0] = a;
+      d[1] = b;
+    }
   }
 };
+
+__device__ __forceinline__ void get8(float (&x)[8], const float* s) {
+  const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 // Sum over the GL lanes of a row's group, the same order on every lane.
 template <int GL>
@@ -101,40 +124,24 @@ __device__ __forceinline__ float group_sum(float v, int lane0) {
 }
 
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(32 * kRopeWarps) qk_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, 4) qk_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int GL = D / 16;       // lanes of a row
   constexpr int RPW = 32 / GL;     // rows of a warp
   __shared__ unsigned long long turn[kRopeMaxPairs];          // inv_freq / 2 pi as a 2^-64 fraction of a turn
-  __shared__ float2 trig[kRopeWarps][kRopeMaxPairs];          // cosine, sine of the warp's token
+  __shared__ __align__(16) float trig[kRopeWarps][2][kRopeMaxPairs];  // cosines, sines of the warp's token
+  __shared__ __align__(16) float weights[2][D];               // of the norms of q and k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < p.rot; i += blockDim.x) {
-    const double t = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    turn[i] = __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
-  }
-  __syncthreads();
   const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp;
   const int64_t token = gw / p.segs;
   const int seg = (int)(gw % p.segs);
-  if (token >= (int64_t)p.B * p.N) return;
-  const int b = (int)(token / p.N), n = (int)(token % p.N);
-  if (p.lens && n >= p.lens[b]) return;  // the batch's padding
-  const int start = p.starts ? p.starts[b] : 0;
-  for (int i = lane; i < p.rot; i += 32) {
-    const int axis = i < p.axis_end[0] ? 0 : (i < p.axis_end[1] ? 1 : 2);
-    const int64_t pos = p.positions ? p.positions[((int64_t)axis * p.B + b) * p.N + n] : (int64_t)start + n;
-    // half turns in [-1, 1)
-    const float x = __ll2float_rn((long long)((unsigned long long)pos * turn[i])) * 1.0842021724855044e-19f;  // 2^-63
-    float s, c;
-    sincospif(x, &s, &c);
-    trig[warp][i] = make_float2(c, s);
-  }
-  __syncwarp();
+  const bool live = token < (int64_t)p.B * p.N;
+  const int b = live ? (int)(token / p.N) : 0, n = live ? (int)(token % p.N) : 0;
 
   const int grp = lane / GL, sub = lane - grp * GL;
   const bool idle = grp >= RPW;  // lanes past the last whole row (d = 80, 96)
   const int lane0 = grp * GL;
   const int r8 = p.rot / 8;      // lanes of a row that hold rotated pairs
-  // the lane's two pieces of the row and, for each of its eight pairs, the angle
+  // the lane's two pieces of the row, of 8 values each
   int ca, cb;
   if (INTER) {
     ca = 2 * sub;
@@ -147,52 +154,77 @@ __global__ void __launch_bounds__(32 * kRopeWarps) qk_rope_kernel(const __grid_c
     cb = ca + 1;
   }
   const bool rotated = !idle && sub < r8;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 t = rotated ? trig[warp][sub * 8 + i] : make_float2(1.f, 0.f);
-    cs[i] = t.x;
-    sn[i] = t.y;
-  }
 
-  const int its[3] = {(p.H + RPW - 1) / RPW, (p.H_kv + RPW - 1) / RPW, p.dst[2] ? (p.H_kv + RPW - 1) / RPW : 0};
-  const int total = its[0] + its[1] + its[2];
+  // the token's rows in steps of RPW heads: its of q, then of k, then of v;
+  // this warp's are [i_lo, i_hi)
+  const int its_q = (p.H + RPW - 1) / RPW, its_k = (p.H_kv + RPW - 1) / RPW, its_v = p.dst[2] ? its_k : 0;
+  const int total = its_q + its_k + its_v;
   const int i_lo = (int)((int64_t)total * seg / p.segs), i_hi = (int)((int64_t)total * (seg + 1) / p.segs);
+  Piece<F32> a[kRopeBatch], c[kRopeBatch];
+  // steps it .. of tensor t, at src0
+  auto load = [&](const void* src, int64_t src0, int heads, int it, int hi) {
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) {
+      const int head = (it + u) * RPW + grp;
+      if (!idle && it + u < hi && head < heads) {
+        a[u].load(src, src0 + (int64_t)head * D + ca * 8, p.wide);
+        c[u].load(src, src0 + (int64_t)head * D + cb * 8, p.wide);
+      } else {
+        a[u].zero();
+        c[u].zero();
+      }
+    }
+  };
+  // (the first rows, the length and the position are on their way while the
+  // frequencies are turned into fractions)
+  if (live) {
+    const int t = i_lo < its_q ? 0 : (i_lo < its_q + its_k ? 1 : 2);
+    const int base = t == 0 ? 0 : (t == 1 ? its_q : its_q + its_k);
+    load(p.src[t], (int64_t)b * p.batch_stride[t] + (int64_t)n * p.token_stride[t], t == 0 ? p.H : p.H_kv, i_lo - base,
+         min(i_hi - base, t == 0 ? its_q : its_k));
+  }
+  const int len = live && p.lens ? p.lens[b] : p.N;
+  const int start = live && p.starts ? p.starts[b] : 0;
+  for (int i = threadIdx.x; i < p.rot; i += blockDim.x) {
+    const double t = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    turn[i] = __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    if (p.weight[t])
+      for (int i = threadIdx.x; i < D; i += blockDim.x) weights[t][i] = __ldg(p.weight[t] + i);
+  __syncthreads();
+  if (!live || n >= len) return;  // the batch's padding
+  for (int i = lane; i < p.rot; i += 32) {
+    const int axis = i < p.axis_end[0] ? 0 : (i < p.axis_end[1] ? 1 : 2);
+    const int64_t pos = p.positions ? p.positions[((int64_t)axis * p.B + b) * p.N + n] : (int64_t)start + n;
+    // half turns in [-1, 1)
+    const float x = __ll2float_rn((long long)((unsigned long long)pos * turn[i])) * 1.0842021724855044e-19f;  // 2^-63
+    float s, co;
+    sincospif(x, &s, &co);
+    trig[warp][0][i] = co;
+    trig[warp][1][i] = s;
+  }
+  __syncwarp();
+
+  bool loaded = true;  // the first rows
   int base = 0;
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
-    const int lo = max(i_lo, base) - base, hi = min(i_hi, base + its[t]) - base;
-    base += its[t];
+    const int its = t == 0 ? its_q : (t == 1 ? its_k : its_v);
+    const int lo = max(i_lo, base) - base, hi = min(i_hi, base + its) - base;
+    base += its;
     if (lo >= hi) continue;
     const int heads = t == 0 ? p.H : p.H_kv;
-    const int64_t row = t == 0 ? (int64_t)n : (int64_t)start + n;
-    const int64_t rows = t == 0 ? p.N : p.L;
-    if (row < 0 || row >= rows) continue;  // outside the cache: not written
+    const int64_t to = t == 0 ? (int64_t)n : (int64_t)start + n, rows = t == 0 ? p.N : p.L;
+    const bool there = to >= 0 && to < rows;  // rows outside the cache are not written
     const void* src = p.src[t];
     const int64_t src0 = (int64_t)b * p.batch_stride[t] + (int64_t)n * p.token_stride[t];
-    const int64_t dst0 = ((int64_t)b * heads * rows + row) * D;
-    float wa[8], wb[8];
+    const int64_t dst0 = ((int64_t)b * heads * rows + to) * D;
     const bool norm = t < 2 && p.weight[t < 2 ? t : 0];
-    if (norm && !idle) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        wa[i] = __ldg(p.weight[t < 2 ? t : 0] + ca * 8 + i);
-        wb[i] = __ldg(p.weight[t < 2 ? t : 0] + cb * 8 + i);
-      }
-    }
     for (int it = lo; it < hi; it += kRopeBatch) {
-      Piece<F32> a[kRopeBatch], c[kRopeBatch];
-#pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int head = (it + u) * RPW + grp;
-        if (!idle && it + u < hi && head < heads) {
-          a[u].load(src, src0 + (int64_t)head * D + ca * 8);
-          c[u].load(src, src0 + (int64_t)head * D + cb * 8);
-        } else {
-          a[u].zero();
-          c[u].zero();
-        }
-      }
+      if (!loaded) load(src, src0, heads, it, hi);
+      loaded = false;
 #pragma unroll
       for (int u = 0; u < kRopeBatch; ++u) {
         if (it + u >= hi) break;  // warp-uniform
@@ -207,13 +239,18 @@ __global__ void __launch_bounds__(32 * kRopeWarps) qk_rope_kernel(const __grid_c
             for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
             ss = group_sum<GL>(ss, lane0);
             const float r = rsqrtf(ss * (1.f / D) + p.eps);
+            float w[8];
+            get8(w, &weights[t < 2 ? t : 0][(idle ? 0 : ca) * 8]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] *= r * wa[i];
-              y[i] *= r * wb[i];
-            }
+            for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+            get8(w, &weights[t < 2 ? t : 0][(idle ? 0 : cb) * 8]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= r * w[i];
           }
           if (rotated) {
+            float cs[8], sn[8];
+            get8(cs, &trig[warp][0][sub * 8]);
+            get8(sn, &trig[warp][1][sub * 8]);
             if (INTER) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -235,9 +272,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps) qk_rope_kernel(const __grid_c
           a[u].set(x);
           c[u].set(y);
         }
-        if (!idle && head < heads) {
-          a[u].store(p.dst[t], dst0 + (int64_t)head * rows * D + ca * 8);
-          c[u].store(p.dst[t], dst0 + (int64_t)head * rows * D + cb * 8);
+        if (there && !idle && head < heads) {
+          a[u].store(p.dst[t], dst0 + (int64_t)head * rows * D + ca * 8, p.wide);
+          c[u].store(p.dst[t], dst0 + (int64_t)head * rows * D + cb * 8, p.wide);
         }
       }
     }
