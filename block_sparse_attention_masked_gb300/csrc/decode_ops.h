@@ -74,11 +74,18 @@ struct DecodeRowsParams {
   int list_tiles;           // tiles of a list of top_k blocks (0: by the sequence's length)
   int min_tiles;            // of a warp's share
   int ctas;                 // of the grid
+  int cluster;              // decode_lists_kernel: CTAs per group
+  const float* sink;        // decode_lists_kernel writes o itself: [H] or null
+  void* o;                  // [B][H][d] bf16
+  float* lse;               // [B][H] or null
   float scale_log2;
 };
 // `after`: launched as a programmatic dependent of the stream's previous
 // grid, whose results it does not read; it completes only after that grid.
 cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cudaStream_t stream);
+
+cudaError_t launch_decode_lists(const DecodeRowsParams& p, int d, cudaStream_t stream);
+int decode_lists_cluster(int64_t groups, int top_k, int list_tiles, int d);
 
 // ------------------------------------------------------------ decode_shared.cu
 struct SharedPlan {

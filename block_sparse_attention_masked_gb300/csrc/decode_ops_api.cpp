@@ -128,6 +128,7 @@ int check_blocks(int B, int H, int H_kv, int top_k, int block, int d, int dtype)
   if (rc) return rc;
   if (block < 16 || block % 16)
     return report_error(MATTN_ERR_UNSUPPORTED, "decode_blocks: block size %d is not a multiple of 16", block);
+  if (block > (1 << 20)) return report_error(MATTN_ERR_UNSUPPORTED, "decode_blocks: block size %d exceeds 2^20", block);
   if (top_k < 1) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: top_k must be >= 1");
   if ((int64_t)top_k * block > kMaxRows)
     return report_error(MATTN_ERR_UNSUPPORTED, "decode_blocks: top_k * block exceeds 2^30");
@@ -392,7 +393,9 @@ int mattn_decode_blocks_workspace(int B, int H, int H_kv, int top_k, int block, 
   if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: bytes_out is NULL");
   const int rc = check_blocks(B, H, H_kv, top_k, block, d, MATTN_BF16);
   if (rc) return rc;
-  *bytes_out = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d).all();
+  *bytes_out = decode_lists_cluster((int64_t)B * H_kv, top_k, list_tiles(top_k, block, d), d)
+                   ? 0
+                   : rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d).all();
   return MATTN_OK;
 }
 
@@ -411,8 +414,9 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   if ((rc = check_small("decode_blocks", lse, seq_lens, sink))) return rc;
   if (!aligned(block_ids, 4)) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: block_ids must be 4-byte aligned");
   if ((rc = check_scale("decode_blocks", softmax_scale))) return rc;
+  const int tiles = list_tiles(top_k, block, d), cluster = decode_lists_cluster((int64_t)B * H_kv, top_k, tiles, d);
   const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d);
-  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, lay.all()))) return rc;
+  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, cluster ? 0 : lay.all()))) return rc;
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   DecodeRowsParams p;
@@ -422,17 +426,24 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   p.q = q;
   p.seq_lens = seq_lens;
   p.ids = block_ids;
-  place_rows(&p, lay, static_cast<char*>(workspace));
   p.err = err;
   p.timeout_ns = device_wait_timeout_ns();
   p.B = B; p.H = H; p.H_kv = H_kv; p.L = L;
   p.top_k = top_k;
   p.block = block;
   p.box16 = block / 16;
-  p.list_tiles = list_tiles(top_k, block, d);
+  p.list_tiles = tiles;
   p.min_tiles = 1;
   p.ctas = kPlanSms;
   p.scale_log2 = scale_log2(softmax_scale, d);
+  if (cluster) {
+    p.cluster = cluster;
+    p.sink = sink;
+    p.o = o;
+    p.lse = lse;
+    return launched(launch_decode_lists(p, d, stream), "list launch");
+  }
+  place_rows(&p, lay, static_cast<char*>(workspace));
   if ((rc = launched(launch_decode_rows(p, d, false, stream), "block launch"))) return rc;
   MergeParams m;
   memset(&m, 0, sizeof(m));

@@ -69,6 +69,192 @@ cudaError_t launch_nt(const DecodeRowsParams& p, bool after, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, kern, p, after ? 1 : 0);
 }
 
+// Few groups or short lists: a cluster of CTAs per (sequence, key/value head),
+// one warp's tile after another's, no states in memory and no second launch.
+// The warps of a CTA meet in its shared memory, the CTAs of the cluster in each
+// other's, each CTA finishing a share of the G x D outputs.
+constexpr int kListIds = 1024;  // list entries that fit the kernel's table
+
+template <int D, int NT>
+struct ListSmem {
+  static constexpr int kWarps = decode_rows_warps(D), HP = 8 * NT;
+  static constexpr size_t kRing = (size_t)kWarps * rows::Geo<D>::kRing;
+  // over the ring, once every tile is read: the warps' states, then the CTA's
+  static constexpr size_t kStates = (size_t)(kWarps + 1) * HP * (D + 2) * 4;
+  static_assert(kStates <= kRing, "the states must fit in the ring");
+  static constexpr size_t kBytes = 1024 + kRing + kWarps * rows::Geo<D>::NS * 8 + 16 + kListIds * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+  uint32_t a;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
+    decode_lists_kernel(const __grid_constant__ DecodeRowsParams p) {
+  using Geo = rows::Geo<D>;
+  using Mem = ListSmem<D, NT>;
+  constexpr int kWarps = Mem::kWarps, MT = Geo::MT, NS = Geo::NS, HP = Mem::HP;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring_all = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_all = reinterpret_cast<uint64_t*>(ring_all + Mem::kRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full_all + kWarps * NS);
+  int* ids = reinterpret_cast<int*>(full_all + kWarps * NS + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.cluster, bkv = blockIdx.x / p.cluster;
+  const int b = bkv / p.H_kv, G = p.H / p.H_kv;
+  const int64_t bh0 = (int64_t)bkv * G;
+  for (int i = threadIdx.x; i < p.top_k; i += 32 * kWarps) ids[i] = __ldg(p.ids + (int64_t)bkv * p.top_k + i);
+  const int len = rows::cached_keys(p, b);
+  if (threadIdx.x < kWarps * NS) ptx::mbar_init(full_all + threadIdx.x, 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  ptx::fence_barrier_init();
+  __syncthreads();
+
+  uint8_t* ring = ring_all + warp * Geo::kRing;
+  uint64_t* full = full_all + warp * NS;
+  const int blocks = (len + p.block - 1) / p.block;
+  const int first = rank + warp * p.cluster, step = p.cluster * kWarps;  // this warp's tiles: first, first + step, ..
+  const int mine = first < p.list_tiles ? (p.list_tiles - first + step - 1) / step : 0;
+  auto issue = [&](int n) -> uint32_t {
+    int pos[MT], cnt[MT];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      const int box = (first + n * step) * MT + x, j = box / p.box16;
+      const int id = j < p.top_k ? ids[j] : -1;
+      pos[x] = (uint32_t)id < (uint32_t)blocks ? id * p.block + ((box - j * p.box16) << 4) : len;
+      const int left = len - pos[x];
+      cnt[x] = left < 0 ? 0 : (left < 16 ? left : 16);
+    }
+    return rows::issue_tile<D>(p, ring, full, n & 1, bkv, pos, cnt);
+  };
+  uint32_t masks[2] = {0, 0};
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    if (n < mine) masks[n] = issue(n);
+  rows::State<D, NT> st;
+  st.begin(p.q, bh0, G);
+  const uint32_t at_k = rows::lane_k(ptx::smem_addr(ring)), at_v = rows::lane_v(ptx::smem_addr(ring) + Geo::kTensor);
+  for (int n = 0; n < mine; ++n) {
+    const int stage = n & 1;
+    const uint32_t mask = stage ? masks[1] : masks[0];
+    if (!rows::await(p, full + stage, (n >> 1) & 1, abort_flag)) break;
+    if (mask)  // warp-uniform
+      st.step(at_k + stage * Geo::kStage, at_v + stage * Geo::kStage, ring + stage * Geo::kStage + Geo::kTensor, mask,
+              p.scale_log2);
+    __syncwarp();
+    if (n + NS < mine) {
+      if (mask != Geo::kAll) ptx::fence_proxy_async_shared();  // the zeros of step before the copy that overwrites them
+      __syncwarp();
+      const uint32_t x = issue(n + NS);
+      if (stage) masks[1] = x;
+      else masks[0] = x;
+    }
+  }
+  __syncthreads();  // every tile of every warp is read
+  // the warps' states: O [kWarps + 1][HP][D], then reference and sum [kWarps + 1][HP][2]
+  float* so = reinterpret_cast<float*>(ring_all);
+  float* sml = so + (kWarps + 1) * HP * D;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float s = st.sum(nt, e);
+      const int head = nt * 8 + (lane & 3) * 2 + e;
+      if (lane < 4) {
+        sml[(warp * HP + head) * 2] = st.m[nt][e];
+        sml[(warp * HP + head) * 2 + 1] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        so[(warp * HP + head) * D + i * 16 + (lane >> 2)] = st.o[nt][i][e];
+        so[(warp * HP + head) * D + i * 16 + 8 + (lane >> 2)] = st.o[nt][i][e + 2];
+      }
+    }
+  __syncthreads();
+  // the CTA's state
+  for (int t = threadIdx.x; t < G * D; t += 32 * kWarps) {
+    const int g = t / D, c = t % D;
+    float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * HP + g) * 2]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = sml[(w * HP + g) * 2], e = mw == M ? 1.f : ptx::ex2(mw - M);
+      L = fmaf(sml[(w * HP + g) * 2 + 1], e, L);
+      O = fmaf(so[(w * HP + g) * D + c], e, O);
+    }
+    so[(kWarps * HP + g) * D + c] = O;
+    if (c == 0) {
+      sml[(kWarps * HP + g) * 2] = M;
+      sml[(kWarps * HP + g) * 2 + 1] = L;
+    }
+  }
+  if (p.cluster > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+  // this CTA's share of the outputs (a CTA that gave up leaves no number behind:
+  // its cluster's outputs are then undefined, and the error word says so)
+  const int share = (G * D + p.cluster - 1) / p.cluster;
+  const int t1 = (rank + 1) * share < G * D ? (rank + 1) * share : G * D;
+  for (int t = rank * share + threadIdx.x; t < t1; t += 32 * kWarps) {
+    const int g = t / D, c = t % D;
+    const float* ml = sml + (kWarps * HP + g) * 2;
+    const float* o = so + (kWarps * HP + g) * D + c;
+    const float b2 = p.sink ? p.sink[(bkv % p.H_kv) * G + g] * kLog2eR : -INFINITY;
+    float mr[8], M = b2;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      mr[r] = r < p.cluster ? cluster_ld(ml, r) : -INFINITY;
+      M = fmaxf(M, mr[r]);
+    }
+    float z = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - M), O = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (r < p.cluster) {
+        const float e = mr[r] == M ? 1.f : ptx::ex2(mr[r] - M);
+        z = fmaf(cluster_ld(ml + 1, r), e, z);
+        O = fmaf(cluster_ld(o, r), e, O);
+      }
+    reinterpret_cast<__nv_bfloat16*>(p.o)[(bh0 + g) * D + c] = __float2bfloat16_rn(z == 0.f ? 0.f : O / z);
+    if (c == 0 && p.lse) p.lse[bh0 + g] = z == 0.f ? -INFINITY : (M + __log2f(z)) * kLn2R;
+  }
+  if (p.cluster > 1) {  // no CTA leaves while another reads its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
+  auto kern = decode_lists_kernel<D, NT>;
+  const size_t smem = ListSmem<D, NT>::kBytes;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kern, smem, &done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv * p.cluster));
+  cfg.blockDim = dim3(32 * decode_rows_warps(D));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 // The merge.  Row (b, h)'s states: `na` of the prefix, then the pieces of its
 // own list.  o = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s + exp(sink)).
 // LPS lanes take a state (16 bytes each) of SL dims of one row; WPR warps share
@@ -229,6 +415,19 @@ cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cud
   }
 }
 
+cudaError_t launch_decode_lists(const DecodeRowsParams& p, int d, cudaStream_t stream) {
+  const int nt = (p.H / p.H_kv + 7) / 8;
+  switch (d * 4 + nt) {
+    case 64 * 4 + 1: return launch_lists_nt<64, 1>(p, stream);
+    case 64 * 4 + 2: return launch_lists_nt<64, 2>(p, stream);
+    case 128 * 4 + 1: return launch_lists_nt<128, 1>(p, stream);
+    case 128 * 4 + 2: return launch_lists_nt<128, 2>(p, stream);
+    case 256 * 4 + 1: return launch_lists_nt<256, 1>(p, stream);
+    case 256 * 4 + 2: return launch_lists_nt<256, 2>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 cudaError_t launch_decode_merge(const MergeParams& p, int d, bool after, cudaStream_t stream) {
   switch (d) {
     case 64: return launch_merge_d<64>(p, after, stream);
@@ -236,6 +435,21 @@ cudaError_t launch_decode_merge(const MergeParams& p, int d, bool after, cudaStr
     case 256: return launch_merge_d<256>(p, after, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// CTAs of a cluster per group where decode_lists_kernel is to be used, else 0.
+// In rounds of a tile per warp of the machine: the clusters leave SMs idle or
+// come in several waves, equal shares (decode_rows_kernel) cost a merge of two
+// rounds' time.
+int decode_lists_cluster(int64_t groups, int top_k, int list_tiles, int d) {
+  if (top_k > kListIds) return 0;
+  const int64_t warps = decode_rows_warps(d);
+  int cluster = 1;
+  while (cluster < 8 && groups * cluster * 2 <= kPlanSms && cluster * warps < list_tiles) cluster *= 2;
+  const int64_t waves = (groups * cluster + kPlanSms - 1) / kPlanSms;
+  const int64_t lists = waves * ((list_tiles + cluster * warps - 1) / (cluster * warps));
+  const int64_t shares = (groups * list_tiles + kPlanSms * warps - 1) / (kPlanSms * warps) + 2;
+  return lists <= shares + shares / 8 ? cluster : 0;
 }
 
 }  // namespace mattn

@@ -54,6 +54,7 @@ struct Geo {
   static constexpr int kTensor = kChunks * kChunk;   // K or V of a tile
   static constexpr int kStage = 2 * kTensor;         // 8 KB; 16 KB at d = 256
   static constexpr int NS = 2;                       // stages per warp
+  static constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : ((1u << (TK & 31)) - 1u);
   static constexpr int kRing = NS * kStage;          // bytes per warp
 };
 
@@ -93,6 +94,235 @@ __device__ __forceinline__ int list_tiles(const DecodeRowsParams& p, int len) {
   return p.ids ? p.list_tiles : (len + TK - 1) / TK;
 }
 
+// One warp's running state of one (sequence, key/value head)'s query heads.
+template <int D, int NT>
+struct State {
+  using S = Geo<D>;
+  static constexpr int TK = S::TK, MT = S::MT;
+  float m[NT][2], l[NT][2], o[NT][D / 16][4];
+  uint32_t qf[NT][D / 16][2];  // queries as B operands: k = dims, n = heads
+
+  // Head columns 2 (lane % 4) + e of each group of eight are this lane's.
+  __device__ __forceinline__ void begin(const void* q, int64_t bh0, int G) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = nt * 8 + (lane >> 2);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(q) +
+                                                              (bh0 + (g < G ? g : 0)) * D) + (lane & 3);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        qf[nt][i][0] = g < G ? __ldg(src + i * 8) : 0u;
+        qf[nt][i][1] = g < G ? __ldg(src + i * 8 + 4) : 0u;
+      }
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+    }
+  }
+
+  // The sums over a tile's keys end up spread over the lanes of a head column:
+  // the whole sums, on all of them.
+  __device__ __forceinline__ float sum(int nt, int e) const {
+    float s = l[nt][e];
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
+  }
+
+  // Adds a landed tile: ks, vs are the lane's addresses of its K and V rows (see
+  // lane_k, lane_v), v_rows the V tile, mask (not 0) the rows that hold a key.
+  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, uint8_t* v_rows, uint32_t mask, float scale_log2) {
+    const int lane = threadIdx.x & 31;
+          if (mask != S::kAll) {
+      // value rows without a key: zeros (their weights are 0, and 0 x NaN is NaN)
+      for (int r = 0; r < TK; ++r) {
+        if ((mask >> r) & 1u) continue;
+        for (int i = lane; i < S::kChunks * 8; i += 32)
+          *reinterpret_cast<uint4*>(v_rows + (i >> 3) * S::kChunk + r * 128 +
+                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+    // S^T: two accumulators per tile so that neighbouring products do not wait on each other
+    float s[NT][MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float acc[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nt][a][j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t a[4];
+        ldsm4(a, (ks ^ ((2 * i & 7) << 4)) + (i >> 2) * S::kChunk + mt * 2048);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i & 1], a, qf[nt][i][0], qf[nt][i][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][mt][j] = acc[nt][0][j] + acc[nt][1][j];
+    }
+    if (mask != S::kAll) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const bool v0 = (mask >> (mt * 16 + (lane >> 2))) & 1u, v1 = (mask >> (mt * 16 + 8 + (lane >> 2))) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!v0) s[nt][mt][0] = s[nt][mt][1] = -INFINITY;
+          if (!v1) s[nt][mt][2] = s[nt][mt][3] = -INFINITY;
+        }
+      }
+    }
+    // online softmax per head column: the reference m in the log2 domain
+    float mx[NT][2];
+    bool moved = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(s[nt][0][e], s[nt][0][e + 2]);
+        if (MT == 2) x = fmaxf(x, fmaxf(s[nt][MT - 1][e], s[nt][MT - 1][e + 2]));
+        mx[nt][e] = x;
+      }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[nt][e] = fmaxf(m[nt][e], mx[nt][e] * scale_log2);
+        moved = moved || mx[nt][e] != m[nt][e];
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          alpha[e] = m[nt][e] == mx[nt][e] ? 1.f : ptx::ex2(m[nt][e] - mx[nt][e]);
+          m[nt][e] = mx[nt][e];
+          l[nt][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[nt][i][0] *= alpha[0];
+          o[nt][i][1] *= alpha[1];
+          o[nt][i][2] *= alpha[0];
+          o[nt][i][3] *= alpha[1];
+        }
+      }
+    }
+    uint32_t pf[NT][MT][2], pg[NT][MT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+        float sum = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          s[nt][mt][e] = ptx::ex2(fmaf(s[nt][mt][e], scale_log2, -ref));
+          s[nt][mt][e + 2] = ptx::ex2(fmaf(s[nt][mt][e + 2], scale_log2, -ref));
+          sum += s[nt][mt][e] + s[nt][mt][e + 2];
+        }
+        l[nt][e] += sum;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        // P^T as B operand (k = keys, n = heads), each weight as the sum of two
+        // bf16 values, 2^-17 of it off at most: one alone would add an error
+        // as large as the output's own rounding, and the tensor cores idle here
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float a = s[nt][mt][2 * r], b = s[nt][mt][2 * r + 1];
+          const uint32_t hi = ptx::pack_bf16x2(a, b);
+          pf[nt][mt][r] = movm_t(hi);
+          pg[nt][mt][r] = movm_t(ptx::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u)));
+        }
+      }
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t a[4];
+        ldsm4_t(a, (vs ^ ((2 * i & 7) << 4)) + (i >> 2) * S::kChunk + mt * 2048);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[nt][i], a, pf[nt][mt][0], pf[nt][mt][1]);
+          mma16816(o[nt][i], a, pg[nt][mt][0], pg[nt][mt][1]);
+        }
+      }
+    }
+  }
+};
+
+// 16-byte piece u = 2 i + e of row r lies at piece (u & 7) ^ (r & 7) of the
+// row's 128 bytes in chunk u >> 3: the lane's row and e make one address, from
+// which i's is an exclusive or and a constant away.
+__device__ __forceinline__ uint32_t lane_k(uint32_t tile) {
+  const int lane = threadIdx.x & 31;
+  return tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t lane_v(uint32_t tile) {
+  const int lane = threadIdx.x & 31;
+  return tile + ((lane & 7) + (lane >> 4) * 8) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+}
+
+// Loads a tile of (sequence, key/value head) bkv into `stage` of a warp's ring, a
+// lane per copy: boxes x < MT start at key pos[x] and cnt[x] of their rows hold
+// keys (a box without any is not loaded); returns the rows that do.
+template <int D>
+__device__ __forceinline__ uint32_t issue_tile(const DecodeRowsParams& p, uint8_t* ring, uint64_t* full, int stage,
+                                               int bkv, const int (&pos)[Geo<D>::MT], const int (&cnt)[Geo<D>::MT]) {
+  using S = Geo<D>;
+  constexpr int MT = S::MT, kPer = S::kChunks * 2;  // copies per box
+  const int lane = threadIdx.x & 31;
+  uint32_t mask = 0, bytes = 0;
+#pragma unroll
+  for (int x = 0; x < MT; ++x) {
+    mask |= ((1u << cnt[x]) - 1u) << (16 * x);
+    bytes += cnt[x] > 0 ? kPer * 2048u : 0u;
+  }
+  if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
+  __syncwarp();
+  const int x = lane / kPer, ch = (lane >> 1) % S::kChunks, tensor = lane & 1;
+  const int n = MT == 2 && x ? cnt[MT - 1] : cnt[0], at = MT == 2 && x ? pos[MT - 1] : pos[0];
+  if (x < MT && n > 0 &&
+      debug_check(p.err, at >= 0 && at < p.L && bkv >= 0 && bkv < p.B * p.H_kv && stage < S::NS, kSiteLoad))
+    ptx::tma_load_3d(ring + stage * S::kStage + tensor * S::kTensor + ch * S::kChunk + x * 2048, tensor ? &p.tv : &p.tk,
+                     full + stage, ch * 64, at, bkv);
+  return mask;
+}
+
+// Waits for a warp's stage; false if the wait gave up (the abort flag is then
+// raised, and copies already in flight have landed before the shared memory goes).
+__device__ __forceinline__ bool await(const DecodeRowsParams& p, uint64_t* bar, uint32_t parity,
+                                      volatile int* abort_flag) {
+  const bool got = ptx::mbar_wait(bar, parity, p.timeout_ns, abort_flag);
+  if (__all_sync(0xffffffffu, got)) return true;
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    atomicOr(p.err, kErrProducer);
+  }
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
+  return false;
+}
+
 // Where a tile lies: sequence b, key/value head h, tile t of its list.
 struct Cursor {
   int b, h, t, tiles, len;
@@ -111,7 +341,7 @@ template <int D, int NT>
 __device__ __forceinline__ bool work(const DecodeRowsParams& p, int w, int W, uint8_t* ring, uint64_t* full,
                                      volatile int* abort_flag) {
   using G_ = Geo<D>;
-  constexpr int TK = G_::TK, MT = G_::MT, NS = G_::NS;
+  constexpr int MT = G_::MT, NS = G_::NS;
   static_assert(NS == 2, "the masks of the stages are two registers");
   const int lane = threadIdx.x & 31;
   const int G = p.H / p.H_kv;
@@ -212,72 +442,33 @@ __device__ __forceinline__ bool work(const DecodeRowsParams& p, int w, int W, ui
     *cnt = left < 0 ? 0 : (left < 16 ? left : 16);
     return pos;
   };
-  // Loads the feed's tile into `stage`, a lane per copy (a box without keys is
-  // not loaded); returns the rows that hold a key.
   auto issue = [&](const Feed& f, int stage) -> uint32_t {
-    constexpr int kPer = G_::kChunks * 2;  // copies per box
     int pos[MT], cnt[MT];
-    uint32_t mask = 0, bytes = 0;
 #pragma unroll
-    for (int x = 0; x < MT; ++x) {
-      pos[x] = box_at(f, x, &cnt[x]);
-      mask |= ((1u << cnt[x]) - 1u) << (16 * x);
-      bytes += cnt[x] > 0 ? kPer * 2048u : 0u;
-    }
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
-    __syncwarp();
-    const int x = lane / kPer, ch = (lane >> 1) % G_::kChunks, tensor = lane & 1;
-    const int n = MT == 2 && x ? cnt[MT - 1] : cnt[0], at = MT == 2 && x ? pos[MT - 1] : pos[0];
+    for (int x = 0; x < MT; ++x) pos[x] = box_at(f, x, &cnt[x]);
     const int bkv = f.b * p.H_kv + f.h;
-    // the list's queries into L1, for begin_group two tiles later
-    if (f.t == 0 && lane * 64 < G * D) ptx::prefetch_l1(reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)bkv * G * D + lane * 64);
-    if (x < MT && n > 0 &&
-        debug_check(p.err, at >= 0 && at < p.L && bkv >= 0 && bkv < p.B * p.H_kv && stage < NS, kSiteLoad))
-      ptx::tma_load_3d(ring + stage * G_::kStage + tensor * G_::kTensor + ch * G_::kChunk + x * 2048,
-                       tensor ? &p.tv : &p.tk, full + stage, ch * 64, at, bkv);
-    return mask;
+    // the list's queries into L1, for the state that begins two tiles later
+    if (f.t == 0 && lane * 64 < G * D)
+      ptx::prefetch_l1(reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)bkv * G * D + lane * 64);
+    return issue_tile<D>(p, ring, full, stage, bkv, pos, cnt);
   };
 
-  const int hc = (lane & 3) * 2;  // this lane's head columns hc, hc + 1 (of each group of eight)
-  float m[NT][2], l[NT][2], o[NT][D / 16][4];
-  uint32_t qf[NT][D / 16][2];  // queries of the group as B operands: k = dims, n = heads
-  auto begin_group = [&](int b, int h) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int g = nt * 8 + (lane >> 2);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                              ((int64_t)b * p.H + h * G + (g < G ? g : 0)) * D) +
-                            (lane & 3);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        qf[nt][i][0] = g < G ? __ldg(src + i * 8) : 0u;
-        qf[nt][i][1] = g < G ? __ldg(src + i * 8 + 4) : 0u;
-      }
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-    }
-  };
+  State<D, NT> st;
   auto end_group = [&](int g) {  // the piece's state
     const int64_t slot = (int64_t)w + g;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float s = l[nt][e];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const int head = nt * 8 + hc + e;
+        const float s = st.sum(nt, e);
+        const int head = nt * 8 + (lane & 3) * 2 + e;
         if (head < G) {
-          if (lane < 4) *reinterpret_cast<float2*>(p.part_ml + (slot * G + head) * 2) = make_float2(m[nt][e], s);
+          if (lane < 4) *reinterpret_cast<float2*>(p.part_ml + (slot * G + head) * 2) = make_float2(st.m[nt][e], s);
           float* dst = p.part_o + (slot * G + head) * D + (lane >> 2);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            dst[i * 16] = o[nt][i][e];
-            dst[i * 16 + 8] = o[nt][i][e + 2];
+            dst[i * 16] = st.o[nt][i][e];
+            dst[i * 16 + 8] = st.o[nt][i][e + 2];
           }
         }
       }
@@ -294,168 +485,21 @@ __device__ __forceinline__ bool work(const DecodeRowsParams& p, int w, int W, ui
       if (n) feed_on(f);
       masks[n] = issue(f, n);
     }
-  // 16-byte piece u = 2 i + e of row r lies at piece (u & 7) ^ (r & 7) of the
-  // row's 128 bytes in chunk u >> 3: the lane's row and e make one address,
-  // from which i's is an exclusive or and a constant away.
-  const int row_k = (lane & 7) + ((lane >> 3) & 1) * 8, row_v = (lane & 7) + (lane >> 4) * 8;
-  const uint32_t at_k = ptx::smem_addr(ring) + row_k * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-  const uint32_t at_v =
-      ptx::smem_addr(ring) + G_::kTensor + row_v * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-  constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : ((1u << (TK & 31)) - 1u);
+  const uint32_t at_k = lane_k(ptx::smem_addr(ring)), at_v = lane_v(ptx::smem_addr(ring) + G_::kTensor);
   for (int n = 0; n < n_mine; ++n) {
     if (n == 0 || c.t == 0) {
       if (c.t == 0 && lane == 0) p.group_start[c.b * p.H_kv + c.h] = x0 + n;
-      begin_group(c.b, c.h);
+      st.begin(p.q, (int64_t)c.b * p.H + c.h * G, G);
     }
     const int stage = n & 1;
     const uint32_t mask = stage ? masks[1] : masks[0];
-    const bool got = ptx::mbar_wait(full + stage, (n >> 1) & 1, p.timeout_ns, abort_flag);
-    if (!__all_sync(0xffffffffu, got)) {
-      if (lane == 0) {
-        *abort_flag = 1;
-        atomicOr(p.err, kErrProducer);
-      }
-      // let copies already in flight land before the shared memory goes away
-      const uint64_t t0 = ptx::globaltimer_ns();
-      for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
-      return false;
-    }
-    if (mask) {  // warp-uniform
-      const uint32_t ks = at_k + stage * G_::kStage, vs = at_v + stage * G_::kStage;
-      if (mask != kAll) {
-        // value rows without a key: zeros (their weights are 0, and 0 x NaN is NaN)
-        for (int r = 0; r < TK; ++r) {
-          if ((mask >> r) & 1u) continue;
-          for (int i = lane; i < G_::kChunks * 8; i += 32)
-            *reinterpret_cast<uint4*>(ring + stage * G_::kStage + G_::kTensor + (i >> 3) * G_::kChunk + r * 128 +
-                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
-      // S^T: two accumulators per tile so that neighbouring products do not wait on each other
-      float s[NT][MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float acc[NT][2][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[nt][a][j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t a[4];
-          ldsm4(a, (ks ^ ((2 * i & 7) << 4)) + (i >> 2) * G_::kChunk + mt * 2048);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i & 1], a, qf[nt][i][0], qf[nt][i][1]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][mt][j] = acc[nt][0][j] + acc[nt][1][j];
-      }
-      if (mask != kAll) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const bool v0 = (mask >> (mt * 16 + (lane >> 2))) & 1u, v1 = (mask >> (mt * 16 + 8 + (lane >> 2))) & 1u;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (!v0) s[nt][mt][0] = s[nt][mt][1] = -INFINITY;
-            if (!v1) s[nt][mt][2] = s[nt][mt][3] = -INFINITY;
-          }
-        }
-      }
-      // online softmax per head column: the reference m in the log2 domain
-      float mx[NT][2];
-      bool moved = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[nt][0][e], s[nt][0][e + 2]);
-          if (MT == 2) x = fmaxf(x, fmaxf(s[nt][MT - 1][e], s[nt][MT - 1][e + 2]));
-          mx[nt][e] = x;
-        }
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = fmaxf(m[nt][e], mx[nt][e] * p.scale_log2);
-          moved = moved || mx[nt][e] != m[nt][e];
-        }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float alpha[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            alpha[e] = m[nt][e] == mx[nt][e] ? 1.f : ptx::ex2(m[nt][e] - mx[nt][e]);
-            m[nt][e] = mx[nt][e];
-            l[nt][e] *= alpha[e];
-          }
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            o[nt][i][0] *= alpha[0];
-            o[nt][i][1] *= alpha[1];
-            o[nt][i][2] *= alpha[0];
-            o[nt][i][3] *= alpha[1];
-          }
-        }
-      }
-      uint32_t pf[NT][MT][2], pg[NT][MT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-          float sum = 0.f;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            s[nt][mt][e] = ptx::ex2(fmaf(s[nt][mt][e], p.scale_log2, -ref));
-            s[nt][mt][e + 2] = ptx::ex2(fmaf(s[nt][mt][e + 2], p.scale_log2, -ref));
-            sum += s[nt][mt][e] + s[nt][mt][e + 2];
-          }
-          l[nt][e] += sum;
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          // P^T as B operand (k = keys, n = heads), each weight as the sum of two
-          // bf16 values, 2^-17 of it off at most: one alone would add an error
-          // as large as the output's own rounding, and the tensor cores idle here
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float a = s[nt][mt][2 * r], b = s[nt][mt][2 * r + 1];
-            const uint32_t hi = ptx::pack_bf16x2(a, b);
-            pf[nt][mt][r] = movm_t(hi);
-            pg[nt][mt][r] = movm_t(ptx::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u)));
-          }
-        }
-      }
-      // O^T += V^T P^T
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t a[4];
-          ldsm4_t(a, (vs ^ ((2 * i & 7) << 4)) + (i >> 2) * G_::kChunk + mt * 2048);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(o[nt][i], a, pf[nt][mt][0], pf[nt][mt][1]);
-            mma16816(o[nt][i], a, pg[nt][mt][0], pg[nt][mt][1]);
-          }
-        }
-      }
-    }
+    if (!await(p, full + stage, (n >> 1) & 1, abort_flag)) return false;
+    if (mask)  // warp-uniform
+      st.step(at_k + stage * G_::kStage, at_v + stage * G_::kStage, ring + stage * G_::kStage + G_::kTensor, mask,
+              p.scale_log2);
     __syncwarp();
     if (n + NS < n_mine) {
-      if (mask != kAll) ptx::fence_proxy_async_shared();  // the zeros above before the copy that overwrites them
+      if (mask != G_::kAll) ptx::fence_proxy_async_shared();  // the zeros above before the copy that overwrites them
       __syncwarp();
       feed_on(f);
       const uint32_t x = issue(f, stage);

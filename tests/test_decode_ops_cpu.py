@@ -158,7 +158,8 @@ def _blocks(lib, **kw):
     ("block 8", {"block": 8}, -2),
     ("no cache", {"L": 0}, -1),
     ("a list past 2^30 keys", {"top_k": 1 << 20, "block": 2048}, -2),
-    ("a small workspace", {"ws_bytes": 16}, -6),
+    ("a block past 2^20 keys", {"block": (1 << 20) + 16, "top_k": 1}, -2),
+    ("a small workspace", {"top_k": 2000, "ws_bytes": 16}, -6),
 ])
 def test_decode_blocks_refuses(L, why, args, code):
     assert _blocks(L, **args) == code, why
