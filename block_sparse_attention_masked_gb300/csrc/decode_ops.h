@@ -80,9 +80,7 @@ struct DecodeRowsParams {
   float* lse;               // [B][H] or null
   float scale_log2;
 };
-// `after`: launched as a programmatic dependent of the stream's previous
-// grid, whose results it does not read; it completes only after that grid.
-cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cudaStream_t stream);
+cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, cudaStream_t stream);
 
 cudaError_t launch_decode_lists(const DecodeRowsParams& p, int d, cudaStream_t stream);
 int decode_lists_cluster(int64_t groups, int top_k, int list_tiles, int d);
@@ -95,14 +93,17 @@ struct SharedPlan {
   int n_split;  // key splits
   int tiles;    // key tiles of the prefix
   int per_split;
-  int own_ctas; // CTAs of the own keys' grid
+  int own_ctas; // CTAs of the own keys, behind the prefix's
 };
 constexpr int shared_key_tile(int d) { return d == 256 ? 64 : 128; }
+// Row workers of a CTA among the prefix's (decode_rows_warps where there is no prefix).
+constexpr int shared_row_warps(int d, int sub) { return d == 256 ? 6 : (sub == 2 ? 12 : 8); }
 SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d);
 
 struct SharedParams {
   CUtensorMap tk, tv;       // [H_kv][P][d] bf16 views, boxes of 64 columns x shared_key_tile(d) keys
   CUtensorMap tq;           // [B][H][d] bf16 view, boxes of 64 columns x G heads x plan.seqs sequences
+  DecodeRowsParams own;     // the sequences' own keys (L = 0: none)
   CUtensorMap to;           // part_o as [H_kv][B * G][n_split][d]: boxes of 32 columns (128 bytes) x 32 rows
   float* part_o;            // [H_kv * B * G][n_split][d]
   float* part_ml;           // [H_kv * B * G][n_split][2]

@@ -105,7 +105,7 @@ SharedLayout shared_layout(int B, int H, int H_kv, int P, int L, int d) {
   SharedLayout s;
   s.prefix = shared_plan(B, H, H_kv, P, L, d);
   s.prefix_bytes = P > 0 ? state_bytes((int64_t)B * H, s.prefix.n_split, d) : 0;
-  s.own = rows_layout((int64_t)B * H_kv, H / H_kv, s.prefix.own_ctas * decode_rows_warps(d), d);
+  s.own = rows_layout((int64_t)B * H_kv, H / H_kv, s.prefix.own_ctas * (P > 0 ? shared_row_warps(d, s.prefix.sub) : decode_rows_warps(d)), d);
   s.own_bytes = L > 0 ? s.own.all() : 0;
   return s;
 }
@@ -308,8 +308,13 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
   m.o = o;
   m.lse = lse;
   m.B = B; m.H = H; m.H_kv = H_kv;
-  if (P > 0 && (rc = launched(launch_decode_shared(sp, d, stream), "prefix launch"))) return rc;
-  if (L > 0 && (rc = launched(launch_decode_rows(rp, d, P > 0, stream), "own-key launch"))) return rc;
+  if (P > 0) {
+    if (L > 0) sp.own = rp;
+    rc = launched(launch_decode_shared(sp, d, stream), "prefix launch");
+  } else if (L > 0) {
+    rc = launched(launch_decode_rows(rp, d, stream), "own-key launch");
+  }
+  if (rc) return rc;
   return launched(launch_decode_merge(m, d, P > 0 || L > 0, stream), "merge launch");
 }
 
@@ -444,7 +449,7 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
     return launched(launch_decode_lists(p, d, stream), "list launch");
   }
   place_rows(&p, lay, static_cast<char*>(workspace));
-  if ((rc = launched(launch_decode_rows(p, d, false, stream), "block launch"))) return rc;
+  if ((rc = launched(launch_decode_rows(p, d, stream), "block launch"))) return rc;
   MergeParams m;
   memset(&m, 0, sizeof(m));
   m.b_o = p.part_o;

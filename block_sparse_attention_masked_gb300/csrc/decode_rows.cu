@@ -26,7 +26,7 @@ struct RowsSmem {
 // w / grid of CTA w % grid, so that few shares spread over the SMs.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
-    decode_rows_kernel(const __grid_constant__ DecodeRowsParams p, int after) {
+    decode_rows_kernel(const __grid_constant__ DecodeRowsParams p) {
   using Geo = rows::Geo<D>;
   constexpr int kWarps = decode_rows_warps(D);
   extern __shared__ uint8_t smem_raw[];
@@ -43,30 +43,18 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
   const int warp = threadIdx.x >> 5;
   rows::work<D, NT>(p, warp * gridDim.x + blockIdx.x, gridDim.x * kWarps, ring + warp * Geo::kRing,
                     full + warp * Geo::NS, abort_flag);
-  // launched beside the previous grid: complete only after it, so that a
-  // grid that waits for this one finds both results
-  if (after) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, int NT>
-cudaError_t launch_nt(const DecodeRowsParams& p, bool after, cudaStream_t stream) {
+cudaError_t launch_nt(const DecodeRowsParams& p, cudaStream_t stream) {
   const size_t smem = RowsSmem<D>::kBytes;
   static_assert(RowsSmem<D>::kBytes <= 227 * 1024, "shared memory");
   auto kern = decode_rows_kernel<D, NT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas);
-  cfg.blockDim = dim3(32 * decode_rows_warps(D));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p, after ? 1 : 0);
+  kern<<<p.ctas, 32 * decode_rows_warps(D), smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 // Few groups or short lists: a cluster of CTAs per (sequence, key/value head),
@@ -257,34 +245,32 @@ cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
 
 // The merge.  Row (b, h)'s states: `na` of the prefix, then the pieces of its
 // own list.  o = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s + exp(sink)).
-// LPS lanes take a state (16 bytes each) of SL dims of one row; WPR warps share
-// a row.  Few rows: a CTA of four warps for 32 dims of a row; many: a warp for a
-// whole row.  Latency-bound: references and
-// values of eight states per lane group are loaded together, and the running
+// LPS lanes take a state (16 bytes each) of SL <= 128 dims of one row; WPR warps
+// share them.  Few rows: a CTA of four warps for 32 dims of a row; many: a warp
+// for 128.  Latency-bound: references and
+// values of sixteen states per lane group are loaded together, and the running
 // maximum is moved per batch, so that the chain is two loads deep (the prefix's
 // states, beside the place of the own ones; the own ones).
-constexpr int kMergeBatch = 8;
+constexpr int kMergeBatch = 16;
 
-template <int V>
 struct Running {
   float m, l;
-  float4 o[V];
+  float4 o;
 };
 
 // Adds states first, first + step, .. < n (rows `row` + s * stride of `ml` and `o`).
-template <int D, int V, int LPS>
-__device__ __forceinline__ void add_states(Running<V>& r, const float* ml, const float* o, int64_t row, int64_t stride,
+template <int D>
+__device__ __forceinline__ void add_states(Running& r, const float* ml, const float* o, int64_t row, int64_t stride,
                                            int first, int step, int n) {
   for (int s0 = first; s0 < n; s0 += step * kMergeBatch) {
     float2 a[kMergeBatch];
-    float4 x[kMergeBatch][V];
+    float4 x[kMergeBatch];
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
       const int s = s0 + i * step;
       const int64_t at = row + (int64_t)(s < n ? s : s0) * stride;
       a[i] = *reinterpret_cast<const float2*>(ml + at * 2);
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[i][v] = *reinterpret_cast<const float4*>(o + at * D + v * LPS * 4);
+      x[i] = *reinterpret_cast<const float4*>(o + at * D);
     }
     float m = r.m;
 #pragma unroll
@@ -292,27 +278,24 @@ __device__ __forceinline__ void add_states(Running<V>& r, const float* ml, const
     const float k = r.m == m ? 1.f : ptx::ex2(r.m - m);
     r.m = m;
     r.l *= k;
-#pragma unroll
-    for (int v = 0; v < V; ++v) r.o[v] = make_float4(r.o[v].x * k, r.o[v].y * k, r.o[v].z * k, r.o[v].w * k);
+    r.o = make_float4(r.o.x * k, r.o.y * k, r.o.z * k, r.o.w * k);
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
       if (s0 + i * step >= n) break;  // the same on all lanes of a state
       const float e = a[i].x == m ? 1.f : ptx::ex2(a[i].x - m);
       r.l = fmaf(a[i].y, e, r.l);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        r.o[v].x = fmaf(x[i][v].x, e, r.o[v].x);
-        r.o[v].y = fmaf(x[i][v].y, e, r.o[v].y);
-        r.o[v].z = fmaf(x[i][v].z, e, r.o[v].z);
-        r.o[v].w = fmaf(x[i][v].w, e, r.o[v].w);
-      }
+      r.o.x = fmaf(x[i].x, e, r.o.x);
+      r.o.y = fmaf(x[i].y, e, r.o.y);
+      r.o.z = fmaf(x[i].z, e, r.o.z);
+      r.o.w = fmaf(x[i].w, e, r.o.w);
     }
   }
 }
 
 template <int D, int SL, int WPR, int TK>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ MergeParams p) {
-  constexpr int LPS = SL / 4 < 32 ? SL / 4 : 32, SPW = 32 / LPS, V = SL / 4 / LPS, U = WPR * SPW;
+  constexpr int LPS = SL / 4, SPW = 32 / LPS, U = WPR * SPW;
+  static_assert(SL <= 128, "a warp's lanes hold four dims each");
   static_assert(WPR == 4 || WPR == 1, "a row is a CTA's or a warp's");
   __shared__ float sm_all[4 * SPW], sl_all[4 * SPW], so_all[4 * SPW][SL];
   const int warp = WPR == 4 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
@@ -340,23 +323,18 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     }
   }
   const float b2 = p.sink ? p.sink[h] * kLog2eR : -INFINITY;
-  Running<V> r;
-  r.m = -INFINITY;
-  r.l = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) r.o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  add_states<D, V, LPS>(r, p.a_ml, p.a_o + c0 + part * 4, ra, 1, unit, U, p.na);
+  Running r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  add_states<D>(r, p.a_ml, p.a_o + c0 + part * 4, ra, 1, unit, U, p.na);
   if (tiles) {
     // state s of the own list: slot w0 + s + g, head h % G of the group
     const int w0 = start / per, nb = (start + tiles - 1) / per - w0 + 1;
-    add_states<D, V, LPS>(r, p.b_ml, p.b_o + c0 + part * 4, ((int64_t)w0 + g) * G + h % G, G, unit, U, nb);
+    add_states<D>(r, p.b_ml, p.b_o + c0 + part * 4, ((int64_t)w0 + g) * G + h % G, G, unit, U, nb);
   }
   if (part == 0) {
     sm[unit] = r.m;
     sl[unit] = r.l;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) *reinterpret_cast<float4*>(&so[unit][(v * LPS + part) * 4]) = r.o[v];
+  *reinterpret_cast<float4*>(&so[unit][part * 4]) = r.o;
   if (WPR == 4) __syncthreads();
   else __syncwarp();
   float M = b2;
@@ -394,23 +372,25 @@ cudaError_t launch_merge_sl(const MergeParams& p, bool after, cudaStream_t strea
 
 template <int D>
 cudaError_t launch_merge_d(const MergeParams& p, bool after, cudaStream_t stream) {
+  // as many CTAs as the SMs hold at once, at most
+  constexpr int SL = D < 128 ? D : 128;
   const int rows = p.B * p.H;
-  if (rows <= 2 * kPlanSms) return launch_merge_sl<D, 32, 4>(p, after, stream);
-  if (rows <= 8 * kPlanSms) return launch_merge_sl<D, D, 4>(p, after, stream);
-  return launch_merge_sl<D, D, 1>(p, after, stream);
+  if (rows <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, after, stream);
+  if (rows <= 4 * kPlanSms) return launch_merge_sl<D, SL, 4>(p, after, stream);
+  return launch_merge_sl<D, SL, 1>(p, after, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, bool after, cudaStream_t stream) {
+cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, cudaStream_t stream) {
   const int nt = (p.H / p.H_kv + 7) / 8;
   switch (d * 4 + nt) {
-    case 64 * 4 + 1: return launch_nt<64, 1>(p, after, stream);
-    case 64 * 4 + 2: return launch_nt<64, 2>(p, after, stream);
-    case 128 * 4 + 1: return launch_nt<128, 1>(p, after, stream);
-    case 128 * 4 + 2: return launch_nt<128, 2>(p, after, stream);
-    case 256 * 4 + 1: return launch_nt<256, 1>(p, after, stream);
-    case 256 * 4 + 2: return launch_nt<256, 2>(p, after, stream);
+    case 64 * 4 + 1: return launch_nt<64, 1>(p, stream);
+    case 64 * 4 + 2: return launch_nt<64, 2>(p, stream);
+    case 128 * 4 + 1: return launch_nt<128, 1>(p, stream);
+    case 128 * 4 + 2: return launch_nt<128, 2>(p, stream);
+    case 256 * 4 + 1: return launch_nt<256, 1>(p, stream);
+    case 256 * 4 + 2: return launch_nt<256, 2>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -2,8 +2,8 @@
 // for sm_103a: the states (reference m, sum l, unnormalised O) of all
 // B * G query rows of a key/value head against the P prefix keys, so that the
 // prefix is read once per key/value head and not once per sequence.  The
-// sequences' own keys follow in decode_rows.cu, and decode_merge_kernel joins
-// the states with the sink logit:
+// sequences' own keys are the row worker's (decode_rows.cuh), in further CTAs of
+// the same grid, and decode_merge_kernel joins the states with the sink logit:
 //   o = (sum_s 2^(m_s - M) O_s) / (sum_s 2^(m_s - M) l_s + exp(sink)).
 //
 // B * G rows against P keys is a matrix product of 4 d B G P FLOPs over 4 d P
@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include "decode_ops.h"
+#include "decode_rows.cuh"
 #include "kernel_params.h"
 #include "ptx.cuh"
 
@@ -76,13 +77,36 @@ __device__ __forceinline__ void fail_sh(const SharedParams& p, ShBar* bar, uint3
   atomicOr(p.err, bit);
 }
 
-template <int D, int SUB>
+// NT: groups of eight query heads of the row workers in the grid's last CTAs,
+// 0 = none.
+template <int D, int SUB, int NT>
 __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     decode_shared_kernel(const __grid_constant__ SharedParams p) {
   using Geo = ShGeo<D, SUB>;
   constexpr int KT = Geo::KT, NSL = Geo::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if constexpr (NT > 0) {
+    const int first = p.plan.row_tiles * p.plan.n_split * p.H_kv;
+    if ((int)blockIdx.x >= first) {
+      // ------------------------------------------------------ the sequences' own keys
+      using Rows = rows::Geo<D>;
+      constexpr int kWarps = shared_row_warps(D, SUB);
+      static_assert((size_t)kWarps * Rows::kRing + kWarps * Rows::NS * 8 + 16 <= Geo::kSmem - 1024, "shared memory");
+      uint64_t* full = reinterpret_cast<uint64_t*>(sq + kWarps * Rows::kRing);
+      volatile int* stop = reinterpret_cast<volatile int*>(full + kWarps * Rows::NS);
+      asm volatile("griddepcontrol.launch_dependents;");
+      if (threadIdx.x < kWarps * Rows::NS) ptx::mbar_init(full + threadIdx.x, 1);
+      if (threadIdx.x == 0) *stop = 0;
+      ptx::fence_barrier_init();
+      __syncthreads();
+      const int w = threadIdx.x >> 5, ctas = gridDim.x - first;
+      if (w < kWarps)
+        rows::work<D, NT>(p.own, w * ctas + (int)blockIdx.x - first, ctas * kWarps, sq + w * Rows::kRing,
+                          full + w * Rows::NS, stop);
+      return;
+    }
+  }
   uint8_t* ring = sq + SUB * Geo::kQTile;
   ShBar* bar = reinterpret_cast<ShBar*>(ring + NSL * Geo::kSlot);
   volatile int* abort_flag = &bar->abort_flag;
@@ -428,17 +452,24 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   }
 }
 
-template <int D, int SUB>
-cudaError_t launch_sub(const SharedParams& p, cudaStream_t stream) {
+template <int D, int SUB, int NT>
+cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   using Geo = ShGeo<D, SUB>;
   const size_t smem = Geo::kSmem + sizeof(ShBar);
   static_assert(Geo::kSmem + sizeof(ShBar) <= 227 * 1024, "shared memory");
-  auto kern = decode_shared_kernel<D, SUB>;
+  auto kern = decode_shared_kernel<D, SUB, NT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  kern<<<p.plan.row_tiles * p.plan.n_split * p.H_kv, Geo::kThreads, smem, stream>>>(p);
+  const int grid = p.plan.row_tiles * p.plan.n_split * p.H_kv + (NT ? p.plan.own_ctas : 0);
+  kern<<<grid, Geo::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, int SUB>
+cudaError_t launch_sub(const SharedParams& p, cudaStream_t stream) {
+  if (p.own.L == 0) return launch_nt<D, SUB, 0>(p, stream);
+  return p.H / p.H_kv <= 8 ? launch_nt<D, SUB, 1>(p, stream) : launch_nt<D, SUB, 2>(p, stream);
 }
 
 }  // namespace
@@ -477,15 +508,15 @@ static double split_over(SharedPlan* s, int H_kv, int sms) {
   return best;
 }
 
-// The own keys' grid runs beside the prefix's on SMs of its own (it is launched
-// as soon as that one's CTAs have all started), as many as make both end
-// together if the sequences hold half of their capacity: the prefix is bound by
-// the tensor cores or the memory, the own keys by the memory's latency, and one
-// after the other they take their sum.  Measured beside each other: own keys 60
-// GB/s an SM and 6 us of start-up, a prefix step (128 rows x a key tile) 0.95
-// us, at most 6.5 TB/s; own keys on all SMs 4.5 TB/s and 8 us.  (64 sequences,
-// 32 / 8 heads of 128, 32K prefix, 256 own keys on average: 60.2 us one after the
-// other, 52.5 with 32 SMs for the own keys; 128 over 8K: 55.0 and 35.0.)
+// The own keys' CTAs run beside the prefix's on SMs of their own, as many as make
+// both end together if the sequences hold half of their capacity: the prefix is
+// bound by the tensor cores or the memory, the own keys by the memory's latency,
+// and one after the other (take = 0: the own keys' CTAs wait for free SMs) they
+// take their sum.  Measured beside each other: own keys 60 GB/s an SM and 6 us of
+// start-up, a prefix step (128 rows x a key tile) 0.95 us, at most 6.5 TB/s; own
+// keys on all SMs 4.5 TB/s and 8 us.  (64 sequences, 32 / 8 heads of 128, 32K
+// prefix, 256 own keys on average: 60.2 us one after the other, 52.5 with 32 SMs
+// for the own keys; 128 over 8K: 55.0 and 35.0.)
 SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d) {
   SharedPlan s = {};
   s.seqs = 128 / (H / H_kv);
