@@ -246,31 +246,36 @@ cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
 // The merge.  Row (b, h)'s states: `na` of the prefix, then the pieces of its
 // own list.  o = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s + exp(sink)).
 // LPS lanes take a state (16 bytes each) of SL <= 128 dims of one row; WPR warps
-// share them.  Few rows: a CTA of four warps for 32 dims of a row; many: a warp
-// for 128.  Latency-bound: references and
-// values of sixteen states per lane group are loaded together, and the running
-// maximum is moved per batch, so that the chain is two loads deep (the prefix's
-// states, beside the place of the own ones; the own ones).
-constexpr int kMergeBatch = 16;
+// share them: four and 32 dims where there are few rows, down to one and 128.
+// Bound by what each warp issues and by its chain of loads (the prefix's states,
+// beside the place of the own ones; the own ones): a handful of states a warp,
+// their references and values loaded together, pointers moved and not formed
+// anew (2,048 rows of 18 states: 7.6 us with 16 states in flight a warp and a
+// warp a row).
+constexpr int kMergeBatch = 4;
 
 struct Running {
   float m, l;
   float4 o;
 };
 
-// Adds states first, first + step, .. < n (rows `row` + s * stride of `ml` and `o`).
-template <int D>
-__device__ __forceinline__ void add_states(Running& r, const float* ml, const float* o, int64_t row, int64_t stride,
-                                           int first, int step, int n) {
-  for (int s0 = first; s0 < n; s0 += step * kMergeBatch) {
+// Adds n states, `step` apart: reference and sum at `ml`, the lane's dims at `o`
+// (ml_step and o_step floats from one to the next).
+__device__ __forceinline__ void add_states(Running& r, const float* ml, const float* o, int n, int64_t ml_step,
+                                           int64_t o_step) {
+  for (; n > 0; n -= kMergeBatch) {
     float2 a[kMergeBatch];
     float4 x[kMergeBatch];
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
-      const int s = s0 + i * step;
-      const int64_t at = row + (int64_t)(s < n ? s : s0) * stride;
-      a[i] = *reinterpret_cast<const float2*>(ml + at * 2);
-      x[i] = *reinterpret_cast<const float4*>(o + at * D);
+      a[i] = make_float2(-INFINITY, 0.f);
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        a[i] = *reinterpret_cast<const float2*>(ml);
+        x[i] = *reinterpret_cast<const float4*>(o);
+        ml += ml_step;
+        o += o_step;
+      }
     }
     float m = r.m;
 #pragma unroll
@@ -281,7 +286,6 @@ __device__ __forceinline__ void add_states(Running& r, const float* ml, const fl
     r.o = make_float4(r.o.x * k, r.o.y * k, r.o.z * k, r.o.w * k);
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
-      if (s0 + i * step >= n) break;  // the same on all lanes of a state
       const float e = a[i].x == m ? 1.f : ptx::ex2(a[i].x - m);
       r.l = fmaf(a[i].y, e, r.l);
       r.o.x = fmaf(x[i].x, e, r.o.x);
@@ -296,15 +300,15 @@ template <int D, int SL, int WPR, int TK>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int LPS = SL / 4, SPW = 32 / LPS, U = WPR * SPW;
   static_assert(SL <= 128, "a warp's lanes hold four dims each");
-  static_assert(WPR == 4 || WPR == 1, "a row is a CTA's or a warp's");
+  static_assert(WPR == 4 || WPR == 2 || WPR == 1, "a CTA has four warps");
   __shared__ float sm_all[4 * SPW], sl_all[4 * SPW], so_all[4 * SPW][SL];
-  const int warp = WPR == 4 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
-  const int mine = WPR == 4 ? 0 : (threadIdx.x >> 5) * SPW;  // the row's first unit in shared memory
+  const int all = threadIdx.x >> 5, warp = all % WPR, lane = threadIdx.x & 31;
+  const int mine = all / WPR * U;  // the row's first unit in shared memory
   float *sm = sm_all + mine, *sl = sl_all + mine;
   float(*so)[SL] = so_all + mine;
   const int sub = lane / LPS, part = lane % LPS, unit = warp * SPW + sub;
-  const int64_t bh = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (bh >= (int64_t)p.B * p.H) return;  // (a whole warp, WPR == 1)
+  const int64_t bh = (int64_t)blockIdx.x * (4 / WPR) + all / WPR;
+  if (bh >= (int64_t)p.B * p.H) return;  // (all warps of a row)
   const int c0 = blockIdx.y * SL;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H), G = p.H / p.H_kv;
   const int g = b * p.H_kv + h / G;
@@ -324,11 +328,14 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   }
   const float b2 = p.sink ? p.sink[h] * kLog2eR : -INFINITY;
   Running r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  add_states<D>(r, p.a_ml, p.a_o + c0 + part * 4, ra, 1, unit, U, p.na);
+  // this unit's states: unit, unit + U, ..
+  add_states(r, p.a_ml + (ra + unit) * 2, p.a_o + (ra + unit) * D + c0 + part * 4, (p.na - unit + U - 1) / U, U * 2, U * D);
   if (tiles) {
     // state s of the own list: slot w0 + s + g, head h % G of the group
     const int w0 = start / per, nb = (start + tiles - 1) / per - w0 + 1;
-    add_states<D>(r, p.b_ml, p.b_o + c0 + part * 4, ((int64_t)w0 + g) * G + h % G, G, unit, U, nb);
+    const int64_t at = ((int64_t)w0 + g + unit) * G + h % G;
+    add_states(r, p.b_ml + at * 2, p.b_o + at * D + c0 + part * 4, (nb - unit + U - 1) / U, (int64_t)U * G * 2,
+               (int64_t)U * G * D);
   }
   if (part == 0) {
     sm[unit] = r.m;
@@ -336,6 +343,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   }
   *reinterpret_cast<float4*>(&so[unit][part * 4]) = r.o;
   if (WPR == 4) __syncthreads();
+  else if (WPR == 2) asm volatile("bar.sync %0, 64;" ::"r"(1 + all / WPR) : "memory");
   else __syncwarp();
   float M = b2;
 #pragma unroll
@@ -346,7 +354,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     e[u] = sm[u] == M ? 1.f : ptx::ex2(sm[u] - M);
     z = fmaf(sl[u], e[u], z);
   }
-  for (int c = WPR == 4 ? threadIdx.x : lane; c < SL; c += WPR * 32) {
+  for (int c = warp * 32 + lane; c < SL; c += WPR * 32) {
     float x = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) x = fmaf(so[u][c], e[u], x);
@@ -359,7 +367,7 @@ template <int D, int SL, int WPR>
 cudaError_t launch_merge_sl(const MergeParams& p, bool after, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const int rows = p.B * p.H;
-  cfg.gridDim = dim3(WPR == 4 ? rows : (rows + 3) / 4, D / SL);
+  cfg.gridDim = dim3((rows + 4 / WPR - 1) / (4 / WPR), D / SL);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -372,11 +380,12 @@ cudaError_t launch_merge_sl(const MergeParams& p, bool after, cudaStream_t strea
 
 template <int D>
 cudaError_t launch_merge_d(const MergeParams& p, bool after, cudaStream_t stream) {
-  // as many CTAs as the SMs hold at once, at most
+  // about as many warps as the SMs hold at once, at most
   constexpr int SL = D < 128 ? D : 128;
-  const int rows = p.B * p.H;
-  if (rows <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, after, stream);
-  if (rows <= 4 * kPlanSms) return launch_merge_sl<D, SL, 4>(p, after, stream);
+  const int64_t warps = (int64_t)p.B * p.H * (D / SL), most = kPlanSms * 36;
+  if (p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, after, stream);
+  if (warps * 4 <= most) return launch_merge_sl<D, SL, 4>(p, after, stream);
+  if (warps * 2 <= most) return launch_merge_sl<D, SL, 2>(p, after, stream);
   return launch_merge_sl<D, SL, 1>(p, after, stream);
 }
 
