@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(32 * kMeanWarps) block_means_kernel(const __gr
   const int64_t w = (int64_t)blockIdx.x * kMeanBlocks + slot;
   const int64_t row = w / p.span;     // (sequence, key/value head)
   int n = 0;                          // cached keys of the block, 0: not one to form
+  after_previous();
   int64_t blk = 0;
   if (row < (int64_t)p.B * p.H_kv) {
     const int b = (int)(row / p.H_kv);
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % p.ctas, bkv = blockIdx.x / p.ctas;
   const int b = bkv / p.H_kv, kvh = bkv % p.H_kv, G = p.H / p.H_kv;
+  after_previous();
   // (before the length is known: where every block fits, the scores go unread)
   if (p.n_blocks > p.top_k) score_blocks<D, NT>(p, sh, b, kvh, rank, p.ctas);
   const int n = blocks_of(p, b);
@@ -685,23 +687,12 @@ cudaError_t launch_select_nt(const DecodeSelectParams& p0, cudaStream_t stream) 
   const int steps = (p.n_blocks + 16 * kSelWarps - 1) / (16 * kSelWarps);
   p.ctas = 1;
   while (p.ctas < 8 && rows * p.ctas * 2 <= slots && p.ctas * 2 <= steps) p.ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * p.ctas));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelShared);
-  cfg.stream = stream;
+  static_assert(2 * (sizeof(SelShared) + 1024) <= 228 * 1024, "two CTAs per SM");
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(decode_select_kernel<D, NT>, sizeof(SelShared), &done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  static_assert(2 * (sizeof(SelShared) + 1024) <= 228 * 1024, "two CTAs per SM");
-  return cudaLaunchKernelEx(&cfg, decode_select_kernel<D, NT>, p);
+  return launch_chained(decode_select_kernel<D, NT>, (unsigned)(rows * p.ctas), 1, kSelThreads, sizeof(SelShared), p.ctas,
+                        p, stream);
 }
 
 template <int D>
@@ -712,8 +703,8 @@ cudaError_t launch_select_d(const DecodeSelectParams& p, cudaStream_t stream) {
 template <int D, int PARTS>
 cudaError_t launch_means_parts(const BlockMeansParams& p, cudaStream_t stream) {
   const int64_t warps = (int64_t)p.B * p.H_kv * p.span * PARTS;
-  block_means_kernel<D, PARTS><<<(unsigned)((warps + kMeanWarps - 1) / kMeanWarps), 32 * kMeanWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(block_means_kernel<D, PARTS>, (unsigned)((warps + kMeanWarps - 1) / kMeanWarps), 1,
+                        32 * kMeanWarps, 0, 1, p, stream);
 }
 
 template <int D>

@@ -32,6 +32,40 @@ cudaError_t allow_shared(Kernel kern, size_t bytes, std::atomic<uint64_t>* done)
   return e;
 }
 
+// Launches a kernel as a programmatic dependent of the stream's previous grid:
+// its CTAs are set up while that one ends, and each of these kernels begins with
+// after_previous() (its first access to memory comes after the previous grid has
+// completed), so that a chain of short calls does not pay a launch between each
+// two (one token's rows for 64 requests: 6.1 us a call in a chain, 3.5 so).
+template <class Kernel, class Params>
+cudaError_t launch_chained(Kernel kern, unsigned grid_x, unsigned grid_y, int threads, size_t smem, int cluster,
+                           const Params& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid_x, grid_y);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+#ifdef __CUDACC__
+// Waits until the previous grid has completed and its results are visible, then
+// lets the next one's CTAs be set up.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+#endif
+
 // ------------------------------------------------------------ qk_rope.cu
 struct RopeParams {
   const void* src[3];       // q, k, v rows: element (b, n, head, c) at b * batch_stride + n * token_stride + head * d + c
@@ -130,7 +164,7 @@ struct MergeParams {
   float* lse;
   int B, H, H_kv;
 };
-cudaError_t launch_decode_merge(const MergeParams& p, int d, bool after, cudaStream_t stream);
+cudaError_t launch_decode_merge(const MergeParams& p, int d, cudaStream_t stream);
 
 // ------------------------------------------------------------ block_select.cu
 struct BlockMeansParams {

@@ -315,7 +315,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     rc = launched(launch_decode_rows(rp, d, stream), "own-key launch");
   }
   if (rc) return rc;
-  return launched(launch_decode_merge(m, d, P > 0 || L > 0, stream), "merge launch");
+  return launched(launch_decode_merge(m, d, stream), "merge launch");
 }
 
 int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const int32_t* first, int B, int H_kv,
@@ -462,7 +462,7 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   m.o = o;
   m.lse = lse;
   m.B = B; m.H = H; m.H_kv = H_kv;
-  return launched(launch_decode_merge(m, d, true, stream), "merge launch");
+  return launched(launch_decode_merge(m, d, stream), "merge launch");
 }
 
 }  // extern "C"

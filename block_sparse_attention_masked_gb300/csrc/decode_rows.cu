@@ -33,13 +33,11 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kWarps * Geo::kRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kWarps * Geo::NS);
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * Geo::NS; ++i) ptx::mbar_init(full + i, 1);
-    *abort_flag = 0;
-    ptx::fence_barrier_init();
-  }
+  if (threadIdx.x < kWarps * Geo::NS) ptx::mbar_init(full + threadIdx.x, 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  ptx::fence_barrier_init();
   __syncthreads();
+  after_previous();
   const int warp = threadIdx.x >> 5;
   rows::work<D, NT>(p, warp * gridDim.x + blockIdx.x, gridDim.x * kWarps, ring + warp * Geo::kRing,
                     full + warp * Geo::NS, abort_flag);
@@ -53,8 +51,7 @@ cudaError_t launch_nt(const DecodeRowsParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  kern<<<p.ctas, 32 * decode_rows_warps(D), smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(kern, (unsigned)p.ctas, 1, 32 * decode_rows_warps(D), smem, 1, p, stream);
 }
 
 // Few groups or short lists: a cluster of CTAs per (sequence, key/value head),
@@ -97,11 +94,12 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
   const int rank = blockIdx.x % p.cluster, bkv = blockIdx.x / p.cluster;
   const int b = bkv / p.H_kv, G = p.H / p.H_kv;
   const int64_t bh0 = (int64_t)bkv * G;
-  for (int i = threadIdx.x; i < p.top_k; i += 32 * kWarps) ids[i] = __ldg(p.ids + (int64_t)bkv * p.top_k + i);
-  const int len = rows::cached_keys(p, b);
   if (threadIdx.x < kWarps * NS) ptx::mbar_init(full_all + threadIdx.x, 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   ptx::fence_barrier_init();
+  after_previous();
+  for (int i = threadIdx.x; i < p.top_k; i += 32 * kWarps) ids[i] = __ldg(p.ids + (int64_t)bkv * p.top_k + i);
+  const int len = rows::cached_keys(p, b);
   __syncthreads();
 
   uint8_t* ring = ring_all + warp * Geo::kRing;
@@ -228,19 +226,8 @@ cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv * p.cluster));
-  cfg.blockDim = dim3(32 * decode_rows_warps(D));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_chained(kern, (unsigned)(p.B * p.H_kv * p.cluster), 1, 32 * decode_rows_warps(D), smem, p.cluster, p,
+                        stream);
 }
 
 // The merge.  Row (b, h)'s states: `na` of the prefix, then the pieces of its
@@ -313,7 +300,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const int b = (int)(bh / p.H), h = (int)(bh % p.H), G = p.H / p.H_kv;
   const int g = b * p.H_kv + h / G;
   const int64_t ra = (((int64_t)(h / G) * p.B + b) * G + h % G) * p.na;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   // the pieces of the group's own list: warps w0 .. w0 + nb - 1 of decode_rows
   int tiles = 0, per = 1, start = 0;
   if (p.group_start) {
@@ -364,29 +351,21 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
 }
 
 template <int D, int SL, int WPR>
-cudaError_t launch_merge_sl(const MergeParams& p, bool after, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
+cudaError_t launch_merge_sl(const MergeParams& p, cudaStream_t stream) {
   const int rows = p.B * p.H;
-  cfg.gridDim = dim3((rows + 4 / WPR - 1) / (4 / WPR), D / SL);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, SL, WPR, decode_rows_tile(D)>, p);
+  return launch_chained(decode_merge_kernel<D, SL, WPR, decode_rows_tile(D)>,
+                        (unsigned)((rows + 4 / WPR - 1) / (4 / WPR)), D / SL, 128, 0, 1, p, stream);
 }
 
 template <int D>
-cudaError_t launch_merge_d(const MergeParams& p, bool after, cudaStream_t stream) {
+cudaError_t launch_merge_d(const MergeParams& p, cudaStream_t stream) {
   // about as many warps as the SMs hold at once, at most
   constexpr int SL = D < 128 ? D : 128;
   const int64_t warps = (int64_t)p.B * p.H * (D / SL), most = kPlanSms * 36;
-  if (p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, after, stream);
-  if (warps * 4 <= most) return launch_merge_sl<D, SL, 4>(p, after, stream);
-  if (warps * 2 <= most) return launch_merge_sl<D, SL, 2>(p, after, stream);
-  return launch_merge_sl<D, SL, 1>(p, after, stream);
+  if (p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, stream);
+  if (warps * 4 <= most) return launch_merge_sl<D, SL, 4>(p, stream);
+  if (warps * 2 <= most) return launch_merge_sl<D, SL, 2>(p, stream);
+  return launch_merge_sl<D, SL, 1>(p, stream);
 }
 
 }  // namespace
@@ -417,11 +396,11 @@ cudaError_t launch_decode_lists(const DecodeRowsParams& p, int d, cudaStream_t s
   }
 }
 
-cudaError_t launch_decode_merge(const MergeParams& p, int d, bool after, cudaStream_t stream) {
+cudaError_t launch_decode_merge(const MergeParams& p, int d, cudaStream_t stream) {
   switch (d) {
-    case 64: return launch_merge_d<64>(p, after, stream);
-    case 128: return launch_merge_d<128>(p, after, stream);
-    case 256: return launch_merge_d<256>(p, after, stream);
+    case 64: return launch_merge_d<64>(p, stream);
+    case 128: return launch_merge_d<128>(p, stream);
+    case 256: return launch_merge_d<256>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

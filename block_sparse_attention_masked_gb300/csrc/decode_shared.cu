@@ -95,11 +95,11 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
       static_assert((size_t)kWarps * Rows::kRing + kWarps * Rows::NS * 8 + 16 <= Geo::kSmem - 1024, "shared memory");
       uint64_t* full = reinterpret_cast<uint64_t*>(sq + kWarps * Rows::kRing);
       volatile int* stop = reinterpret_cast<volatile int*>(full + kWarps * Rows::NS);
-      asm volatile("griddepcontrol.launch_dependents;");
       if (threadIdx.x < kWarps * Rows::NS) ptx::mbar_init(full + threadIdx.x, 1);
       if (threadIdx.x == 0) *stop = 0;
       ptx::fence_barrier_init();
       __syncthreads();
+      after_previous();
       const int w = threadIdx.x >> 5, ctas = gridDim.x - first;
       if (w < kWarps)
         rows::work<D, NT>(p.own, w * ctas + (int)blockIdx.x - first, ctas * kWarps, sq + w * Rows::kRing,
@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   ShBar* bar = reinterpret_cast<ShBar*>(ring + NSL * Geo::kSlot);
   volatile int* abort_flag = &bar->abort_flag;
 
-  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // neighbouring CTAs: the row tiles of one key split, which share its keys in L2
   const int rt = blockIdx.x % p.plan.row_tiles;
@@ -186,6 +185,7 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     ptx::fence_barrier_init();
     ptx::fence_proxy_async_shared();
     __syncwarp();
+    after_previous();
     if (lane == 0) {
       ptx::mbar_arrive_expect_tx(&bar->q_full, (uint32_t)(SUB * (D / 64) * p.plan.seqs * G * 128));
 #pragma unroll
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     }
     ptx::fence_proxy_async_shared();
   }
+  if (warp > 0) after_previous();  // (the states are written over what the previous grid may read)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -462,8 +463,7 @@ cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = p.plan.row_tiles * p.plan.n_split * p.H_kv + (NT ? p.plan.own_ctas : 0);
-  kern<<<grid, Geo::kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(kern, (unsigned)grid, 1, Geo::kThreads, smem, 1, p, stream);
 }
 
 template <int D, int SUB>

@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 4) qk_rope_kernel(const __gri
       }
     }
   };
+  after_previous();
   // (the first rows, the length and the position are on their way while the
   // frequencies are turned into fractions)
   if (live) {
@@ -285,11 +286,8 @@ template <int D, bool F32>
 cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
   const int64_t warps = (int64_t)p.B * p.N * p.segs;
   const unsigned grid = (unsigned)((warps + kRopeWarps - 1) / kRopeWarps);
-  if (p.interleaved)
-    qk_rope_kernel<D, F32, true><<<grid, 32 * kRopeWarps, 0, stream>>>(p);
-  else
-    qk_rope_kernel<D, F32, false><<<grid, 32 * kRopeWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(p.interleaved ? qk_rope_kernel<D, F32, true> : qk_rope_kernel<D, F32, false>, grid, 1,
+                        32 * kRopeWarps, 0, 1, p, stream);
 }
 
 template <bool F32>

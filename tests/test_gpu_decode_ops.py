@@ -675,6 +675,80 @@ def test_shared_replays_in_a_graph():
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_chained_calls_see_what_came_before():
+    """Long runs of calls without a wait between them, on buffers that torch's
+    own kernels and copies rewrite before each: every call begins only after
+    what came before it on the stream, and what follows begins after it."""
+    s = _step_inputs(41)
+    g = _gen(42)
+    rows = [_randn(g, *s["qkv"].shape) for _ in range(8)]
+    host = [r.cpu().pin_memory() for r in rows]
+    want = []
+    for i in range(24):  # one at a time
+        s["qkv"].copy_(rows[i % 8])
+        _step(s)
+        torch.cuda.synchronize()
+        want.append(_outs(s))
+    got = []
+    for i in range(24):
+        if i % 3 == 0:
+            s["qkv"].zero_()
+            s["qkv"].add_(rows[i % 8])
+        else:
+            s["qkv"].copy_(rows[i % 8] if i % 3 == 1 else host[i % 8], non_blocking=True)
+        for x in ("q", "o", "lse", "ids"):
+            s[x].zero_()
+        _step(s)
+        got.append(_outs(s))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_capture_among_other_work():
+    """A captured step behind memory sets, copies and work joined from another
+    stream, followed by torch's kernels: the replay equals the eager run."""
+    s = _step_inputs(51)
+    src = torch.empty_like(s["qkv"])
+    side = torch.cuda.Stream()
+    total = torch.zeros((), device="cuda")
+
+    def run():
+        here = torch.cuda.current_stream()
+        s["qkv"].zero_()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            half = src * 0.5
+        here.wait_stream(side)
+        s["qkv"].copy_(half)
+        s["qkv"].add_(half)
+        s["o"].zero_()
+        _step(s)
+        total.copy_(s["o"].float().sum())
+        mattn.decode_shared(s["q"].view(3, 8, 128), s["kc"][0, :, :500].contiguous(), s["vc"][0, :, :500].contiguous(),
+                            s["kc"], s["vc"], seq_lens=s["lens"], out=s["o2"], lse=s["lse"])
+        half.record_stream(here)
+
+    s["o2"] = torch.empty_like(s["o"])
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (1, 2, 3):
+        src.copy_(_randn(_gen(seed), *src.shape))
+        run()
+        torch.cuda.synchronize()
+        want = _outs(s) + [s["o2"].clone(), total.clone()]
+        for x in ("q", "o", "o2", "lse"):
+            s[x].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(_outs(s) + [s["o2"], total], want):
+            assert torch.equal(x, y)
+
+
 def test_binding_refusals():
     g = _gen(0)
     q, kp, c = _randn(g, 2, 4, 128), _randn(g, 2, 64, 128), _randn(g, 2, 2, 32, 128)
