@@ -150,7 +150,7 @@ constexpr float kScoreErr = 3.0517578125e-05f;  // 2^-15 (see above)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -186,6 +186,7 @@ __device__ __forceinline__ int blocks_of(const DecodeSelectParams& p, int b) {
   return n < p.n_blocks ? (int)n : p.n_blocks;
 }
 
+static_assert(kSmallBand * 16 * sizeof(double) <= kSelKept * sizeof(uint2), "the products of a band take the scores' place");
 constexpr uint32_t kKeyMin = 0x00800000u, kKeyMax = 0xff7fffffu;  // keys of the least and largest finite float
 
 struct SelShared {
@@ -548,56 +549,49 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
     pick_sync();
     const int band = sh->n_band, need = want - sh->n_in;  // 0 < need <= band
     double* again = p.again + (int64_t)bkv * p.n_blocks;
-    // one warp: the score of block i in 64 bits (NaN ranks below everything); a
-    // lane takes D / 32 dims, the queries' from the operands in shared memory
+    // one warp: block i's product with head g in 64 bits; a lane takes D / 32
+    // dims, the queries' from the operands in shared memory
     constexpr int VPL = D / 32;
     const int piece = lane * VPL / 8, at = lane * VPL % 8;
-    auto score64 = [&](int i) -> double {
+    auto dot64 = [&](int i, int g) -> double {
       const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p.means) +
                                  ((int64_t)bkv * p.n_blocks + i) * D + lane * VPL;
-      float m[VPL];
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(
+                              &sh->q[g >> 3][(piece >> 3) * 2 + (piece & 1)][(g & 7) * 4 + ((piece & 7) >> 1)]) + at / 2;
+      double s = 0.0;
 #pragma unroll
       for (int c = 0; c < VPL; c += 2) {
-        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + c));
-        m[c] = bfl(u);
-        m[c + 1] = bfh(u);
+        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + c)), v = q[c / 2];
+        // (the products are exact in 64 bits; in 32 they could overflow)
+        s = fma((double)bfl(v), (double)bfl(u), s);
+        s = fma((double)bfh(v), (double)bfh(u), s);
       }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      return s;
+    };
+    // the greatest of a block's products; NaN ranks below everything
+    auto greatest = [&](const double* s) -> double {
       double best = -INFINITY;
-      bool bad = false;
-#pragma unroll 1
-      for (int g0 = 0; g0 < G; g0 += 4) {
-        double s[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int g = g0 + k < G ? g0 + k : g0;
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(
-                                  &sh->q[g >> 3][(piece >> 3) * 2 + (piece & 1)][(g & 7) * 4 + ((piece & 7) >> 1)]) + at / 2;
-          s[k] = 0.0;
-#pragma unroll
-          for (int c = 0; c < VPL; c += 2) {
-            s[k] = fma((double)bfl(q[c / 2]), (double)m[c], s[k]);
-            s[k] = fma((double)bfh(q[c / 2]), (double)m[c + 1], s[k]);
-          }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          bad = bad || s[k] != s[k];
-          best = s[k] > best ? s[k] : best;
-        }
+      for (int g = 0; g < G; ++g) {
+        if (s[g] != s[g]) return -INFINITY;
+        best = s[g] > best ? s[g] : best;
       }
-      return bad ? -INFINITY : best;
+      return best;
     };
     if (need >= band) {
       for (int w = tid; w < words; w += kPick) sh->member[w] |= sh->band[w];
     } else if (band <= kSmallBand) {
-      for (int x = warp; x < band; x += kPickWarps) {
-        const double s = score64(sh->idx[x]);
-        if (lane == 0) sh->val[x] = s;
+      // a warp per (block, head): 64-bit arithmetic is slow here (two products a
+      // clock and SM), and mostly two or three blocks are left to tell apart
+      double* dots = reinterpret_cast<double*>(sh->kept);  // (the scores there are done with)
+      pick_sync();
+      for (int x = warp; x < band * G; x += kPickWarps) {
+        const double s = dot64(sh->idx[x / G], x % G);
+        if (lane == 0) dots[x] = s;
       }
+      pick_sync();
+      for (int x = tid; x < band; x += kPick) sh->val[x] = greatest(dots + x * G);
       pick_sync();
       for (int x = tid; x < band; x += kPick) {
         const double s = sh->val[x];
@@ -611,8 +605,14 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
       // lowest indices among those equal to the last one in
       for (int i = f0 + warp; i < f1; i += kPickWarps)
         if ((sh->band[i >> 5] >> (i & 31)) & 1u) {
-          const double s = score64(i);
-          if (lane == 0) again[i] = s;
+          double best = -INFINITY;
+          bool bad = false;
+          for (int g = 0; g < G; ++g) {
+            const double s = dot64(i, g);
+            bad = bad || s != s;
+            best = s > best ? s : best;
+          }
+          if (lane == 0) again[i] = bad ? -INFINITY : best;
         }
       __threadfence_block();
       unsigned long long pre = 0;

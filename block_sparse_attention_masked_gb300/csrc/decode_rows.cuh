@@ -72,12 +72,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // c += a b, 16 x 8 x 16, bf16 inputs and fp32 sums.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -147,15 +147,15 @@ struct State {
       }
       __syncwarp();
     }
-    // S^T: two accumulators per tile so that neighbouring products do not wait on each other
+    // S^T: four accumulators per tile so that neighbouring products do not wait on each other
     float s[NT][MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float acc[NT][2][4];
+      float acc[NT][4][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < 4; ++a)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[nt][a][j] = 0.f;
 #pragma unroll
@@ -163,12 +163,12 @@ struct State {
         uint32_t a[4];
         ldsm4(a, (ks ^ ((2 * i & 7) << 4)) + (i >> 2) * S::kChunk + mt * 2048);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i & 1], a, qf[nt][i][0], qf[nt][i][1]);
+        for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i & 3], a, qf[nt][i][0], qf[nt][i][1]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][mt][j] = acc[nt][0][j] + acc[nt][1][j];
+        for (int j = 0; j < 4; ++j) s[nt][mt][j] = (acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][2][j] + acc[nt][3][j]);
     }
     if (mask != S::kAll) {
 #pragma unroll
@@ -253,17 +253,21 @@ struct State {
         }
       }
     }
-    // O^T += V^T P^T
+    // O^T += V^T P^T, four pieces' first parts before their second ones, which
+    // add into the same sums
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t a[4];
-        ldsm4_t(a, (vs ^ ((2 * i & 7) << 4)) + (i >> 2) * S::kChunk + mt * 2048);
+      for (int i0 = 0; i0 < D / 16; i0 += 4) {
+        uint32_t a[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ldsm4_t(a[i], (vs ^ ((2 * (i0 + i) & 7) << 4)) + ((i0 + i) >> 2) * S::kChunk + mt * 2048);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16816(o[nt][i], a, pf[nt][mt][0], pf[nt][mt][1]);
-          mma16816(o[nt][i], a, pg[nt][mt][0], pg[nt][mt][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16816(o[nt][i0 + i], a[i], pf[nt][mt][0], pf[nt][mt][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16816(o[nt][i0 + i], a[i], pg[nt][mt][0], pg[nt][mt][1]);
         }
       }
     }
