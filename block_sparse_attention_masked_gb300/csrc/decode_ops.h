@@ -88,8 +88,8 @@ struct RopeParams {
 cudaError_t launch_qk_rope(const RopeParams& p, bool f32, cudaStream_t stream);
 
 // ------------------------------------------------------------ decode_rows.cu
-// Keys per tile (8 KB of K and V, 16 KB at d = 256) and warps per SM of the row
-// kernel: each warp has two tiles in flight, 192 KB per SM.
+// Keys per tile (8 KB of K and V, 16 KB at d = 256) and warps of a CTA at most, each
+// with two tiles in flight: 192 KB per SM.
 constexpr int decode_rows_tile(int d) { return d == 64 ? 32 : 16; }
 constexpr int decode_rows_warps(int d) { return d == 256 ? 6 : 12; }
 
@@ -108,6 +108,7 @@ struct DecodeRowsParams {
   int list_tiles;           // tiles of a list of top_k blocks (0: by the sequence's length)
   int min_tiles;            // of a warp's share
   int ctas;                 // of the grid
+  int warps;                // of a CTA
   int cluster;              // decode_lists_kernel: CTAs per group
   const float* sink;        // decode_lists_kernel writes o itself: [H] or null
   void* o;                  // [B][H][d] bf16
@@ -117,7 +118,13 @@ struct DecodeRowsParams {
 cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, cudaStream_t stream);
 
 cudaError_t launch_decode_lists(const DecodeRowsParams& p, int d, cudaStream_t stream);
-int decode_lists_cluster(int64_t groups, int top_k, int list_tiles, int d);
+
+int decode_share_warps(int64_t tiles, int d);
+struct ListPlan {
+  int cluster;  // CTAs per group of decode_lists_kernel, or 0: decode_rows_kernel
+  int warps;    // of a CTA
+};
+ListPlan decode_list_plan(int64_t groups, int top_k, int list_tiles, int d);
 
 // ------------------------------------------------------------ decode_shared.cu
 struct SharedPlan {
@@ -130,7 +137,11 @@ struct SharedPlan {
   int own_ctas; // CTAs of the own keys, behind the prefix's
 };
 constexpr int shared_key_tile(int d) { return d == 256 ? 64 : 128; }
-// Row workers of a CTA among the prefix's (decode_rows_warps where there is no prefix).
+// Tiles in flight of a CTA (32 KB; 16 KB at d = 64).  More than the latency asks for
+// cost bandwidth: 6 against 4 at 128 rows of 128 take 107.1 and 102.8 us for 640 MB,
+// 12 against 6 at 256 rows of 64 110.9 and 107.5 for 320.
+constexpr int shared_slots(int d, int sub) { return d == 64 ? 6 : (d == 256 || sub == 2 ? 5 : 4); }
+// Row workers of a CTA among the prefix's (decode_share_warps where there is no prefix).
 constexpr int shared_row_warps(int d, int sub) { return d == 256 ? 6 : (sub == 2 ? 12 : 8); }
 SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d);
 

@@ -95,8 +95,14 @@ void place_rows(DecodeRowsParams* p, const RowsLayout& r, char* ws) {
   p->group_start = reinterpret_cast<int*>(ws + r.o_bytes + r.ml_bytes);
 }
 
+int list_tiles(int top_k, int block, int d) {
+  const int tk = decode_rows_tile(d);
+  return (int)(((int64_t)top_k * block + tk - 1) / tk);
+}
+
 struct SharedLayout {
   SharedPlan prefix;
+  int own_warps;  // of a CTA of the own keys
   RowsLayout own;
   size_t prefix_bytes, own_bytes;
 };
@@ -105,7 +111,9 @@ SharedLayout shared_layout(int B, int H, int H_kv, int P, int L, int d) {
   SharedLayout s;
   s.prefix = shared_plan(B, H, H_kv, P, L, d);
   s.prefix_bytes = P > 0 ? state_bytes((int64_t)B * H, s.prefix.n_split, d) : 0;
-  s.own = rows_layout((int64_t)B * H_kv, H / H_kv, s.prefix.own_ctas * (P > 0 ? shared_row_warps(d, s.prefix.sub) : decode_rows_warps(d)), d);
+  const int64_t groups = (int64_t)B * H_kv;
+  s.own_warps = P > 0 ? shared_row_warps(d, s.prefix.sub) : decode_share_warps(groups * list_tiles(L, 1, d), d);
+  s.own = rows_layout(groups, H / H_kv, s.prefix.own_ctas * s.own_warps, d);
   s.own_bytes = L > 0 ? s.own.all() : 0;
   return s;
 }
@@ -116,11 +124,6 @@ int check_shared(int B, int H, int H_kv, int P, int L, int d, int dtype) {
   if (P < 0 || L < 0) return report_error(MATTN_ERR_INVALID_ARG, "decode_shared: P and L must be >= 0");
   if (P > kMaxRows || L > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "decode_shared: P or L exceeds 2^30");
   return MATTN_OK;
-}
-
-int list_tiles(int top_k, int block, int d) {
-  const int tk = decode_rows_tile(d);
-  return (int)(((int64_t)top_k * block + tk - 1) / tk);
 }
 
 int check_blocks(int B, int H, int H_kv, int top_k, int block, int d, int dtype) {
@@ -297,6 +300,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     rp.box16 = 1;
     rp.min_tiles = 1;
     rp.ctas = s.prefix.own_ctas;
+    rp.warps = s.own_warps;
     rp.scale_log2 = scale_log2(softmax_scale, d);
     m.b_o = rp.part_o;
     m.b_ml = rp.part_ml;
@@ -398,9 +402,8 @@ int mattn_decode_blocks_workspace(int B, int H, int H_kv, int top_k, int block, 
   if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: bytes_out is NULL");
   const int rc = check_blocks(B, H, H_kv, top_k, block, d, MATTN_BF16);
   if (rc) return rc;
-  *bytes_out = decode_lists_cluster((int64_t)B * H_kv, top_k, list_tiles(top_k, block, d), d)
-                   ? 0
-                   : rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d).all();
+  const ListPlan plan = decode_list_plan((int64_t)B * H_kv, top_k, list_tiles(top_k, block, d), d);
+  *bytes_out = plan.cluster ? 0 : rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * plan.warps, d).all();
   return MATTN_OK;
 }
 
@@ -419,9 +422,10 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   if ((rc = check_small("decode_blocks", lse, seq_lens, sink))) return rc;
   if (!aligned(block_ids, 4)) return report_error(MATTN_ERR_INVALID_ARG, "decode_blocks: block_ids must be 4-byte aligned");
   if ((rc = check_scale("decode_blocks", softmax_scale))) return rc;
-  const int tiles = list_tiles(top_k, block, d), cluster = decode_lists_cluster((int64_t)B * H_kv, top_k, tiles, d);
-  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_rows_warps(d), d);
-  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, cluster ? 0 : lay.all()))) return rc;
+  const int tiles = list_tiles(top_k, block, d);
+  const ListPlan plan = decode_list_plan((int64_t)B * H_kv, top_k, tiles, d);
+  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * plan.warps, d);
+  if ((rc = check_workspace("decode_blocks", workspace, workspace_bytes, plan.cluster ? 0 : lay.all()))) return rc;
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   DecodeRowsParams p;
@@ -440,9 +444,10 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   p.list_tiles = tiles;
   p.min_tiles = 1;
   p.ctas = kPlanSms;
+  p.warps = plan.warps;
   p.scale_log2 = scale_log2(softmax_scale, d);
-  if (cluster) {
-    p.cluster = cluster;
+  if (plan.cluster) {
+    p.cluster = plan.cluster;
     p.sink = sink;
     p.o = o;
     p.lse = lse;

@@ -17,41 +17,41 @@ constexpr float kLog2eR = 1.4426950408889634f;
 constexpr float kLn2R = 0.6931471805599453f;
 
 template <int D>
-struct RowsSmem {
-  static constexpr int kWarps = decode_rows_warps(D);
-  static constexpr size_t kBytes = 1024 + (size_t)kWarps * rows::Geo<D>::kRing + kWarps * rows::Geo<D>::NS * 8 + 16;
-};
+constexpr size_t rows_smem(int warps) {
+  return 1024 + (size_t)warps * (rows::Geo<D>::kRing + rows::Geo<D>::NS * 8) + 16;
+}
 
-// One CTA per SM it runs on (192 KB of tiles in flight); warp w of the grid is warp
+// One CTA per SM it runs on, of p.warps warps; warp w of the grid is warp
 // w / grid of CTA w % grid, so that few shares spread over the SMs.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
     decode_rows_kernel(const __grid_constant__ DecodeRowsParams p) {
   using Geo = rows::Geo<D>;
-  constexpr int kWarps = decode_rows_warps(D);
+  const int warps = blockDim.x >> 5;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kWarps * Geo::kRing);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kWarps * Geo::NS);
-  if (threadIdx.x < kWarps * Geo::NS) ptx::mbar_init(full + threadIdx.x, 1);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + warps * Geo::kRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + warps * Geo::NS);
+  if (threadIdx.x < warps * Geo::NS) ptx::mbar_init(full + threadIdx.x, 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   ptx::fence_barrier_init();
   __syncthreads();
   after_previous();
   const int warp = threadIdx.x >> 5;
-  rows::work<D, NT>(p, warp * gridDim.x + blockIdx.x, gridDim.x * kWarps, ring + warp * Geo::kRing,
+  rows::work<D, NT>(p, warp * gridDim.x + blockIdx.x, gridDim.x * warps, ring + warp * Geo::kRing,
                     full + warp * Geo::NS, abort_flag);
 }
 
 template <int D, int NT>
 cudaError_t launch_nt(const DecodeRowsParams& p, cudaStream_t stream) {
-  const size_t smem = RowsSmem<D>::kBytes;
-  static_assert(RowsSmem<D>::kBytes <= 227 * 1024, "shared memory");
+  constexpr size_t most = rows_smem<D>(decode_rows_warps(D));
+  static_assert(most <= 227 * 1024, "shared memory");
+  if (p.warps < 1 || p.warps > decode_rows_warps(D)) return cudaErrorInvalidValue;
   auto kern = decode_rows_kernel<D, NT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_shared(kern, smem, &done);
+  cudaError_t e = allow_shared(kern, most, &done);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, (unsigned)p.ctas, 1, 32 * decode_rows_warps(D), smem, 1, p, stream);
+  return launch_chained(kern, (unsigned)p.ctas, 1, 32 * p.warps, rows_smem<D>(p.warps), 1, p, stream);
 }
 
 // Few groups or short lists: a cluster of CTAs per (sequence, key/value head),
@@ -60,9 +60,9 @@ cudaError_t launch_nt(const DecodeRowsParams& p, cudaStream_t stream) {
 // other's, each CTA finishing a share of the G x D outputs.
 constexpr int kListIds = 1024;  // list entries that fit the kernel's table
 
-template <int D, int NT>
+template <int D, int NT, int W>
 struct ListSmem {
-  static constexpr int kWarps = decode_rows_warps(D), HP = 8 * NT;
+  static constexpr int kWarps = W, HP = 8 * NT;
   static constexpr size_t kRing = (size_t)kWarps * rows::Geo<D>::kRing;
   // over the ring, once every tile is read: the warps' states, then the CTA's
   static constexpr size_t kStates = (size_t)(kWarps + 1) * HP * (D + 2) * 4;
@@ -79,11 +79,11 @@ __device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
   return x;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W, 1)
     decode_lists_kernel(const __grid_constant__ DecodeRowsParams p) {
   using Geo = rows::Geo<D>;
-  using Mem = ListSmem<D, NT>;
+  using Mem = ListSmem<D, NT, W>;
   constexpr int kWarps = Mem::kWarps, MT = Geo::MT, NS = Geo::NS, HP = Mem::HP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring_all = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -219,15 +219,23 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
   }
 }
 
-template <int D, int NT>
-cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
-  auto kern = decode_lists_kernel<D, NT>;
-  const size_t smem = ListSmem<D, NT>::kBytes;
+template <int D, int NT, int W>
+cudaError_t launch_lists_w(const DecodeRowsParams& p, cudaStream_t stream) {
+  auto kern = decode_lists_kernel<D, NT, W>;
+  const size_t smem = ListSmem<D, NT, W>::kBytes;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, (unsigned)(p.B * p.H_kv * p.cluster), 1, 32 * decode_rows_warps(D), smem, p.cluster, p,
+  return launch_chained(kern, (unsigned)(p.B * p.H_kv * p.cluster), 1, 32 * W, smem, p.cluster, p,
                         stream);
+}
+
+template <int D, int NT>
+cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
+  constexpr int W = decode_rows_warps(D);
+  if (p.warps == W) return launch_lists_w<D, NT, W>(p, stream);
+  if (p.warps == W / 2) return launch_lists_w<D, NT, W / 2>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 // The merge.  Row (b, h)'s states: `na` of the prefix, then the pieces of its
@@ -405,19 +413,32 @@ cudaError_t launch_decode_merge(const MergeParams& p, int d, cudaStream_t stream
   }
 }
 
-// CTAs of a cluster per group where decode_lists_kernel is to be used, else 0.
-// In rounds of a tile per warp of the machine: the clusters leave SMs idle or
-// come in several waves, equal shares (decode_rows_kernel) cost a merge of two
-// rounds' time.
-int decode_lists_cluster(int64_t groups, int top_k, int list_tiles, int d) {
-  if (top_k > kListIds) return 0;
-  const int64_t warps = decode_rows_warps(d);
+// Warps of a CTA of decode_rows_kernel, whose lists come to `tiles` tiles at most:
+// half where each would have few (32 groups of 256 tiles of 128: 18.7 us with 12 warps,
+// 17.0 with 6; 192 groups: 68.2 and 69.1).
+int decode_share_warps(int64_t tiles, int d) {
+  const int warps = decode_rows_warps(d);
+  return tiles <= (int64_t)10 * kPlanSms * warps ? warps / 2 : warps;
+}
+
+// How block lists are read.  Clusters (decode_lists_kernel) need no states in
+// memory and no merge, but leave SMs idle; equal shares (decode_rows_kernel)
+// take them all.  More groups than SMs: CTAs of half the warps, two an SM, of
+// which one loads while the other finishes (512 groups of 2,048 keys of 128: 88.5 us with
+// 12 warps, 81.9 with 6, 91.0 in shares).  Else by the rounds of a tile per
+// warp: 128 groups of 4,096 keys 44.4 us in clusters and 48.1 in shares, 4 groups of
+// 2,048 keys of 256 9.4 and 8.0.
+ListPlan decode_list_plan(int64_t groups, int top_k, int list_tiles, int d) {
+  const int full = decode_rows_warps(d), shared = decode_share_warps(groups * list_tiles, d);
+  const ListPlan shares{0, shared};
+  if (top_k > kListIds) return shares;
+  if (groups > kPlanSms) return {1, full / 2};
   int cluster = 1;
-  while (cluster < 8 && groups * cluster * 2 <= kPlanSms && cluster * warps < list_tiles) cluster *= 2;
-  const int64_t waves = (groups * cluster + kPlanSms - 1) / kPlanSms;
-  const int64_t lists = waves * ((list_tiles + cluster * warps - 1) / (cluster * warps));
-  const int64_t shares = (groups * list_tiles + kPlanSms * warps - 1) / (kPlanSms * warps) + 2;
-  return lists <= shares + shares / 8 ? cluster : 0;
+  while (cluster < 8 && groups * cluster * 2 <= kPlanSms && cluster * full < list_tiles) cluster *= 2;
+  const int64_t rounds = (list_tiles + cluster * full - 1) / (cluster * full);
+  const int64_t share_rounds = (groups * list_tiles + kPlanSms * shared - 1) / (kPlanSms * shared);
+  if (rounds * 4 > share_rounds * 5) return shares;
+  return {cluster, full};
 }
 
 }  // namespace mattn

@@ -52,12 +52,14 @@ struct ShGeo {
   static constexpr int kQTile = (D / 64) * kQChunk;
   static constexpr int kKVChunk = KT * 128;
   static constexpr int kSlot = (D / 64) * kKVChunk;          // one K or V tile: 32 KB (16 KB at d = 64)
-  static constexpr int kSlots = D == 64 ? 12 : (SUB == 2 || D == 256 ? 5 : 6);
+  static constexpr int kSlots = shared_slots(D, SUB);
   static constexpr int kThreads = 128 + 128 * SUB;
   static constexpr int kOcol = 2 * KT > 256 ? 2 * KT : 256;  // first tensor-memory column of O
   static_assert(kOcol + SUB * D <= 512, "tensor memory");
-  static_assert(SUB * 128 * D * 4 <= kSlots * kSlot, "the staged O must fit in the ring");
-  static constexpr size_t kSmem = 1024 + (size_t)SUB * kQTile + (size_t)kSlots * kSlot;
+  static_assert(SUB * 128 * D * 4 <= SUB * kQTile + kSlots * kSlot, "the staged O must fit");
+  // of the prefix's CTAs, and of the own keys'
+  static constexpr size_t kPrefix = (size_t)SUB * kQTile + (size_t)kSlots * kSlot;
+  static constexpr size_t kRows = (size_t)shared_row_warps(D, SUB) * (rows::Geo<D>::kRing + rows::Geo<D>::NS * 8) + 16;
 };
 
 struct ShBar {
@@ -92,7 +94,6 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
       // ------------------------------------------------------ the sequences' own keys
       using Rows = rows::Geo<D>;
       constexpr int kWarps = shared_row_warps(D, SUB);
-      static_assert((size_t)kWarps * Rows::kRing + kWarps * Rows::NS * 8 + 16 <= Geo::kSmem - 1024, "shared memory");
       uint64_t* full = reinterpret_cast<uint64_t*>(sq + kWarps * Rows::kRing);
       volatile int* stop = reinterpret_cast<volatile int*>(full + kWarps * Rows::NS);
       if (threadIdx.x < kWarps * Rows::NS) ptx::mbar_init(full + threadIdx.x, 1);
@@ -408,14 +409,14 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     if (!ok) {
       if (lane == 0) fail_sh(p, bar, kErrSoftmax);
     } else {
-      // O leaves through shared memory (the ring is idle by now: every tile was
-      // consumed), as boxes of 32 rows x 32 columns in the 128-byte swizzle,
+      // O leaves through shared memory (the queries and the ring are idle by
+      // now: every tile was consumed), as boxes of 32 rows x 32 columns in the 128-byte swizzle,
       // whose rows the threads write without bank conflicts.  (16-byte stores
       // from the registers touch 32 rows each, and a copy per row costs the
       // copy engine 8 ns: 2 us for 256 rows.)
       const bool valid = local < used && row < p.rows;
       const int64_t at = ((int64_t)kvh * p.rows + (valid ? row : 0)) * p.plan.n_split + split;
-      uint8_t* stage = ring + (warp - 4) * (32 * D * 4);
+      uint8_t* stage = sq + (warp - 4) * (32 * D * 4);
 #pragma unroll 2
       for (int c0 = 0; c0 < D; c0 += 32) {
         float ov[32];
@@ -456,8 +457,9 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
 template <int D, int SUB, int NT>
 cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   using Geo = ShGeo<D, SUB>;
-  const size_t smem = Geo::kSmem + sizeof(ShBar);
-  static_assert(Geo::kSmem + sizeof(ShBar) <= 227 * 1024, "shared memory");
+  constexpr size_t prefix = Geo::kPrefix + sizeof(ShBar), own = NT ? Geo::kRows : 0;
+  constexpr size_t smem = 1024 + (prefix > own ? prefix : own);
+  static_assert(smem <= 227 * 1024, "shared memory");
   auto kern = decode_shared_kernel<D, SUB, NT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);

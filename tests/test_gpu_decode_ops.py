@@ -243,6 +243,28 @@ def test_blocks_long_lists(top_k):
     blocks_case(1, 8, 2, 128, n * 32, 32, ids, [n * 32 - 7], seed=top_k)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_blocks_more_groups_than_sms(d):
+    """More groups than one wave of CTAs, with lists of none, one and every block."""
+    B, Hkv = 20, 8
+    ids = [[[(b + h + j) % 5 if j < (b + h) % 6 else -1 for j in range(6)] for h in range(Hkv)] for b in range(B)]
+    blocks_case(B, 16, Hkv, d, 5 * 32, 32, ids, [160 - 7 * b for b in range(B)], sink=True, seed=d)
+
+
+@pytest.mark.parametrize("d,top_k", [(64, 1025), (128, 1100), (256, 1025), (256, 200)])
+def test_blocks_in_equal_shares(d, top_k):
+    """Lists past the clusters' table, and one long list of one group, read in equal shares."""
+    rng = np.random.default_rng(d + top_k)
+    ids = [[rng.integers(-3, 40, size=top_k).tolist()]]
+    blocks_case(1, 4, 1, d, 40 * 16, 16, ids, [40 * 16 - 3], sink=True, seed=top_k)
+
+
+@pytest.mark.parametrize("B,Hkv,d,L", [(2, 1, 128, 150000), (1, 1, 256, 147001), (1, 2, 64, 300001)])
+def test_shared_long_own_lists(B, Hkv, d, L):
+    """Own keys alone, long enough for whole CTAs of row workers."""
+    shared_case(B, 2 * Hkv, Hkv, d, 0, L, [L - 9 * b for b in range(B)], seed=d)
+
+
 def test_blocks_everything_equals_decode():
     """All blocks listed: the plain decode step's result."""
     from workloads import MaskSpec
