@@ -123,6 +123,9 @@ int check_shared(int B, int H, int H_kv, int P, int L, int d, int dtype) {
   if (rc) return rc;
   if (P < 0 || L < 0) return report_error(MATTN_ERR_INVALID_ARG, "decode_shared: P and L must be >= 0");
   if (P > kMaxRows || L > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "decode_shared: P or L exceeds 2^30");
+  // (numbered in 32 bits)
+  if ((int64_t)B * H_kv * list_tiles(L, 1, d) > INT32_MAX)
+    return report_error(MATTN_ERR_UNSUPPORTED, "decode_shared: more than 2^31 - 1 tiles of own keys");
   return MATTN_OK;
 }
 
@@ -149,6 +152,12 @@ int check_select(int B, int H, int H_kv, int n_blocks, int d, int dtype) {
     return report_error(MATTN_ERR_UNSUPPORTED, "decode_select: n_blocks = %d exceeds %d", n_blocks, kSelectMaxBlocks);
   return MATTN_OK;
 }
+
+// A buffer's bytes [lo, hi); hi wraps for no buffer that can exist.
+struct Extent {
+  uintptr_t lo, hi;
+  bool meets(const Extent& x) const { return lo < x.hi && x.lo < hi; }
+};
 
 size_t select_bytes(int B, int H_kv, int n_blocks) { return 2 * round256((size_t)B * H_kv * n_blocks * 8); }
 
@@ -197,19 +206,30 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
     return report_error(MATTN_ERR_INVALID_ARG, "qk_rope: eps must be finite and >= 0");
   const void* in[3] = {q, k, v};
   void* out[3] = {q_out, k_out, v_out};
-  const int es = dtype == MATTN_F32 ? 4 : 2;
+  const int es = dtype == MATTN_F32 ? 4 : 2, n_tensors = v ? 3 : 2;
+  Extent read[3], written[3];
   p.wide = true;
-  for (int t = 0; t < (v ? 3 : 2); ++t) {
+  for (int t = 0; t < n_tensors; ++t) {
     const int64_t ts = desc->token_stride[t], bs = desc->batch_stride[t];
     if (!aligned(in[t], 16) || !aligned(out[t], 16) || (ts * es) % 16 || (bs * es) % 16)
       return report_error(MATTN_ERR_UNSUPPORTED, "qk_rope: rows must start on 16-byte boundaries");
     if (ts < 0 || bs < 0) return report_error(MATTN_ERR_INVALID_ARG, "qk_rope: strides must be >= 0");
     p.wide = p.wide && aligned(in[t], 32) && aligned(out[t], 32) && (ts * es) % 32 == 0 && (bs * es) % 32 == 0;
+    const int64_t heads = t ? H_kv : H, rows = t ? L : N;
+    read[t].lo = reinterpret_cast<uintptr_t>(in[t]);
+    read[t].hi = read[t].lo + ((uint64_t)(B - 1) * bs + (uint64_t)(N - 1) * ts + heads * d) * es;
+    written[t].lo = reinterpret_cast<uintptr_t>(out[t]);
+    written[t].hi = written[t].lo + (uint64_t)B * heads * rows * d * es;
     p.src[t] = in[t];
     p.dst[t] = out[t];
     p.token_stride[t] = ts;
     p.batch_stride[t] = bs;
   }
+  // warps read and write rows in no order
+  for (int t = 0; t < n_tensors; ++t)
+    for (int u = 0; u < n_tensors; ++u)
+      if (written[t].meets(read[u]) || (t < u && written[t].meets(written[u])))
+        return report_error(MATTN_ERR_INVALID_ARG, "qk_rope: an output overlaps an input or another output");
   uint32_t* err = nullptr;
   const int rc = device_error_word(static_cast<cudaStream_t>(stream), &err);
   if (rc) return rc;

@@ -1,6 +1,8 @@
 // The row worker: one warp's share of decode attention over the sequences' own
 // keys or their selected blocks, for sm_103a.  It runs on every warp of
-// decode_rows_kernel (decode_rows.cu).
+// decode_rows_kernel (decode_rows.cu) and of the own keys' CTAs of
+// decode_shared_kernel; decode_lists_kernel takes its tiles and its state, and
+// shares the work its own way.
 //
 //   o_h = sum_j p_hj v_j / (sum_j p_hj + exp(sink_h)),  p_hj = exp(scale q_h . k_j)
 //
@@ -137,13 +139,12 @@ struct State {
   // lane_k, lane_v), v_rows the V tile, mask (not 0) the rows that hold a key.
   __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, uint8_t* v_rows, uint32_t mask, float scale_log2) {
     const int lane = threadIdx.x & 31;
-          if (mask != S::kAll) {
+    if (mask != S::kAll) {
       // value rows without a key: zeros (their weights are 0, and 0 x NaN is NaN)
       for (int r = 0; r < TK; ++r) {
         if ((mask >> r) & 1u) continue;
         for (int i = lane; i < S::kChunks * 8; i += 32)
-          *reinterpret_cast<uint4*>(v_rows + (i >> 3) * S::kChunk + r * 128 +
-                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(v_rows + (i >> 3) * S::kChunk + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
       }
       __syncwarp();
     }

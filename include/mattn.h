@@ -381,7 +381,8 @@ int mattn_rr_select(const void* q, const void* k, int B, int H, int N, int d, in
  * They take their workspace from the caller and keep nothing between
  * calls: `workspace` is DEVICE memory, 256-byte aligned, of at least the
  * bytes that the operator's _workspace function reports for the same sizes
- * (host only, no device needed; 0 = may be NULL).  Calls that may overlap on
+ * (host only, no device needed; 0 = may be NULL; other sizes, smaller ones
+ * too, may need more).  Calls that may overlap on
  * the GPU need workspaces of their own; a captured graph keeps its own
  * alive.  A first call on a device makes the library's error word and must
  * not be under stream capture (MATTN_ERR_UNSUPPORTED); every other call can
@@ -421,9 +422,10 @@ typedef struct {
  *              its capacity).  Rows outside 0..L-1 are not written.
  *   positions  DEVICE int32 [n_axes][B][N], or NULL: starts_b + n on every axis.
  *   starts     DEVICE int32 [B] or NULL (0).
- *   lens       DEVICE int32 [B] or NULL (N): tokens n >= lens_b are padding;
- *              nothing of theirs is read or written.
- *   d in {32, 64, 80, 96, 128, 256}.  Outputs must not overlap inputs.
+ *   lens       DEVICE int32 [B] or NULL (N): tokens n >= lens_b are padding:
+ *              nothing of theirs is used or written.
+ *   d in {32, 64, 80, 96, 128, 256}.  An output that overlaps an input or
+ *   another output is MATTN_ERR_INVALID_ARG.
  */
 int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
                   const int32_t* positions, const int32_t* starts, const int32_t* lens, int B, int H, int H_kv, int N,
@@ -442,7 +444,9 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
  *                      clamped.  Rows past a sequence's length are not used.
  *   sink               DEVICE fp32 [H] sink logits or NULL
  *   softmax_scale      0 => 1/sqrt(d)
- *   d in {64, 128, 256}, H / H_kv <= 16, B * H_kv <= 65535.
+ *   d in {64, 128, 256}, H / H_kv <= 16, B * H_kv <= 65535, P and L <= 2^30,
+ *   at most 2^31 - 1 tiles of own keys (of 32 keys at d = 64, else 16) in all.
+ *   q, o and the key and value buffers 16-byte aligned.
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).
  */
 int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
@@ -462,7 +466,8 @@ int mattn_decode_shared_workspace(int B, int H, int H_kv, int P, int L, int d, s
  *             again from all their keys; every other block is left as it is.
  *   first     DEVICE int32 [B] or NULL (0; negative values count as 0).
  *   max_new   new keys of a sequence at most (L: whole caches; 1: a decode step).
- *   block     a multiple of 16;  d in {64, 128, 256}.
+ *   block     a multiple of 16;  d in {64, 128, 256};  k, means 16-byte aligned;
+ *             at most 2^31 blocks to look at in all.
  */
 int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const int32_t* first, int B, int H_kv,
                       int L, int d, int dtype, int block, int max_new, void* stream);
@@ -480,7 +485,7 @@ int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const
  *   block_ids  DEVICE int32 [B][H_kv][top_k]: block indices, ascending, -1
  *              behind the last one.
  *   keep_first + keep_recent <= top_k; n_blocks <= 32768; d, H / H_kv and
- *   B * H_kv as for mattn_decode_shared.
+ *   B * H_kv as for mattn_decode_shared;  q 16-byte, means 32-byte aligned.
  */
 int mattn_decode_select(const void* q, const void* means, const int32_t* seq_lens, int32_t* block_ids, int B, int H,
                         int H_kv, int n_blocks, int d, int dtype, int block, int top_k, int keep_first,
@@ -495,7 +500,9 @@ int mattn_decode_select_workspace(int B, int H, int H_kv, int n_blocks, int d, s
  * end) are skipped; a block listed twice counts twice.
  *   q, o, lse, sink, softmax_scale, d, H / H_kv, B * H_kv: as for
  *   mattn_decode_shared;  k, v  DEVICE bf16 [B][H_kv][L][d];
- *   block_ids  DEVICE int32 [B][H_kv][top_k];  block  a multiple of 16.
+ *   block_ids  DEVICE int32 [B][H_kv][top_k];  block  a multiple of 16 of at
+ *   most 2^20; top_k * block <= 2^30 and at most 2^31 - 1 key tiles (as above)
+ *   in all lists.
  */
 int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* seq_lens,
                         const int32_t* block_ids, int B, int H, int H_kv, int L, int d, int dtype, int block,

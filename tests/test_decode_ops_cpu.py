@@ -73,6 +73,27 @@ def test_qk_rope_refuses(L, why, args, desc, code):
     assert L.mattn_last_error()
 
 
+# q [2][64][8][128] bf16 with token stride 1024 and batch stride 65536: 256 KB; k and v 64 KB each
+APART = dict(ROPE, q=1 << 24, k=2 << 24, v=3 << 24, q_out=4 << 24, k_out=5 << 24, v_out=6 << 24)
+
+
+@pytest.mark.parametrize("why,args", [
+    ("queries in place", {"q_out": 1 << 24}),
+    ("an output that begins in the last row of q", {"k_out": (1 << 24) + 262144 - 256}),
+    ("an output that ends in the first row of v", {"k_out": (3 << 24) - 65536 + 256}),
+    ("one cache for keys and values", {"v_out": 5 << 24}),
+    ("a value cache that ends in the queries' output", {"v_out": (4 << 24) - 65536 + 256}),
+    ("a long cache that reaches the next one", {"L": 1 << 20}),
+])
+def test_qk_rope_refuses_overlaps(L, why, args):
+    """Rows are read and written in no order: an output over an input would be read half written."""
+    a = dict(APART, **args)
+    rc = L.mattn_qk_rope(a["q"], a["k"], a["v"], a["q_out"], a["k_out"], a["v_out"], None, None, None, a["B"], a["H"],
+                         a["H_kv"], a["N"], a["L"], a["d"], 0, ctypes.byref(_rope_desc()), None)
+    assert rc == mattn.ERR_INVALID_ARG, why
+    assert b"overlaps" in L.mattn_last_error()
+
+
 def test_qk_rope_refuses_a_null_descriptor(L):
     a = ROPE
     rc = L.mattn_qk_rope(a["q"], a["k"], a["v"], a["q_out"], a["k_out"], a["v_out"], None, None, None, 2, 8, 2, 64, 64,
@@ -107,6 +128,7 @@ def _shared(lib, **kw):
     ("P < 0", {"P": -1}, -1),
     ("P past its capacity", {"P": 129}, -1),
     ("L < 0", {"L": -1}, -1),
+    ("own keys past 2^31 tiles", {"B": 64, "L": 1 << 30}, -2),
     ("unaligned prefix", {"kp": P16 + 8}, -2),
     ("scale < 0", {"scale": -1.0}, -1),
     ("scale infinite", {"scale": float("inf")}, -1),
