@@ -473,22 +473,16 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
       above += sh->above;
       left = (int)sh->hist[bin];
       // the bin's keys: listed and ranked where they are few, else an interval again
-      uint32_t f = 0xffffffffu, t = 0;
-      each(kept, [&](int, uint32_t k, float, bool there) {
-        const bool in = there && k - from <= to - from && bin_of(k) == bin;
-        f = min(f, in ? k : 0xffffffffu);
-        t = max(t, in ? k : 0u);
-        if (in && left <= 32) sh->list[atomicAdd(&sh->n_list, 1)] = k;
-      });
-      f = __reduce_min_sync(0xffffffffu, f);
-      t = __reduce_max_sync(0xffffffffu, t);
-      if (lane == 0) sh->bound[warp] = make_uint2(f, t);
-      pick_sync();
       if (left <= 32) {
+        each(kept, [&](int, uint32_t k, float, bool there) {
+          if (there && k - from <= to - from && bin_of(k) == bin) sh->list[atomicAdd(&sh->n_list, 1)] = k;
+        });
+        pick_sync();
         // every warp: the key that fewer than want - above and, with its equals, at least that many pass
-        const uint32_t k = lane < left ? sh->list[lane] : 0u;
+        const uint32_t k = lane < left ? sh->list[lane] : 0u;  // (0 is no score's key)
         int more = 0, same = 0;
-        for (int j = 0; j < left; ++j) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
           const uint32_t o = __shfl_sync(0xffffffffu, k, j);
           more += o > k;
           same += o == k;
@@ -498,6 +492,16 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
         from = to = __shfl_sync(0xffffffffu, k, __ffs(hit) - 1);
         break;
       }
+      uint32_t f = 0xffffffffu, t = 0;
+      each(kept, [&](int, uint32_t k, float, bool there) {
+        const bool in = there && k - from <= to - from && bin_of(k) == bin;
+        f = min(f, in ? k : 0xffffffffu);
+        t = max(t, in ? k : 0u);
+      });
+      f = __reduce_min_sync(0xffffffffu, f);
+      t = __reduce_max_sync(0xffffffffu, t);
+      if (lane == 0) sh->bound[warp] = make_uint2(f, t);
+      pick_sync();
       const uint2 now = lane < kPickWarps ? sh->bound[lane] : make_uint2(0xffffffffu, 0u);
       from = __reduce_min_sync(0xffffffffu, now.x);
       to = __reduce_max_sync(0xffffffffu, now.y);
@@ -656,26 +660,27 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 || NT == 2 ? 1 : 2)
     }
   }
   pick_sync();
-  // the chosen blocks in ascending order, -1 behind them: one warp
-  if (warp) return;
+  // the chosen blocks in ascending order, -1 behind them: a share of the words per
+  // warp, whose place is the number of bits in the words before
   int32_t* out = p.ids + (int64_t)bkv * p.top_k;
-  const int wper = (words + 31) / 32, w0 = lane * wper, w1 = w0 + wper < words ? w0 + wper : words;
-  int cnt = 0;
-  for (int w = w0; w < w1; ++w) cnt += __popc(sh->member[w]);
-  int at = cnt;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, at, off);
-    if (lane >= off) at += y;
+  const int wper = (words + kPickWarps - 1) / kPickWarps;
+  const int w0 = warp * wper, w1 = w0 + wper < words ? w0 + wper : words;
+  int before = 0, all = 0;
+  for (int w = lane; w < words; w += 32) {
+    const int c = __popc(sh->member[w]);
+    before += w < w0 ? c : 0;
+    all += c;
   }
-  const int total = __shfl_sync(0xffffffffu, at, 31);
-  at -= cnt;
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t u = sh->member[w]; u; u &= u - 1) {
-      if (at < p.top_k) out[at] = w * 32 + __ffs(u) - 1;
-      ++at;
-    }
-  for (int i = total + lane; i < p.top_k; i += 32) out[i] = -1;
+  int at = __reduce_add_sync(0xffffffffu, before);
+  const int total = __reduce_add_sync(0xffffffffu, all);
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t u = sh->member[w];
+    const int i = at + __popc(u & ((1u << lane) - 1u));
+    if ((u >> lane & 1u) && i < p.top_k) out[i] = w * 32 + lane;
+    at += __popc(u);
+  }
+  for (int i = total + tid; i < p.top_k; i += kPick) out[i] = -1;
 }
 
 template <int D, int NT>
