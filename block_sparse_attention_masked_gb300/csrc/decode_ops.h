@@ -169,6 +169,7 @@ struct MergeParams {
   const int* group_start;    // DecodeRowsParams'; null: no own lists
   const int32_t* seq_lens;
   int na;
+  int states;                // of a row, about
   int L, list_tiles;
   const float* sink;
   void* o;

@@ -332,6 +332,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
   m.o = o;
   m.lse = lse;
   m.B = B; m.H = H; m.H_kv = H_kv;
+  m.states = m.na + (L > 0 ? 1 + (int)(s.own.warps / ((int64_t)B * H_kv)) : 0);
   if (P > 0) {
     if (L > 0) sp.own = rp;
     rc = launched(launch_decode_shared(sp, d, stream), "prefix launch");
@@ -487,6 +488,7 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   m.o = o;
   m.lse = lse;
   m.B = B; m.H = H; m.H_kv = H_kv;
+  m.states = 1 + (int)(lay.warps / ((int64_t)B * H_kv));
   return launched(launch_decode_merge(m, d, stream), "merge launch");
 }
 
