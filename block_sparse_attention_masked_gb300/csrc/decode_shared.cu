@@ -20,8 +20,12 @@
 // during the other's softmax.
 //
 // Up to 128 rows a key tile costs ~1,000 tensor-core cycles against ~2,800 of
-// an SM's share of HBM, so the prefix streams at memory speed; from 256 rows
-// on the tensor cores and the exponentials bound it.
+// an SM's share of HBM, so the prefix streams at memory speed (16 sequences of
+// 4 heads of 256 a key/value head over 128K: 94 us with the merge, 6.1 TB/s);
+// from 256 rows on the tensor cores and the exponentials bound it (1.63 us for
+// 256 rows x 128 keys of 128 on an SM, 10.3 TFLOP/s; 1.9 beside own keys), and the
+// states' way to memory and back (64 sequences over 32K: 48.2 us, of which the
+// products end after 38).
 //
 // K and V tiles share one ring of slots in the order the products take them;
 // the split of the keys over CTAs (shared_plan) fills the SMs, and every wait
@@ -517,8 +521,9 @@ static double split_over(SharedPlan* s, int H_kv, int sms) {
 // take their sum.  Measured beside each other: own keys 60 GB/s an SM and 6 us of
 // start-up, a prefix step (128 rows x a key tile) 0.95 us, at most 6.5 TB/s; own
 // keys on all SMs 4.5 TB/s and 8 us.  (64 sequences, 32 / 8 heads of 128, 32K
-// prefix, 256 own keys on average: 60.2 us one after the other, 52.5 with 32 SMs
-// for the own keys; 128 over 8K: 55.0 and 35.0.)
+// prefix, 256 own keys on average: 55.0 us one after the other, 53.1, 48.4 and
+// 52.8 with 16, 32 and 48 SMs for the own keys; 128 over 8K: 58.3 one after the
+// other, 42.5 and 34.1 with 32 and 56.  The plan takes 32 and 56.)
 SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d) {
   SharedPlan s = {};
   s.seqs = 128 / (H / H_kv);
