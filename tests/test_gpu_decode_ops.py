@@ -657,6 +657,79 @@ def test_two_captured_steps_replayed_together():
                 assert torch.equal(x, y)
 
 
+def _guarded(shape, dtype, fill):
+    """A tensor inside a buffer of `fill`, with 4 KB of it on either side."""
+    n = int(np.prod(shape))
+    pad = 4096 // torch.empty((), dtype=dtype).element_size()
+    whole = torch.full((n + 2 * pad,), fill, dtype=dtype, device="cuda")
+    return whole[pad:pad + n].view(shape), (whole[:pad], whole[pad + n:])
+
+
+@pytest.mark.parametrize("B,H,Hkv,d,P,L", [(1, 4, 1, 64, 130, 0), (5, 12, 1, 128, 1000, 45), (37, 8, 2, 128, 257, 33),
+                                           (70, 6, 2, 64, 300, 17), (33, 4, 1, 256, 129, 50), (3, 8, 2, 256, 0, 700)])
+def test_writes_stay_in_their_buffers(B, H, Hkv, d, P, L):
+    """Outputs and workspaces of exactly the bytes asked for, between guards."""
+    g = _gen(B + d)
+    q, kp, k = _randn(g, B, H, d), _randn(g, Hkv, P, d), _randn(g, B, Hkv, L, d)
+    guards = []
+
+    def buf(shape, dtype, fill):
+        t, around = _guarded(shape, dtype, fill)
+        guards.append((around, fill))
+        return t
+
+    def workspace(made):
+        return buf((made.numel() * made.element_size(),), torch.uint8, 165)
+
+    o, lse = buf((B, H, d), torch.bfloat16, 7.0), buf((B, H), torch.float32, 7.0)
+    mattn.decode_shared(q, kp, kp, k, k, out=o, lse=lse, workspace=workspace(mattn.decode_shared_workspace(B, H, Hkv, P, L, d)))
+    if L:
+        n = -(-L // 16)
+        means, ids = buf((B, Hkv, n, d), torch.bfloat16, 7.0), buf((B, Hkv, 2), torch.int32, 7)
+        mattn.block_means(k, 16, out=means)
+        mattn.decode_select(q, means, 16, 2, out=ids, workspace=workspace(mattn.decode_select_workspace(B, H, Hkv, n, d)))
+        o, lse = buf((B, H, d), torch.bfloat16, 7.0), buf((B, H), torch.float32, 7.0)
+        mattn.decode_blocks(q, k, k, ids, 16, out=o, lse=lse,
+                            workspace=workspace(mattn.decode_blocks_workspace(B, H, Hkv, 2, 16, d)))
+        many = torch.zeros((B, Hkv, 1100), dtype=torch.int32, device="cuda")
+        mattn.decode_blocks(q, k, k, many, 16, out=o, lse=lse,
+                            workspace=workspace(mattn.decode_blocks_workspace(B, H, Hkv, 1100, 16, d)))
+        x = _randn(g, B, 3, H + 2 * Hkv, d)
+        plan = mattn.RopePlan(torch.ones(16, device="cuda"))
+        qo, kc, vc = (buf((B, h, r, d), torch.bfloat16, 7.0) for h, r in ((H, 3), (Hkv, L), (Hkv, L)))
+        starts = _i32([(-2, L - 1, L, 5, (1 << 31) - 1, -(1 << 31))[b % 6] for b in range(B)])
+        mattn.qk_rope(x[:, :, :H], x[:, :, H:H + Hkv], x[:, :, H + Hkv:], plan, qo, kc, vc, starts=starts)
+        for b, n0 in enumerate(starts.tolist()):
+            for c, at in ((kc, H), (vc, H + Hkv)):
+                there = [n0 + i for i in range(3) if 0 <= n0 + i < L]
+                rest = torch.ones(L, dtype=torch.bool)
+                rest[there] = False
+                assert bool((c[b][:, rest.cuda()] == 7.0).all()), "a cache row that no token has"
+                if c is vc and there:
+                    assert torch.equal(c[b][:, there], x[b, [r - n0 for r in there], at:].transpose(0, 1))
+    torch.cuda.synchronize()
+    for around, fill in guards:
+        for t in around:
+            assert bool((t == fill).all()), "a write outside the buffer"
+
+
+def test_lengths_of_any_32_bit_value():
+    """Lengths past the cache count as its own, negative ones as 0, to the ends of int32."""
+    g = _gen(77)
+    B, H, Hkv, d, L = 4, 8, 2, 128, 100
+    q, k, v, kp = _randn(g, B, H, d), _randn(g, B, Hkv, L, d), _randn(g, B, Hkv, L, d), _randn(g, Hkv, 70, d)
+    wild, tame = _i32([-(1 << 31), (1 << 31) - 1, 37, -1]), _i32([0, L, 37, 0])
+    ids = torch.tensor([0, 3, 6, (1 << 31) - 1, -(1 << 31)], dtype=torch.int32, device="cuda").expand(B, Hkv, 5).contiguous()
+    means = mattn.block_means(k, 16)
+    for run in (lambda n: mattn.decode_shared(q, kp, kp, k, v, seq_lens=n),
+                lambda n: mattn.decode_blocks(q, k, v, ids, 16, seq_lens=n),
+                lambda n: (mattn.block_means(k, 16, seq_lens=n),),
+                lambda n: (mattn.block_means(k, 16, seq_lens=n, first=n, max_new=(1 << 31) - 1, out=means.clone()),),
+                lambda n: (mattn.decode_select(q, means, 16, 3, seq_lens=n),)):
+        for x, y in zip(run(wild), run(tame)):
+            assert torch.equal(x, y)
+
+
 def test_calls_on_other_streams_overlap_safely():
     """Shared-prefix calls without a given workspace on two streams, one named by
     its handle, repeated: bit-identical results."""
