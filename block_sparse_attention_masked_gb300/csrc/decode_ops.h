@@ -64,6 +64,18 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 }
+
+// Two softmax weights as pairs of bf16 values, hi + lo, 2^-16 of a weight off at
+// most.  Of a positive weight both are positive (its last bit is taken as set), so
+// that an infinite value stays infinite in both products: a part that is 0 or
+// negative would make it NaN.
+__device__ __forceinline__ void two_bf16(float a, float b, uint32_t* hi, uint32_t* lo) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  *hi = __byte_perm(ua, ub, 0x7632);
+  const float x = __uint_as_float(ua | 1u) - __uint_as_float(ua & 0xffff0000u);
+  const float y = __uint_as_float(ub | 1u) - __uint_as_float(ub & 0xffff0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(*lo) : "f"(y), "f"(x));
+}
 #endif
 
 // ------------------------------------------------------------ qk_rope.cu

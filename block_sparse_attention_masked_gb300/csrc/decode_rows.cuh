@@ -242,15 +242,15 @@ struct State {
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        // P^T as B operand (k = keys, n = heads), each weight as the sum of two
-        // bf16 values, 2^-17 of it off at most: one alone would add an error
-        // as large as the output's own rounding, and the tensor cores idle here
+        // P^T as B operand (k = keys, n = heads), each weight in two parts: one
+        // alone would add an error as large as the output's own rounding, and the
+        // tensor cores idle here
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float a = s[nt][mt][2 * r], b = s[nt][mt][2 * r + 1];
-          const uint32_t hi = ptx::pack_bf16x2(a, b);
+          uint32_t hi, lo;
+          two_bf16(s[nt][mt][2 * r], s[nt][mt][2 * r + 1], &hi, &lo);
           pf[nt][mt][r] = movm_t(hi);
-          pg[nt][mt][r] = movm_t(ptx::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u)));
+          pg[nt][mt][r] = movm_t(lo);
         }
       }
     }

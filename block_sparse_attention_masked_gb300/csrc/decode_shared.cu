@@ -84,8 +84,11 @@ __device__ __forceinline__ void fail_sh(const SharedParams& p, ShBar* bar, uint3
 }
 
 // NT: groups of eight query heads of the row workers in the grid's last CTAs,
-// 0 = none.
-template <int D, int SUB, int NT>
+// 0 = none.  TWO: one row tile.  The tensor cores idle for half of the time then,
+// and P goes to them as the sum of two bf16 values (the lower parts in the other half of
+// S's columns).  It would cost half as much again with more row tiles, where
+// P is rounded to bf16 as in the forward kernels.
+template <int D, int SUB, int NT, bool TWO>
 __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     decode_shared_kernel(const __grid_constant__ SharedParams p) {
   using Geo = ShGeo<D, SUB>;
@@ -125,11 +128,6 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   const int t_lo = split * p.plan.per_split;
   const int t_hi = t_lo + p.plan.per_split < p.plan.tiles ? t_lo + p.plan.per_split : p.plan.tiles;
   const int nt = t_hi - t_lo;       // key tiles of this CTA (>= 1: shared_plan)
-  // One row tile: the tensor cores idle for half of the time, and P goes to
-  // them as the sum of two bf16 values (the rest of the rounding to one in the
-  // other half of S's columns).  It would cost half as much again with more
-  // row tiles, where P is rounded to bf16 as in the forward kernels.
-  const bool two_part = SUB == 1 && p.plan.row_tiles == 1;
   const int n_steps = nt * SUB;
 
   // Load order = the order the products take the tiles.  SUB 1: K0 K1 V0 K2 V1
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
           const uint32_t vo = (uint32_t)((slot * Geo::kSlot + k * 16 * 128) >> 4) + lbo_v;
           ptx::mma_ts(o_tm, p_tm + k * 8, desc64(r4 + vo, hi128), idesc_pv, t > 0 || k > 0);
         }
-        if (two_part) {
+        if constexpr (TWO) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k) {
             const uint32_t vo = (uint32_t)((slot * Geo::kSlot + k * 16 * 128) >> 4) + lbo_v;
@@ -346,13 +344,12 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
           for (int i = 0; i < 32; ++i) {
             const float2 tt = ptx::ffma2(make_float2(x[c0 + 2 * i], x[c0 + 2 * i + 1]), sl2v, negm);
             const float2 pp = make_float2(ptx::ex2(tt.x), ptx::ex2(tt.y));
-            pk[i] = ptx::pack_bf16x2(pp.x, pp.y);
-            if (SUB == 1)
-              lo[i] = ptx::pack_bf16x2(pp.x - __uint_as_float(pk[i] << 16), pp.y - __uint_as_float(pk[i] & 0xffff0000u));
+            if constexpr (TWO) two_bf16(pp.x, pp.y, &pk[i], &lo[i]);
+            else pk[i] = ptx::pack_bf16x2(pp.x, pp.y);
             acc[i & 1] = ptx::fadd2(acc[i & 1], pp);
           }
           ptx::tmem_st32(s_tmem + c0 / 2, pk);
-          if (two_part) ptx::tmem_st32(s_tmem + KT / 2 + c0 / 2, lo);
+          if constexpr (TWO) ptx::tmem_st32(s_tmem + KT / 2 + c0 / 2, lo);
         }
         const float2 a = ptx::fadd2(acc[0], acc[1]);
         sum = a.x + a.y;
@@ -458,13 +455,13 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
   }
 }
 
-template <int D, int SUB, int NT>
+template <int D, int SUB, int NT, bool TWO>
 cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   using Geo = ShGeo<D, SUB>;
   constexpr size_t prefix = Geo::kPrefix + sizeof(ShBar), own = NT ? Geo::kRows : 0;
   constexpr size_t smem = 1024 + (prefix > own ? prefix : own);
   static_assert(smem <= 227 * 1024, "shared memory");
-  auto kern = decode_shared_kernel<D, SUB, NT>;
+  auto kern = decode_shared_kernel<D, SUB, NT, TWO>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
@@ -472,21 +469,21 @@ cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   return launch_chained(kern, (unsigned)grid, 1, Geo::kThreads, smem, 1, p, stream);
 }
 
-template <int D, int SUB>
+template <int D, int SUB, bool TWO>
 cudaError_t launch_sub(const SharedParams& p, cudaStream_t stream) {
-  if (p.own.L == 0) return launch_nt<D, SUB, 0>(p, stream);
-  return p.H / p.H_kv <= 8 ? launch_nt<D, SUB, 1>(p, stream) : launch_nt<D, SUB, 2>(p, stream);
+  if (p.own.L == 0) return launch_nt<D, SUB, 0, TWO>(p, stream);
+  return p.H / p.H_kv <= 8 ? launch_nt<D, SUB, 1, TWO>(p, stream) : launch_nt<D, SUB, 2, TWO>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stream) {
-  switch (d * 4 + p.plan.sub) {
-    case 64 * 4 + 1: return launch_sub<64, 1>(p, stream);
-    case 64 * 4 + 2: return launch_sub<64, 2>(p, stream);
-    case 128 * 4 + 1: return launch_sub<128, 1>(p, stream);
-    case 128 * 4 + 2: return launch_sub<128, 2>(p, stream);
-    case 256 * 4 + 1: return launch_sub<256, 1>(p, stream);
+  switch (d * 4 + p.plan.sub) {  // (d <= 128: two query tiles a CTA from the second row tile on)
+    case 64 * 4 + 1: return launch_sub<64, 1, true>(p, stream);
+    case 64 * 4 + 2: return launch_sub<64, 2, false>(p, stream);
+    case 128 * 4 + 1: return launch_sub<128, 1, true>(p, stream);
+    case 128 * 4 + 2: return launch_sub<128, 2, false>(p, stream);
+    case 256 * 4 + 1: return p.plan.row_tiles == 1 ? launch_sub<256, 1, true>(p, stream) : launch_sub<256, 1, false>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

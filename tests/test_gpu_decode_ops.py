@@ -280,6 +280,28 @@ def test_blocks_everything_equals_decode():
     assert float((lse - lse2).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("B", [2, 40])
+def test_infinite_values(d, B):
+    """An infinite value of an attended key makes its dim infinite, and no other dim or sequence."""
+    g = _gen(d + B)
+    H, Hkv, P, L = 8, 2, 200, 64
+    q, kp, vp = _randn(g, B, H, d), _randn(g, Hkv, P, d), _randn(g, Hkv, P, d)
+    k, v = _randn(g, B, Hkv, L, d), _randn(g, B, Hkv, L, d)
+    vp[0, 131, 7], v[1, 1, 20, 9], v[0, 0, 63, 5] = math.inf, -math.inf, math.inf
+    lens = _i32([63] + [L] * (B - 1))  # (sequence 0's one is past its end)
+    want = torch.zeros((B, H, d), device="cuda")
+    want[1, 4:, 9] = -math.inf
+    ids = torch.arange(4, dtype=torch.int32, device="cuda").expand(B, Hkv, 4).contiguous()
+    many = torch.cat([ids, ids.new_full((B, Hkv, 1100), -1)], dim=-1)
+    outs = [mattn.decode_blocks(q, k, v, x, 16, seq_lens=lens)[0] for x in (ids, many)]
+    for o in outs:
+        assert torch.equal(torch.where(o.isfinite(), 0.0, o.float()), want)
+    o = mattn.decode_shared(q, kp, vp, k, v, seq_lens=lens)[0]
+    want[:, :4, 7] = math.inf
+    assert torch.equal(torch.where(o.isfinite(), 0.0, o.float()), want)
+
+
 def test_offsets_past_32_bits():
     """Caches of more than 2^32 bytes: the last sequence's rows and its means."""
     B, Hkv, L, d, block = 9, 8, 131072, 256, 64
