@@ -12,10 +12,13 @@
 // pairs, so no lane needs another's values but for the row's mean square) and
 // forms the token's cosines and sines once for all its heads.  What counts is
 // loads in flight: with the angles and weights in shared memory and two rows a
-// lane group at a time the kernel keeps 64 registers and 32 warps an SM (805 MB
-// in bf16: 136 us, 5.9 TB/s; 156 us with both in registers, four rows and 16
-// warps); fp32 rows move 32 bytes an access (503 MB: 83 us, 100 with 16).
-// Where tokens are few, warps share a token's rows.
+// lane group at a time the kernel keeps 64 registers and 32 warps an SM (28 and
+// 72 in fp32), in small CTAs, whose warps wait for no more than three others (805 MB
+// in bf16: 131 us, 6.1 TB/s; 136 with eight warps a CTA, 143 with sixteen; 156
+// with angles and weights in registers, four rows and 16 warps an SM).  fp32 rows
+// move 32 bytes an access (503 MB: 77.7 us, 6.5 TB/s; 80.5 with 32 warps an SM; 100
+// with 16 bytes).  Two values an instruction (f32x2) change nothing.  Where
+// tokens are few, warps share a token's rows.
 //
 // Angles: inv_freq / 2 pi is held as a 64-bit fraction of a turn (rounded
 // once, below 2^-53 of itself), so position times it modulo a whole turn is
@@ -30,7 +33,7 @@
 namespace mattn {
 namespace {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeBatch = 2;  // rows in flight per lane group
 
@@ -124,7 +127,7 @@ __device__ __forceinline__ float group_sum(float v, int lane0) {
 }
 
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(32 * kRopeWarps, 4) qk_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, F32 ? 7 : 8) qk_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int GL = D / 16;       // lanes of a row
   constexpr int RPW = 32 / GL;     // rows of a warp
   __shared__ unsigned long long turn[kRopeMaxPairs];          // inv_freq / 2 pi as a 2^-64 fraction of a turn
