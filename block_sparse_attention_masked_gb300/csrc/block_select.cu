@@ -56,7 +56,7 @@ __device__ __forceinline__ float bfl(uint32_t x) { return __uint_as_float(x << 1
 __device__ __forceinline__ float bfh(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // ------------------------------------------------------------ block means
-constexpr int kMeanWarps = 8;
+constexpr int kMeanWarps = 4;
 
 // PARTS: warps per block.
 template <int D, int PARTS>
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(32 * kMeanWarps) block_means_kernel(const __gr
   constexpr int RPI = 32 / LPR;       // keys per warp load
   constexpr int U = 8;                // loads in flight per lane
   constexpr int kMeanBlocks = kMeanWarps / PARTS;
+  static_assert(kMeanBlocks * PARTS == kMeanWarps, "whole blocks in a CTA");
   __shared__ float sums[PARTS > 1 ? kMeanWarps : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = warp / PARTS, part = warp % PARTS;
