@@ -302,6 +302,50 @@ def test_infinite_values(d, B):
     assert torch.equal(torch.where(o.isfinite(), 0.0, o.float()), want)
 
 
+@pytest.mark.parametrize("B,H,Hkv,d", [(3000, 2, 1, 64), (5001, 4, 4, 128), (700, 16, 16, 256), (65535, 1, 1, 64)])
+def test_large_batches(B, H, Hkv, d):
+    """Thousands of sequences of 0 to 40 own keys: shared prefix and block lists."""
+    g = _gen(B)
+    P, L, G, scale = 70, 40, H // Hkv, d ** -0.5
+    q, kp, vp = _randn(g, B, H, d), _randn(g, Hkv, P, d), _randn(g, Hkv, P, d)
+    k, v = _randn(g, B, Hkv, L, d), _randn(g, B, Hkv, L, d)
+    lens = torch.randint(0, L + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    ids = torch.tensor([2, 0, -1], dtype=torch.int32, device="cuda").expand(B, Hkv, 3).contiguous()
+    o, lse = mattn.decode_shared(q, kp, vp, k, v, seq_lens=lens)
+    o2, lse2 = mattn.decode_blocks(q, k, v, ids, 16, seq_lens=lens)
+    pos = torch.arange(L, device="cuda")
+    live = pos < lens[:, None]
+    listed = live & ((pos < 16) | (pos >= 32))
+    for b0 in range(0, B, 2000):
+        sl = slice(b0, b0 + 2000)
+        n = q[sl].shape[0]
+        qd = q[sl].double().view(n, Hkv, G, d)
+        own = (qd @ k[sl].double().transpose(-1, -2)) * scale
+        pre = torch.einsum("bhgd,hpd->bhgp", qd, kp.double()) * scale
+        vo, vpd = v[sl].double(), vp.double()
+        # the scores' error: d e max sum |q k| scale, with |q| |k| as a bound of the sum
+        tol = float(qd.norm(dim=-1).max() * torch.maximum(k.float().norm(dim=-1).max(), kp.float().norm(dim=-1).max())) * scale * d * E
+        for got, gl, mask, prefix in ((o, lse, live, True), (o2, lse2, listed, False)):
+            x = own.masked_fill(~mask[sl][:, None, None, :], -math.inf)
+            if prefix:
+                x = torch.cat((pre, x), dim=-1)
+            m = x.amax(-1, keepdim=True).clamp_min(-1e300)
+            w = torch.exp(x - m)
+            z = w.sum(-1, keepdim=True)
+            p = torch.where(z > 0, w / z, 0.0)
+            wo = p[..., P:] if prefix else p
+            r, a = wo @ vo, wo @ vo.abs()
+            if prefix:
+                r, a = (y + torch.einsum("bhgp,hpd->bhgd", p[..., :P], u) for y, u in ((r, vpd), (a, vpd.abs())))
+            err = (got[sl].double().view_as(r) - r).abs() - (U * r.abs() + (U + 2 * tol + 2.0 ** -13) * a)
+            assert float(err.max()) <= 1e-30
+            l = (m + torch.log(z)).squeeze(-1)
+            gld = gl[sl].double().view_as(l)
+            none = z.squeeze(-1) == 0
+            assert bool((gld[none] == -math.inf).all())
+            assert bool(((gld - l).abs()[~none] <= tol + 2.0 ** -19 * (1 + l.abs()[~none])).all())
+
+
 def test_offsets_past_32_bits():
     """Caches of more than 2^32 bytes: the last sequence's rows and its means."""
     B, Hkv, L, d, block = 9, 8, 131072, 256, 64
