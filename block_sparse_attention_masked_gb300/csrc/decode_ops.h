@@ -118,7 +118,6 @@ struct DecodeRowsParams {
   int B, H, H_kv, L;
   int top_k, block, box16;  // block = 16 box16 keys
   int list_tiles;           // tiles of a list of top_k blocks (0: by the sequence's length)
-  int min_tiles;            // of a warp's share
   int ctas;                 // of the grid
   int warps;                // of a CTA
   int cluster;              // decode_lists_kernel: CTAs per group

@@ -318,7 +318,6 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     rp.B = B; rp.H = H; rp.H_kv = H_kv; rp.L = L;
     rp.block = 16;
     rp.box16 = 1;
-    rp.min_tiles = 1;
     rp.ctas = s.prefix.own_ctas;
     rp.warps = s.own_warps;
     rp.scale_log2 = scale_log2(softmax_scale, d);
@@ -463,7 +462,6 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   p.block = block;
   p.box16 = block / 16;
   p.list_tiles = tiles;
-  p.min_tiles = 1;
   p.ctas = kPlanSms;
   p.warps = plan.warps;
   p.scale_log2 = scale_log2(softmax_scale, d);

@@ -361,8 +361,7 @@ __device__ __forceinline__ bool work(const DecodeRowsParams& p, int w, int W, ui
     for (int b = lane; b < p.B; b += 32) sum += list_tiles<D>(p, cached_keys(p, b));
     total = __reduce_add_sync(0xffffffffu, sum) * p.H_kv;
   }
-  int per = (total + W - 1) / W;
-  per = per < p.min_tiles ? p.min_tiles : per;
+  const int per = total ? (total - 1) / W + 1 : 1;  // (total: to 2^31 - 1)
   if (w == 0 && lane == 0) p.group_start[p.B * p.H_kv] = per;
   const int64_t first = (int64_t)w * per;
   if (first >= total) return true;

@@ -60,6 +60,7 @@ struct ShGeo {
   static constexpr int kThreads = 128 + 128 * SUB;
   static constexpr int kOcol = 2 * KT > 256 ? 2 * KT : 256;  // first tensor-memory column of O
   static_assert(kOcol + SUB * D <= 512, "tensor memory");
+  static_assert(kSlots <= 6, "barriers");
   static_assert(SUB * 128 * D * 4 <= SUB * kQTile + kSlots * kSlot, "the staged O must fit");
   // of the prefix's CTAs, and of the own keys'
   static constexpr size_t kPrefix = (size_t)SUB * kQTile + (size_t)kSlots * kSlot;
@@ -67,7 +68,7 @@ struct ShGeo {
 };
 
 struct ShBar {
-  uint64_t full[12], empty[12];
+  uint64_t full[6], empty[6];  // of each slot
   uint64_t q_full;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t o_final;
