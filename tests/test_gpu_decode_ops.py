@@ -816,6 +816,46 @@ def test_calls_on_other_streams_overlap_safely():
         assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_calls_from_threads():
+    """Four threads on streams of their own: every result as if alone."""
+    import threading
+
+    cases, wrong = [], []
+    for i in range(4):
+        g = _gen(60 + i)
+        B = 3 + 7 * i
+        x = (_randn(g, B, 8, 128), _randn(g, 2, 900, 128), _randn(g, 2, 900, 128), _randn(g, B, 2, 200, 128),
+             _randn(g, B, 2, 200, 128))
+        cases.append(x)
+
+    def run(x):
+        means = mattn.block_means(x[3], 16)
+        ids = mattn.decode_select(x[0], means, 16, 5)
+        return [*mattn.decode_shared(*x), means, ids, *mattn.decode_blocks(x[0], x[3], x[4], ids, 16)]
+
+    want = [run(x) for x in cases]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(60):
+                    got = run(cases[i])
+                st.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append(i)
+        except Exception as e:  # (an exception in a thread would pass unseen)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_shared_replays_in_a_graph():
     g = _gen(12)
     B, H, Hkv, d, P, L = 33, 8, 2, 64, 700, 40
