@@ -172,6 +172,24 @@ struct SharedParams {
 };
 cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stream);
 
+// The pieces of a group's own list: the row workers w0 .. w0 + n - 1 of `warps`,
+// from the list's first tile, its tiles and the tiles of a worker's share.  A
+// worker that gave up a wait leaves the rest of its share's entries unwritten, so
+// the table may hold anything: n = 0 where it names no place among the workers.
+struct ListPieces {
+  int w0, n;
+};
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline ListPieces list_pieces(int start, int tiles, int per, int warps) {
+  if (start < 0 || tiles < 1 || per < 1) return {0, 0};
+  const uint32_t first = (uint32_t)start / (uint32_t)per;
+  const uint32_t last = ((uint32_t)start + (uint32_t)(tiles - 1)) / (uint32_t)per;  // (below 2^32)
+  if (last >= (uint32_t)warps) return {0, 0};
+  return {(int)first, (int)(last - first) + 1};
+}
+
 // One merge for all: row (b, h)'s states of the prefix and of its own list,
 // with the sink logit, into o and the log-sum-exp.
 struct MergeParams {
@@ -180,6 +198,7 @@ struct MergeParams {
   const int* group_start;    // DecodeRowsParams'; null: no own lists
   const int32_t* seq_lens;
   int na;
+  int warps;                 // row workers of the own lists
   int states;                // of a row, about
   int L, list_tiles;
   const float* sink;

@@ -324,6 +324,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     m.b_o = rp.part_o;
     m.b_ml = rp.part_ml;
     m.group_start = rp.group_start;
+    m.warps = s.own.warps;
     m.seq_lens = seq_lens;
     m.L = L;
   }
@@ -479,6 +480,7 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   m.b_o = p.part_o;
   m.b_ml = p.part_ml;
   m.group_start = p.group_start;
+  m.warps = lay.warps;
   m.seq_lens = seq_lens;
   m.L = L;
   m.list_tiles = p.list_tiles;
@@ -488,6 +490,14 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   m.B = B; m.H = H; m.H_kv = H_kv;
   m.states = 1 + (int)(lay.warps / ((int64_t)B * H_kv));
   return launched(launch_decode_merge(m, d, stream), "merge launch");
+}
+
+// Test hook (not in the public header), host only: where the merge looks for
+// the states of a list whose first tile the table gives as `start`.
+void mattn_internal_list_pieces(int start, int tiles, int per, int warps, int* w0, int* n) {
+  const ListPieces own = list_pieces(start, tiles, per, warps);
+  *w0 = own.w0;
+  *n = own.n;
 }
 
 }  // extern "C"

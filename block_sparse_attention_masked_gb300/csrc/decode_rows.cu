@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   add_states(r, p.a_ml + (ra + unit) * 2, p.a_o + (ra + unit) * D + c0 + part * 4, (p.na - unit + U - 1) / U, U * 2, U * D);
   if (tiles) {
     // state s of the own list: slot w0 + s + g, head h % G of the group
-    const int w0 = start / per, nb = (start + tiles - 1) / per - w0 + 1;
-    const int64_t at = ((int64_t)w0 + g + unit) * G + h % G;
-    add_states(r, p.b_ml + at * 2, p.b_o + at * D + c0 + part * 4, (nb - unit + U - 1) / U, (int64_t)U * G * 2,
+    const ListPieces own = list_pieces(start, tiles, per, p.warps);
+    const int64_t at = ((int64_t)own.w0 + g + unit) * G + h % G;
+    add_states(r, p.b_ml + at * 2, p.b_o + at * D + c0 + part * 4, (own.n - unit + U - 1) / U, (int64_t)U * G * 2,
                (int64_t)U * G * D);
   }
   if (part == 0) {
