@@ -125,6 +125,7 @@ struct DecodeRowsParams {
   void* o;                  // [B][H][d] bf16
   float* lse;               // [B][H] or null
   float scale_log2;
+  int selftest;             // 1: every worker's first copies are left out, so that its wait runs out
 };
 cudaError_t launch_decode_rows(const DecodeRowsParams& p, int d, cudaStream_t stream);
 
@@ -169,6 +170,7 @@ struct SharedParams {
   int rows;                 // B * G
   SharedPlan plan;
   float scale_log2;
+  int selftest;             // 2: the queries' copies are left out, so that the wait for them runs out
 };
 cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stream);
 

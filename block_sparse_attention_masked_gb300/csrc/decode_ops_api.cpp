@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -16,6 +17,9 @@
 
 namespace mattn {
 namespace {
+
+// Test hook: the copies that the next launches leave out (DecodeRowsParams, SharedParams).
+std::atomic<int> g_wait_selftest{0};
 
 constexpr int64_t kMaxRows = 1 << 30;
 constexpr int kMaxGroup = 16;  // query heads per key/value head
@@ -301,6 +305,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     sp.B = B; sp.H = H; sp.H_kv = H_kv; sp.P = P;
     sp.rows = (int)(rows / H_kv);
     sp.plan = s.prefix;
+    sp.selftest = g_wait_selftest.load();
     sp.scale_log2 = scale_log2(softmax_scale, d);
     m.a_o = sp.part_o;
     m.a_ml = sp.part_ml;
@@ -320,6 +325,7 @@ int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefi
     rp.box16 = 1;
     rp.ctas = s.prefix.own_ctas;
     rp.warps = s.own_warps;
+    rp.selftest = g_wait_selftest.load();
     rp.scale_log2 = scale_log2(softmax_scale, d);
     m.b_o = rp.part_o;
     m.b_ml = rp.part_ml;
@@ -465,6 +471,7 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
   p.list_tiles = tiles;
   p.ctas = kPlanSms;
   p.warps = plan.warps;
+  p.selftest = g_wait_selftest.load();
   p.scale_log2 = scale_log2(softmax_scale, d);
   if (plan.cluster) {
     p.cluster = plan.cluster;
@@ -498,6 +505,16 @@ void mattn_internal_list_pieces(int start, int tiles, int per, int warps, int* w
   const ListPieces own = list_pieces(start, tiles, per, warps);
   *w0 = own.w0;
   *n = own.n;
+}
+
+// Test hook (not in the public header): the launches of decode_shared and
+// decode_blocks until the next call leave out copies that their kernels wait for,
+// so that the bounded waits and the error word can be exercised without a hang:
+// 1 the row workers' first keys, 2 the prefix's queries, 0 none.
+int mattn_internal_decode_wait_selftest(int what) {
+  if (what < 0 || what > 2) return report_error(MATTN_ERR_INVALID_ARG, "what must be 0, 1 or 2");
+  g_wait_selftest.store(what);
+  return MATTN_OK;
 }
 
 }  // extern "C"

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   uint32_t masks[2] = {0, 0};
 #pragma unroll
   for (int n = 0; n < NS; ++n)
-    if (n < mine) masks[n] = issue(n);
+    if (n < mine && (n || p.selftest != 1)) masks[n] = issue(n);
   rows::State<D, NT> st;
   st.begin(p.q, bh0, G);
   const uint32_t at_k = rows::lane_k(ptx::smem_addr(ring)), at_v = rows::lane_v(ptx::smem_addr(ring) + Geo::kTensor);

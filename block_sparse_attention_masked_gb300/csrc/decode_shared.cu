@@ -191,13 +191,15 @@ __global__ void __launch_bounds__(ShGeo<D, SUB>::kThreads, 1)
     __syncwarp();
     after_previous();
     if (lane == 0) {
-      ptx::mbar_arrive_expect_tx(&bar->q_full, (uint32_t)(SUB * (D / 64) * p.plan.seqs * G * 128));
+      if (p.selftest != 2) {
+        ptx::mbar_arrive_expect_tx(&bar->q_full, (uint32_t)(SUB * (D / 64) * p.plan.seqs * G * 128));
 #pragma unroll
-      for (int x = 0; x < SUB; ++x)
+        for (int x = 0; x < SUB; ++x)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          ptx::tma_load_3d(sq + x * Geo::kQTile + c * Geo::kQChunk, &p.tq, &bar->q_full, c * 64, kvh * G,
-                           (rt * SUB + x) * p.plan.seqs);
+          for (int c = 0; c < D / 64; ++c)
+            ptx::tma_load_3d(sq + x * Geo::kQTile + c * Geo::kQChunk, &p.tq, &bar->q_full, c * 64, kvh * G,
+                             (rt * SUB + x) * p.plan.seqs);
+      }
       for (int i = 0; i < kAhead && i < 2 * nt; ++i) issue_load(i);
     }
   } else if (warp == 1) {
