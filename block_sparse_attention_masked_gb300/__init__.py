@@ -421,10 +421,6 @@ def _on_stream(stream, call, first, *args):
         return call(first, *args)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _workspace(fn, device, *sizes):
     import torch
 
@@ -440,7 +436,10 @@ class RopePlan:
     sections: rotated pairs of each position axis (1 to 3 axes, sum R, a
     multiple of 8 of at most d / 2; None = one axis); q_weight, k_weight: CUDA
     fp32 [d] or None (no norm); interleaved: pairs (2p, 2p + 1) instead of
-    (p, p + R).  The tensors are kept and read at every call."""
+    (p, p + R).  The tensors are kept, and read where they lie at each call
+    (new values, new storage or another tensor set on the plan count from the
+    next call on; a captured graph reads the storage of its capture).  The
+    sections, eps and the pairing are fixed."""
 
     def __init__(self, inv_freq, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False):
@@ -451,27 +450,33 @@ class RopePlan:
         sections = [inv_freq.shape[0]] if sections is None else [int(n) for n in sections]
         if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
             raise ValueError("sections must be 1 to 3 pair counts that add up to inv_freq's length")
-        self.device = inv_freq.get_device()
         for t in (inv_freq, q_weight, k_weight):
-            if t is not None and (t.dtype != torch.float32 or t.get_device() != self.device or not t.is_contiguous()):
+            if t is not None and (t.dtype != torch.float32 or t.device != inv_freq.device or not t.is_contiguous()):
                 raise ValueError("inv_freq and the norm weights must be contiguous fp32 tensors on one CUDA device")
         for w in (q_weight, k_weight):
             if w is not None and (w.dim() != 1 or w.shape != (q_weight if q_weight is not None else w).shape):
                 raise ValueError("norm weights must be [d]")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
-        self.sections, self.eps, self.interleaved = sections, float(eps), bool(interleaved)
-        w = q_weight if q_weight is not None else k_weight
-        self.width = 0 if w is None else w.shape[0]
+        self._sections, self._eps, self._interleaved = sections, float(eps), bool(interleaved)
         d = RopeDesc()
         d.n_axes = len(sections)
         for a, n in enumerate(sections):
             d.sections[a] = n
-        d.interleaved = int(self.interleaved)
-        d.eps = self.eps
-        d.inv_freq = inv_freq.data_ptr()
-        d.q_weight = _ptr(q_weight)
-        d.k_weight = _ptr(k_weight)
-        self._head = bytes(d)[:RopeDesc.token_stride.offset]  # all but a call's strides
+        d.interleaved = int(self._interleaved)
+        d.eps = self._eps
+        self._head = bytes(d)[:RopeDesc.inv_freq.offset]  # what no tensor holds
+
+    @property
+    def sections(self):
+        return list(self._sections)
+
+    @property
+    def eps(self):
+        return self._eps
+
+    @property
+    def interleaved(self):
+        return self._interleaved
 
 
 def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positions=None, starts=None, lens=None,
@@ -490,7 +495,7 @@ def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positio
     Returns (q_out, k_out, v_out)."""
     if stream is not None:
         return _on_stream(stream, qk_rope, q, k, v, plan, q_out, k_out, v_out, positions, starts, lens)
-    return _result(_torch_calls().qk_rope(q, k, v, plan._head, plan.device, plan.width, len(plan.sections), q_out, k_out,
+    return _result(_torch_calls().qk_rope(q, k, v, plan._head, plan.inv_freq, plan.q_weight, plan.k_weight, q_out, k_out,
                                           v_out, positions, starts, lens))
 
 

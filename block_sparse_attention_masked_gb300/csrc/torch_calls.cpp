@@ -207,22 +207,34 @@ struct Outputs {
 };
 
 PyObject* qk_rope(Args a) {
-  // q, k, v, descriptor bytes (all but the strides), plan device, plan width (0: no weights), axes, then the rest
+  // q, k, v, the descriptor's bytes before its pointers, the plan's tensors, then the rest
   const at::Tensor& q = a.tensor("q");
   const at::Tensor& k = a.tensor("k");
   const at::Tensor* v = a.optional("v");
   PyObject* head = a.next();
-  const int64_t plan_device = a.integer("device"), width = a.integer("width"), axes = a.integer("axes");
+  const at::Tensor& inv_freq = a.tensor("inv_freq");
+  const at::Tensor *q_weight = a.optional("q_weight"), *k_weight = a.optional("k_weight");
   const at::Tensor *q_out = a.optional("q_out"), *k_out = a.optional("k_out"), *v_out = a.optional("v_out");
   const at::Tensor *positions = a.optional("positions"), *starts = a.optional("starts"), *lens = a.optional("lens");
   need(q.is_cuda() && q.dim() == 4 && k.dim() == 4, "q and k must be CUDA tensors [B, N, heads, d]");
   const int64_t B = q.size(0), N = q.size(1), H = q.size(2), d = q.size(3), H_kv = k.size(2);
-  need(plan_device == q.get_device() && (!width || width == d),
-       "the plan's tensors must be on q's device and its weights [d]");
-  mattn_rope_desc desc;
-  static_assert(offsetof(mattn_rope_desc, token_stride) % 8 == 0, "strides follow the pointers");
-  need(PyBytes_Check(head) && PyBytes_GET_SIZE(head) == (Py_ssize_t)offsetof(mattn_rope_desc, token_stride), "bad plan");
-  memcpy(&desc, PyBytes_AS_STRING(head), offsetof(mattn_rope_desc, token_stride));
+  mattn_rope_desc desc = {};
+  constexpr size_t kHead = offsetof(mattn_rope_desc, inv_freq);
+  need(PyBytes_Check(head) && PyBytes_GET_SIZE(head) == (Py_ssize_t)kHead, "bad plan");
+  memcpy(&desc, PyBytes_AS_STRING(head), kHead);
+  // the plan's tensors as they are now: a tensor may have got other storage since the plan was made
+  need(desc.n_axes >= 1 && desc.n_axes <= 3, "bad plan");
+  const int64_t axes = desc.n_axes;
+  int64_t R = 0;
+  for (int64_t i = 0; i < axes; ++i) R += desc.sections[i];
+  fits(&inv_freq, q, at::kFloat, "inv_freq");
+  fits(q_weight, q, at::kFloat, "q_weight");
+  fits(k_weight, q, at::kFloat, "k_weight");
+  need(shape(inv_freq, {R}), "inv_freq must be [R], R the sum of the sections");
+  need((!q_weight || shape(*q_weight, {d})) && (!k_weight || shape(*k_weight, {d})), "the norm weights must be [d]");
+  desc.inv_freq = static_cast<const float*>(inv_freq.data_ptr());
+  desc.q_weight = ptr<const float>(q_weight);
+  desc.k_weight = ptr<const float>(k_weight);
   const at::Tensor* in[3] = {&q, &k, v};
   for (int t = 0; t < 3; ++t) {
     desc.token_stride[t] = desc.batch_stride[t] = 0;

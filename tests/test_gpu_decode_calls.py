@@ -1,0 +1,106 @@
+"""GPU tests of the decode step's operators: what a call reads and returns when
+the tensors of a plan move, outputs are left to the call, and rows start off
+the widest alignment.  Tolerances as in test_gpu_decode_ops.py, whose 64-bit
+forms are used."""
+
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+mattn = pytest.importorskip("block_sparse_attention_masked_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    if not os.path.exists(mattn.LIB_PATH):
+        from block_sparse_attention_masked_gb300 import build
+
+        build.build()
+    mattn.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    yield
+    rc, word = mattn.device_status()
+    assert rc == 0, f"device error word {word:#x}"
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=torch.bfloat16, scale=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ a plan's tensors
+def _rope_inputs(seed=1, B=2, N=3, H=4, Hkv=2, d=128):
+    g = _gen(seed)
+    return tuple(_randn(g, B, N, h, d) for h in (H, Hkv, Hkv))
+
+
+def _freq(n=64, base=1e4):
+    return (base ** (-torch.arange(n, device="cuda") / n)).float()
+
+
+@pytest.mark.parametrize("which", ["inv_freq", "q_weight", "k_weight"])
+@pytest.mark.parametrize("how", ["values", "storage", "attribute"])
+def test_rope_plan_reads_its_tensors_at_each_call(which, how):
+    """New values, new storage behind the same tensor (the old one kept alive here
+    and overwritten) and another tensor on the plan: the next call uses them."""
+    x = _rope_inputs()
+    g = _gen(2)
+    old = {"inv_freq": _freq(), "q_weight": 1 + 0.2 * torch.randn(128, generator=g, device="cuda"),
+           "k_weight": 1 + 0.2 * torch.randn(128, generator=g, device="cuda")}
+    new = dict(old, **{which: _freq(base=50.0) if which == "inv_freq" else 2 + torch.rand(128, generator=g, device="cuda")})
+    kw = lambda t: dict(inv_freq=t["inv_freq"].clone(), q_weight=t["q_weight"].clone(), k_weight=t["k_weight"].clone())  # noqa: E731
+    starts = _i32([5, 90])
+    caches = lambda: dict(k_out=torch.zeros((2, 2, 100, 128), dtype=torch.bfloat16, device="cuda"),  # noqa: E731
+                          v_out=torch.zeros((2, 2, 100, 128), dtype=torch.bfloat16, device="cuda"), starts=starts)
+    want = mattn.qk_rope(*x, mattn.RopePlan(**kw(new)), **caches())
+    plan = mattn.RopePlan(**kw(old))
+    before = mattn.qk_rope(*x, plan, **caches())
+    assert not all(torch.equal(a, b) for a, b in zip(before, want))
+    t = getattr(plan, which)
+    if how == "values":
+        t.copy_(new[which])
+    elif how == "storage":
+        keep = t.data
+        t.data = new[which].clone()
+        keep.fill_(-3.0)
+    else:
+        setattr(plan, which, new[which].clone())
+        t.fill_(-3.0)
+    got = mattn.qk_rope(*x, plan, **caches())
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_rope_plan_checks_its_tensors_at_each_call():
+    x = _rope_inputs()
+    for name, bad in (("q_weight", torch.ones(128)), ("k_weight", torch.ones(128, device="cuda", dtype=torch.bfloat16)),
+                      ("q_weight", torch.ones(64, device="cuda")), ("k_weight", torch.ones(256, device="cuda")[::2]),
+                      ("inv_freq", torch.ones(64)), ("inv_freq", torch.ones(56, device="cuda")),
+                      ("inv_freq", torch.ones((8, 8), device="cuda")), ("inv_freq", None)):
+        plan = mattn.RopePlan(_freq(), q_weight=torch.ones(128, device="cuda"), k_weight=torch.ones(128, device="cuda"))
+        setattr(plan, name, bad)
+        with pytest.raises(ValueError):
+            mattn.qk_rope(*x, plan)
+    plan = mattn.RopePlan(_freq(), [16, 24, 24])
+    assert plan.sections == [16, 24, 24] and plan.eps == 1e-6 and plan.interleaved is False
+    for name, value in (("sections", [64]), ("eps", 1.0), ("interleaved", True)):
+        with pytest.raises(AttributeError):
+            setattr(plan, name, value)
+    plan.q_weight = torch.ones(128, device="cuda")  # (one norm alone)
+    assert torch.isfinite(mattn.qk_rope(*x, plan)[0].float()).all()
