@@ -491,7 +491,8 @@ def qk_rope(q, k, v, plan: RopePlan, q_out=None, k_out=None, v_out=None, positio
     outputs or caches: token n of sequence b goes to row starts[b] + n (rows
     outside the cache are not written); positions: int32 [axes, B, N] or None
     (starts[b] + n); starts, lens: int32 [B] or None (0 and N; tokens past
-    lens[b] are padding and leave the outputs as they are).
+    lens[b] are padding and leave the outputs as they are; in an output that
+    the call makes their rows are zeros).  starts needs given caches.
     Returns (q_out, k_out, v_out)."""
     if stream is not None:
         return _on_stream(stream, qk_rope, q, k, v, plan, q_out, k_out, v_out, positions, starts, lens)

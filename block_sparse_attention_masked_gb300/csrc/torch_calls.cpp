@@ -253,6 +253,9 @@ PyObject* qk_rope(Args a) {
   need(!q_out || shape(*q_out, {B, H, N, d}), "q_out must be [B, H, N, d]");
   need((!k_out || shape(*k_out, {B, H_kv, L, d})) && (!v_out || shape(*v_out, {B, H_kv, L, d})),
        "k_out and v_out must be [B, H_kv, L, d]");
+  // rows that no token goes to are the caller's: an output made here has none
+  need(!starts || (k_out && (!v || v_out)), "starts needs the caches that its rows lie in (k_out, and v_out with v)");
+  need(!v || v_out || L == N, "a cache of keys (k_out with L != N) needs one of values (v_out)");
   need(!positions || shape(*positions, {axes, B, N}), "positions must be [axes, B, N]");
   need((!starts || shape(*starts, {B})) && (!lens || shape(*lens, {B})), "starts and lens must be [B]");
   const at::ScalarType t = q.scalar_type();
@@ -264,9 +267,13 @@ PyObject* qk_rope(Args a) {
   fits(lens, q, at::kInt, "lens");
   const int code = type_code(q);
   On on(q);
-  const at::Tensor qo = q_out ? *q_out : empty({B, H, N, d}, q, t), ko = k_out ? *k_out : empty({B, H_kv, L, d}, q, t);
+  // (padding, which the kernel leaves as it is: zeros)
+  auto made = [&](int64_t heads, int64_t rows) {
+    return lens ? at::zeros({B, heads, rows, d}, q.options()) : empty({B, heads, rows, d}, q, t);
+  };
+  const at::Tensor qo = q_out ? *q_out : made(H, N), ko = k_out ? *k_out : made(H_kv, L);
   at::Tensor vo;
-  if (v) vo = v_out ? *v_out : empty({B, H_kv, L, d}, q, t);
+  if (v) vo = v_out ? *v_out : made(H_kv, L);
   done(g_fn.qk_rope(q.data_ptr(), k.data_ptr(), v ? v->data_ptr() : nullptr, qo.data_ptr(), ko.data_ptr(),
                     v ? vo.data_ptr() : nullptr, ptr<int32_t>(positions), ptr<int32_t>(starts), ptr<int32_t>(lens),
                     size32(B), size32(H), size32(H_kv), size32(N), size32(L), size32(d), code, &desc, on.stream));

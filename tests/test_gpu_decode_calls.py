@@ -104,3 +104,41 @@ def test_rope_plan_checks_its_tensors_at_each_call():
             setattr(plan, name, value)
     plan.q_weight = torch.ones(128, device="cuda")  # (one norm alone)
     assert torch.isfinite(mattn.qk_rope(*x, plan)[0].float()).all()
+
+
+# ------------------------------------------------------------------ outputs that the call makes
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_outputs_made_by_the_call_hold_nothing_else(dtype):
+    """Padding rows of outputs that the call makes are zeros, the others as in given outputs."""
+    g = _gen(3)
+    B, N, H, Hkv, d = 3, 50, 4, 2, 64
+    x = tuple(_randn(g, B, N, h, d, dtype=dtype) for h in (H, Hkv, Hkv))
+    plan = mattn.RopePlan(_freq(32), q_weight=torch.ones(d, device="cuda"))
+    lens = _i32([50, 0, 17])
+    given = [torch.zeros((B, h, N, d), dtype=dtype, device="cuda") for h in (H, Hkv, Hkv)]
+    mattn.qk_rope(*x, plan, *given, lens=lens)
+    for _ in range(4):
+        junk = [torch.full_like(t, float("nan")) for t in given]  # what the allocator hands out next
+        del junk
+        for a, b in zip(mattn.qk_rope(*x, plan, lens=lens), given):
+            assert torch.equal(a, b)
+    q, k, v = mattn.qk_rope(x[0], x[1], None, plan, lens=lens)
+    assert v is None and torch.equal(q, given[0]) and torch.equal(k, given[1])
+    got = mattn.qk_rope(*x, plan, lens=lens, v_out=given[2].clone())  # one of them given
+    for a, b in zip(got, given):
+        assert torch.equal(a, b)
+
+
+def test_rope_refuses_starts_without_caches():
+    x = _rope_inputs()
+    plan = mattn.RopePlan(_freq())
+    starts = _i32([0, 1])
+    cache = torch.zeros((2, 2, 9, 128), dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(starts=starts), dict(starts=starts, k_out=cache), dict(k_out=cache),
+               dict(starts=starts, v_out=torch.zeros((2, 2, 3, 128), dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises(ValueError):
+            mattn.qk_rope(*x, plan, **kw)
+    with pytest.raises(ValueError):
+        mattn.qk_rope(x[0], x[1], None, plan, starts=starts)
+    mattn.qk_rope(x[0], x[1], None, plan, starts=starts, k_out=cache)
+    mattn.qk_rope(*x, plan, starts=starts, k_out=cache, v_out=cache.clone())
