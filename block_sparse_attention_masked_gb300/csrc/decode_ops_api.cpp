@@ -517,4 +517,15 @@ int mattn_internal_decode_wait_selftest(int what) {
   return MATTN_OK;
 }
 
+// Test hook (not in the public header), host only: the plan of a decode_shared
+// call: {sub, seqs, row_tiles, n_split, tiles, per_split, own_ctas}.
+int mattn_internal_shared_plan(int B, int H, int H_kv, int P, int L, int d, int* out) {
+  const int rc = check_shared(B, H, H_kv, P, L, d, MATTN_BF16);
+  if (rc) return rc;
+  const SharedPlan s = shared_plan(B, H, H_kv, P, L, d);
+  const int v[7] = {s.sub, s.seqs, s.row_tiles, s.n_split, s.tiles, s.per_split, s.own_ctas};
+  memcpy(out, v, sizeof(v));
+  return MATTN_OK;
+}
+
 }  // extern "C"

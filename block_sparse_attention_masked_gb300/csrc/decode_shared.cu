@@ -494,7 +494,7 @@ cudaError_t launch_decode_shared(const SharedParams& p, int d, cudaStream_t stre
 // The prefix's split over `sms` SMs: a CTA holds its SM, so the launch runs in
 // waves; of the splits that fill one to four waves (and of none) the one whose
 // waves cost least, a wave costing its key tiles and a start-up and state output
-// of about six steps.
+// of about six steps, and each split 0.02 for its states' merge.  Returns the steps.
 static double split_over(SharedPlan* s, int H_kv, int sms) {
   const int64_t units = (int64_t)s->row_tiles * H_kv;
   double best = 1e300;
@@ -517,13 +517,18 @@ static double split_over(SharedPlan* s, int H_kv, int sms) {
 // The own keys' CTAs run beside the prefix's on SMs of their own, as many as make
 // both end together if the sequences hold half of their capacity: the prefix is
 // bound by the tensor cores or the memory, the own keys by the memory's latency,
-// and one after the other (take = 0: the own keys' CTAs wait for free SMs) they
-// take their sum.  Measured beside each other: own keys 60 GB/s an SM and 6 us of
+// and one after the other (a CTA for every SM, which wait for free ones) they take
+// their sum at most.  Measured beside each other: own keys 60 GB/s an SM and 6 us of
 // start-up, a prefix step (128 rows x a key tile) 0.95 us, at most 6.5 TB/s; own
 // keys on all SMs 4.5 TB/s and 8 us.  (64 sequences, 32 / 8 heads of 128, 32K
 // prefix, 256 own keys on average: 55.0 us one after the other, 53.1, 48.4 and
 // 52.8 with 16, 32 and 48 SMs for the own keys; 128 over 8K: 58.3 one after the
-// other, 42.5 and 34.1 with 32 and 56.  The plan takes 32 and 56.)
+// other, 42.5 and 34.1 with 32 and 56.  The plan takes 32 and 56.)  Of each split
+// the SMs that it leaves free are priced, and the own keys get those alone only
+// where that is the lower price: their shares are dealt out once, and no SM that
+// ends the prefix takes any of them over (64 sequences of 16,384 own keys behind
+// 2,048 and 2,304 shared ones: 1,729 and 5,096 us with the 24 and 8 SMs left free,
+// 745 and 735 with a CTA on every SM; the bytes at the copy rate take 644).
 SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d) {
   SharedPlan s = {};
   s.seqs = 128 / (H / H_kv);
@@ -538,24 +543,27 @@ SharedPlan shared_plan(int B, int H, int H_kv, int P, int L, int d) {
   const double own_bytes = 2.0 * d * H_kv * (double)B * L;
   const double stream_us = 4.0 * d * H_kv * (double)P / 6.5e6;
   double best = 1e300;
-  int take = 0;
+  SharedPlan chosen = s;
   for (int r = 0; r <= kPlanSms / 2; r += 8) {
     SharedPlan t = s;
     const double steps = split_over(&t, H_kv, kPlanSms - r);
     const double prefix = steps * 0.95 > stream_us ? steps * 0.95 : stream_us;
-    const double own = own_bytes <= 0.0 ? 0.0 : r > 0 ? 6.0 + own_bytes / (r * 60e3) : 8.0 + own_bytes / 4.5e6;
-    const double total = r == 0 ? prefix + own : (prefix > own ? prefix : own);
-    if (total < best - 1e-9) {
-      best = total;
-      take = r;
+    double cost = prefix + (L > 0 ? 8.0 + own_bytes / 4.5e6 : 0.0);
+    const int64_t free = kPlanSms - (int64_t)t.row_tiles * t.n_split * H_kv;
+    if (L > 0 && free >= 8) {
+      const double own = 6.0 + own_bytes / ((double)free * 60e3), beside = prefix > own ? prefix : own;
+      if (beside < cost) {
+        cost = beside;
+        t.own_ctas = (int)free;
+      }
+    }
+    if (cost < best - 1e-9) {
+      best = cost;
+      chosen = t;
     }
     if (L <= 0) break;
   }
-  split_over(&s, H_kv, kPlanSms - take);
-  // SMs that the prefix leaves free are the own keys' too
-  const int64_t ctas = (int64_t)s.row_tiles * s.n_split * H_kv;
-  if (ctas <= kPlanSms - 8) s.own_ctas = kPlanSms - (int)ctas;
-  return s;
+  return chosen;
 }
 
 }  // namespace mattn

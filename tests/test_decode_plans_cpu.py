@@ -1,5 +1,6 @@
 """CPU checks of the host-side arithmetic behind the decode step's operators
-(no GPU): where the merge looks for the states of a list."""
+(no GPU): where the merge looks for the states of a list, and how a call over a
+shared prefix is split between the prefix and the sequences' own keys."""
 
 import ctypes
 import os
@@ -56,3 +57,53 @@ def test_merge_stays_among_the_workers_whatever_the_table_holds(L):
         tiles, warps = rng.choice((0, 1, 3, 70000, I32 - 1)), rng.choice((1, 912, 1824))
         w0, n = _pieces(L, start, tiles, per, warps)
         assert n == 0 or (0 <= w0 and 1 <= n and w0 + n <= warps), (start, tiles, per, warps)
+
+
+SMS = 152
+
+
+def _shared_plan(L, B, H, Hkv, P, own, d):
+    out = (ctypes.c_int * 7)()
+    assert L.mattn_internal_shared_plan(B, H, Hkv, P, own, d, out) == 0
+    return dict(zip(("sub", "seqs", "row_tiles", "n_split", "tiles", "per_split", "own_ctas"), out))
+
+
+def _prices(plan, B, Hkv, P, own, d):
+    """Microseconds of a call by the rates that the plan is made with (decode_shared.cu):
+    as planned, and with a CTA of own keys on every SM behind the prefix's."""
+    ctas = plan["row_tiles"] * plan["n_split"] * Hkv
+    waves = -(-ctas // SMS)
+    steps = waves * (plan["per_split"] * plan["sub"] + 6) + 0.02 * plan["n_split"]
+    prefix = max(0.95 * steps, 4 * d * Hkv * P / 6.5e6)
+    keys = 2 * d * Hkv * B * own  # bytes, the sequences half full
+    after = prefix + 8 + keys / 4.5e6
+    n = plan["own_ctas"]
+    return (after if n >= SMS else max(prefix, 6 + keys / (n * 60e3))), after
+
+
+@pytest.mark.parametrize("B,H,Hkv", [(1, 8, 1), (4, 16, 4), (16, 32, 8), (64, 32, 8), (128, 8, 8), (300, 8, 2)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_own_keys_get_their_share_of_the_machine(L, B, H, Hkv, d):
+    """Own keys are kept to SMs of their own only where that is no slower than a
+    CTA of them on every SM, by the plan's own rates; a long prefix and few own
+    keys still run beside each other."""
+    beside = 0
+    for P in (1, 100, 512, 1024, 2048, 2304, 2560, 4096, 8192, 16384, 131071):
+        for own in (1, 64, 512, 4096, 16384, 100000):
+            if 4 * d * Hkv * B * own > 1e11:
+                continue
+            plan = _shared_plan(L, B, H, Hkv, P, own, d)
+            assert 8 <= plan["own_ctas"] <= SMS
+            ctas = plan["row_tiles"] * plan["n_split"] * Hkv
+            planned, after = _prices(plan, B, Hkv, P, own, d)
+            assert planned <= after * (1 + 1e-6), (P, own, plan)
+            if plan["own_ctas"] < SMS:
+                assert ctas + plan["own_ctas"] <= SMS, (P, own, plan)
+                beside += 1
+    assert beside
+
+
+@pytest.mark.parametrize("P", [512, 1024, 2048, 2304, 2560, 4096])
+def test_long_own_keys_behind_a_short_prefix_take_most_of_the_machine(L, P):
+    """64 sequences of 16,384 own keys hold more than 99% of the bytes."""
+    assert _shared_plan(L, 64, 32, 8, P, 16384, 128)["own_ctas"] >= SMS // 2
