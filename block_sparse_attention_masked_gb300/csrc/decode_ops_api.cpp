@@ -234,8 +234,7 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
     for (int u = 0; u < n_tensors; ++u)
       if (written[t].meets(read[u]) || (t < u && written[t].meets(written[u])))
         return report_error(MATTN_ERR_INVALID_ARG, "qk_rope: an output overlaps an input or another output");
-  uint32_t* err = nullptr;
-  const int rc = device_error_word(static_cast<cudaStream_t>(stream), &err);
+  const int rc = check_device();
   if (rc) return rc;
   p.positions = positions;
   p.starts = starts;
@@ -361,8 +360,7 @@ int mattn_block_means(const void* k, void* means, const int32_t* seq_lens, const
   if (!aligned(k, 16) || !aligned(means, 16))
     return report_error(MATTN_ERR_UNSUPPORTED, "block_means: buffers must be 16-byte aligned");
   if ((rc = check_small("block_means", nullptr, seq_lens, first))) return rc;
-  uint32_t* err = nullptr;
-  if ((rc = device_error_word(static_cast<cudaStream_t>(stream), &err))) return rc;
+  if ((rc = check_device())) return rc;
   BlockMeansParams p;
   p.k = k;
   p.means = means;
@@ -407,8 +405,7 @@ int mattn_decode_select(const void* q, const void* means, const int32_t* seq_len
   if ((rc = check_small("decode_select", block_ids, seq_lens, nullptr))) return rc;
   const size_t need = select_bytes(B, H_kv, n_blocks);
   if ((rc = check_workspace("decode_select", workspace, workspace_bytes, need))) return rc;
-  uint32_t* err = nullptr;
-  if ((rc = device_error_word(stream, &err))) return rc;
+  if ((rc = check_device())) return rc;
   DecodeSelectParams p;
   p.q = q;
   p.means = means;

@@ -44,6 +44,10 @@ int report_error(int code, const char* fmt, ...);
 // (MATTN_ERR_UNSUPPORTED) where that first use is a call under stream capture.
 int device_error_word(cudaStream_t stream, uint32_t** err);
 
+// MATTN_ERR_NO_DEVICE where the current device is not sm_103.  Allocates nothing
+// and takes no lock: for kernels without an error word.
+int check_device();
+
 // Limit of a device-side wait (mattn_set_wait_timeout_ns).
 unsigned long long device_wait_timeout_ns();
 

@@ -511,16 +511,22 @@ struct DeviceState {
 std::mutex g_mutex;
 std::map<int, std::unique_ptr<DeviceState>> g_devices;
 
+int check_sm103(int dev) {
+  int major = 0, minor = 0;
+  MATTN_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev), "compute capability");
+  MATTN_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev), "compute capability");
+  if (major != 10 || minor != 3)
+    return fail(MATTN_ERR_NO_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a", dev, major, minor);
+  return MATTN_OK;
+}
+
 int device_state(DeviceState** out) {
   int dev = -1;
   MATTN_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   auto it = g_devices.find(dev);
   if (it == g_devices.end()) {
-    int major = 0, minor = 0;
-    MATTN_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev), "compute capability");
-    MATTN_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev), "compute capability");
-    if (major != 10 || minor != 3)
-      return fail(MATTN_ERR_NO_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a", dev, major, minor);
+    const int rc = check_sm103(dev);
+    if (rc) return rc;
     auto st = std::make_unique<DeviceState>();
     MATTN_CUDA(cudaDeviceGetAttribute(&st->sm_count, cudaDevAttrMultiProcessorCount, dev), "SM count");
     MATTN_CUDA(cudaMalloc(&st->err, sizeof(uint32_t)), "cudaMalloc(error word)");
@@ -987,6 +993,17 @@ int device_error_word(cudaStream_t stream, uint32_t** err) try {
   return MATTN_OK;
 } catch (const std::exception& e) {  // no exception leaves a C entry point
   return fail(MATTN_ERR_CUDA, "device state: %s", e.what());
+}
+
+int check_device() {
+  static std::atomic<uint64_t> fine{0};  // a bit per device seen; devices past 64 are asked every time
+  int dev = -1;
+  MATTN_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (fine.load(std::memory_order_relaxed) & bit) return MATTN_OK;
+  const int rc = check_sm103(dev);
+  if (rc == MATTN_OK) fine.fetch_or(bit, std::memory_order_relaxed);
+  return rc;
 }
 
 unsigned long long device_wait_timeout_ns() { return wait_timeout_ns(); }

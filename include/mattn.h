@@ -384,9 +384,9 @@ int mattn_rr_select(const void* q, const void* k, int B, int H, int N, int d, in
  * (host only, no device needed; 0 = may be NULL; other sizes, smaller ones
  * too, may need more).  Calls that may overlap on
  * the GPU need workspaces of their own; a captured graph keeps its own
- * alive.  A first call on a device makes the library's error word and must
- * not be under stream capture (MATTN_ERR_UNSUPPORTED); every other call can
- * be captured.  All are asynchronous on `stream`; errors as for mattn_fwd,
+ * alive.  A first call of mattn_decode_shared or mattn_decode_blocks on a
+ * device makes the library's error word and must not be under stream capture
+ * (MATTN_ERR_UNSUPPORTED); every other call can be captured.  All are asynchronous on `stream`; errors as for mattn_fwd,
  * MATTN_ERR_CAPACITY for a workspace that is too small.
  */
 

@@ -4,6 +4,8 @@ the widest alignment.  Tolerances as in test_gpu_decode_ops.py, whose 64-bit
 forms are used."""
 
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -142,3 +144,48 @@ def test_rope_refuses_starts_without_caches():
         mattn.qk_rope(x[0], x[1], None, plan, starts=starts)
     mattn.qk_rope(x[0], x[1], None, plan, starts=starts, k_out=cache)
     mattn.qk_rope(*x, plan, starts=starts, k_out=cache, v_out=cache.clone())
+
+
+# ------------------------------------------------------------------ first calls
+FIRST_UNDER_CAPTURE = """
+import torch
+import block_sparse_attention_masked_gb300 as mattn
+torch.manual_seed(1)
+def randn(*s):
+    return torch.randn(s, device="cuda").to(torch.bfloat16)
+q, k, v, qd, cache = randn(2, 3, 8, 128), randn(2, 3, 2, 128), randn(2, 3, 2, 128), randn(2, 8, 128), randn(2, 2, 640, 128)
+plan = mattn.RopePlan(torch.ones(64, device="cuda"))
+calls = {"rope": lambda: mattn.qk_rope(q, k, v, plan),
+         "means": lambda: (mattn.block_means(cache, 16),),
+         "select": lambda: (mattn.decode_select(qd, cache, 16, 7),),
+         "refused": lambda: mattn.decode_shared(qd, cache[0], cache[1], cache, cache)}
+call = calls[WHICH]
+torch.cuda.synchronize()
+if WHICH == "refused":
+    graph = torch.cuda.CUDAGraph()
+    try:
+        with torch.cuda.graph(graph):
+            call()
+        raise SystemExit("captured an allocation")
+    except mattn.MattnError as e:
+        assert e.code == mattn.ERR_UNSUPPORTED, e
+else:
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, call()):
+        assert torch.equal(a, b)
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("which", ["rope", "means", "select", "refused"])
+def test_first_call_of_a_process_under_capture(which):
+    """qk_rope, block_means and decode_select need nothing of the device before their
+    first launch; decode_shared makes the error word, and says so."""
+    env = dict(os.environ, PYTHONPATH=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    r = subprocess.run([sys.executable, "-c", f"WHICH = {which!r}\n" + FIRST_UNDER_CAPTURE], env=env, timeout=240,
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
