@@ -93,16 +93,24 @@ def _build_torch_calls(verbose: bool = False) -> str:
 def build(verbose: bool = False, debug: bool = True) -> str:
     """Compiles every source (twice with `debug`: product and debug objects,
     all in parallel), links libmattn.so and libmattn_debug.so, and builds
-    _torch_calls.so beside them."""
+    _torch_calls.so beside them.  The libraries need nvcc alone: they are there
+    also where the torch calls fail to build (an error), and without torch on
+    this machine those are left out (a note on stderr)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = [(s, False) for s in SOURCES] + ([(s, True) for s in SOURCES] if debug else [])
     with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, max(4, os.cpu_count() or 4))) as ex:
         calls = ex.submit(_build_torch_calls, verbose)
         objs = list(ex.map(lambda j: _compile(j[0], verbose, j[1]), jobs))
-        calls.result()
     _link(objs[:len(SOURCES)], LIB)
     if debug:
         _link(objs[len(SOURCES):], DEBUG_LIB)
+    try:
+        calls.result()
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        print(f"{os.path.basename(TORCH_CALLS)} not built: torch is not installed; the Python calls of the decode "
+              "step's operators need it", file=sys.stderr)
     return LIB
 
 
