@@ -20,10 +20,14 @@
 // with 16 bytes).  Two values an instruction (f32x2) change nothing.  Where
 // tokens are few, warps share a token's rows.
 //
-// Angles: inv_freq / 2 pi is held as a 64-bit fraction of a turn (rounded
-// once, below 2^-53 of itself), so position times it modulo a whole turn is
-// one wrapping 64-bit product: far positions lose nothing, where a 32-bit
-// product is off by 0.06 rad at position 2^20.
+// Angles: inv_freq / 2 pi is held as a 64-bit fraction of a turn: the constant
+// and the product round in 64 bits (2^-52 of the turns together), and the fraction is cut
+// to 2^-64 of a turn.  Position times it modulo a whole turn is one wrapping
+// 64-bit product, so nothing else is lost at far positions, where a 32-bit product is
+// off by 0.06 rad at position 2^20.  The nearest quarter turn is taken off in
+// whole numbers, and the rest, an eighth of a turn at most, is rounded to 32 bits:
+// relative to itself, so that cosines and sines are right to 2^-22 of their own values
+// next to their zeros too.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -202,10 +206,21 @@ __global__ void __launch_bounds__(32 * kRopeWarps, F32 ? 7 : 8) qk_rope_kernel(c
   for (int i = lane; i < p.rot; i += 32) {
     const int axis = i < p.axis_end[0] ? 0 : (i < p.axis_end[1] ? 1 : 2);
     const int64_t pos = p.positions ? p.positions[((int64_t)axis * p.B + b) * p.N + n] : (int64_t)start + n;
-    // half turns in [-1, 1)
-    const float x = __ll2float_rn((long long)((unsigned long long)pos * turn[i])) * 1.0842021724855044e-19f;  // 2^-63
+    // whole quarter turns, and what is left in half turns of [-1/4, 1/4)
+    const unsigned long long f = (unsigned long long)pos * turn[i];
+    const unsigned quarter = (unsigned)((f + (1ull << 61)) >> 62);
+    const float x = __ll2float_rn((long long)(f - ((unsigned long long)quarter << 62))) * 1.0842021724855044e-19f;  // 2^-63
     float s, co;
     sincospif(x, &s, &co);
+    if (quarter & 1u) {
+      const float t = co;
+      co = -s;
+      s = t;
+    }
+    if (quarter & 2u) {
+      co = -co;
+      s = -s;
+    }
     trig[warp][0][i] = co;
     trig[warp][1][i] = s;
   }

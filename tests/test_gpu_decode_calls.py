@@ -3,6 +3,7 @@ the tensors of a plan move, outputs are left to the call, and rows start off
 the widest alignment.  Tolerances as in test_gpu_decode_ops.py, whose 64-bit
 forms are used."""
 
+import math
 import os
 import subprocess
 import sys
@@ -189,3 +190,27 @@ def test_first_call_of_a_process_under_capture(which):
     r = subprocess.run([sys.executable, "-c", f"WHICH = {which!r}\n" + FIRST_UNDER_CAPTURE], env=env, timeout=240,
                        capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------ angles
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rope_angles_next_to_quarter_turns(inter, sign):
+    """Rows (1, 0) in fp32 come out as the cosine and sine of their angle: each within
+    four half steps of its own value (one step of sincospi, half a step of the
+    reduced angle), next to its zeros too, and 2^-51 of the whole angle (the 64-bit
+    fraction's two roundings, and the formula's)."""
+    n, R = 20000, 32
+    f = _freq(R)
+    x = torch.zeros((1, n, 1, 2 * R), device="cuda")
+    x[..., (slice(0, None, 2) if inter else slice(0, R))] = 1.0
+    # positions whose angle at pair 0 (1 radian a position) comes near quarter turns, among others
+    near = [round(j * math.pi / 2) for j in range(1, n // 2)] + [355 * j for j in range(1, 200)] + [103993, 104348, 208341, 312689]
+    pos = torch.cat((torch.tensor(near), torch.arange(n - len(near)))).to(torch.int32).cuda() * sign
+    q, _, _ = mattn.qk_rope(x, x, None, mattn.RopePlan(f, interleaved=inter), positions=pos.view(1, 1, n).contiguous())
+    got = q[0, 0].double()
+    t = pos.double()[:, None] * f.double()
+    c, s = (got[:, 0::2], got[:, 1::2]) if inter else (got[:, :R], got[:, R:])
+    for value, ref in ((c, t.cos()), (s, t.sin())):
+        bound = 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -51 * t.abs()
+        assert bool(((value - ref).abs() <= bound).all()), float(((value - ref).abs() - bound).max())
