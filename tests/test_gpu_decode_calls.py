@@ -15,6 +15,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 mattn = pytest.importorskip("block_sparse_attention_masked_gb300")
+import test_gpu_decode_ops as ops  # noqa: E402  (the 64-bit forms)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -214,3 +215,161 @@ def test_rope_angles_next_to_quarter_turns(inter, sign):
     for value, ref in ((c, t.cos()), (s, t.sin())):
         bound = 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -51 * t.abs()
         assert bool(((value - ref).abs() <= bound).all()), float(((value - ref).abs() - bound).max())
+
+
+# ------------------------------------------------------------------ rows off the widest alignment
+def _off(t, by, row_pad=0):
+    """A copy of t, `by` elements off the start of its allocation, tokens row_pad elements further apart."""
+    B, N, h, d = t.shape
+    row = h * d + row_pad
+    buf = torch.full((B * N * row + by + 64,), float("nan"), dtype=t.dtype, device="cuda")
+    v = buf[by:].as_strided((B, N, h, d), (N * row, row, d, 1), by)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 80, 96, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_rows_on_16_byte_boundaries(dtype, d, inter):
+    """Inputs, outputs or token strides 16 but not 32 bytes aligned, each alone and together:
+    the result of aligned rows."""
+    g = _gen(d)
+    B, N, H, Hkv = 2, 5, 3, 2
+    e = 16 // torch.empty((), dtype=dtype).element_size()
+    x = [_randn(g, B, N, h, d, dtype=dtype) for h in (H, Hkv, Hkv)]
+    plan = mattn.RopePlan(_freq(d // 2 // 8 * 8), q_weight=1 + 0.1 * torch.randn(d, generator=g, device="cuda"), interleaved=inter)
+    want = mattn.qk_rope(*x, plan)
+    ref, mag = ops.ref_rope(x[0], plan.q_weight, torch.arange(N, device="cuda").expand(1, B, N), plan.inv_freq,
+                            [plan.inv_freq.numel()], 1e-6, inter)
+    h = torch.finfo(dtype).eps / 2
+    assert bool(((want[0].transpose(1, 2).double().cpu() - ref).abs() <= h * ref.abs() + 2.0 ** -19 * mag).all())
+
+    def outs(off):
+        made = []
+        for w in want:
+            buf = torch.zeros(w.numel() + 64, dtype=dtype, device="cuda")
+            made.append(buf[off:off + w.numel()].view(w.shape))
+        return made
+
+    for moved in ((0,), (1,), (2,), (0, 1, 2)):
+        for off, pad in ((e, 0), (0, e), (e, e)):
+            y = [_off(t, off if i in moved else 0, pad if i in moved else 0) for i, t in enumerate(x)]
+            for o in (0, e):
+                for a, b in zip(mattn.qk_rope(*y, plan, *outs(o)), want):
+                    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_batch_and_token_strides(dtype):
+    """Expanded batches and tokens (stride 0), sequences further apart than their tokens, and one token of a longer run."""
+    g = _gen(4)
+    d, H, Hkv, N = 64, 4, 2, 6
+    plan = mattn.RopePlan(_freq(32), k_weight=1 + 0.1 * torch.randn(d, generator=g, device="cuda"))
+    one = [_randn(g, 1, N, h, d, dtype=dtype) for h in (H, Hkv, Hkv)]
+    token = [t[:, :1] for t in one]
+    long = [_randn(g, 3, 4 * N, h, d, dtype=dtype) for h in (H, Hkv, Hkv)]
+    for x in ([t.expand(3, N, *t.shape[2:]) for t in one], [t.expand(3, N, *t.shape[2:]) for t in token],
+              [t[:, 3:3 + N] for t in long], [t[:, ::4] for t in long], [t[:, 7:8] for t in long], [t[1:2, ::2] for t in long]):
+        for a, b in zip(mattn.qk_rope(*x, plan), mattn.qk_rope(*(t.contiguous() for t in x), plan)):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ near-equal scores past what shared memory keeps
+@pytest.mark.parametrize("n", [6144 + 2, 9000, 32768])
+@pytest.mark.parametrize("kind", ["few near the border", "many near the border", "ties", "extremes"])
+def test_select_near_border_of_many_blocks(n, kind):
+    """More competing blocks than the 6,144 whose scores fit in shared memory."""
+    g = _gen(n)
+    q = _randn(g, 1, 4, 64, scale=8.0)
+    means = _randn(g, 1, 1, n, 64, scale=0.25)
+    top_k = n // 3
+    if kind == "few near the border":
+        # a dozen copies of the border's block that differ by one step in one value
+        s = (means[0, 0].double() @ q[0].double().T).amax(1)
+        at = int(s.argsort(descending=True)[top_k - 6])
+        to = torch.randperm(n, generator=g, device="cuda")[:12]
+        means[0, 0, to] = means[0, 0, at].clone()
+        c = torch.arange(12, device="cuda") * 5
+        means[0, 0, to, c] = (means[0, 0, to, c].float() * (1 + 2.0 ** -7)).to(torch.bfloat16)
+    elif kind == "many near the border":
+        means = means[:, :, :1].expand(1, 1, n, 64).clone()
+        c = torch.randint(0, 64, (n,), generator=g, device="cuda")
+        i = torch.arange(n, device="cuda")
+        means[0, 0, i, c] = (means[0, 0, i, c].float() * (1 + 2.0 ** -7)).to(torch.bfloat16)
+    elif kind == "ties":
+        means = means[:, :, torch.randint(0, 7, (n,), generator=g, device="cuda")].contiguous()
+    else:
+        means[0, 0, 17] *= 1e30
+        means[0, 0, 300, 5], means[0, 0, 301, 6], means[0, 0, 302, 7] = float("nan"), math.inf, -math.inf
+        means[0, 0, 400:900] = 0
+    ops.select_case(q, means, 64, top_k, [n * 64])
+    ops.select_case(q, means, 64, 64, [n * 64], first=2, recent=3)
+
+
+# ------------------------------------------------------------------ weights in two parts
+def _cancelling(g, n, d):
+    """Keys, values and a query such that the output is almost 0 while the weighted
+    values are not: the output's own rounding is small then, and what is left is
+    the weights'.  -> q, k, v, the 64-bit output, sum of weights times |values|."""
+    q, k, v = _randn(g, d, scale=0.5), _randn(g, n, d), _randn(g, n, d)
+    p = torch.softmax(k.double() @ q.double() * d ** -0.5, 0)
+    for j in (n - 3, n - 2, n - 1):  # each takes off what is left, to the half step of its own type
+        left = (p[:, None] * v.double()).sum(0) - p[j] * v[j].double()
+        v[j] = (-left / p[j]).to(torch.bfloat16)
+    return q, k, v, p @ v.double(), p @ v.double().abs()
+
+
+def _runs(q, k, v, n):
+    """The same list of n keys by every path that sends weights in two parts, as 8 query heads of one key/value head."""
+    d = q.shape[0]
+    qs = q.expand(1, 8, d).contiguous()
+    cache = [torch.full((1, 1, -(-n // 16) * 16, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for c, x in zip(cache, (k, v)):
+        c[0, 0, :n] = x
+    lens, none = _i32([n]), k.new_zeros((1, 1, 0, d))
+    ids = torch.arange(-(-n // 16), dtype=torch.int32, device="cuda").view(1, 1, -1)
+    many = torch.cat((ids, ids.new_full((1, 1, 1100), -1)), -1)
+    yield "block lists in a cluster", mattn.decode_blocks(qs, *cache, ids, 16, seq_lens=lens)[0]
+    yield "block lists in shares", mattn.decode_blocks(qs, *cache, many, 16, seq_lens=lens)[0]
+    yield "own keys", mattn.decode_shared(qs, none[0], none[0], *cache, seq_lens=lens)[0]
+    yield "prefix of one row tile", mattn.decode_shared(qs, k[None], v[None], none, none)[0]
+    m = n // 2
+    own = [torch.cat((c[:, :, m:], c[:, :, :m]), 2) for c in cache]
+    yield "prefix and own keys", mattn.decode_shared(qs, k[None, :m].contiguous(), v[None, :m].contiguous(),
+                                                     own[0], own[1], seq_lens=_i32([n - m]))[0]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [8, 50, 300])
+def test_weights_keep_sixteen_bits(d, n):
+    """|do| <= u |o| + (2^-15 + 2 t + 2^-13) A where weights go to the tensor cores
+    as two bf16 parts (2^-16 of a weight off at most, and twice that after the division by
+    their sum); one part alone is off by up to 2^-8 of a weight, and at 8 keys about
+    2^-10 A.  t and 2^-13: see test_gpu_decode_ops.py."""
+    q, k, v, ref, a = _cancelling(_gen(d + n), n, d)
+    t = float((k.double().abs() @ q.double().abs()).max()) * d ** -0.5 * d * 2.0 ** -24
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -15 + 2 * t + 2.0 ** -13) * a
+    if n <= 50:  # (one part alone, by the formula: over the bound in many of the dims)
+        w = torch.exp(k.double() @ q.double() * d ** -0.5)
+        one = w.to(torch.bfloat16).double() @ v.double() / w.sum()
+        assert float(((one - ref).abs() > tol).double().mean()) > 0.1
+    for name, o in _runs(q, k, v, n):
+        over = (o.double() - ref).abs() - tol
+        assert bool((over <= 0).all()), f"{name}: {float(over.max()):.3e} over its bound"
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_one_key_gives_its_value(d):
+    """A single visible key: its value row, bit for bit (2^-16 of a value is far below
+    its half step); with more than 128 query rows a key/value head, where weights have
+    one part, one step off at most."""
+    g = _gen(d)
+    for seed in range(6):
+        q, k, v = _randn(g, d, scale=1 + seed), _randn(g, 1, d), _randn(g, 1, d)
+        for name, o in _runs(q, k, v, 1):
+            if name != "prefix and own keys":  # (0 and 1 keys: the same as own keys)
+                assert torch.equal(o, v[0].expand(1, 8, d)), name
+        none = k.new_zeros((40, 1, 0, d))
+        o = mattn.decode_shared(_randn(g, 40, 8, d), k[None], v[None], none, none)[0].double()
+        assert bool(((o - v[0].double()).abs() <= 2 * 2.0 ** -8 * v[0].double().abs()).all())
