@@ -525,4 +525,15 @@ int mattn_internal_shared_plan(int B, int H, int H_kv, int P, int L, int d, int*
   return MATTN_OK;
 }
 
+// Test hook (not in the public header), host only: how decode_blocks reads its
+// lists: {CTAs of a group's cluster or 0 for equal shares, warps of a CTA}.
+int mattn_internal_list_plan(int B, int H, int H_kv, int top_k, int block, int d, int* out) {
+  const int rc = check_blocks(B, H, H_kv, top_k, block, d, MATTN_BF16);
+  if (rc) return rc;
+  const ListPlan s = decode_list_plan((int64_t)B * H_kv, top_k, list_tiles(top_k, block, d), d);
+  out[0] = s.cluster;
+  out[1] = s.warps;
+  return MATTN_OK;
+}
+
 }  // extern "C"

@@ -426,15 +426,23 @@ int decode_share_warps(int64_t tiles, int d) {
 // How block lists are read.  Clusters (decode_lists_kernel) need no states in
 // memory and no merge, but leave SMs idle; equal shares (decode_rows_kernel)
 // take them all.  More groups than SMs: CTAs of half the warps, two an SM, of
-// which one loads while the other finishes (512 groups of 2,048 keys of 128: 88.5 us with
-// 12 warps, 81.9 with 6, 91.0 in shares).  Else by the rounds of a tile per
-// warp: 128 groups of 4,096 keys 44.4 us in clusters and 48.1 in shares, 4 groups of
-// 2,048 keys of 256 9.4 and 8.0.
+// which one loads while the other finishes (512 groups of 2,048 keys of 128: 91.7 us with
+// 12 warps, 84.3 with 6, 90.0 in shares), but for a last wave that leaves the SMs
+// half empty: shares where the waves' places are more than 7/5 of the groups and
+// the lists long enough for the states and the merge (312 groups of 2,048 keys of 128:
+// 68.5 and 60.0, 384: 72.4 and 72.8, 456: 76.6 and 80.7, 640: 114.1 and 111.9, 768: 121.0 and
+// 130.4; 312 of 1,024 keys of 256: 77.9 and 61.8; 312 of 1,024 keys of 64, 32 tiles: 19.1 and
+// 21.6).  Else by the rounds of a tile per warp: 128 groups of 4,096 keys 44.4 us in
+// clusters and 48.1 in shares, 4 groups of 2,048 keys of 256 9.4 and 8.0.
 ListPlan decode_list_plan(int64_t groups, int top_k, int list_tiles, int d) {
   const int full = decode_rows_warps(d), shared = decode_share_warps(groups * list_tiles, d);
   const ListPlan shares{0, shared};
   if (top_k > kListIds) return shares;
-  if (groups > kPlanSms) return {1, full / 2};
+  if (groups > kPlanSms) {
+    const int64_t wave = 2 * kPlanSms, places = (groups + wave - 1) / wave * wave;
+    if (places > wave && places * 5 > groups * 7 && list_tiles >= 64) return shares;
+    return {1, full / 2};
+  }
   int cluster = 1;
   while (cluster < 8 && groups * cluster * 2 <= kPlanSms && cluster * full < list_tiles) cluster *= 2;
   const int64_t rounds = (list_tiles + cluster * full - 1) / (cluster * full);

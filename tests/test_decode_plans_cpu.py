@@ -1,6 +1,7 @@
 """CPU checks of the host-side arithmetic behind the decode step's operators
-(no GPU): where the merge looks for the states of a list, and how a call over a
-shared prefix is split between the prefix and the sequences' own keys."""
+(no GPU): where the merge looks for the states of a list, how a call over a
+shared prefix is split between the prefix and the sequences' own keys, and how
+block lists are dealt."""
 
 import ctypes
 import os
@@ -107,3 +108,22 @@ def test_own_keys_get_their_share_of_the_machine(L, B, H, Hkv, d):
 def test_long_own_keys_behind_a_short_prefix_take_most_of_the_machine(L, P):
     """64 sequences of 16,384 own keys hold more than 99% of the bytes."""
     assert _shared_plan(L, 64, 32, 8, P, 16384, 128)["own_ctas"] >= SMS // 2
+
+
+@pytest.mark.parametrize("d,block,top_k", [(64, 64, 32), (128, 64, 16), (128, 64, 64), (256, 16, 64), (256, 64, 128)])
+def test_block_lists_do_not_wait_for_a_wave_of_a_few(L, d, block, top_k):
+    """More groups than places of one wave (two CTAs an SM): clusters only where
+    the groups fill five sevenths of the waves' places."""
+    out = (ctypes.c_int * 2)()
+    seen = set()
+    for groups in [*range(1, 1300), 5000, 65535]:
+        assert L.mattn_internal_list_plan(groups, 4, 1, top_k, block, d, out) == 0
+        cluster, warps = out
+        assert cluster in (0, 1, 2, 4, 8) and warps >= 1
+        seen.add(cluster)
+        places = -(-groups // (2 * SMS)) * 2 * SMS
+        if groups > 2 * SMS:
+            assert (cluster == 0) == (places * 5 > groups * 7), groups
+        elif groups > SMS:
+            assert cluster == 1
+    assert {0, 1} <= seen

@@ -373,3 +373,17 @@ def test_one_key_gives_its_value(d):
         none = k.new_zeros((40, 1, 0, d))
         o = mattn.decode_shared(_randn(g, 40, 8, d), k[None], v[None], none, none)[0].double()
         assert bool(((o - v[0].double()).abs() <= 2 * 2.0 ** -8 * v[0].double().abs()).all())
+
+
+# ------------------------------------------------------------------ block lists of a few more groups than a wave holds
+@pytest.mark.parametrize("d,block,B", [(64, 32, 39), (128, 16, 40), (256, 16, 39), (128, 16, 80)])
+def test_blocks_of_more_groups_than_a_wave(d, block, B):
+    """Long lists of 312 to 640 groups, read in equal shares: entries unused, repeated
+    and past the end; sequences without a key."""
+    Hkv, L = 8, 70 * block
+    rng = torch.Generator().manual_seed(d + B)
+    ids = torch.randint(-5, 72, (B, Hkv, 64), generator=rng)
+    ids[1], ids[2, 3] = -1, 0
+    lens = torch.randint(0, L + 9, (B,), generator=rng)
+    lens[0], lens[3] = L, 0
+    ops.blocks_case(B, 2 * Hkv, Hkv, d, L, block, ids.tolist(), lens.tolist(), sink=bool(B % 2), seed=d)
