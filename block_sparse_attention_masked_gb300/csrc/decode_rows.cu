@@ -367,13 +367,14 @@ cudaError_t launch_merge_sl(const MergeParams& p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_merge_d(const MergeParams& p, cudaStream_t stream) {
-  // Warps of a row: four while they fill the SMs once, or three times where a row
-  // has the states for them (2,048 rows of 17: 50.9 us with two a row, 48.5 with
-  // four; 8,192 rows of 5: 45.5 with one, 55.8 with two).
+  // Warps of a row: four while they fill the SMs once, or twice where a row has the
+  // states for them (shared prefix of 32K, 512 own keys, 8 key/value heads of 128, in us with
+  // four, two and one: 1,536 rows 43.5, 47.3, 46.9; 2,048 54.4, 57.5, 56.7; 4,096 83.2,
+  // 84.4, 80.1; 8,192 166.9, 168.4, 158.7).
   constexpr int SL = D < 128 ? D : 128;
   const int64_t warps = (int64_t)p.B * p.H * (D / SL), most = kPlanSms * 36;
   if (p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, stream);
-  if (warps * 4 <= (p.states >= 8 ? 3 * most : most)) return launch_merge_sl<D, SL, 4>(p, stream);
+  if (warps * 4 <= (p.states >= 8 ? 2 * most : most)) return launch_merge_sl<D, SL, 4>(p, stream);
   if (warps * 2 <= most) return launch_merge_sl<D, SL, 2>(p, stream);
   return launch_merge_sl<D, SL, 1>(p, stream);
 }
