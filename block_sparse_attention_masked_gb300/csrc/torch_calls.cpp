@@ -15,9 +15,11 @@
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <exception>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -81,7 +83,14 @@ struct Args {
     if (v != (int)v) throw Bad(std::string(name) + " is out of range");
     return (int)v;
   }
-  bool truth() { return PyObject_IsTrue(next()) == 1; }
+  bool truth(const char* name) {
+    const int v = PyObject_IsTrue(next());
+    if (v < 0) {
+      PyErr_Clear();
+      throw Bad(std::string(name) + " must be true or false");
+    }
+    return v == 1;
+  }
   float scale() {  // None: 0, the default
     PyObject* o = next();
     if (o == Py_None) return 0.f;
@@ -293,7 +302,7 @@ PyObject* decode_shared(Args a) {
   const at::Tensor* sink = a.optional("sink");
   const float scale = a.scale();
   const at::Tensor *out = a.optional("out"), *lse = a.optional("lse");
-  const bool want = a.truth();
+  const bool want = a.truth("want_lse");
   const at::Tensor* ws = a.optional("workspace");
   const Decode s = decode_sizes(q, k, lens, sink);
   need(kp.dim() == 3 && kp.size(0) == s.H_kv && kp.size(2) == s.d && vp.sizes() == kp.sizes() && v.sizes() == k.sizes(),
@@ -374,7 +383,7 @@ PyObject* decode_blocks(Args a) {
   const at::Tensor *lens = a.optional("seq_lens"), *sink = a.optional("sink");
   const float scale = a.scale();
   const at::Tensor *out = a.optional("out"), *lse = a.optional("lse");
-  const bool want = a.truth();
+  const bool want = a.truth("want_lse");
   const at::Tensor* ws = a.optional("workspace");
   const Decode s = decode_sizes(q, k, lens, sink);
   need(v.sizes() == k.sizes() && ids.dim() == 3 && ids.size(0) == s.B && ids.size(1) == s.H_kv,
@@ -401,10 +410,8 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const Refused& r) {
     return PyLong_FromLong(r.rc);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown exception");
+  } catch (...) {  // torch's own, as torch raises them (OutOfMemoryError among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

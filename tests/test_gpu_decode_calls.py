@@ -193,6 +193,39 @@ def test_first_call_of_a_process_under_capture(which):
     assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
 
 
+# ------------------------------------------------------------------ errors of calls that allocate
+def test_out_of_memory_is_torchs_own_error():
+    """Outputs and workspaces that torch's allocator has no room for raise its
+    OutOfMemoryError, and the next call runs."""
+    g = _gen(6)
+    cache, q = _randn(g, 8, 8, 16384, 128), _randn(g, 8, 8, 128)
+    want = mattn.block_means(cache[:, :, :64].contiguous(), 16)
+    small = cache[:, :, :64].contiguous()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (4 << 20)) / total)
+    try:
+        hold = []
+        with pytest.raises(torch.OutOfMemoryError):
+            for _ in range(64):
+                hold.append(mattn.block_means(cache, 16))
+        with pytest.raises(torch.OutOfMemoryError):
+            for _ in range(100000):
+                hold.append(mattn.decode_shared(q, cache[0], cache[0], cache, cache))
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(mattn.block_means(small, 16), want)
+
+
+def test_want_lse_must_be_a_truth_value():
+    g = _gen(7)
+    q, c = _randn(g, 1, 2, 64), _randn(g, 1, 2, 16, 64)
+    with pytest.raises(ValueError):
+        mattn.decode_shared(q, c[0], c[0], c, c, want_lse=torch.ones(2, device="cuda"))
+    assert mattn.decode_shared(q, c[0], c[0], c, c, want_lse=False)[1] is None
+
+
 # ------------------------------------------------------------------ angles
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("sign", [1, -1])
@@ -387,3 +420,19 @@ def test_blocks_of_more_groups_than_a_wave(d, block, B):
     lens = torch.randint(0, L + 9, (B,), generator=rng)
     lens[0], lens[3] = L, 0
     ops.blocks_case(B, 2 * Hkv, Hkv, d, L, block, ids.tolist(), lens.tolist(), sink=bool(B % 2), seed=d)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_select_products_below_the_least_normal_number(d):
+    """Scores that are sums of many products below 2^-126 against one product of
+    nearly their sum: the larger sum is chosen, however small."""
+    n = 40
+    q = torch.full((1, 2, d), 2.0 ** -70, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 2.0 ** -60
+    means = torch.zeros((1, 1, n, d), dtype=torch.bfloat16, device="cuda")
+    means[0, 0, 7, 1:] = 1.9921875 * 2.0 ** -57  # d - 1 products of almost 2^-126
+    for share in (0.96875, 1.0078125):  # of their sum, as one product
+        means[0, 0, 20] = 0
+        means[0, 0, 20, 0] = share * float((means[0, 0, 7].double() @ q[0, 0].double())) / 2.0 ** -60
+        for top_k in (1, 2, 5):
+            ops.select_case(q, means, 16, top_k, [n * 16], first=0, recent=0)
