@@ -464,6 +464,10 @@ cudaError_t launch_nt(const SharedParams& p, cudaStream_t stream) {
   constexpr size_t prefix = Geo::kPrefix + sizeof(ShBar), own = NT ? Geo::kRows : 0;
   constexpr size_t smem = 1024 + (prefix > own ? prefix : own);
   static_assert(smem <= 227 * 1024, "shared memory");
+  // A CTA takes all of an SM's tensor memory before it waits for the previous grid.
+  // If a second one could lie beside it, a CTA of that grid might find the tensor memory
+  // taken by one that waits for it, and neither would end: no SM holds two.
+  static_assert(2 * (smem + 1024) > 228 * 1024, "one CTA per SM, by its shared memory");
   auto kern = decode_shared_kernel<D, SUB, NT, TWO>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
