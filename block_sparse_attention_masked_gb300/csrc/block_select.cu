@@ -153,13 +153,6 @@ constexpr int kBins = 1 << kDigit;
 constexpr int kSmallBand = 256;  // candidates ranked in shared memory; more go through the digits again
 constexpr float kScoreErr = 3.0517578125e-05f;  // 2^-15 (see above)
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // 32 bytes of a mean's row (a whole 128-byte line by four lanes).
 __device__ __forceinline__ void ld32(const uint4* p, uint4& a, uint4& b) {
   asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -316,8 +309,8 @@ __device__ __forceinline__ void score_blocks(const DecodeSelectParams& p, SelSha
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 q = sh->q[nt][i][lane];
-        mma_bf16(acc[nt][0], x[i].x, y[i].x, x[i].y, y[i].y, q.x, q.y);
-        mma_bf16(acc[nt][1], x[i].z, y[i].z, x[i].w, y[i].w, q.z, q.w);
+        ptx::mma16816(acc[nt][0], {x[i].x, y[i].x, x[i].y, y[i].y}, q.x, q.y);
+        ptx::mma16816(acc[nt][1], {x[i].z, y[i].z, x[i].w, y[i].w}, q.z, q.w);
       }
       sx = sq8(x[i], sx);
       sy = sq8(y[i], sy);

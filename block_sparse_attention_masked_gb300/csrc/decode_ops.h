@@ -90,7 +90,7 @@ struct RopeParams {
   const float* inv_freq;    // [rot]
   const float* weight[2];   // [d] norm weights of q and k, or null: no norm
   int B, H, H_kv, N, L, d;
-  int axes, axis_end[3];    // pairs [axis_end[a - 1], axis_end[a]) turn with axis a
+  int axis_end[3];          // pairs [axis_end[a - 1], axis_end[a]) turn with axis a
   int rot;                  // rotated pairs
   int interleaved;          // pairs (2p, 2p + 1) instead of (p, p + rot)
   bool wide;                // fp32: every row starts on a 32-byte boundary

@@ -243,7 +243,6 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
   p.weight[0] = desc->q_weight;
   p.weight[1] = desc->k_weight;
   p.B = B; p.H = H; p.H_kv = H_kv; p.N = N; p.L = L; p.d = d;
-  p.axes = desc->n_axes;
   p.rot = (int)rot;
   p.interleaved = desc->interleaved ? 1 : 0;
   p.eps = desc->eps;

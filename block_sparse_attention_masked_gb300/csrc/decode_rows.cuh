@@ -77,14 +77,6 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// c += a b, 16 x 8 x 16, bf16 inputs and fp32 sums.
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ int cached_keys(const DecodeRowsParams& p, int b) {
   const int len = p.seq_lens ? __ldg(p.seq_lens + b) : p.L;
   return len < 0 ? 0 : (len > p.L ? p.L : len);
@@ -164,7 +156,7 @@ struct State {
         uint32_t a[4];
         ldsm4(a, (ks ^ ((2 * i & 7) << 4)) + (i >> 2) * S::kChunk + mt * 2048);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i & 3], a, qf[nt][i][0], qf[nt][i][1]);
+        for (int nt = 0; nt < NT; ++nt) ptx::mma16816(acc[nt][i & 3], a, qf[nt][i][0], qf[nt][i][1]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -266,9 +258,9 @@ struct State {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma16816(o[nt][i0 + i], a[i], pf[nt][mt][0], pf[nt][mt][1]);
+          for (int i = 0; i < 4; ++i) ptx::mma16816(o[nt][i0 + i], a[i], pf[nt][mt][0], pf[nt][mt][1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma16816(o[nt][i0 + i], a[i], pg[nt][mt][0], pg[nt][mt][1]);
+          for (int i = 0; i < 4; ++i) ptx::mma16816(o[nt][i0 + i], a[i], pg[nt][mt][0], pg[nt][mt][1]);
         }
       }
     }
