@@ -513,7 +513,9 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, seq_lens=None, prefix
     q: CUDA bf16 [B, H, d]; k_prefix, v_prefix: [H_kv, P, d], of which the
     first ``prefix_len`` (None = all) are read, once for the whole batch;
     k_cache, v_cache: [B, H_kv, L, d] (L may be 0); seq_lens: CUDA int32 [B]
-    own keys of each sequence (None = L); sink: fp32 [H] or None.
+    own keys of each sequence (None = L); sink: fp32 [H] or None.  Softmax
+    weights keep 16 bits, the prefix's in batches of more than
+    128 // (H // H_kv) sequences the 8 of bf16, as in ``attention``.
     Returns (o [B, H, d], lse [B, H] fp32 or None)."""
     if stream is not None:
         return _on_stream(stream, decode_shared, q, k_prefix, v_prefix, k_cache, v_cache, seq_lens, prefix_len, sink, scale,

@@ -39,7 +39,7 @@
 // selection's stages are short and end in a sum over the threads, so that its
 // time is what each warp issues once: eight of the sixteen warps go on to it.
 // (128 groups of 2,048 blocks of 128, 50 MB: 21.2 us, the means read after 6 to
-// 15, as the memory serves the SMs unevenly.  The scores as a grid of small CTAs
+// 15: of the 256 CTAs 48 have an SM to themselves and the others share one in pairs.  The scores as a grid of small CTAs
 // before the selection: 23.3.  The scores straight to the first CTA's shared memory:
 // 21.5.  Prefetching a warp's later steps to L2: 1.2 us later.)
 #include <cuda_bf16.h>

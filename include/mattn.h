@@ -398,7 +398,8 @@ typedef struct {
   int32_t interleaved;       /* 0: pair p is (x[p], x[p + R]); 1: (x[2p], x[2p + 1])           */
   float eps;                 /* of the norm; finite, >= 0                                      */
   const float* inv_freq;     /* DEVICE fp32 [R], finite: pair p turns by position * inv_freq[p] */
-                             /* radians, exact in the position (any int32)                     */
+                             /* radians (any int32), taken modulo a turn in 64 bits: 2^-52 of  */
+                             /* the whole angle off at most                                    */
   const float* q_weight;     /* DEVICE fp32 [d] norm weights, NULL: no norm of the queries     */
   const float* k_weight;     /* DEVICE fp32 [d], NULL: no norm of the keys                     */
   int64_t token_stride[3];   /* of q, k, v, in elements: head h of token n of sequence b is at  */
@@ -448,6 +449,10 @@ int mattn_qk_rope(const void* q, const void* k, const void* v, void* q_out, void
  *   at most 2^31 - 1 tiles of own keys (of 32 keys at d = 64, else 16) in all.
  *   q, o and the key and value buffers 16-byte aligned.
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).
+ * Softmax weights meet the values as two bf16 parts, 2^-16 of a weight off at
+ * most; in batches of more than floor(128 / (H / H_kv)) sequences the prefix's
+ * weights as one, rounded to bf16 as in mattn_fwd.  Sums, statistics and
+ * states are fp32.
  */
 int mattn_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
                         void* o, float* lse, const int32_t* seq_lens, int B, int H, int H_kv, int P, int P_cap, int L,
