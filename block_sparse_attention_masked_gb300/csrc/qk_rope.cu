@@ -195,7 +195,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps, F32 ? 7 : 8) qk_rope_kernel(c
   const int start = live && p.starts ? p.starts[b] : 0;
   for (int i = threadIdx.x; i < p.rot; i += blockDim.x) {
     const double t = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    turn[i] = __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+    // (of a negative frequency the fraction's negative: 1 less it would round to 2^-54)
+    const unsigned long long f = __double2ull_rz((fabs(t) - floor(fabs(t))) * 18446744073709551616.0);
+    turn[i] = t < 0.0 ? 0ull - f : f;
   }
 #pragma unroll
   for (int t = 0; t < 2; ++t)

@@ -399,7 +399,7 @@ typedef struct {
   float eps;                 /* of the norm; finite, >= 0                                      */
   const float* inv_freq;     /* DEVICE fp32 [R], finite: pair p turns by position * inv_freq[p] */
                              /* radians (any int32), taken modulo a turn in 64 bits: 2^-52 of  */
-                             /* the whole angle off at most                                    */
+                             /* the whole angle and 2^-30 off at most                          */
   const float* q_weight;     /* DEVICE fp32 [d] norm weights, NULL: no norm of the queries     */
   const float* k_weight;     /* DEVICE fp32 [d], NULL: no norm of the keys                     */
   int64_t token_stride[3];   /* of q, k, v, in elements: head h of token n of sequence b is at  */

@@ -250,6 +250,25 @@ def test_rope_angles_next_to_quarter_turns(inter, sign):
         assert bool(((value - ref).abs() <= bound).all()), float(((value - ref).abs() - bound).max())
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rope_angles_of_small_frequencies_at_far_positions(sign):
+    """Frequencies of either sign down to 10^-9 at positions of any size: within four
+    half steps of each value, 2^-51 of the whole angle and 2^-30 (the fraction's last bit, 2^-64 of
+    a turn, at 2^31 positions is 2^-30.3)."""
+    n, R = 4000, 32
+    f = sign * _freq(R, base=1e9)
+    x = torch.zeros((1, n, 1, 2 * R), device="cuda")
+    x[..., :R] = 1.0
+    pos = torch.randint(-(1 << 31), 1 << 31, (n,), generator=_gen(9), device="cuda", dtype=torch.int64).to(torch.int32)
+    pos[:4] = _i32([(1 << 31) - 1, -(1 << 31), 0, 1])
+    q, _, _ = mattn.qk_rope(x, x, None, mattn.RopePlan(f), positions=pos.view(1, 1, n))
+    got = q[0, 0].double()
+    t = pos.double()[:, None] * f.double()
+    for value, ref in ((got[:, :R], t.cos()), (got[:, R:], t.sin())):
+        bound = 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -51 * t.abs() + 2.0 ** -30
+        assert bool(((value - ref).abs() <= bound).all()), float(((value - ref).abs() - bound).max())
+
+
 # ------------------------------------------------------------------ rows off the widest alignment
 def _off(t, by, row_pad=0):
     """A copy of t, `by` elements off the start of its allocation, tokens row_pad elements further apart."""
