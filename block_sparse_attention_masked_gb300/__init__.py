@@ -107,6 +107,7 @@ EXPORTS = (
     "mattn_fwd", "mattn_fwd_gqa", "mattn_fwd_host", "mattn_fwd_noalloc", "mattn_decode", "mattn_rr_select",
     "mattn_received", "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
     "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks", "mattn_decode_blocks_workspace",
+    "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged", "mattn_decode_paged_workspace",
     "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles", "mattn_plan_tiles_device",
     "mattn_device_status", "mattn_debug_checks", "mattn_set_wait_timeout_ns", "mattn_status_string",
     "mattn_last_error", "mattn_version",
@@ -160,6 +161,11 @@ def lib() -> ctypes.CDLL:
     L.mattn_decode_select_workspace.argtypes = [i32] * 5 + [szp]
     L.mattn_decode_blocks.argtypes = [vp] * 7 + [i32] * 8 + [vp, f32, vp, sz, vp]
     L.mattn_decode_blocks_workspace.argtypes = [i32] * 6 + [szp]
+    i64p, cp = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(PagedCache)
+    L.mattn_cache_write.argtypes = [vp, vp, i64p, i64p, cp, vp, vp] + [i32] * 5 + [vp]
+    L.mattn_cache_read.argtypes = [vp, vp, i64p, i64p, cp, vp, vp] + [i32] * 5 + [vp]
+    L.mattn_decode_paged.argtypes = [vp, cp, vp, vp, vp] + [i32] * 7 + [vp, f32, vp, sz, vp]
+    L.mattn_decode_paged_workspace.argtypes = [i32] * 7 + [szp]
     L.mattn_count_pairs.argtypes = [dp, i32, i32, i32, u64p]
     L.mattn_plan_schedule.argtypes = [dp, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_uint32)]
     L.mattn_plan_tiles.argtypes = [dp, i32, i32, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
@@ -175,7 +181,8 @@ def lib() -> ctypes.CDLL:
     for name in ("mattn_fwd", "mattn_fwd_gqa", "mattn_fwd_host", "mattn_fwd_noalloc", "mattn_decode", "mattn_rr_select", "mattn_received",
                  "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
                  "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
-                 "mattn_decode_blocks_workspace",
+                 "mattn_decode_blocks_workspace", "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged",
+                 "mattn_decode_paged_workspace",
                  "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles",
                  "mattn_plan_tiles_device", "mattn_device_status", "mattn_debug_checks",
                  "mattn_set_wait_timeout_ns", "mattn_version"):
@@ -204,6 +211,16 @@ def pack_block_bits(block: np.ndarray) -> np.ndarray:
     padded[:, :, :nb] = block
     by = np.packbits(padded.reshape(hb, nb, wpr, 64), axis=-1, bitorder="little")  # [hb, nb, wpr, 8]
     return by.view("<u8").reshape(hb, nb, wpr).copy()
+
+
+class PagedCache(ctypes.Structure):
+    """mattn_paged_cache"""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exponents", ctypes.c_void_p),
+                ("v_exponents", ctypes.c_void_p)] + \
+               [(f"{what}_stride", ctypes.c_int64 * 2) for what in ("page", "head", "row", "exp_page", "exp_head", "exp_row")] + \
+               [("page_table", ctypes.c_void_p), ("table_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class PreparedMask:
@@ -381,7 +398,8 @@ def decode(q, k_cache, v_cache, mask: PreparedMask, seq_lens=None, out=None, lse
 # of a few microseconds, and the checks alone take as long from Python).
 _CALLS = ("mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
           "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
-          "mattn_decode_blocks_workspace")
+          "mattn_decode_blocks_workspace", "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged",
+          "mattn_decode_paged_workspace")
 _calls = None
 _calls_lib = None
 
@@ -575,6 +593,71 @@ def decode_blocks(q, k_cache, v_cache, block_ids, block: int, seq_lens=None, sin
                           workspace)
     return _result(_torch_calls().decode_blocks(q, k_cache, v_cache, block_ids, block, seq_lens, sink, scale, out, lse,
                                                 want_lse, workspace))
+
+
+def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens=None, starts=None, k_exponents=None, v_exponents=None,
+                stream=None):
+    """Rows of packed sequences into a paged cache (``mattn_cache_write``).
+
+    k, v: CUDA bf16 [T, H_kv, d], any strides over T and H_kv; k_pages,
+    v_pages: [n_pages, H_kv, page, d] bf16 or float8_e4m3fn, any strides over
+    the first three; page_table: int32 [B, table_pages]; cu_seqlens: int32
+    [B + 1] or None (T = B: one token for each sequence); starts: int32 [B]
+    position of each sequence's first row or None (0).  Position j of sequence
+    b is row j % page of page page_table[b, j // page].  e4m3 pages have
+    k_exponents, v_exponents: uint8 [n_pages, H_kv, page], written with the
+    rows: a row's values are code * 2 ** (e - 127), e the least that leaves
+    none above 448 (255: a row with an infinite or NaN value, NaN throughout).
+    Rows of no sequence and positions without a page are left out.
+    Returns (k_pages, v_pages)."""
+    if stream is not None:
+        return _on_stream(stream, cache_write, k, v, k_pages, v_pages, page_table, cu_seqlens, starts, k_exponents,
+                          v_exponents)
+    return _result(_torch_calls().cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, starts, k_exponents,
+                                              v_exponents))
+
+
+def cache_read(k_pages, v_pages, page_table, cu_seqlens, total=None, starts=None, k_exponents=None, v_exponents=None,
+               k_out=None, v_out=None, stream=None):
+    """Rows of a paged cache back as packed bf16 rows (``mattn_cache_read``):
+    rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the outputs get positions
+    starts[b], starts[b] + 1, .. of sequence b.
+
+    The cache as for ``cache_write``; k_out, v_out: [total, H_kv, d] bf16, any
+    strides over the first two.  Positions without a page give zeros; rows of
+    no sequence are left as they are (zeros in an output that the call makes,
+    for which ``total`` is needed).  Returns (k_out, v_out)."""
+    if stream is not None:
+        return _on_stream(stream, cache_read, k_pages, v_pages, page_table, cu_seqlens, total, starts, k_exponents,
+                          v_exponents, k_out, v_out)
+    return _result(_torch_calls().cache_read(k_pages, v_pages, page_table, cu_seqlens, total, starts, k_exponents,
+                                             v_exponents, k_out, v_out))
+
+
+def decode_paged_workspace(B: int, H: int, H_kv: int, table_pages: int, page: int, d: int, e4m3: bool = False,
+                           device="cuda"):
+    """A workspace for ``decode_paged`` calls of these sizes that do not overlap."""
+    return _workspace(lib().mattn_decode_paged_workspace, device, B, H, H_kv, table_pages, page, d, 2 if e4m3 else 0)
+
+
+def decode_paged(q, k_pages, v_pages, page_table, seq_lens=None, k_exponents=None, v_exponents=None, window=None,
+                 sink_tokens: int = 0, sink=None, scale=None, out=None, lse=None, want_lse: bool = True, workspace=None,
+                 stream=None):
+    """Decode attention over a paged cache (``mattn_decode_paged``): one query per
+    sequence against its cached keys.
+
+    q: CUDA bf16 [B, H, d]; the cache as for ``cache_write``; seq_lens: int32
+    [B] or None (the whole table); window: the last ``window`` keys and the
+    first ``sink_tokens`` alone, or None; sink: fp32 [H] or None.
+    Returns (o [B, H, d], lse [B, H] fp32 or None)."""
+    if window is not None and int(window) < 1:
+        raise ValueError("window must be >= 1 (None: every key)")
+    if stream is not None:
+        return _on_stream(stream, decode_paged, q, k_pages, v_pages, page_table, seq_lens, k_exponents, v_exponents,
+                          window, sink_tokens, sink, scale, out, lse, want_lse, workspace)
+    return _result(_torch_calls().decode_paged(q, k_pages, v_pages, page_table, seq_lens, k_exponents, v_exponents,
+                                               0 if window is None else window, sink_tokens, sink, scale, out, lse,
+                                               want_lse, workspace))
 
 
 def attention_noalloc(q, k, v, mask: PreparedMask, out, lse=None, stream=None, check_wait: bool = True):

@@ -192,6 +192,26 @@ inline ListPieces list_pieces(int start, int tiles, int per, int warps) {
   return {(int)first, (int)(last - first) + 1};
 }
 
+// The keys of one sequence that its query sees, in tiles of 1 << shift keys: those of
+// [0, first) and of [w0, len), w0 = len - window (window 0: every key).  The list is
+// the first `head` tiles, then those from tile t0 on.
+struct KeySpan {
+  int len, w0, head, t0, tiles;
+};
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline KeySpan key_span(int len, int window, int first, int shift) {
+  KeySpan s;
+  s.len = len;
+  s.w0 = window > 0 && len > window ? len - window : 0;
+  s.t0 = s.w0 >> shift;
+  const int sink = (first + (1 << shift) - 1) >> shift;
+  s.head = sink < s.t0 ? sink : s.t0;
+  s.tiles = s.head + (int)(((uint32_t)len + (1u << shift) - 1) >> shift) - s.t0;
+  return s;
+}
+
 // One merge for all: row (b, h)'s states of the prefix and of its own list,
 // with the sink logit, into o and the log-sum-exp.
 struct MergeParams {
@@ -203,6 +223,8 @@ struct MergeParams {
   int warps;                 // row workers of the own lists
   int states;                // of a row, about
   int L, list_tiles;
+  int tile_shift;            // 1 << tile_shift keys a tile of the own lists
+  int window, first;         // KeySpan's
   const float* sink;
   void* o;
   float* lse;

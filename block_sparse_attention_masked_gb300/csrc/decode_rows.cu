@@ -291,7 +291,7 @@ __device__ __forceinline__ void add_states(Running& r, const float* ml, const fl
   }
 }
 
-template <int D, int SL, int WPR, int TK>
+template <int D, int SL, int WPR>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int LPS = SL / 4, SPW = 32 / LPS, U = WPR * SPW;
   static_assert(SL <= 128, "a warp's lanes hold four dims each");
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     if (!tiles) {
       int len = p.seq_lens ? p.seq_lens[b] : p.L;
       len = len < 0 ? 0 : (len > p.L ? p.L : len);
-      tiles = (len + TK - 1) / TK;
+      tiles = key_span(len, p.window, p.first, p.tile_shift).tiles;
     }
   }
   const float b2 = p.sink ? p.sink[h] * kLog2eR : -INFINITY;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
 template <int D, int SL, int WPR>
 cudaError_t launch_merge_sl(const MergeParams& p, cudaStream_t stream) {
   const int rows = p.B * p.H;
-  return launch_chained(decode_merge_kernel<D, SL, WPR, decode_rows_tile(D)>,
+  return launch_chained(decode_merge_kernel<D, SL, WPR>,
                         (unsigned)((rows + 4 / WPR - 1) / (4 / WPR)), D / SL, 128, 0, 1, p, stream);
 }
 

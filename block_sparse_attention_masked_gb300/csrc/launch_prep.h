@@ -63,5 +63,10 @@ int make_box_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_
 // columns (as 64 16-bit columns: a copy does not look at the type), 128-byte
 // swizzle.
 int make_state_map(CUtensorMap* map, const void* base, int d, int64_t splits, int64_t rows, int64_t heads);
+// View of pages [n_pages][heads][rows][d] of 16-bit (bf16) or 8-bit elements with the
+// given strides (in elements): boxes of 16 rows x 128 bytes, or of a whole row of 64
+// bytes, swizzled by their row's bytes.
+int make_pages_map(CUtensorMap* map, const void* base, bool e4m3, int d, int64_t rows, int64_t heads, int64_t n_pages,
+                   int64_t row_stride, int64_t head_stride, int64_t page_stride);
 
 }  // namespace mattn

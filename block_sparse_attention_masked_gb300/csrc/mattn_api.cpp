@@ -654,9 +654,10 @@ int get_encoder() {
 }
 
 int encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-           const cuuint32_t* box, CUtensorMapSwizzle sw) {
+           const cuuint32_t* box, CUtensorMapSwizzle sw,
+           CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = g_encode(tm, type, rank, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -1031,6 +1032,19 @@ int make_state_map(CUtensorMap* map, const void* base, int d, int64_t splits, in
   cuuint64_t strides[3] = {(cuuint64_t)d * 4, row, row * (cuuint64_t)rows};
   cuuint32_t box[4] = {64, 1, 32, 1};
   return encode(map, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int make_pages_map(CUtensorMap* map, const void* base, bool e4m3, int d, int64_t rows, int64_t heads, int64_t n_pages,
+                   int64_t row_stride, int64_t head_stride, int64_t page_stride) {
+  const int rc = get_encoder();
+  if (rc) return rc;
+  const cuuint64_t es = e4m3 ? 1 : 2;
+  const cuuint32_t cols = e4m3 ? (d < 128 ? d : 128) : 64;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)n_pages};
+  cuuint64_t strides[3] = {row_stride * es, head_stride * es, page_stride * es};
+  cuuint32_t box[4] = {cols, 16, 1, 1};
+  return encode(map, base, 4, dims, strides, box, cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 int prepare_in_place_launch(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N,

@@ -1,0 +1,59 @@
+// Launch parameters and host-side plans of the operators around a paged cache:
+// rows written into it and read back (paged_cache.cu), decode attention over
+// it (decode_paged.cu) and attention over packed prompts (attention_packed.cu).
+// Their C entry points are in paged_ops_api.cpp.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "decode_ops.h"
+
+namespace mattn {
+
+// ------------------------------------------------------------ paged_cache.cu
+struct CacheRowsParams {
+  void* rows[2];             // k and v rows: (t, h, c) at t * row_token + h * row_head + c (bf16)
+  int64_t row_token[2], row_head[2];
+  void* pages[2];            // (page, h, r, c) at page * page_stride + h * head_stride + r * row_stride + c
+  int64_t page_stride[2], head_stride[2], row_stride[2];  // in elements
+  uint8_t* exps[2];          // e4m3: (page, h, r) at ..
+  int64_t exp_page[2], exp_head[2], exp_row[2];
+  const int32_t* table;      // [B][table_pages]
+  const int32_t* cu;         // [B + 1], or null: token t is sequence t's
+  const int32_t* starts;     // [B] position of a sequence's first row, or null: 0
+  int B, T, H_kv, d;
+  int page, table_pages, n_pages;
+  int per_warp;              // groups of rows of a warp
+};
+cudaError_t launch_cache_write(const CacheRowsParams& p, bool e4m3, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheRowsParams& p, bool e4m3, cudaStream_t stream);
+
+// ------------------------------------------------------------ decode_paged.cu
+// Keys per tile: as the row workers' of decode_rows.cuh in bf16, 32 in eight bits
+// (8 KB of K and V, 16 KB at d = 256, 4 KB at 64).
+constexpr int paged_tile(int d, bool e4m3) { return e4m3 ? 32 : decode_rows_tile(d); }
+
+struct DecodePagedParams {
+  CUtensorMap tk, tv;        // [n_pages][H_kv][page][d] views, boxes of 16 keys x 128 bytes (or a row of 64)
+  const void* q;             // [B][H][d] bf16
+  const int32_t* table;      // [B][table_pages]
+  const int32_t* seq_lens;   // [B] or null: table_pages * page
+  const uint8_t* exps[2];    // e4m3
+  int64_t exp_page[2], exp_head[2], exp_row[2];
+  float* part_o;             // states and the lists' starts as DecodeRowsParams has them
+  float* part_ml;
+  int* group_start;
+  uint32_t* err;
+  unsigned long long timeout_ns;
+  int B, H, H_kv;
+  int page, table_pages, n_pages, L;  // L = table_pages * page
+  int window, first;         // keys [len - window, len) and [0, first); window 0: all
+  int ctas, warps;
+  float scale_log2;
+  int selftest;              // 1: every worker's first copies are left out, so that its wait runs out
+};
+cudaError_t launch_decode_paged(const DecodePagedParams& p, int d, bool e4m3, cudaStream_t stream);
+
+}  // namespace mattn

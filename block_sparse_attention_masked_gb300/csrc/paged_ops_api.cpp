@@ -1,0 +1,292 @@
+// C entry points of the operators around a paged cache (include/mattn.h): argument
+// checks, TMA views, workspace layout and launches.  Nothing here allocates device
+// memory but the device's error word on its first use (mattn_decode_paged,
+// mattn_attention_packed); mattn_cache_write and mattn_cache_read need none.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "kernel_params.h"
+#include "launch_prep.h"
+#include "mattn.h"
+#include "op_checks.h"
+#include "paged_ops.h"
+
+namespace mattn {
+namespace {
+
+// Test hook: the copies that the next launches leave out (DecodePagedParams).
+std::atomic<int> g_wait_selftest{0};
+
+bool cache_dtype(int t) { return t == MATTN_BF16 || t == MATTN_E4M3; }
+
+// Whether x[..] of three dimensions with these strides (in elements, rows of d last)
+// lies in rows that do not overlap: sorted by stride, each dimension steps over the
+// whole of those below it.
+bool rows_apart(const int64_t (&stride)[3], const int64_t (&size)[3], int64_t row) {
+  int o[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[o[j]] > stride[o[j + 1]]) {
+        const int x = o[j];
+        o[j] = o[j + 1];
+        o[j + 1] = x;
+      }
+  int64_t end = row;
+  for (int i = 0; i < 3; ++i) {
+    if (size[o[i]] == 1) continue;
+    if (stride[o[i]] < end) return false;
+    end += stride[o[i]] * (size[o[i]] - 1);
+  }
+  return true;
+}
+
+int check_cache(const char* what, const mattn_paged_cache* c, int B, int H_kv, int d) {
+  if (!c) return report_error(MATTN_ERR_INVALID_ARG, "%s: the cache is NULL", what);
+  if (B < 1 || H_kv < 1) return report_error(MATTN_ERR_INVALID_ARG, "%s: B and H_kv must be >= 1", what);
+  if (d != 64 && d != 128 && d != 256)
+    return report_error(MATTN_ERR_UNSUPPORTED, "%s: head dim %d (64, 128, 256)", what, d);
+  if (!cache_dtype(c->dtype)) return report_error(MATTN_ERR_UNSUPPORTED, "%s: a cache is bf16 or e4m3", what);
+  const bool e8 = c->dtype == MATTN_E4M3;
+  if (!c->k || !c->v || !c->page_table)
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: the pages and the page table must be non-NULL", what);
+  if (e8 ? !c->k_exponents || !c->v_exponents : c->k_exponents || c->v_exponents)
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: exponents come with e4m3 pages, and only with them", what);
+  if (c->page < 16 || c->page % 16)
+    return report_error(MATTN_ERR_UNSUPPORTED, "%s: page size %d is not a multiple of 16", what, c->page);
+  if (c->table_pages < 1 || c->n_pages < 1)
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: table_pages and n_pages must be >= 1", what);
+  if ((int64_t)c->table_pages * c->page > kMaxRows)
+    return report_error(MATTN_ERR_UNSUPPORTED, "%s: table_pages * page exceeds 2^30", what);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4))
+    return report_error(MATTN_ERR_UNSUPPORTED, "%s: pages must be 16-byte and the page table 4-byte aligned", what);
+  const int es = e8 ? 1 : 2;
+  const int64_t size[3] = {c->n_pages, H_kv, c->page};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t s[3] = {c->page_stride[i], c->head_stride[i], c->row_stride[i]};
+    const int64_t e[3] = {c->exp_page_stride[i], c->exp_head_stride[i], c->exp_row_stride[i]};
+    for (int j = 0; j < 3; ++j) {
+      if (s[j] <= 0 || (s[j] * es) % 16)
+        return report_error(MATTN_ERR_UNSUPPORTED, "%s: strides of the pages must be positive multiples of 16 bytes", what);
+      if (s[j] >= (int64_t(1) << 40) / es)
+        return report_error(MATTN_ERR_UNSUPPORTED, "%s: a stride of the pages exceeds 2^40 bytes", what);
+      if (e8 && e[j] <= 0) return report_error(MATTN_ERR_UNSUPPORTED, "%s: strides of the exponents must be positive", what);
+    }
+    if (!rows_apart(s, size, d) || (e8 && !rows_apart(e, size, 1)))
+      return report_error(MATTN_ERR_INVALID_ARG, "%s: rows of the cache overlap", what);
+  }
+  return MATTN_OK;
+}
+
+// Lowest and one past the highest byte of rows with these strides.
+Extent pages_extent(const mattn_paged_cache* c, int i, int H_kv, int d) {
+  const int es = c->dtype == MATTN_E4M3 ? 1 : 2;
+  Extent x;
+  x.lo = reinterpret_cast<uintptr_t>(i ? c->v : c->k);
+  x.hi = x.lo + ((uint64_t)(c->n_pages - 1) * c->page_stride[i] + (uint64_t)(H_kv - 1) * c->head_stride[i] +
+                 (uint64_t)(c->page - 1) * c->row_stride[i] + d) * es;
+  return x;
+}
+
+int fill_rows(const char* what, const void* k, const void* v, const int64_t* token_stride, const int64_t* head_stride,
+              const mattn_paged_cache* c, const int32_t* cu, const int32_t* starts, int B, int T, int H_kv, int d,
+              int dtype, bool reads, CacheRowsParams* p) {
+  int rc = check_cache(what, c, B, H_kv, d);
+  if (rc) return rc;
+  if (dtype != MATTN_BF16) return report_error(MATTN_ERR_UNSUPPORTED, "%s takes bf16 rows", what);
+  if (!k || !v || !token_stride || !head_stride)
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: k, v and their strides must be non-NULL", what);
+  if (T < 0) return report_error(MATTN_ERR_INVALID_ARG, "%s: T must be >= 0", what);
+  if (!cu && T != B) return report_error(MATTN_ERR_INVALID_ARG, "%s: without cu_seqlens there is one token for each sequence", what);
+  if ((int64_t)T * H_kv > INT32_MAX) return report_error(MATTN_ERR_UNSUPPORTED, "%s: T * H_kv exceeds 2^31 - 1", what);
+  if (!aligned(k, 16) || !aligned(v, 16)) return report_error(MATTN_ERR_UNSUPPORTED, "%s: k and v must be 16-byte aligned", what);
+  if (!aligned(cu, 4) || !aligned(starts, 4))
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: cu_seqlens and starts must be 4-byte aligned", what);
+  memset(p, 0, sizeof(*p));
+  const void* rows[2] = {k, v};
+  void* pages[2] = {c->k, c->v};
+  void* exps[2] = {c->k_exponents, c->v_exponents};
+  Extent at[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t ts = token_stride[i], hs = head_stride[i];
+    if (ts % 8 || hs % 8) return report_error(MATTN_ERR_UNSUPPORTED, "%s: rows must start on 16-byte boundaries", what);
+    if (ts < 0 || hs < 0) return report_error(MATTN_ERR_INVALID_ARG, "%s: strides must be >= 0", what);
+    const int64_t s[3] = {ts, hs, 0}, size[3] = {T, H_kv, 1};
+    if (reads && T > 0 && !rows_apart(s, size, d))
+      return report_error(MATTN_ERR_INVALID_ARG, "%s: rows of an output overlap", what);
+    at[i].lo = reinterpret_cast<uintptr_t>(rows[i]);
+    at[i].hi = at[i].lo + (T > 0 ? ((uint64_t)(T - 1) * ts + (uint64_t)(H_kv - 1) * hs + d) * 2 : 0);
+    p->rows[i] = const_cast<void*>(rows[i]);
+    p->row_token[i] = ts;
+    p->row_head[i] = hs;
+    p->pages[i] = pages[i];
+    p->page_stride[i] = c->page_stride[i];
+    p->head_stride[i] = c->head_stride[i];
+    p->row_stride[i] = c->row_stride[i];
+    p->exps[i] = static_cast<uint8_t*>(exps[i]);
+    p->exp_page[i] = c->exp_page_stride[i];
+    p->exp_head[i] = c->exp_head_stride[i];
+    p->exp_row[i] = c->exp_row_stride[i];
+  }
+  // rows are read and written in no order.  (Interleaved views, as k and v of one
+  // projection or of one pool, share an extent without sharing a byte: the two
+  // tensors of a side may; whole sides may not.)
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (at[i].meets(pages_extent(c, j, H_kv, d)))
+        return report_error(MATTN_ERR_INVALID_ARG, "%s: the rows overlap the cache", what);
+  if ((reads && rows[0] == rows[1]) || (!reads && (pages[0] == pages[1] || (exps[0] && exps[0] == exps[1]))))
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: k and v are written to one place", what);
+  p->table = c->page_table;
+  p->cu = cu;
+  p->starts = starts;
+  p->B = B; p->T = T; p->H_kv = H_kv; p->d = d;
+  p->page = c->page;
+  p->table_pages = c->table_pages;
+  p->n_pages = c->n_pages;
+  return check_device();
+}
+
+int paged_shift(int d, bool e8) { return paged_tile(d, e8) == 32 ? 5 : 4; }
+
+// The tiles of all lists at most, and the warps of a CTA that share them.
+int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dtype, int64_t* tiles) {
+  const int rc = check_heads("decode_paged", B, H, H_kv, d, MATTN_BF16);
+  if (rc) return rc;
+  if (!cache_dtype(dtype)) return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: a cache is bf16 or e4m3");
+  if (table_pages < 1 || page < 1)
+    return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: table_pages and page must be >= 1");
+  const int64_t L = (int64_t)table_pages * page;
+  if (L > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: table_pages * page exceeds 2^30");
+  const int tk = paged_tile(d, dtype == MATTN_E4M3);
+  *tiles = (int64_t)B * H_kv * ((L + tk - 1) / tk + 1);  // (a window's first tile and the first tokens' last one are parts)
+  if (*tiles > INT32_MAX) return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: more than 2^31 - 1 tiles of keys");
+  return MATTN_OK;
+}
+
+}  // namespace
+}  // namespace mattn
+
+using namespace mattn;
+
+extern "C" {
+
+int mattn_cache_write(const void* k, const void* v, const int64_t token_stride[2], const int64_t head_stride[2],
+                      const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,
+                      int H_kv, int d, int dtype, void* stream) {
+  CacheRowsParams p;
+  const int rc = fill_rows("cache_write", k, v, token_stride, head_stride, cache, cu_seqlens, starts, B, T, H_kv, d, dtype,
+                           false, &p);
+  if (rc || T == 0) return rc;
+  return launched(launch_cache_write(p, cache->dtype == MATTN_E4M3, static_cast<cudaStream_t>(stream)), "cache_write launch");
+}
+
+int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int64_t head_stride[2],
+                     const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,
+                     int H_kv, int d, int dtype, void* stream) {
+  CacheRowsParams p;
+  const int rc = fill_rows("cache_read", k, v, token_stride, head_stride, cache, cu_seqlens, starts, B, T, H_kv, d, dtype,
+                           true, &p);
+  if (rc || T == 0) return rc;
+  return launched(launch_cache_read(p, cache->dtype == MATTN_E4M3, static_cast<cudaStream_t>(stream)), "cache_read launch");
+}
+
+int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int page, int d, int cache_dtype,
+                                 size_t* bytes_out) {
+  if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: bytes_out is NULL");
+  int64_t tiles = 0;
+  const int rc = check_paged(B, H, H_kv, table_pages, page, d, cache_dtype, &tiles);
+  if (rc) return rc;
+  *bytes_out = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * decode_share_warps(tiles, d), d).all();
+  return MATTN_OK;
+}
+
+int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, float* lse, const int32_t* seq_lens,
+                       int B, int H, int H_kv, int d, int dtype, int window, int sink_tokens, const float* sink,
+                       float softmax_scale, void* workspace, size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  int rc = check_heads("decode_paged", B, H, H_kv, d, dtype);
+  if (rc) return rc;
+  if ((rc = check_cache("decode_paged", cache, B, H_kv, d))) return rc;
+  int64_t tiles = 0;
+  if ((rc = check_paged(B, H, H_kv, cache->table_pages, cache->page, d, cache->dtype, &tiles))) return rc;
+  if (!q || !o) return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: q and o must be non-NULL");
+  if (!aligned(q, 16) || !aligned(o, 16))
+    return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: q and o must be 16-byte aligned");
+  if (window < 0 || sink_tokens < 0 || (!window && sink_tokens))
+    return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: window and sink_tokens must be >= 0, sink_tokens 0 without a window");
+  if ((rc = check_small("decode_paged", lse, seq_lens, sink))) return rc;
+  if ((rc = check_scale("decode_paged", softmax_scale))) return rc;
+  const bool e8 = cache->dtype == MATTN_E4M3;
+  const int warps = decode_share_warps(tiles, d);
+  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * warps, d);
+  if ((rc = check_workspace("decode_paged", workspace, workspace_bytes, lay.all()))) return rc;
+  uint32_t* err = nullptr;
+  if ((rc = device_error_word(stream, &err))) return rc;
+  DecodePagedParams p;
+  memset(&p, 0, sizeof(p));
+  void* pages[2] = {cache->k, cache->v};
+  void* exps[2] = {cache->k_exponents, cache->v_exponents};
+  for (int i = 0; i < 2; ++i) {
+    if ((rc = make_pages_map(i ? &p.tv : &p.tk, pages[i], e8, d, cache->page, H_kv, cache->n_pages, cache->row_stride[i],
+                             cache->head_stride[i], cache->page_stride[i])))
+      return rc;
+    p.exps[i] = static_cast<const uint8_t*>(exps[i]);
+    p.exp_page[i] = cache->exp_page_stride[i];
+    p.exp_head[i] = cache->exp_head_stride[i];
+    p.exp_row[i] = cache->exp_row_stride[i];
+  }
+  p.q = q;
+  p.table = cache->page_table;
+  p.seq_lens = seq_lens;
+  DecodeRowsParams at;
+  place_rows(&at, lay, static_cast<char*>(workspace));
+  p.part_o = at.part_o;
+  p.part_ml = at.part_ml;
+  p.group_start = at.group_start;
+  p.err = err;
+  p.timeout_ns = device_wait_timeout_ns();
+  p.B = B; p.H = H; p.H_kv = H_kv;
+  p.page = cache->page;
+  p.table_pages = cache->table_pages;
+  p.n_pages = cache->n_pages;
+  p.L = cache->table_pages * cache->page;
+  p.window = window;
+  p.first = sink_tokens < p.L ? sink_tokens : p.L;
+  p.ctas = kPlanSms;
+  p.warps = warps;
+  p.selftest = g_wait_selftest.load();
+  p.scale_log2 = scale_log2(softmax_scale, d);
+  if ((rc = launched(launch_decode_paged(p, d, e8, stream), "paged launch"))) return rc;
+  MergeParams m;
+  memset(&m, 0, sizeof(m));
+  m.b_o = p.part_o;
+  m.b_ml = p.part_ml;
+  m.group_start = p.group_start;
+  m.warps = lay.warps;
+  m.seq_lens = seq_lens;
+  m.L = p.L;
+  m.tile_shift = paged_shift(d, e8);
+  m.window = p.window;
+  m.first = p.first;
+  m.sink = sink;
+  m.o = o;
+  m.lse = lse;
+  m.B = B; m.H = H; m.H_kv = H_kv;
+  m.states = 1 + (int)(lay.warps / ((int64_t)B * H_kv));
+  return launched(launch_decode_merge(m, d, stream), "merge launch");
+}
+
+// Test hook (not in the public header): the launches of decode_paged until the next
+// call leave out the row workers' first keys (1), so that the bounded waits and the
+// error word can be exercised without a hang; 0: nothing.
+int mattn_internal_paged_wait_selftest(int what) {
+  if (what < 0 || what > 1) return report_error(MATTN_ERR_INVALID_ARG, "what must be 0 or 1");
+  g_wait_selftest.store(what);
+  return MATTN_OK;
+}
+
+}  // extern "C"

@@ -1,4 +1,4 @@
-// Calls of the decode step's operators on torch tensors, for the Python
+// Calls of the operators of serving (a decode step's, a paged cache's) on torch tensors, for the Python
 // binding (__init__.py documents them): checks of the tensors, outputs and
 // workspaces where none are given, the device and the current stream, and the C
 // entry point, whose address the binding sets.  A decode step makes many such
@@ -37,6 +37,10 @@ struct Functions {
   decltype(&mattn_decode_select_workspace) decode_select_workspace;
   decltype(&mattn_decode_blocks) decode_blocks;
   decltype(&mattn_decode_blocks_workspace) decode_blocks_workspace;
+  decltype(&mattn_cache_write) cache_write;
+  decltype(&mattn_cache_read) cache_read;
+  decltype(&mattn_decode_paged) decode_paged;
+  decltype(&mattn_decode_paged_workspace) decode_paged_workspace;
 } g_fn = {};
 
 struct Bad : std::runtime_error {
@@ -401,6 +405,150 @@ PyObject* decode_blocks(Args a) {
   return o.result();
 }
 
+// The pages of a cache [n_pages, H_kv, page, d] and what belongs to them.
+struct Pages {
+  mattn_paged_cache c = {};
+  int B, H_kv, d;
+  Pages(const at::Tensor& like, const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, const at::Tensor* ke,
+        const at::Tensor* ve) {
+    need(k.dim() == 4 && v.sizes() == k.sizes(), "k_pages and v_pages must be [n_pages, H_kv, page, d]");
+    need(k.scalar_type() == v.scalar_type() && (k.scalar_type() == at::kBFloat16 || k.scalar_type() == at::kFloat8_e4m3fn),
+         "k_pages and v_pages must both be bf16 or float8_e4m3fn");
+    const bool e8 = k.scalar_type() == at::kFloat8_e4m3fn;
+    need(e8 ? ke && ve : !ke && !ve, "k_exponents and v_exponents come with e4m3 pages, and only with them");
+    need(table.dim() == 2, "page_table must be [B, table_pages]");
+    fits(&table, like, at::kInt, "page_table");
+    B = size32(table.size(0));
+    H_kv = size32(k.size(1));
+    d = size32(k.size(3));
+    c.n_pages = size32(k.size(0));
+    c.page = size32(k.size(2));
+    c.table_pages = size32(table.size(1));
+    c.dtype = e8 ? MATTN_E4M3 : MATTN_BF16;
+    c.page_table = static_cast<const int32_t*>(table.data_ptr());
+    const at::Tensor* x[2] = {&k, &v};
+    const at::Tensor* e[2] = {ke, ve};
+    for (int i = 0; i < 2; ++i) {
+      need(x[i]->device() == like.device(), "the pages must be on the inputs' device");
+      need(x[i]->stride(3) == 1, "a row of the pages must lie in one piece");
+      // (the stride of a dimension of one entry says nothing)
+      const int64_t dense = k.size(2) * k.size(3);
+      c.page_stride[i] = x[i]->size(0) > 1 ? x[i]->stride(0) : dense;
+      c.head_stride[i] = x[i]->size(1) > 1 ? x[i]->stride(1) : dense;
+      c.row_stride[i] = x[i]->stride(2);
+      if (!e8) continue;
+      need(e[i]->scalar_type() == at::kByte && e[i]->device() == like.device() &&
+               shape(*e[i], {k.size(0), k.size(1), k.size(2)}),
+           "k_exponents and v_exponents must be uint8 [n_pages, H_kv, page] on the inputs' device");
+      c.exp_page_stride[i] = e[i]->size(0) > 1 ? e[i]->stride(0) : 1;
+      c.exp_head_stride[i] = e[i]->size(1) > 1 ? e[i]->stride(1) : 1;
+      c.exp_row_stride[i] = e[i]->stride(2);
+    }
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.k_exponents = ke ? ke->data_ptr() : nullptr;
+    c.v_exponents = ve ? ve->data_ptr() : nullptr;
+  }
+};
+
+// Rows [T, H_kv, d] beside a cache, and the sequences they are of.
+struct PackedRows {
+  int64_t token[2], head[2];
+  int T;
+  PackedRows(const at::Tensor& k, const at::Tensor& v, const Pages& p, const at::Tensor* cu, const at::Tensor* starts) {
+    need(k.dim() == 3 && v.sizes() == k.sizes() && k.size(1) == p.H_kv && k.size(2) == p.d,
+         "k and v must be [T, H_kv, d] as the pages' rows");
+    const at::Tensor* x[2] = {&k, &v};
+    for (int i = 0; i < 2; ++i) {
+      need(x[i]->device() == k.device() && x[i]->scalar_type() == k.scalar_type(), "k and v must be of one type and device");
+      need(x[i]->stride(2) == 1, "a row must lie in one piece");
+      token[i] = x[i]->size(0) > 1 ? x[i]->stride(0) : 0;
+      head[i] = x[i]->size(1) > 1 ? x[i]->stride(1) : 0;
+    }
+    need((!cu || shape(*cu, {(int64_t)p.B + 1})) && (!starts || shape(*starts, {p.B})),
+         "cu_seqlens must be [B + 1] and starts [B]");
+    fits(cu, k, at::kInt, "cu_seqlens");
+    fits(starts, k, at::kInt, "starts");
+    T = size32(k.size(0));
+  }
+};
+
+PyObject* cache_write(Args a) {
+  const at::Tensor &k = a.tensor("k"), &v = a.tensor("v"), &kp = a.tensor("k_pages"), &vp = a.tensor("v_pages");
+  const at::Tensor& table = a.tensor("page_table");
+  const at::Tensor *cu = a.optional("cu_seqlens"), *starts = a.optional("starts");
+  const at::Tensor *ke = a.optional("k_exponents"), *ve = a.optional("v_exponents");
+  need(k.is_cuda(), "k must be a CUDA tensor [T, H_kv, d]");
+  const Pages p(k, kp, vp, table, ke, ve);
+  const PackedRows r(k, v, p, cu, starts);
+  const int code = type_code(k);
+  On on(k);
+  done(g_fn.cache_write(k.data_ptr(), v.data_ptr(), r.token, r.head, &p.c, ptr<int32_t>(cu), ptr<int32_t>(starts), p.B,
+                        r.T, p.H_kv, p.d, code, on.stream));
+  return pair(kp, &vp);
+}
+
+PyObject* cache_read(Args a) {
+  const at::Tensor &kp = a.tensor("k_pages"), &vp = a.tensor("v_pages"), &table = a.tensor("page_table");
+  const at::Tensor& cu = a.tensor("cu_seqlens");
+  PyObject* total = a.next();
+  const at::Tensor* starts = a.optional("starts");
+  const at::Tensor *ke = a.optional("k_exponents"), *ve = a.optional("v_exponents");
+  const at::Tensor *ko = a.optional("k_out"), *vo = a.optional("v_out");
+  need(kp.is_cuda(), "k_pages must be a CUDA tensor [n_pages, H_kv, page, d]");
+  const Pages p(kp, kp, vp, table, ke, ve);
+  int64_t T = 0;
+  if (total != Py_None) {
+    Args one{&total, 1};
+    T = one.small("total");
+    need(T >= 0, "total must be >= 0");
+    need((!ko || ko->size(0) == T) && (!vo || vo->size(0) == T), "k_out and v_out must have total rows");
+  } else {
+    need(ko || vo, "total is needed where no output is given");
+    T = ko ? (ko->dim() ? ko->size(0) : 0) : (vo->dim() ? vo->size(0) : 0);
+  }
+  On on(kp);
+  // (rows of no sequence, which the kernel leaves as they are: zeros)
+  auto made = [&]() { return at::zeros({T, p.H_kv, p.d}, kp.options().dtype(at::kBFloat16)); };
+  const at::Tensor k = ko ? *ko : made(), v = vo ? *vo : made();
+  need(k.device() == kp.device(), "k_out and v_out must be on the pages' device");
+  const PackedRows r(k, v, p, &cu, starts);
+  const int code = type_code(k);
+  done(g_fn.cache_read(k.data_ptr(), v.data_ptr(), r.token, r.head, &p.c, ptr<int32_t>(&cu), ptr<int32_t>(starts), p.B,
+                       r.T, p.H_kv, p.d, code, on.stream));
+  return pair(k, &v);
+}
+
+PyObject* decode_paged(Args a) {
+  const at::Tensor &q = a.tensor("q"), &kp = a.tensor("k_pages"), &vp = a.tensor("v_pages");
+  const at::Tensor& table = a.tensor("page_table");
+  const at::Tensor* lens = a.optional("seq_lens");
+  const at::Tensor *ke = a.optional("k_exponents"), *ve = a.optional("v_exponents");
+  const int window = a.small("window"), first = a.small("sink_tokens");
+  const at::Tensor* sink = a.optional("sink");
+  const float scale = a.scale();
+  const at::Tensor *out = a.optional("out"), *lse = a.optional("lse");
+  const bool want = a.truth("want_lse");
+  const at::Tensor* ws = a.optional("workspace");
+  need(q.is_cuda() && q.dim() == 3, "q must be a CUDA tensor [B, H, d]");
+  const Pages p(q, kp, vp, table, ke, ve);
+  need(q.size(0) == p.B && q.size(2) == p.d, "q must be [B, H, d], B that of page_table and d that of the pages");
+  const int H = size32(q.size(1));
+  need((!lens || shape(*lens, {p.B})) && (!sink || shape(*sink, {H})), "seq_lens must be [B] and sink [H]");
+  fits(&q, q, q.scalar_type(), "q");
+  fits(lens, q, at::kInt, "seq_lens");
+  fits(sink, q, at::kFloat, "sink");
+  const int code = type_code(q);
+  On on(q);
+  Outputs o(q, out, lse, want);
+  Workspace w(ws, q, [&](size_t* n) {
+    return g_fn.decode_paged_workspace(p.B, H, p.H_kv, p.c.table_pages, p.c.page, p.d, p.c.dtype, n);
+  });
+  done(g_fn.decode_paged(q.data_ptr(), &p.c, o.out.data_ptr(), o.lse_ptr(), ptr<int32_t>(lens), p.B, H, p.H_kv, p.d, code,
+                         window, first, ptr<float>(sink), scale, w.p, w.bytes, on.stream));
+  return o.result();
+}
+
 // No C++ exception leaves for Python.
 template <PyObject* (*F)(Args)>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -442,6 +590,9 @@ PyMethodDef g_methods[] = {
     {"block_means", FAST((call<block_means>))},
     {"decode_select", FAST((call<decode_select>))},
     {"decode_blocks", FAST((call<decode_blocks>))},
+    {"cache_write", FAST((call<cache_write>))},
+    {"cache_read", FAST((call<cache_read>))},
+    {"decode_paged", FAST((call<decode_paged>))},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

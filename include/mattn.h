@@ -88,7 +88,7 @@ typedef enum {
   MATTN_BLOCK_SPARSE = 4   /* B[floor(p/Bs)][floor(q/Bs)] and q <= p                */
 } mattn_kind;
 
-typedef enum { MATTN_BF16 = 0, MATTN_F32 = 1 } mattn_dtype;
+typedef enum { MATTN_BF16 = 0, MATTN_F32 = 1, MATTN_E4M3 = 2 /* pages of a cache alone */ } mattn_dtype;
 
 /* Per-head token order codes for mattn_mask_desc.head_order. */
 #define MATTN_ORDER_RASTER (-1)       /* identity: position p holds token p             */
@@ -514,6 +514,88 @@ int mattn_decode_blocks(const void* q, const void* k, const void* v, void* o, fl
                         int top_k, const float* sink, float softmax_scale, void* workspace, size_t workspace_bytes,
                         void* stream);
 int mattn_decode_blocks_workspace(int B, int H, int H_kv, int top_k, int block, int d, size_t* bytes_out);
+
+/*
+ * A key/value cache in pages of `page` rows, one row per token and key/value
+ * head.  Position j of sequence b lies in row j % page of page
+ * page_table[b][j / page]; a table entry outside 0..n_pages-1 is no page (its
+ * positions hold nothing).  Element (page, h, row, c) of k is at
+ * page * page_stride[0] + h * head_stride[0] + row * row_stride[0] + c; of v
+ * with strides [1].  dtype MATTN_BF16: bf16 values.  MATTN_E4M3: e4m3 codes and
+ * for each row one byte e at page * exp_page_stride + h * exp_head_stride +
+ * row * exp_row_stride of k_exponents / v_exponents: the row's values are
+ * code * 2^(e - 127), e = 255: NaN.
+ */
+typedef struct {
+  void* k;                    /* DEVICE, 16-byte aligned                                         */
+  void* v;
+  void* k_exponents;          /* DEVICE uint8, MATTN_E4M3 alone (else NULL)                      */
+  void* v_exponents;
+  int64_t page_stride[2];     /* in elements, > 0, multiples of 16 bytes; rows must not overlap  */
+  int64_t head_stride[2];
+  int64_t row_stride[2];
+  int64_t exp_page_stride[2]; /* in bytes, > 0                                                   */
+  int64_t exp_head_stride[2];
+  int64_t exp_row_stride[2];
+  const int32_t* page_table;  /* DEVICE int32 [B][table_pages]                                   */
+  int32_t table_pages;        /* table_pages * page <= 2^30                                      */
+  int32_t n_pages;
+  int32_t page;               /* rows of a page: a multiple of 16                                */
+  int32_t dtype;              /* MATTN_BF16 or MATTN_E4M3                                        */
+} mattn_paged_cache;
+
+/*
+ * mattn_cache_write -- rows of packed sequences into a paged cache: tokens
+ * cu_seqlens_b .. cu_seqlens_{b+1} - 1 of k and v go to positions starts_b,
+ * starts_b + 1, .. of sequence b.  Tokens of no sequence, positions outside the
+ * table and positions without a page are left out.  bf16 rows are copied; a row's
+ * e4m3 codes are its values times 2^(127 - e), rounded to nearest even, with the
+ * least e >= 0 for which 448 * 2^(e - 127) is at least every |value|; a row with an
+ * infinite or NaN value gets e = 255 and NaN codes.  Where two tokens go to one row
+ * of a page, the row holds either.
+ *   k, v        DEVICE bf16, element (t, h, c) at t * token_stride + h *
+ *               head_stride + c ([0] of k, [1] of v); 16-byte aligned, strides
+ *               multiples of 8 and >= 0
+ *   cu_seqlens  DEVICE int32 [B + 1], ascending, or NULL (T = B: one token each)
+ *   starts      DEVICE int32 [B] or NULL (0)
+ *   d in {64, 128, 256}; T * H_kv < 2^31.  The cache must not overlap k and v.
+ */
+int mattn_cache_write(const void* k, const void* v, const int64_t token_stride[2], const int64_t head_stride[2],
+                      const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,
+                      int H_kv, int d, int dtype, void* stream);
+
+/*
+ * mattn_cache_read -- the mirror of mattn_cache_write: rows cu_seqlens_b ..
+ * cu_seqlens_{b+1} - 1 of k and v get positions starts_b, starts_b + 1, .. of
+ * sequence b, rounded to bf16.  Positions outside the table or without a page give
+ * zeros; rows of no sequence are left as they are.  The arguments are
+ * mattn_cache_write's (token and head strides > 0).
+ */
+int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int64_t head_stride[2],
+                     const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,
+                     int H_kv, int d, int dtype, void* stream);
+
+/*
+ * mattn_decode_paged -- mattn_decode over a paged cache: the query of sequence b
+ * sees the cached keys at positions [0, seq_lens_b), or with window > 0 those of
+ * [seq_lens_b - window, seq_lens_b) and of [0, sink_tokens).
+ *   q, o, lse, sink, softmax_scale, d, H / H_kv, B * H_kv: as for mattn_decode_shared
+ *   seq_lens    DEVICE int32 [B] or NULL (table_pages * page); values outside
+ *               0 .. table_pages * page are clamped.  Positions without a page are
+ *               no keys.  What rows hold that no query sees is not used.
+ *   window      0: every key; sink_tokens >= 0, 0 without a window
+ *   At most 2^31 - 1 tiles of keys (of 32 keys in e4m3 or at d = 64, else 16) in
+ *   all of B tables.
+ * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Sums,
+ * statistics and states are fp32.  Softmax weights meet the values as two bf16
+ * parts, 2^-16 of a weight off at most; in e4m3 as one f16 value, 2^-11 off, with
+ * the row's power of two taken into the weight.
+ */
+int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, float* lse, const int32_t* seq_lens,
+                       int B, int H, int H_kv, int d, int dtype, int window, int sink_tokens, const float* sink,
+                       float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int page, int d, int cache_dtype,
+                                 size_t* bytes_out);
 
 /*
  * mattn_plan_schedule -- the schedule mattn_fwd would run for these

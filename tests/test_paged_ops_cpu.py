@@ -1,0 +1,198 @@
+"""CPU checks of the operators around a paged cache: what they refuse on the host
+before any launch.  The pointers passed here are never read: every call is refused
+first, or reaches the check of the device (there is none here)."""
+
+import ctypes
+import os
+
+import pytest
+
+mattn = pytest.importorskip("block_sparse_attention_masked_gb300")
+
+MB = 1 << 20
+BF16, F32, E4M3 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(mattn.LIB_PATH):
+        from block_sparse_attention_masked_gb300 import build
+
+        build.build()
+    return mattn.lib()
+
+
+def _cache(e4m3=False, n_pages=10, H_kv=2, page=16, d=128, **kw):
+    """Dense pages of k at 256 MB and v at 512 MB, their exponents at 768 and 800 MB."""
+    c = mattn.PagedCache()
+    c.k, c.v = 256 * MB, 512 * MB
+    if e4m3:
+        c.k_exponents, c.v_exponents = 768 * MB, 800 * MB
+    for i in range(2):
+        c.page_stride[i], c.head_stride[i], c.row_stride[i] = H_kv * page * d, page * d, d
+        c.exp_page_stride[i], c.exp_head_stride[i], c.exp_row_stride[i] = H_kv * page, page, 1
+    c.page_table, c.table_pages, c.n_pages, c.page, c.dtype = 900 * MB, 4, n_pages, page, E4M3 if e4m3 else BF16
+    for k, v in kw.items():
+        if isinstance(v, tuple):
+            for i, x in enumerate(v):
+                getattr(c, k)[i] = x
+        else:
+            setattr(c, k, v)
+    return c
+
+
+def _two(a, b):
+    return (ctypes.c_int64 * 2)(a, b)
+
+
+CACHE = [
+    ("no keys", {"k": None}, -1),
+    ("no values", {"v": None}, -1),
+    ("no page table", {"page_table": None}, -1),
+    ("an unknown type", {"dtype": F32}, -2),
+    ("codes without exponents", {"dtype": E4M3}, -1),
+    ("bf16 with exponents", {"k_exponents": MB, "v_exponents": MB}, -1),
+    ("pages of 8 rows", {"page": 8}, -2),
+    ("pages of 24 rows", {"page": 24}, -2),
+    ("an empty table", {"table_pages": 0}, -1),
+    ("no pages", {"n_pages": 0}, -1),
+    ("a table of more than 2^30 positions", {"table_pages": (1 << 26) + 1}, -2),
+    ("keys off a 16-byte boundary", {"k": 256 * MB + 8}, -2),
+    ("a table off a 4-byte boundary", {"page_table": 900 * MB + 2}, -2),
+    ("a stride off 16 bytes", {"row_stride": (132, 128)}, -2),
+    ("a stride of zero", {"head_stride": (0, 2048)}, -2),
+    ("a negative stride", {"page_stride": (4096, -4096)}, -2),
+    ("a stride of 2^40 bytes", {"page_stride": (4096, 1 << 39)}, -2),
+    ("rows that overlap", {"row_stride": (64, 128)}, -1),
+    ("heads that overlap", {"head_stride": (1920, 2048)}, -1),
+    ("pages that overlap", {"page_stride": (4096, 3968)}, -1),
+]
+
+
+def _write(L, cache, k=MB, v=100 * MB, token=(256, 256), head=(128, 128), cu=None, starts=None, B=3, T=3, H_kv=2, d=128,
+           dtype=BF16, read=False):
+    fn = L.mattn_cache_read if read else L.mattn_cache_write
+    return fn(k, v, _two(*token), _two(*head), ctypes.byref(cache) if cache else None, cu, starts, B, T, H_kv, d, dtype, None)
+
+
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("why,kw,code", CACHE)
+def test_cache_rows_refuse_the_cache(L, why, kw, code, read):
+    assert _write(L, _cache(**kw), read=read) == code, why
+    assert L.mattn_last_error()
+
+
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("why,kw,code", [
+    ("no rows", {"k": None}, -1),
+    ("fp32 rows", {"dtype": F32}, -2),
+    ("head dim 96", {"d": 96}, -2),
+    ("no sequence", {"B": 0, "T": 0}, -1),
+    ("no head", {"H_kv": 0}, -1),
+    ("a negative count", {"T": -1, "cu": MB}, -1),
+    ("more rows than sequences and no cu_seqlens", {"T": 4}, -1),
+    ("2^31 rows", {"T": 1 << 30, "cu": MB}, -2),
+    ("rows off a 16-byte boundary", {"v": 100 * MB + 8}, -2),
+    ("a token stride off 16 bytes", {"token": (260, 256)}, -2),
+    ("a negative stride", {"head": (128, -128)}, -1),
+    ("cu_seqlens off a 4-byte boundary", {"cu": MB + 2}, -1),
+    ("starts off a 4-byte boundary", {"starts": MB + 1}, -1),
+    ("rows in the cache", {"k": 256 * MB + 4096}, -1),
+    ("rows that end in the cache", {"v": 512 * MB - 256}, -1),
+    ("a NULL cache", {"cache": None}, -1),
+])
+def test_cache_rows_refuse(L, why, kw, code, read):
+    kw = dict(kw)
+    cache = kw.pop("cache", _cache())
+    assert _write(L, cache, read=read, **kw) == code, why
+    assert L.mattn_last_error()
+
+
+def test_cache_rows_that_would_be_written_twice(L):
+    """k and v in one place; outputs whose rows overlap; inputs may (a broadcast row)."""
+    assert _write(L, _cache(v=256 * MB)) == -1
+    assert _write(L, _cache(True, v_exponents=768 * MB)) == -1
+    assert _write(L, _cache(), v=MB, read=True) == -1
+    assert _write(L, _cache(), token=(0, 256), read=True) == -1
+    assert _write(L, _cache(), token=(128, 256), read=True) == -1
+    for kw in (dict(token=(0, 0)), dict(head=(0, 0)), dict(k=MB, v=MB)):
+        assert _write(L, _cache(), **kw) in (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)  # (nothing but the device is missing)
+
+
+def test_cache_layouts_that_are_accepted(L):
+    """Rows before heads, k and v of a page side by side, rows with room behind them, one page or head of any stride."""
+    ok = (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)
+    for e in (False, True):
+        assert _write(L, _cache(e)) in ok
+        assert _write(L, _cache(e, head_stride=(128, 128), row_stride=(256, 256), exp_head_stride=(1, 1),
+                                exp_row_stride=(2, 2))) in ok
+        assert _write(L, _cache(e, page_stride=(8192, 8192), v=256 * MB + 8192)) in ok
+        assert _write(L, _cache(e, row_stride=(144, 160), head_stride=(2304, 2560), page_stride=(4608, 5120))) in ok
+        assert _write(L, _cache(e, n_pages=1, page_stride=(16, 16))) in ok
+    assert _write(L, _cache(True, exp_row_stride=(1, 3))) == -1  # (the rows' bytes reach into the next head's)
+
+
+def _paged(L, cache, q=MB, o=2 * MB, lse=3 * MB, lens=None, B=3, H=8, H_kv=2, d=128, dtype=BF16, window=0, first=0,
+           sink=None, scale=0.0, ws=200 * MB, ws_bytes=1 << 30):
+    return L.mattn_decode_paged(q, ctypes.byref(cache) if cache else None, o, lse, lens, B, H, H_kv, d, dtype, window, first,
+                                sink, scale, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("why,kw,code", CACHE)
+def test_decode_paged_refuses_the_cache(L, why, kw, code):
+    assert _paged(L, _cache(**kw)) == code, why
+
+
+@pytest.mark.parametrize("why,kw,code", [
+    ("a NULL cache", {"cache": None}, -1),
+    ("no queries", {"q": None}, -1),
+    ("no output", {"o": None}, -1),
+    ("H no multiple of H_kv", {"H": 9}, -1),
+    ("17 query heads per key/value head", {"H": 34}, -2),
+    ("head dim 96", {"d": 96}, -2),
+    ("fp32", {"dtype": F32}, -2),
+    ("65536 groups", {"B": 32768}, -2),
+    ("queries off a 16-byte boundary", {"q": MB + 8}, -2),
+    ("lse off a 4-byte boundary", {"lse": MB + 2}, -1),
+    ("a negative window", {"window": -1}, -1),
+    ("negative first tokens", {"window": 5, "first": -1}, -1),
+    ("first tokens without a window", {"first": 4}, -1),
+    ("a negative scale", {"scale": -1.0}, -1),
+    ("an infinite scale", {"scale": float("inf")}, -1),
+    ("no workspace", {"ws": None}, -6),
+    ("a small workspace", {"ws_bytes": 1000}, -6),
+    ("a workspace off a 256-byte boundary", {"ws": MB + 16}, -1),
+])
+def test_decode_paged_refuses(L, why, kw, code):
+    kw = dict(kw)
+    cache = kw.pop("cache", _cache())
+    assert _paged(L, cache, **kw) == code, why
+    assert L.mattn_last_error()
+
+
+def test_decode_paged_workspace(L):
+    n = ctypes.c_size_t(0)
+    f = L.mattn_decode_paged_workspace
+    assert f(3, 8, 2, 4, 16, 128, BF16, ctypes.byref(n)) == 0 and n.value > 0
+    assert _paged(L, _cache(), ws_bytes=n.value - 1) == mattn.ERR_CAPACITY
+    assert _paged(L, _cache(), ws_bytes=n.value) in (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)
+    assert f(3, 8, 2, 4, 16, 128, BF16, None) == -1
+    assert f(3, 8, 2, 4, 16, 128, F32, ctypes.byref(n)) == -2
+    assert f(3, 8, 2, 0, 16, 128, BF16, ctypes.byref(n)) == -1
+    assert f(3, 8, 2, 1 << 27, 16, 128, BF16, ctypes.byref(n)) == -2
+    assert f(4096, 8, 8, 1 << 24, 64, 128, E4M3, ctypes.byref(n)) == -2  # 2^35 tiles
+
+
+def test_a_null_size_and_the_binding(L):
+    import torch
+
+    for bad in (0, -3):
+        with pytest.raises(ValueError):
+            mattn.decode_paged(None, None, None, None, window=bad)
+    x = torch.zeros((1, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):  # a CPU tensor
+        mattn.decode_paged(x, x, x, x)
+    with pytest.raises(ValueError):
+        mattn.cache_write(x, x, x, x, x)
+    with pytest.raises(ValueError):
+        mattn.cache_read(x, x, x, x)
