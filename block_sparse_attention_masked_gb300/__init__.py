@@ -108,6 +108,7 @@ EXPORTS = (
     "mattn_received", "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
     "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks", "mattn_decode_blocks_workspace",
     "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged", "mattn_decode_paged_workspace",
+    "mattn_attention_packed", "mattn_attention_packed_workspace",
     "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles", "mattn_plan_tiles_device",
     "mattn_device_status", "mattn_debug_checks", "mattn_set_wait_timeout_ns", "mattn_status_string",
     "mattn_last_error", "mattn_version",
@@ -166,6 +167,8 @@ def lib() -> ctypes.CDLL:
     L.mattn_cache_read.argtypes = [vp, vp, i64p, i64p, cp, vp, vp] + [i32] * 5 + [vp]
     L.mattn_decode_paged.argtypes = [vp, cp, vp, vp, vp] + [i32] * 7 + [vp, f32, vp, sz, vp]
     L.mattn_decode_paged_workspace.argtypes = [i32] * 7 + [szp]
+    L.mattn_attention_packed.argtypes = [vp] * 3 + [i64p, i64p] + [vp] * 4 + [i32] * 9 + [vp, f32, vp, sz, vp]
+    L.mattn_attention_packed_workspace.argtypes = [i32] * 3 + [szp]
     L.mattn_count_pairs.argtypes = [dp, i32, i32, i32, u64p]
     L.mattn_plan_schedule.argtypes = [dp, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_uint32)]
     L.mattn_plan_tiles.argtypes = [dp, i32, i32, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
@@ -182,7 +185,7 @@ def lib() -> ctypes.CDLL:
                  "mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
                  "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
                  "mattn_decode_blocks_workspace", "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged",
-                 "mattn_decode_paged_workspace",
+                 "mattn_decode_paged_workspace", "mattn_attention_packed", "mattn_attention_packed_workspace",
                  "mattn_count_pairs", "mattn_plan_schedule", "mattn_plan_tiles",
                  "mattn_plan_tiles_device", "mattn_device_status", "mattn_debug_checks",
                  "mattn_set_wait_timeout_ns", "mattn_version"):
@@ -399,7 +402,7 @@ def decode(q, k_cache, v_cache, mask: PreparedMask, seq_lens=None, out=None, lse
 _CALLS = ("mattn_qk_rope", "mattn_decode_shared", "mattn_decode_shared_workspace", "mattn_block_means",
           "mattn_decode_select", "mattn_decode_select_workspace", "mattn_decode_blocks",
           "mattn_decode_blocks_workspace", "mattn_cache_write", "mattn_cache_read", "mattn_decode_paged",
-          "mattn_decode_paged_workspace")
+          "mattn_decode_paged_workspace", "mattn_attention_packed", "mattn_attention_packed_workspace")
 _calls = None
 _calls_lib = None
 
@@ -658,6 +661,34 @@ def decode_paged(q, k_pages, v_pages, page_table, seq_lens=None, k_exponents=Non
     return _result(_torch_calls().decode_paged(q, k_pages, v_pages, page_table, seq_lens, k_exponents, v_exponents,
                                                0 if window is None else window, sink_tokens, sink, scale, out, lse,
                                                want_lse, workspace))
+
+
+def attention_packed_workspace(T: int, B: int, H: int, device="cuda"):
+    """A workspace for ``attention_packed`` calls of T query rows, B sequences and H
+    query heads that do not overlap."""
+    return _workspace(lib().mattn_attention_packed_workspace, device, B, T, H)
+
+
+def attention_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, causal: bool = True, window=None, sink=None, scale=None,
+                     out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Attention over sequences laid end to end (``mattn_attention_packed``).
+
+    q: CUDA bf16 [T, H, d], k, v: [T_k, H_kv, d], any strides over the first
+    two (e.g. views of one projection output); cu_seqlens: int32 [B + 1], the
+    rows at which the sequences begin, and the end of the last; cu_seqlens_k:
+    the same of the keys, or None (q's; T_k = T), e.g. with cached rows
+    (``cache_read``) in front of a prompt's own.  causal: a sequence's last
+    query sees its last key, each before it one key less, with ``window`` the
+    last ``window`` of them; else every key.  sink: fp32 [H] or None.  Rows of
+    no sequence are left as they are (zeros in outputs that the call makes).
+    Returns (o [T, H, d], lse [H, T] fp32 or None)."""
+    if window is not None and int(window) < 1:
+        raise ValueError("window must be >= 1 (None: every key)")
+    if stream is not None:
+        return _on_stream(stream, attention_packed, q, k, v, cu_seqlens, cu_seqlens_k, causal, window, sink, scale, out, lse,
+                          want_lse, workspace)
+    return _result(_torch_calls().attention_packed(q, k, v, cu_seqlens, cu_seqlens_k, causal, 0 if window is None else window,
+                                                   sink, scale, out, lse, want_lse, workspace))
 
 
 def attention_noalloc(q, k, v, mask: PreparedMask, out, lse=None, stream=None, check_wait: bool = True):

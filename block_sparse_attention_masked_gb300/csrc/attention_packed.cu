@@ -1,0 +1,774 @@
+// Attention over packed sequences (mattn_attention_packed), for sm_103a: sequence b has
+// queries cu_q[b] .. cu_q[b + 1] - 1 and keys cu_k[b] .. cu_k[b + 1] - 1 of the packed
+// rows, and query i of n sees, of its sequence's m keys, all, or (causal) those up to
+// m - n + i, of them the last `window`:
+//   O_i = sum_j p_ij v_j / (sum_j p_ij + exp(sink)),  p_ij = exp(scale q_i . k_j).
+// 4 d FLOPs a visible (head, pair): bound by the tensor cores and the exponentials, as
+// the persistent forward (attention_persist.cu), whose schedule this one has: a CTA per
+// SM takes pairs of 128-row query tiles of one (sequence, head), runs each tile's
+//     S = Q K^T, P = exp2(S scale log2e - m), O += P V
+// over its key tiles (tcgen05, P from tensor memory) with the two tiles sharing the
+// staged K and V, and begins the next pair's products while the last one is written.
+//
+// What differs: the work is known to the device alone.  packed_plan_kernel, one CTA,
+// lists the pairs with most key tiles first; item i of the grid is pair i / H, head i % H
+// (the heads of one pair run side by side and share K and V in L2), and a CTA takes the
+// next item that none has (a counter) when the K tiles of its current one run out: long
+// prompts first, short ones fill the end.
+//
+// Rows that are not the sequence's.  Tiles begin at any packed row and reach into the
+// next sequence (past the last row TMA fills zeros): query rows past the end are not
+// written, keys past it are masked, and their value rows, whose weight is 0 but which may
+// hold an infinity or NaN, are zeroed in shared memory before the product.  For the same
+// reason values in tiles that some row sees in part are looked over, and those that are
+// not finite taken out of the product and added, row by row where they are seen, to the
+// output.  Both are the V producer's warp's work, beside the pipeline: a diagonal tile's
+// values are needed last.
+//
+// Roles (384 threads) and tensor memory: as attention_persist.cu; every wait is bounded
+// in time and gives up by raising a CTA-wide abort flag and a device error bit.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attention_tiles.cuh"
+#include "kernel_params.h"
+#include "paged_ops.h"
+#include "plan_rules.h"
+#include "ptx.cuh"
+#include "tile_mma.cuh"
+
+namespace mattn {
+namespace {
+
+// ------------------------------------------------------------ the plan
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+
+// Sequence b's rows and keys, inside the packed rows whatever the arrays hold.
+struct Sequence {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Sequence sequence(const PackedParams& p, int b) {
+  auto in = [](int x, int n) { return x < 0 ? 0 : (x > n ? n : x); };
+  Sequence s;
+  s.q0 = in(__ldg(p.cu_q + b), p.T);
+  s.nq = in(__ldg(p.cu_q + b + 1), p.T) - s.q0;
+  s.k0 = in(__ldg(p.cu_k + b), p.T_k);
+  s.nk = in(__ldg(p.cu_k + b + 1), p.T_k) - s.k0;
+  if (s.nq < 0) s.nq = 0;
+  if (s.nk < 0) s.nk = 0;
+  return s;
+}
+
+// The key tiles [lo, hi] that rows r0 .. r0 + n - 1 of a pair see (n < 1 or lo > hi: none).
+__device__ __forceinline__ void seen_tiles(const PackedParams& p, int pos, int n, int keys, int* lo, int* hi) {
+  int last = keys - 1, first = 0;
+  if (p.causal) {
+    last = min(last, pos + n - 1);
+    if (p.window) first = max(0, pos - p.window + 1);
+  }
+  *lo = first >> 7;
+  *hi = n > 0 && last >= first ? last >> 7 : -1;
+  if (*hi < 0) *lo = 0;
+}
+
+__device__ __forceinline__ int pair_work(const PackedParams& p, const PackedPair& x) {
+  int w = 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    int lo, hi;
+    seen_tiles(p, x.pos0 + 128 * s, min(x.rows - 128 * s, 128), x.keys, &lo, &hi);
+    w += hi - lo + 1;
+  }
+  return w;
+}
+
+// Lists the pairs by the number of key tiles they multiply, most first (a counting sort;
+// the order inside a bin is any: an item's result does not depend on it).
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const __grid_constant__ PackedParams p) {
+  __shared__ int before[kPlanThreads + 1];  // pairs of the chunk's sequences before each
+  __shared__ int bins[kBins];
+  __shared__ int sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  after_previous();
+  // exclusive sums of x over the CTA; the whole sum in `total`
+  auto scan = [&](int x, int* total) {
+    int incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    const int mine = sums[lane];
+    int all = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, all, off);
+      if (lane >= off) all += y;
+    }
+    *total = __shfl_sync(0xffffffffu, all, 31);
+    const int base = __shfl_sync(0xffffffffu, all - mine, warp);
+    __syncthreads();
+    return base + incl - x;
+  };
+  auto chunk = [&](int b0) {  // pairs of sequences b0 .. b0 + kPlanThreads - 1 into `before`; how many
+    int n = 0, total;
+    if (b0 + tid < p.B) n = (sequence(p, b0 + tid).nq + 255) / 256;
+    before[tid] = scan(n, &total);
+    if (tid == 0) before[kPlanThreads] = total;
+    __syncthreads();
+    return total;
+  };
+  auto pair_at = [&](int b0, int j) {  // pair j of the chunk
+    int lo = 0, hi = kPlanThreads;     // before[lo] <= j < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= j) lo = mid;
+      else hi = mid;
+    }
+    const Sequence s = sequence(p, b0 + lo);
+    const int i = (j - before[lo]) * 256;
+    PackedPair x;
+    x.q_row = s.q0 + i;
+    x.rows = s.nq - i;
+    x.k_row = s.k0;
+    x.keys = s.nk;
+    x.pos0 = s.nk - s.nq + i;
+    return x;
+  };
+  auto bin_of = [&](const PackedPair& x) {
+    const int w = pair_work(p, x) >> p.work_shift;
+    return kBins - 1 - min(w, kBins - 1);
+  };
+  bins[tid] = 0;
+  __syncthreads();
+  const bool one = p.B <= kPlanThreads;
+  int n = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    n = chunk(b0);
+    for (int j = tid; j < n; j += kPlanThreads) atomicAdd(&bins[bin_of(pair_at(b0, j))], 1);
+    __syncthreads();
+  }
+  int total;
+  bins[tid] = scan(bins[tid], &total);
+  if (tid == 0) {
+    p.plan->next = 0;
+    p.plan->pairs = min(total, p.max_pairs);
+  }
+  __syncthreads();
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    if (!one) n = chunk(b0);
+    for (int j = tid; j < n; j += kPlanThreads) {
+      const PackedPair x = pair_at(b0, j);
+      const int at = atomicAdd(&bins[bin_of(x)], 1);
+      // (sequences that overlap could have more pairs than there is room for)
+      if (at < p.max_pairs) p.plan->pair[at] = x;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ the attention
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
+static_assert(kRegsControl + 2 * kRegsSoftmax == 3 * 168, "register split must match the launch budget");
+constexpr int kItems = 4;   // of the ring
+constexpr int kQSlots = 3;
+constexpr int kReaders = 11;  // of an item: the V producer, two issuers, eight softmax warps
+
+// An item as every role reads it; h < 0: no more.
+struct Item {
+  int q_row, rows, k_row, keys, pos0, h;
+  int lo, n;                    // its key tiles lo .. lo + n - 1
+  int lo0, hi0, lo1, hi1;       // those of each query tile (hi < lo: none)
+  int odd;                      // values that are not finite were taken out of a tile
+  __device__ __forceinline__ bool uses(int s, int kt) const { return s ? kt >= lo1 && kt <= hi1 : kt >= lo0 && kt <= hi0; }
+  __device__ __forceinline__ int first(int s) const { return s ? (hi1 < lo1 ? -1 : lo1) : (hi0 < lo0 ? -1 : lo0); }
+  __device__ __forceinline__ int last(int s) const { return s ? hi1 : hi0; }
+  // whether some row of query tile s (that uses it) does not see all of key tile kt
+  __device__ __forceinline__ bool partial(const PackedParams& p, int s, int kt) const {
+    const int k1 = kt * 128 + 127;
+    if (k1 >= keys) return true;
+    if (!p.causal) return false;
+    const int pos = pos0 + 128 * s;
+    return k1 > pos || (p.window && kt * 128 <= pos + min(rows - 128 * s, 128) - 1 - p.window);
+  }
+};
+
+struct Bar {
+  uint64_t q_full[kQSlots], q_empty[kQSlots];
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t v_land;
+  uint64_t s_full[2], p_full[2], o_full[2], drain[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t mma_turn;
+  Item items[kItems];
+};
+
+__device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t bit) {
+  *reinterpret_cast<volatile int*>(&bar->abort_flag) = 1;
+  atomicOr(p.err, bit);
+}
+__device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
+  if (!*abort_flag) return;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
+}
+
+// 128 rows of one head from packed row `row` on, laid out as tile_mma.cuh has them.
+template <int D>
+__device__ __forceinline__ void load_rows(const CUtensorMap* maps, uint8_t* dst, uint64_t* bar, int h, int row,
+                                          uint64_t policy) {
+  using G = Geo<D>;
+#pragma unroll
+  for (int c = 0; c < G::kChunks; ++c)
+    ptx::tma_load_3d_hint(dst + c * G::kChunkBytes, &maps[0], bar, c * 64, h, row, policy);
+  if (G::kRem) ptx::tma_load_3d_hint(dst + G::kChunks * G::kChunkBytes, &maps[1], bar, 0, h, row, policy);
+}
+
+// The scheduler and the Q and K streams (one thread).  Three cursors over the CTA's
+// items, none of which blocks another: the item to publish, the Q tile to load, the K
+// tile to load.
+template <int D, int KS>
+__device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, uint8_t* sq, uint8_t* sk,
+                                              volatile int* abort_flag) {
+  using G = Geo<D>;
+  const uint64_t keep = ptx::l2_policy_evict_last(), once = ptx::l2_policy_evict_first();
+  const int total = p.plan->pairs * p.H;
+  int id = blockIdx.x;
+  int pub = 0;        // items published
+  bool done = false;  // the last of them is the end
+  int qi = 0, qs = 0, t = 0;
+  int ki = 0, kj = 0, e = 0;
+  uint64_t t_idle = 0;
+  uint32_t idle = 0;
+  while (!(done && qi == pub - 1 && ki == pub - 1)) {
+    bool moved = false;
+    // the next item, once the K tiles of the current one run out
+    if (!done && (pub == ki || (pub == ki + 1 && bar->items[ki % kItems].n - kj <= 4)) && pub < qi + kItems &&
+        ptx::mbar_test_wait(&bar->item_empty[pub % kItems], ((pub / kItems) & 1) ^ 1)) {
+      Item& it = bar->items[pub % kItems];
+      if (id < total) {
+        const PackedPair* src = &p.plan->pair[id / p.H];
+        const int4 a = *reinterpret_cast<const int4*>(src);
+        const int pos0 = src->pos0;
+        it.q_row = a.x; it.rows = a.y; it.k_row = a.z; it.keys = a.w; it.pos0 = pos0;
+        it.h = id % p.H;
+        int lo0, hi0, lo1, hi1;
+        seen_tiles(p, pos0, min(a.y, 128), a.w, &lo0, &hi0);
+        seen_tiles(p, pos0 + 128, min(a.y - 128, 128), a.w, &lo1, &hi1);
+        it.lo0 = lo0; it.hi0 = hi0; it.lo1 = lo1; it.hi1 = hi1;
+        const int lo = hi0 < lo0 ? lo1 : (hi1 < lo1 ? lo0 : min(lo0, lo1)), hi = max(hi0, hi1);
+        it.lo = lo;
+        it.n = hi < lo ? 0 : hi - lo + 1;
+        it.odd = 0;
+        id = gridDim.x + atomicAdd(&p.plan->next, 1);
+      } else {
+        it.h = -1;
+        it.n = 0;
+        done = true;
+      }
+      ptx::mbar_arrive(&bar->item_full[pub % kItems]);
+      ++pub;
+      moved = true;
+    }
+    if (ki < pub - (done ? 1 : 0)) {
+      const Item& it = bar->items[ki % kItems];
+      if (kj == it.n) {
+        ++ki;
+        kj = 0;
+        moved = true;
+      } else if (ptx::mbar_test_wait(&bar->k_empty[e % KS], ((e / KS) & 1) ^ 1)) {
+        const int slot = e % KS;
+        const int row = it.k_row + (it.lo + kj) * kTile;
+        if (!debug_check(p.err, row >= 0 && row < p.T_k && it.h < p.H, kSiteLoad)) {
+          *abort_flag = 1;
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&bar->k_full[slot], G::kTileBytes);
+        if (!(p.selftest == 1 && e == 0))
+          load_rows<D>(p.tk, sk + slot * G::kTileBytes, &bar->k_full[slot], it.h / p.group, row, keep);
+        ++e;
+        ++kj;
+        moved = true;
+      }
+    }
+    if (qi < pub - (done ? 1 : 0)) {
+      const Item& it = bar->items[qi % kItems];
+      if (it.first(qs) < 0) {  // nothing to multiply: no Q tile
+        qi += qs;
+        qs ^= 1;
+        moved = true;
+      } else if (ptx::mbar_test_wait(&bar->q_empty[t % kQSlots], ((t / kQSlots) & 1) ^ 1)) {
+        const int slot = t % kQSlots, row = it.q_row + 128 * qs;
+        if (!debug_check(p.err, row >= 0 && row < p.T, kSiteLoad)) {
+          *abort_flag = 1;
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&bar->q_full[slot], G::kTileBytes);
+        load_rows<D>(p.tq, sq + slot * G::kTileBytes, &bar->q_full[slot], it.h, row, once);
+        ++t;
+        qi += qs;
+        qs ^= 1;
+        moved = true;
+      }
+    }
+    if (moved) {
+      idle = 0;
+    } else if ((++idle & 63u) == 0) {
+      // bounded like every wait: gives up after timeout_ns without progress
+      if (*abort_flag) break;
+      const uint64_t now = ptx::globaltimer_ns();
+      if (idle == 64) {
+        t_idle = now;
+      } else if (now - t_idle > p.timeout_ns) {
+        fail(p, bar, kErrProducer);
+        break;
+      }
+    }
+  }
+  let_copies_land(abort_flag);
+}
+
+// Whether a 16-bit half of x is an infinity or NaN; taken out (a zero) by clean().
+__device__ __forceinline__ uint32_t clean(uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
+
+// A landed V tile: rows from `rows` on become zeros; with `look`, so do values that are
+// not finite in the others (true: there were some).  One warp; the layout does not
+// matter, as a row's columns lie in rows of every chunk.
+template <int D>
+__device__ __forceinline__ bool clean_tile(uint8_t* tile, int rows, bool look) {
+  using G = Geo<D>;
+  constexpr int kRow = G::kVW * 2;
+  const int lane = threadIdx.x & 31;
+  bool odd = false;
+  if (look) {
+    uint32_t top = 0;
+    const int n = rows * kRow / 16;  // 16-byte pieces of a chunk
+    for (int c = 0; c < G::kVChunks; ++c) {
+      const uint4* x = reinterpret_cast<const uint4*>(tile + c * G::kVChunkBytes);
+#pragma unroll 8
+      for (int i = lane; i < n; i += 32) {
+        const uint4 v = x[i];
+        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+      }
+    }
+    odd = __any_sync(0xffffffffu, max(top >> 16, top & 0xffffu) >= 0x7f80u);
+    if (odd) {
+      for (int c = 0; c < G::kVChunks; ++c) {
+        uint4* x = reinterpret_cast<uint4*>(tile + c * G::kVChunkBytes);
+        for (int i = lane; i < n; i += 32) {
+          const uint4 v = x[i];
+          x[i] = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+        }
+      }
+    }
+  }
+  for (int c = 0; c < G::kVChunks; ++c)
+    for (int i = rows * kRow / 16 + lane; i < kTile * kRow / 16; i += 32)
+      *reinterpret_cast<uint4*>(tile + c * G::kVChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+  return odd;
+}
+
+// Waits for the CTA's item i; null if the wait gave up.
+__device__ __forceinline__ const Item* take_item(const PackedParams& p, Bar* bar, int i, volatile int* abort_flag) {
+  const bool got = ptx::mbar_wait(&bar->item_full[i % kItems], (i / kItems) & 1, p.timeout_ns, abort_flag);
+  return __all_sync(0xffffffffu, got) ? &bar->items[i % kItems] : nullptr;
+}
+__device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, after its last read)
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar->item_empty[i % kItems]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __grid_constant__ PackedParams p) {
+  using G = Geo<D>;
+  constexpr int KS = G::kStages, VS = G::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = base;
+  uint8_t* sk = sq + kQSlots * G::kTileBytes;
+  uint8_t* sv = sk + KS * G::kTileBytes;
+  Bar* bar = reinterpret_cast<Bar*>(sv + VS * G::kTileBytes);
+  volatile int* abort_flag = &bar->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&p.tq[0]);
+    ptx::prefetch_tmap(&p.tk[0]);
+    ptx::prefetch_tmap(&p.tv);
+    for (int i = 0; i < kQSlots; ++i) {
+      ptx::mbar_init(&bar->q_full[i], 1);
+      ptx::mbar_init(&bar->q_empty[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      ptx::mbar_init(&bar->k_full[i], 1);
+      ptx::mbar_init(&bar->k_empty[i], 2);  // one commit from each issuer
+      ptx::mbar_init(&bar->v_full[i], 1);
+      ptx::mbar_init(&bar->v_empty[i], 2);
+    }
+    ptx::mbar_init(&bar->v_land, 1);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&bar->s_full[s], 1);
+      ptx::mbar_init(&bar->p_full[s], kTile);
+      ptx::mbar_init(&bar->o_full[s], 1);
+      ptx::mbar_init(&bar->drain[s], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      ptx::mbar_init(&bar->item_full[i], 1);
+      ptx::mbar_init(&bar->item_empty[i], kReaders);
+    }
+    bar->abort_flag = 0;
+    bar->mma_turn = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&bar->tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  after_previous();  // the plan, and whatever the inputs come from
+
+  if (warp == 0) {
+    ptx::setmaxnreg_dec<kRegsControl>();
+    if (lane == 0) produce_items<D, KS>(p, bar, sq, sk, abort_flag);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ V producer
+    ptx::setmaxnreg_dec<kRegsControl>();
+    const uint64_t keep = ptx::l2_policy_evict_last();
+    int e = 0;
+    uint32_t lands = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const Item* it = take_item(p, bar, i, abort_flag);
+      if (!it) {
+        ok = false;
+        break;
+      }
+      if (it->h < 0) break;
+      const int n = it->n, lo = it->lo, keys = it->keys, k_row = it->k_row, h = it->h / p.group;
+      for (int j = 0; j < n; ++j, ++e) {
+        const int slot = e % VS, kt = lo + j;
+        uint8_t* tile = sv + slot * G::kTileBytes;
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_empty[slot], ((e / VS) & 1) ^ 1, p.timeout_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const bool look = (it->uses(0, kt) && it->partial(p, 0, kt)) || (it->uses(1, kt) && it->partial(p, 1, kt));
+        uint64_t* landing = look ? &bar->v_land : &bar->v_full[slot];
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(landing, G::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < G::kVChunks; ++c)
+            ptx::tma_load_3d_hint(tile + c * G::kVChunkBytes, &p.tv, landing, c * G::kVW, h, k_row + kt * kTile, keep);
+        }
+        __syncwarp();
+        if (look) {
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_land, lands & 1, p.timeout_ns, abort_flag))) {
+            ok = false;
+            break;
+          }
+          ++lands;
+          const bool odd = clean_tile<D>(tile, min(keys - kt * kTile, kTile), true);
+          if (lane == 0) {
+            if (odd) const_cast<Item*>(it)->odd = 1;
+            ptx::mbar_arrive(&bar->v_full[slot]);
+          }
+        }
+      }
+      if (ok) drop_item(bar, i);
+    }
+    if (!ok && lane == 0) fail(p, bar, kErrProducer);
+    __syncwarp();
+    let_copies_land(abort_flag);
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers
+    // As attention_persist.cu's: both walk every entry e of the CTA's stream and, in
+    // ticket order 2 e + s, issue P V (e - 1) and S (e).
+    ptx::setmaxnreg_dec<kRegsControl>();
+    const int s = warp - 1;
+    auto wait_all = [&](uint64_t* b, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, p.timeout_ns, abort_flag));
+    };
+    constexpr uint32_t tile4 = G::kTileBytes >> 4;  // descriptor start-address units
+    const uint32_t q4 = ptx::smem_addr(sq) >> 4;
+    const uint32_t k4 = ptx::smem_addr(sk) >> 4;
+    const uint32_t v4 = ptx::smem_addr(sv) >> 4;
+    const uint32_t s_tm = tmem + s * 128;
+    const uint32_t o_tm = tmem + 256 + s * 128;
+    bool ok = true, issued_any = false;
+    bool pend = false, pend_first = false, pend_last = false;
+    uint32_t pcount = 0;  // P tiles consumed
+    int e = 0;
+    int t = 0;  // Q tiles of both query tiles so far
+    for (int i = 0; ok; ++i) {
+      const Item* it = take_item(p, bar, i, abort_flag);
+      if (!it) {
+        ok = false;
+        break;
+      }
+      if (it->h < 0) break;
+      const int n = it->n, lo = it->lo;
+      const int first_use = it->first(s), last_use = it->last(s);
+      const int has0 = it->first(0) >= 0, has1 = it->first(1) >= 0;
+      drop_item(bar, i);
+      const int tq = t + (s ? has0 : 0);  // this query tile's Q
+      t += has0 + has1;
+      const int qslot = tq % kQSlots;
+      const uint32_t qpar = (tq / kQSlots) & 1;
+      for (int j = 0; j < n; ++j, ++e) {
+        const int kt = lo + j;
+        const bool use = first_use >= 0 && kt >= first_use && kt <= last_use;
+        const int ks = e % KS;
+        const bool rel_v = e >= 1;
+        const int ve = e - 1;
+        if (rel_v && !wait_all(&bar->v_full[ve % VS], (ve / VS) & 1)) { ok = false; break; }
+        if (!wait_all(&bar->k_full[ks], (e / KS) & 1)) { ok = false; break; }
+        if (pend) {
+          if (!wait_all(&bar->p_full[s], pcount & 1)) { ok = false; break; }
+          ++pcount;
+          ptx::tc_fence_after();
+        }
+        if (use && kt == first_use && !wait_all(&bar->q_full[qslot], qpar)) { ok = false; break; }
+        const uint32_t ticket = (uint32_t)(2 * e + s);
+        if (!__all_sync(0xffffffffu, mma_turn_wait(bar, ticket, p.timeout_ns, abort_flag))) { ok = false; break; }
+        if (ptx::elect_one()) {
+          if (pend) issue_pv<D>(o_tm, s_tm, v4 + (ve % VS) * tile4, !pend_first);
+          if (use) issue_qk<D>(s_tm, q4 + qslot * tile4, k4 + ks * tile4);
+        }
+        __syncwarp();
+        if (lane == 0) mma_turn_pass(bar, ticket);
+        if (use) {
+          ptx::mma_commit_elect(&bar->s_full[s]);
+          issued_any = true;
+        }
+        if (rel_v) ptx::mma_commit_elect(&bar->v_empty[ve % VS]);
+        ptx::mma_commit_elect(&bar->k_empty[ks]);
+        if (pend && pend_last) ptx::mma_commit_elect(&bar->o_full[s]);
+        if (use && kt == last_use) ptx::mma_commit_elect(&bar->q_empty[qslot]);
+        pend = use;
+        pend_first = use && kt == first_use;
+        pend_last = use && kt == last_use;
+      }
+    }
+    if (ok && e >= 1) {
+      // the last entry: its V slot and this query tile's pending P V
+      const int ve = e - 1;
+      if (!wait_all(&bar->v_full[ve % VS], (ve / VS) & 1)) ok = false;
+      if (ok && pend) {
+        if (!wait_all(&bar->p_full[s], pcount & 1)) {
+          ok = false;
+        } else {
+          ++pcount;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) issue_pv<D>(o_tm, s_tm, v4 + (ve % VS) * tile4, !pend_first);
+          __syncwarp();
+          ptx::mma_commit_elect(&bar->o_full[s]);
+        }
+      }
+      if (ok) ptx::mma_commit_elect(&bar->v_empty[ve % VS]);
+    }
+    if (!ok) {
+      if (lane == 0) fail(p, bar, kErrMma);
+      if (issued_any) {
+        // wait (bounded) for the MMAs already issued before tensor memory is freed
+        ptx::mma_commit_elect(&bar->drain[s]);
+        ptx::mbar_wait_time_only(&bar->drain[s], 0, p.timeout_ns);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    ptx::setmaxnreg_inc<kRegsSoftmax>();
+    const int s = (warp - 4) >> 2;
+    const int quarter = warp & 3;  // tensor-memory lane quarter this warp may access
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + s * 128;
+    const uint32_t o_tmem = tmem + lane_off + 256 + s * 128;
+    const float sl2 = p.scale_log2;
+    uint32_t count = 0;  // S tiles of this query tile so far (all items)
+    int o_items = 0;     // items whose O_s has been read
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const Item* it = take_item(p, bar, i, abort_flag);
+      if (!it) {
+        ok = false;
+        if (lane == 0) fail(p, bar, kErrSoftmax);
+        break;
+      }
+      if (it->h < 0) break;
+      const int keys = it->keys, h = it->h;
+      const bool valid = row < it->rows - 128 * s;
+      const int pos = it->pos0 + 128 * s + row;
+      int lo = 0, hi = keys - 1;  // keys this row sees
+      if (p.causal) {
+        hi = min(hi, pos);
+        if (p.window) lo = max(0, pos - p.window + 1);
+      }
+      if (!valid) hi = -1;
+      const int first = it->first(s), last = it->last(s);
+      float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain
+      float l = 0.f;        // running sum of exp2(x - m)
+      for (int kt = first < 0 ? last + 1 : first; kt <= last; ++kt) {
+        const bool got = ptx::mbar_wait(&bar->s_full[s], count & 1, p.timeout_ns, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) fail(p, bar, kErrSoftmax);
+          ok = false;
+          break;
+        }
+        ++count;
+        ptx::tc_fence_after();
+        float x[128];
+        ptx::tmem_ld32(s_tmem + 0, *reinterpret_cast<float(*)[32]>(&x[0]));
+        ptx::tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+        ptx::tmem_ld32(s_tmem + 64, *reinterpret_cast<float(*)[32]>(&x[64]));
+        ptx::tmem_ld32(s_tmem + 96, *reinterpret_cast<float(*)[32]>(&x[96]));
+        ptx::tmem_wait_ld();
+        bool sees = valid;  // this row sees a key of the tile
+        if (it->partial(p, s, kt)) {
+          const int k0 = kt * kTile;
+          sees = mask_row(x, min(max(lo - k0, -1), 128), min(max(hi - k0, -1), 128), -1);
+        }
+        // P = exp2(s * scale * log2e - m) into tensor memory, by the stale-max rule of
+        // attention_fwd.cu; rows past the sequence's end (another's, or nothing) take
+        // no part in it
+        const bool fresh = m == -INFINITY;
+        float ts = exp_to_tmem(x, sl2, fresh ? 0.f : m, s_tmem);
+        const bool redo = valid && (!(ts <= kMaxTileSum) || (fresh && sees && !(ts >= kMinTileSum)));
+        if (fresh && sees && !redo) m = 0.f;  // the row's reference from here on
+        if (__any_sync(0xffffffffu, redo)) {
+          ptx::tmem_wait_st();  // let these stores land before they are overwritten
+          // the warp's other rows keep their reference, and with it every bit
+          const float m_new = redo ? fmaxf(m, row_max(x) * sl2) : m;
+          const bool need_rescale = !fresh && m_new > m;
+          if (fresh) m = m_new;
+          if (__any_sync(0xffffffffu, need_rescale)) {
+            const float alpha = need_rescale ? ptx::ex2(m - m_new) : 1.f;
+            rescale_o<D>(o_tmem, alpha);
+            if (need_rescale) {
+              l *= alpha;
+              m = m_new;
+            }
+          }
+          ts = exp_to_tmem(x, sl2, (m == -INFINITY) ? 0.f : m, s_tmem);
+        }
+        l += ts;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar->p_full[s]);
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------- epilogue
+      const bool has_o = first >= 0;
+      const float b2 = p.sink ? __ldg(p.sink + h) * kLog2e : -INFINITY;
+      const float M = fmaxf(m, b2);
+      const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
+      const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
+      const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
+      const float o_scale = z == 0.f ? 0.f : em / z;
+      const int64_t q_row = (int64_t)it->q_row + 128 * s + row;
+      if (valid && p.lse) p.lse[(int64_t)h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
+      if (has_o) {
+        const bool got = ptx::mbar_wait(&bar->o_full[s], o_items & 1, p.timeout_ns, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) fail(p, bar, kErrEpilogue);
+          ok = false;
+          break;
+        }
+        ++o_items;
+        ptx::tc_fence_after();
+      }
+      const bool odd = has_o && *reinterpret_cast<const volatile int*>(&it->odd);
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (q_row * p.H + h) * D;
+      const uint64_t o_policy = ptx::l2_policy_evict_first();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        float ov[16];
+        if (has_o) {
+          ptx::tmem_ld16(o_tmem + c0, ov);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) ov[k] *= o_scale;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) ov[k] = 0.f;
+        }
+        if (odd && valid) {
+          // values that are not finite and were taken out of tiles seen in part: each
+          // has a positive weight in the rows that see it
+          for (int kt = it->lo; kt < it->lo + it->n; ++kt) {
+            if (!((it->uses(0, kt) && it->partial(p, 0, kt)) || (it->uses(1, kt) && it->partial(p, 1, kt)))) continue;
+            for (int j = max(lo, kt * kTile); j <= min(hi, kt * kTile + kTile - 1); ++j) {
+              const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + (it->k_row + (int64_t)j) * p.v_token +
+                                       (h / p.group) * p.v_head + c0;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float y = __bfloat162float(v[k]);
+                if (!(fabsf(y) < INFINITY)) ov[k] += y;
+              }
+            }
+          }
+        }
+        if (valid) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pk[k] = ptx::pack_bf16x2(ov[2 * k], ov[2 * k + 1]);
+          uint4* to = reinterpret_cast<uint4*>(dst + c0);
+          ptx::st_global_v4_hint(to, make_uint4(pk[0], pk[1], pk[2], pk[3]), o_policy);
+          ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
+        }
+      }
+      drop_item(bar, i);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PackedParams& p, cudaStream_t stream) {
+  using G = Geo<D>;
+  constexpr size_t need = (size_t)(kQSlots + 2 * G::kStages) * G::kTileBytes + sizeof(Bar) + 1024;
+  // (at least half of an SM's shared memory: one CTA owns the SM and its tensor memory)
+  constexpr size_t smem = need < 120 * 1024 ? 120 * 1024 : need;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  auto kern = attention_packed_kernel<D>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kern, smem, &done);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_chained(packed_plan_kernel, 1, 1, kPlanThreads, 0, 1, p, stream)) != cudaSuccess) return e;
+  const int64_t items = (int64_t)p.max_pairs * p.H;
+  return launch_chained(kern, (unsigned)(items < kPlanSms ? items : kPlanSms), 1, kThreads, smem, 1, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_packed(const PackedParams& p, int d, cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch_d<64>(p, stream);
+    case 80: return launch_d<80>(p, stream);
+    case 96: return launch_d<96>(p, stream);
+    case 128: return launch_d<128>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace mattn

@@ -56,4 +56,39 @@ struct DecodePagedParams {
 };
 cudaError_t launch_decode_paged(const DecodePagedParams& p, int d, bool e4m3, cudaStream_t stream);
 
+// ------------------------------------------------------------ attention_packed.cu
+// A pair of query tiles of one sequence, as the plan kernel lists them (most key tiles
+// first): rows q_row .. q_row + rows - 1 of the packed queries, the sequence's keys
+// k_row .. k_row + keys - 1, the first row's position among them (negative: none).
+struct __align__(16) PackedPair {
+  int q_row, rows, k_row, keys, pos0, pad[3];
+};
+struct PackedPlan {        // in the workspace
+  int next;                // the next item that no CTA has
+  int pairs;
+  int pad[14];
+  PackedPair pair[1];
+};
+// Pairs of T rows in B sequences at most (256 rows each, a shorter one behind).
+inline int64_t packed_pairs(int64_t T, int64_t B) { return T / 256 + (B < T ? B : T); }
+
+struct PackedParams {
+  CUtensorMap tq[2], tk[2], tv;  // [T][heads][d] views: boxes of 128 rows of one head (tile_mma.cuh)
+  void* o;                       // [T][H][d] bf16
+  float* lse;                    // [H][T] or null
+  const float* sink;             // [H] or null
+  const void* v;                 // the values once more, for keys that are not finite (attention_packed.cu)
+  int64_t v_token, v_head;
+  const int32_t *cu_q, *cu_k;    // [B + 1]
+  PackedPlan* plan;
+  uint32_t* err;
+  unsigned long long timeout_ns;
+  int B, T, T_k, H, H_kv, group;
+  int causal, window;            // window 0: none
+  int max_pairs, work_shift;
+  float scale_log2;
+  int selftest;                  // 1: the first K tile is left out, so that the wait for it runs out
+};
+cudaError_t launch_attention_packed(const PackedParams& p, int d, cudaStream_t stream);
+
 }  // namespace mattn

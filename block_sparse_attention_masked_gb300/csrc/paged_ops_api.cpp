@@ -18,7 +18,7 @@
 namespace mattn {
 namespace {
 
-// Test hook: the copies that the next launches leave out (DecodePagedParams).
+// Test hook: the copies that the next launches leave out (DecodePagedParams, PackedParams).
 std::atomic<int> g_wait_selftest{0};
 
 bool cache_dtype(int t) { return t == MATTN_BF16 || t == MATTN_E4M3; }
@@ -167,6 +167,17 @@ int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dt
   return MATTN_OK;
 }
 
+size_t packed_bytes(int64_t T, int64_t B) { return sizeof(PackedPlan) + (size_t)packed_pairs(T, B) * sizeof(PackedPair); }
+
+int check_packed(int B, int T, int H) {
+  if (B < 1 || H < 1 || T < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: B, H must be >= 1 and T >= 0");
+  if (T > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: T exceeds 2^30");
+  // the items are numbered in 32 bits
+  if ((int64_t)H * (T / 256 + (int64_t)B) > INT32_MAX)
+    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: H * (T / 256 + B) exceeds 2^31 - 1");
+  return MATTN_OK;
+}
+
 }  // namespace
 }  // namespace mattn
 
@@ -280,9 +291,92 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   return launched(launch_decode_merge(m, d, stream), "merge launch");
 }
 
-// Test hook (not in the public header): the launches of decode_paged until the next
-// call leave out the row workers' first keys (1), so that the bounded waits and the
-// error word can be exercised without a hang; 0: nothing.
+int mattn_attention_packed_workspace(int B, int T, int H, size_t* bytes_out) {
+  if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: bytes_out is NULL");
+  const int rc = check_packed(B, T, H);
+  if (rc) return rc;
+  *bytes_out = packed_bytes(T, B);
+  return MATTN_OK;
+}
+
+int mattn_attention_packed(const void* q, const void* k, const void* v, const int64_t token_stride[3],
+                           const int64_t head_stride[3], void* o, float* lse, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int B, int T, int T_k, int H, int H_kv, int d, int dtype,
+                           int causal, int window, const float* sink, float softmax_scale, void* workspace,
+                           size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  int rc = check_packed(B, T, H);
+  if (rc) return rc;
+  if (H_kv < 1 || H % H_kv)
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: H = %d is not a multiple of H_kv = %d", H, H_kv);
+  if (d != 64 && d != 80 && d != 96 && d != 128)
+    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: head dim %d (64, 80, 96, 128)", d);
+  if (dtype != MATTN_BF16) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed takes bf16");
+  if (T_k < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: T_k must be >= 0");
+  if (T_k > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: T_k exceeds 2^30");
+  if (!cu_seqlens_q || (T > 0 && (!q || !o)) || (T_k > 0 && (!k || !v)) || !token_stride || !head_stride)
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: q, k, v, o, their strides and cu_seqlens_q must be non-NULL");
+  if (!cu_seqlens_k && T_k != T)
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: other keys than queries need cu_seqlens_k");
+  if (window < 0 || (window && !causal))
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: window must be >= 0, and 0 without causal");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: q, k, v and o must be 16-byte aligned");
+  if (!aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: cu_seqlens must be 4-byte aligned");
+  if ((rc = check_small("attention_packed", lse, nullptr, sink))) return rc;
+  if ((rc = check_scale("attention_packed", softmax_scale))) return rc;
+  int64_t ts[3], hs[3];
+  for (int i = 0; i < 3; ++i) {
+    // (the stride of a dimension of one entry says nothing)
+    ts[i] = (i ? T_k : T) > 1 ? token_stride[i] : d;
+    hs[i] = (i ? H_kv : H) > 1 ? head_stride[i] : d;
+    if (ts[i] <= 0 || hs[i] <= 0 || ts[i] % 8 || hs[i] % 8 || ts[i] >= int64_t(1) << 39 || hs[i] >= int64_t(1) << 39)
+      return report_error(MATTN_ERR_UNSUPPORTED,
+                          "attention_packed: strides must be positive multiples of 16 bytes below 2^40");
+  }
+  if ((rc = check_workspace("attention_packed", workspace, workspace_bytes, packed_bytes(T, B)))) return rc;
+  uint32_t* err = nullptr;
+  if ((rc = device_error_word(stream, &err))) return rc;
+  if (T == 0) return MATTN_OK;
+  PackedParams p;
+  memset(&p, 0, sizeof(p));
+  const int rem = d % 64, vw = d % 64 == 0 ? 64 : (d % 32 == 0 ? 32 : 16);
+  auto maps = [&](CUtensorMap* m, const void* x, int64_t rows, int heads, int i) {  // 64-column chunks and the rest
+    const int e = make_packed_map(&m[0], x, d, 64, rows, heads, ts[i], hs[i]);
+    if (e || !rem) return e;
+    return make_packed_map(&m[1], static_cast<const char*>(x) + (d - rem) * 2, rem, rem, rows, heads, ts[i], hs[i]);
+  };
+  if ((rc = maps(p.tq, q, T, H, 0))) return rc;
+  if (T_k > 0) {  // (else no tile is loaded)
+    if ((rc = maps(p.tk, k, T_k, H_kv, 1))) return rc;
+    if ((rc = make_packed_map(&p.tv, v, d, vw, T_k, H_kv, ts[2], hs[2]))) return rc;
+  }
+  p.o = o;
+  p.lse = lse;
+  p.sink = sink;
+  p.v = v;
+  p.v_token = ts[2];
+  p.v_head = hs[2];
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q;
+  p.plan = static_cast<PackedPlan*>(workspace);
+  p.err = err;
+  p.timeout_ns = device_wait_timeout_ns();
+  p.B = B; p.T = T; p.T_k = T_k; p.H = H; p.H_kv = H_kv;
+  p.group = H / H_kv;
+  p.causal = causal ? 1 : 0;
+  p.window = window < kMaxRows ? window : (int)kMaxRows;
+  p.max_pairs = (int)packed_pairs(T, B);
+  while (((2 * ((int64_t)T_k / 128 + 1)) >> p.work_shift) >= 1024) ++p.work_shift;
+  p.scale_log2 = scale_log2(softmax_scale, d);
+  p.selftest = g_wait_selftest.load();
+  return launched(launch_attention_packed(p, d, stream), "attention_packed launch");
+}
+
+// Test hook (not in the public header): the launches of decode_paged and
+// attention_packed until the next call leave out the first keys' copies (1), so that the
+// bounded waits and the error word can be exercised without a hang; 0: nothing.
 int mattn_internal_paged_wait_selftest(int what) {
   if (what < 0 || what > 1) return report_error(MATTN_ERR_INVALID_ARG, "what must be 0 or 1");
   g_wait_selftest.store(what);

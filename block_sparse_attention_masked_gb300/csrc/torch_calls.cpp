@@ -41,6 +41,8 @@ struct Functions {
   decltype(&mattn_cache_read) cache_read;
   decltype(&mattn_decode_paged) decode_paged;
   decltype(&mattn_decode_paged_workspace) decode_paged_workspace;
+  decltype(&mattn_attention_packed) attention_packed;
+  decltype(&mattn_attention_packed_workspace) attention_packed_workspace;
 } g_fn = {};
 
 struct Bad : std::runtime_error {
@@ -549,6 +551,52 @@ PyObject* decode_paged(Args a) {
   return o.result();
 }
 
+PyObject* attention_packed(Args a) {
+  const at::Tensor &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v"), &cu = a.tensor("cu_seqlens");
+  const at::Tensor* cu_k = a.optional("cu_seqlens_k");
+  const bool causal = a.truth("causal");
+  const int window = a.small("window");
+  const at::Tensor* sink = a.optional("sink");
+  const float scale = a.scale();
+  const at::Tensor *out = a.optional("out"), *lse = a.optional("lse");
+  const bool want = a.truth("want_lse");
+  const at::Tensor* ws = a.optional("workspace");
+  need(q.is_cuda() && q.dim() == 3, "q must be a CUDA tensor [T, H, d]");
+  need(k.dim() == 3 && v.sizes() == k.sizes() && k.size(2) == q.size(2), "k and v must be [T_k, H_kv, d]");
+  need(cu.dim() == 1 && cu.size(0) >= 2 && (!cu_k || cu_k->sizes() == cu.sizes()),
+       "cu_seqlens and cu_seqlens_k must be [B + 1]");
+  fits(&cu, q, at::kInt, "cu_seqlens");
+  fits(cu_k, q, at::kInt, "cu_seqlens_k");
+  const int T = size32(q.size(0)), T_k = size32(k.size(0)), H = size32(q.size(1)), H_kv = size32(k.size(1));
+  const int B = size32(cu.size(0) - 1), d = size32(q.size(2));
+  int64_t token[3], head[3];
+  const at::Tensor* x[3] = {&q, &k, &v};
+  for (int i = 0; i < 3; ++i) {
+    need(x[i]->device() == q.device() && x[i]->scalar_type() == q.scalar_type(), "q, k and v must be of one type and device");
+    need(x[i]->stride(2) == 1, "a row must lie in one piece");
+    token[i] = x[i]->stride(0);
+    head[i] = x[i]->stride(1);
+  }
+  need(!sink || shape(*sink, {H}), "sink must be [H]");
+  need(!out || out->sizes() == q.sizes(), "out must be [T, H, d]");
+  need(!lse || shape(*lse, {H, T}), "lse must be [H, T]");
+  fits(sink, q, at::kFloat, "sink");
+  fits(out, q, q.scalar_type(), "out");
+  fits(lse, q, at::kFloat, "lse");
+  const int code = type_code(q);
+  On on(q);
+  // (rows of no sequence, which the kernel leaves as they are: zeros)
+  const at::Tensor o = out ? *out : at::zeros({T, H, d}, q.options());
+  at::Tensor l;
+  if (lse || want) l = lse ? *lse : at::zeros({H, T}, q.options().dtype(at::kFloat));
+  Workspace w(ws, q, [&](size_t* n) { return g_fn.attention_packed_workspace(B, T, H, n); });
+  done(g_fn.attention_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), token, head, o.data_ptr(),
+                             lse || want ? static_cast<float*>(l.data_ptr()) : nullptr, ptr<int32_t>(&cu),
+                             ptr<int32_t>(cu_k), B, T, T_k, H, H_kv, d, code, causal, window, ptr<float>(sink), scale, w.p,
+                             w.bytes, on.stream));
+  return pair(o, lse || want ? &l : nullptr);
+}
+
 // No C++ exception leaves for Python.
 template <PyObject* (*F)(Args)>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -593,6 +641,7 @@ PyMethodDef g_methods[] = {
     {"cache_write", FAST((call<cache_write>))},
     {"cache_read", FAST((call<cache_read>))},
     {"decode_paged", FAST((call<decode_paged>))},
+    {"attention_packed", FAST((call<attention_packed>))},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

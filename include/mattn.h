@@ -598,6 +598,35 @@ int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int pa
                                  size_t* bytes_out);
 
 /*
+ * mattn_attention_packed -- attention over sequences laid end to end: sequence b has
+ * queries cu_seqlens_q_b .. cu_seqlens_q_{b+1} - 1 and keys cu_seqlens_k_b ..
+ * cu_seqlens_k_{b+1} - 1.  Query i of its n sees of its sequence's m keys
+ *   causal 0   all
+ *   causal 1   keys 0 .. m - n + i (the last query sees the last key; none where that
+ *              is negative), with window > 0 the last `window` of them
+ *   q, k, v    DEVICE bf16: element (t, h, c) at t * token_stride + h * head_stride +
+ *              c ([0] q, [1] k, [2] v), 16-byte aligned, strides positive multiples
+ *              of 8 (of a dimension of one entry: any)
+ *   o          DEVICE bf16 [T][H][d];  lse  DEVICE fp32 [H][T] or NULL
+ *   cu_seqlens_q, cu_seqlens_k  DEVICE int32 [B + 1], ascending, inside 0..T and
+ *              0..T_k (values outside are clamped); cu_seqlens_k NULL: cu_seqlens_q
+ *              (T_k = T).  Rows of no sequence are not used, and o and lse left as
+ *              they are there.  Sequences that share query rows: undefined.
+ *   sink       DEVICE fp32 [H] sink logits or NULL;  softmax_scale  0 => 1/sqrt(d)
+ *   d in {64, 80, 96, 128}; H a multiple of H_kv; T, T_k <= 2^30; H * (T / 256 + B) < 2^31.
+ * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Weights
+ * meet the values in bf16 as in mattn_fwd; sums, statistics and the LSE are fp32.
+ * What a query does not see (other sequences, later keys) has no part in its result,
+ * infinities and NaN among it.
+ */
+int mattn_attention_packed(const void* q, const void* k, const void* v, const int64_t token_stride[3],
+                           const int64_t head_stride[3], void* o, float* lse, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int B, int T, int T_k, int H, int H_kv, int d, int dtype,
+                           int causal, int window, const float* sink, float softmax_scale, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int mattn_attention_packed_workspace(int B, int T, int H, size_t* bytes_out);
+
+/*
  * mattn_plan_schedule -- the schedule mattn_fwd would run for these
  * arguments: one of the MATTN_FLAG_SCHEDULE_* flags (PAIRED, SPLIT, SINGLE,
  * PERSISTENT), the descriptor's own flag if it sets one, else the

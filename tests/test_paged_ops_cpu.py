@@ -196,3 +196,66 @@ def test_a_null_size_and_the_binding(L):
         mattn.cache_write(x, x, x, x, x)
     with pytest.raises(ValueError):
         mattn.cache_read(x, x, x, x)
+
+
+PACKED = dict(q=MB, k=2 * MB, v=3 * MB, token=(1024, 256, 256), head=(128, 128, 128), o=4 * MB, lse=None, cu=5 * MB, cu_k=None, B=3,
+              T=100, T_k=100, H=8, H_kv=2, d=128, dtype=BF16, causal=1, window=0, sink=None, scale=0.0, ws=256 * MB,
+              ws_bytes=1 << 20)
+
+
+def _packed(L, **kw):
+    a = dict(PACKED, **kw)
+    three = ctypes.c_int64 * 3
+    return L.mattn_attention_packed(a["q"], a["k"], a["v"], three(*a["token"]), three(*a["head"]), a["o"], a["lse"], a["cu"],
+                                    a["cu_k"], a["B"], a["T"], a["T_k"], a["H"], a["H_kv"], a["d"], a["dtype"], a["causal"],
+                                    a["window"], a["sink"], a["scale"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("why,kw,code", [
+    ("no queries", {"q": None}, -1),
+    ("no keys", {"k": None}, -1),
+    ("no output", {"o": None}, -1),
+    ("no cu_seqlens", {"cu": None}, -1),
+    ("no sequence", {"B": 0}, -1),
+    ("no head", {"H": 0}, -1),
+    ("H no multiple of H_kv", {"H_kv": 3}, -1),
+    ("a negative count", {"T": -1}, -1),
+    ("a negative count of keys", {"T_k": -1, "cu_k": MB}, -1),
+    ("other keys than queries and no cu_seqlens_k", {"T_k": 99}, -1),
+    ("more than 2^30 rows", {"T": (1 << 30) + 1, "T_k": (1 << 30) + 1}, -2),
+    ("2^31 items", {"T": 1 << 30, "T_k": 1 << 30, "H": 512}, -2),
+    ("head dim 256", {"d": 256}, -2),
+    ("head dim 72", {"d": 72}, -2),
+    ("fp32", {"dtype": F32}, -2),
+    ("a negative window", {"window": -4}, -1),
+    ("a window without causality", {"window": 4, "causal": 0}, -1),
+    ("queries off a 16-byte boundary", {"q": MB + 8}, -2),
+    ("cu_seqlens off a 4-byte boundary", {"cu": MB + 2}, -1),
+    ("lse off a 4-byte boundary", {"lse": MB + 2}, -1),
+    ("a stride off 16 bytes", {"token": (1024, 252, 256)}, -2),
+    ("a stride of zero", {"head": (128, 0, 128)}, -2),
+    ("a negative stride", {"token": (-1024, 256, 256)}, -2),
+    ("a stride of 2^40 bytes", {"token": (1 << 39, 256, 256)}, -2),
+    ("an infinite scale", {"scale": float("inf")}, -1),
+    ("a scale that is NaN", {"scale": float("nan")}, -1),
+    ("no workspace", {"ws": None}, -6),
+    ("a small workspace", {"ws_bytes": 64}, -6),
+    ("a workspace off a 256-byte boundary", {"ws": MB + 16}, -1),
+])
+def test_attention_packed_refuses(L, why, kw, code):
+    assert _packed(L, **kw) == code, why
+    assert L.mattn_last_error()
+
+
+def test_attention_packed_accepts(L):
+    """Only the device is missing: strides of single entries, no keys at all, the least workspace."""
+    ok = (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)
+    n = ctypes.c_size_t(0)
+    f = L.mattn_attention_packed_workspace
+    assert f(3, 100, 8, ctypes.byref(n)) == 0
+    assert _packed(L, ws_bytes=n.value) in ok and _packed(L, ws_bytes=n.value - 1) == mattn.ERR_CAPACITY
+    assert _packed(L, H_kv=1, head=(128, 0, -5)) in ok
+    assert _packed(L, T=1, T_k=1, token=(0, 0, 0)) in ok
+    assert _packed(L, T_k=0, k=None, v=None, cu_k=MB) in ok
+    assert f(0, 100, 8, ctypes.byref(n)) == -1 and f(3, -1, 8, ctypes.byref(n)) == -1 and f(3, 100, 8, None) == -1
+    assert f(1, 1 << 30, 1024, ctypes.byref(n)) == -2
