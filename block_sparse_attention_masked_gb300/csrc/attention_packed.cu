@@ -16,14 +16,15 @@
 // next item that none has (a counter) when the K tiles of its current one run out: long
 // prompts first, short ones fill the end.
 //
-// Rows that are not the sequence's.  Tiles begin at any packed row and reach into the
-// next sequence (past the last row TMA fills zeros): query rows past the end are not
-// written, keys past it are masked, and their value rows, whose weight is 0 but which may
-// hold an infinity or NaN, are zeroed in shared memory before the product.  For the same
-// reason values in tiles that some row sees in part are looked over, and those that are
-// not finite taken out of the product and added, row by row where they are seen, to the
-// output.  Both are the V producer's warp's work, beside the pipeline: a diagonal tile's
-// values are needed last.
+// What a row does not see.  Tiles begin at any packed row and reach into the next sequence
+// (past the last row TMA fills zeros): query rows past the end are not written, keys past
+// it are masked.  A hidden key's weight is 0, but 0 times an infinity or NaN among its
+// values is NaN, so a row whose output is not finite and that saw a tile in part marks its
+// item, and a CTA does its marked items again after its others: with those tiles' values
+// looked over in shared memory before the product, rows past the end and values that are
+// not finite taken out, and the latter added to the output of each row that sees them.
+// (Looking over every such tile the first time, beside the pipeline, cost 5% of the 16,384
+// tokens of eight prompts and 16% of a window of 576.)
 //
 // Roles (384 threads) and tensor memory: as attention_persist.cu; every wait is bounded
 // in time and gives up by raising a CTA-wide abort flag and a device error bit.
@@ -180,22 +181,46 @@ constexpr int kItems = 4;   // of the ring
 constexpr int kQSlots = 3;
 constexpr int kReaders = 11;  // of an item: the V producer, two issuers, eight softmax warps
 
-// An item as every role reads it; h < 0: no more.
+// An item as every role reads it, or (h < 0) the word to finish what is under way, after
+// which there is nothing more (kEnd) or may be (kDrain).
+constexpr int kDrain = -2, kEnd = -1;
 struct Item {
-  int q_row, rows, k_row, keys, pos0, h;
+  int q_row, rows, k_row, keys, pos0, h, id;
   int lo, n;                    // its key tiles lo .. lo + n - 1
   int lo0, hi0, lo1, hi1;       // those of each query tile (hi < lo: none)
-  int odd;                      // values that are not finite were taken out of a tile
+  int marked;                   // some row of its output is not finite
+  int again;                    // the second time
+  __device__ __forceinline__ void set(const PackedParams& p, int item) {
+    const PackedPair* src = &p.plan->pair[item / p.H];
+    const int4 a = *reinterpret_cast<const int4*>(src);
+    q_row = a.x; rows = a.y; k_row = a.z; keys = a.w;
+    pos0 = src->pos0;
+    h = item % p.H;
+    id = item;
+    seen_tiles(p, pos0, min(rows, 128), keys, &lo0, &hi0);
+    seen_tiles(p, pos0 + 128, min(rows - 128, 128), keys, &lo1, &hi1);
+    lo = hi0 < lo0 ? lo1 : (hi1 < lo1 ? lo0 : min(lo0, lo1));
+    const int end = max(hi0, hi1);
+    n = end < lo ? 0 : end - lo + 1;
+  }
   __device__ __forceinline__ bool uses(int s, int kt) const { return s ? kt >= lo1 && kt <= hi1 : kt >= lo0 && kt <= hi0; }
   __device__ __forceinline__ int first(int s) const { return s ? (hi1 < lo1 ? -1 : lo1) : (hi0 < lo0 ? -1 : lo0); }
   __device__ __forceinline__ int last(int s) const { return s ? hi1 : hi0; }
-  // whether some row of query tile s (that uses it) does not see all of key tile kt
-  __device__ __forceinline__ bool partial(const PackedParams& p, int s, int kt) const {
-    const int k1 = kt * 128 + 127;
-    if (k1 >= keys) return true;
-    if (!p.causal) return false;
+  // the key tiles [lo, hi] that every row of query tile s sees whole
+  __device__ __forceinline__ void whole(const PackedParams& p, int s, int* lo, int* hi) const {
     const int pos = pos0 + 128 * s;
-    return k1 > pos || (p.window && kt * 128 <= pos + min(rows - 128 * s, 128) - 1 - p.window);
+    *hi = ((p.causal ? min(keys, pos + 1) : keys) >> 7) - 1;
+    *lo = p.window ? (max(0, pos + min(rows - 128 * s, 128) - p.window) + 127) >> 7 : 0;
+  }
+  // whether some row of a query tile that multiplies key tile kt does not see all of it
+  __device__ __forceinline__ bool partial(const PackedParams& p, int kt) const {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      int whole_lo, whole_hi;
+      whole(p, s, &whole_lo, &whole_hi);
+      if (uses(s, kt) && (kt < whole_lo || kt > whole_hi)) return true;
+    }
+    return false;
   }
 };
 
@@ -208,6 +233,7 @@ struct Bar {
   uint32_t tmem_base;
   int abort_flag;
   uint32_t mma_turn;
+  int marked;              // the CTA's last marked item, from which PackedParams::marked leads to the others; -1: none
   Item items[kItems];
 };
 
@@ -244,6 +270,8 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
   int id = blockIdx.x;
   int pub = 0;        // items published
   bool done = false;  // the last of them is the end
+  bool again = false; // the marked items' turn has come
+  int drain = -1;     // the item whose end it waits for
   int qi = 0, qs = 0, t = 0;
   int ki = 0, kj = 0, e = 0;
   uint64_t t_idle = 0;
@@ -252,27 +280,26 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
     bool moved = false;
     // the next item, once the K tiles of the current one run out
     if (!done && (pub == ki || (pub == ki + 1 && bar->items[ki % kItems].n - kj <= 4)) && pub < qi + kItems &&
-        ptx::mbar_test_wait(&bar->item_empty[pub % kItems], ((pub / kItems) & 1) ^ 1)) {
+        ptx::mbar_test_wait(&bar->item_empty[pub % kItems], ((pub / kItems) & 1) ^ 1) &&
+        (drain < 0 || ptx::mbar_test_wait(&bar->item_empty[drain % kItems], (drain / kItems) & 1))) {
+      if (drain >= 0) {  // every item so far is written
+        drain = -1;
+        again = true;
+        id = *reinterpret_cast<volatile int*>(&bar->marked);
+      }
       Item& it = bar->items[pub % kItems];
-      if (id < total) {
-        const PackedPair* src = &p.plan->pair[id / p.H];
-        const int4 a = *reinterpret_cast<const int4*>(src);
-        const int pos0 = src->pos0;
-        it.q_row = a.x; it.rows = a.y; it.k_row = a.z; it.keys = a.w; it.pos0 = pos0;
-        it.h = id % p.H;
-        int lo0, hi0, lo1, hi1;
-        seen_tiles(p, pos0, min(a.y, 128), a.w, &lo0, &hi0);
-        seen_tiles(p, pos0 + 128, min(a.y - 128, 128), a.w, &lo1, &hi1);
-        it.lo0 = lo0; it.hi0 = hi0; it.lo1 = lo1; it.hi1 = hi1;
-        const int lo = hi0 < lo0 ? lo1 : (hi1 < lo1 ? lo0 : min(lo0, lo1)), hi = max(hi0, hi1);
-        it.lo = lo;
-        it.n = hi < lo ? 0 : hi - lo + 1;
-        it.odd = 0;
-        id = gridDim.x + atomicAdd(&p.plan->next, 1);
+      if (again ? id >= 0 : id < total) {
+        it.set(p, id);
+        it.marked = 0;
+        it.again = again ? 1 : 0;
+        id = again ? p.marked[id] : gridDim.x + atomicAdd(&p.plan->next, 1);
       } else {
-        it.h = -1;
+        it.h = again ? kEnd : kDrain;
         it.n = 0;
-        done = true;
+        it.lo0 = it.lo1 = 0;
+        it.hi0 = it.hi1 = -1;
+        done = again;
+        if (!again) drain = pub;
       }
       ptx::mbar_arrive(&bar->item_full[pub % kItems]);
       ++pub;
@@ -336,47 +363,55 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
   let_copies_land(abort_flag);
 }
 
-// Whether a 16-bit half of x is an infinity or NaN; taken out (a zero) by clean().
+// The 16-bit halves of x that are no infinity or NaN, and zeros for those that are.
 __device__ __forceinline__ uint32_t clean(uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
 
-// A landed V tile: rows from `rows` on become zeros; with `look`, so do values that are
-// not finite in the others (true: there were some).  One warp; the layout does not
-// matter, as a row's columns lie in rows of every chunk.
+// A landed V tile: rows from `rows` on and values that are not finite become zeros.  One
+// warp; the layout does not matter, as a row's columns lie in rows of every chunk.
 template <int D>
-__device__ __forceinline__ bool clean_tile(uint8_t* tile, int rows, bool look) {
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int rows) {
   using G = Geo<D>;
   constexpr int kRow = G::kVW * 2;
-  const int lane = threadIdx.x & 31;
-  bool odd = false;
-  if (look) {
-    uint32_t top = 0;
-    const int n = rows * kRow / 16;  // 16-byte pieces of a chunk
-    for (int c = 0; c < G::kVChunks; ++c) {
-      const uint4* x = reinterpret_cast<const uint4*>(tile + c * G::kVChunkBytes);
-#pragma unroll 8
-      for (int i = lane; i < n; i += 32) {
-        const uint4 v = x[i];
-        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-        top = __vmaxu2(__vmaxu2(top, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
-      }
+  const int lane = threadIdx.x & 31, n = rows * kRow / 16;  // 16-byte pieces of a chunk
+  for (int c = 0; c < G::kVChunks; ++c) {
+    uint4* x = reinterpret_cast<uint4*>(tile + c * G::kVChunkBytes);
+    for (int i = lane; i < kTile * kRow / 16; i += 32) {
+      const uint4 v = x[i];
+      x[i] = i < n ? make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w)) : make_uint4(0, 0, 0, 0);
     }
-    odd = __any_sync(0xffffffffu, max(top >> 16, top & 0xffffu) >= 0x7f80u);
-    if (odd) {
-      for (int c = 0; c < G::kVChunks; ++c) {
-        uint4* x = reinterpret_cast<uint4*>(tile + c * G::kVChunkBytes);
-        for (int i = lane; i < n; i += 32) {
-          const uint4 v = x[i];
-          x[i] = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-        }
+  }
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+}
+
+// A marked item's output, written the second time without the values that are not finite
+// and that some row of their tile does not see: they are added to the rows that see them
+// (with a positive weight each).  A thread a row.
+template <int D>
+__device__ __forceinline__ void add_odd_values(const PackedParams& p, const Item& it, int row) {
+  const int s = row >> 7;
+  int lo = 0, hi = it.keys - 1;
+  if (p.causal) {
+    hi = min(hi, it.pos0 + row);
+    if (p.window) lo = max(0, it.pos0 + row - p.window + 1);
+  }
+  if (row >= it.rows || it.first(s) < 0) return;
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.o) + (((int64_t)it.q_row + row) * p.H + it.h) * D;
+  for (int kt = it.lo; kt < it.lo + it.n; ++kt) {
+    if (!it.partial(p, kt)) continue;
+    for (int j = max(lo, kt * kTile); j <= min(hi, kt * kTile + kTile - 1); ++j) {
+      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + (it.k_row + (int64_t)j) * p.v_token +
+                               (it.h / p.group) * p.v_head;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 2) {
+        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(v + c)), odd = x ^ clean(x);
+        if (!odd) continue;
+        __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(o + c);
+        const float2 y = __bfloat1622float2(*to);
+        *to = __floats2bfloat162_rn(y.x + __uint_as_float(odd << 16), y.y + __uint_as_float(odd & 0xffff0000u));
       }
     }
   }
-  for (int c = 0; c < G::kVChunks; ++c)
-    for (int i = rows * kRow / 16 + lane; i < kTile * kRow / 16; i += 32)
-      *reinterpret_cast<uint4*>(tile + c * G::kVChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
-  ptx::fence_proxy_async_shared();
-  __syncwarp();
-  return odd;
 }
 
 // Waits for the CTA's item i; null if the wait gave up.
@@ -387,6 +422,27 @@ __device__ __forceinline__ const Item* take_item(const PackedParams& p, Bar* bar
 __device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, after its last read)
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar->item_empty[i % kItems]);
+}
+
+// This thread's row of a tile that it sees in part: the scores of columns outside [lo, hi]
+// (none inside where lo > hi) become -inf where they lie, in tensor memory.  In the pass
+// over the scores itself the same selects slow every tile, masked or not (its code is
+// fetched and its registers are held: one sequence of 16,384 363 us,
+// 359 with the tiles' bounds read each time, 348 so).
+__device__ __forceinline__ void mask_scores(uint32_t s_tmem, int lo, int hi) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t vis = range_bits(g, lo, hi);
+    if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
+    float x[32];
+    ptx::tmem_ld32(s_tmem + 32 * g, x);
+    ptx::tmem_wait_ld();
+    uint32_t u[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) u[j] = (vis >> j) & 1u ? __float_as_uint(x[j]) : 0xff800000u;
+    ptx::tmem_st32(s_tmem + 32 * g, u);
+  }
+  ptx::tmem_wait_st();
 }
 
 template <int D>
@@ -429,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     }
     bar->abort_flag = 0;
     bar->mma_turn = 0;
+    bar->marked = -1;
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
@@ -457,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         ok = false;
         break;
       }
-      if (it->h < 0) break;
-      const int n = it->n, lo = it->lo, keys = it->keys, k_row = it->k_row, h = it->h / p.group;
+      if (it->h == kEnd) break;
+      const int n = it->n, lo = it->lo, keys = it->keys, k_row = it->k_row, h = it->h / p.group;  // (kDrain: n = 0)
       for (int j = 0; j < n; ++j, ++e) {
         const int slot = e % VS, kt = lo + j;
         uint8_t* tile = sv + slot * G::kTileBytes;
@@ -466,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           ok = false;
           break;
         }
-        const bool look = (it->uses(0, kt) && it->partial(p, 0, kt)) || (it->uses(1, kt) && it->partial(p, 1, kt));
+        const bool look = it->again && it->partial(p, kt);
         uint64_t* landing = look ? &bar->v_land : &bar->v_full[slot];
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(landing, G::kTileBytes);
@@ -481,11 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
             break;
           }
           ++lands;
-          const bool odd = clean_tile<D>(tile, min(keys - kt * kTile, kTile), true);
-          if (lane == 0) {
-            if (odd) const_cast<Item*>(it)->odd = 1;
-            ptx::mbar_arrive(&bar->v_full[slot]);
-          }
+          clean_tile<D>(tile, min(keys - kt * kTile, kTile));
+          if (lane == 0) ptx::mbar_arrive(&bar->v_full[slot]);
         }
       }
       if (ok) drop_item(bar, i);
@@ -510,16 +564,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     const uint32_t o_tm = tmem + 256 + s * 128;
     bool ok = true, issued_any = false;
     bool pend = false, pend_first = false, pend_last = false;
+    bool open = false;    // entry e - 1's V is not released yet
     uint32_t pcount = 0;  // P tiles consumed
     int e = 0;
     int t = 0;  // Q tiles of both query tiles so far
+    // the last entry so far: its V slot and this query tile's pending P V
+    auto finish = [&]() {
+      if (!open) return true;
+      const int ve = e - 1;
+      if (!wait_all(&bar->v_full[ve % VS], (ve / VS) & 1)) return false;
+      if (pend) {
+        if (!wait_all(&bar->p_full[s], pcount & 1)) return false;
+        ++pcount;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) issue_pv<D>(o_tm, s_tm, v4 + (ve % VS) * tile4, !pend_first);
+        __syncwarp();
+        ptx::mma_commit_elect(&bar->o_full[s]);
+      }
+      ptx::mma_commit_elect(&bar->v_empty[ve % VS]);
+      pend = open = false;
+      return true;
+    };
     for (int i = 0; ok; ++i) {
       const Item* it = take_item(p, bar, i, abort_flag);
       if (!it) {
         ok = false;
         break;
       }
-      if (it->h < 0) break;
+      const int what = it->h;
+      if (what < 0) {
+        drop_item(bar, i);
+        ok = finish();
+        if (what == kEnd) break;
+        continue;
+      }
       const int n = it->n, lo = it->lo;
       const int first_use = it->first(s), last_use = it->last(s);
       const int has0 = it->first(0) >= 0, has1 = it->first(1) >= 0;
@@ -532,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         const int kt = lo + j;
         const bool use = first_use >= 0 && kt >= first_use && kt <= last_use;
         const int ks = e % KS;
-        const bool rel_v = e >= 1;
+        const bool rel_v = open;
         const int ve = e - 1;
         if (rel_v && !wait_all(&bar->v_full[ve % VS], (ve / VS) & 1)) { ok = false; break; }
         if (!wait_all(&bar->k_full[ks], (e / KS) & 1)) { ok = false; break; }
@@ -558,27 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         ptx::mma_commit_elect(&bar->k_empty[ks]);
         if (pend && pend_last) ptx::mma_commit_elect(&bar->o_full[s]);
         if (use && kt == last_use) ptx::mma_commit_elect(&bar->q_empty[qslot]);
+        open = true;
         pend = use;
         pend_first = use && kt == first_use;
         pend_last = use && kt == last_use;
       }
-    }
-    if (ok && e >= 1) {
-      // the last entry: its V slot and this query tile's pending P V
-      const int ve = e - 1;
-      if (!wait_all(&bar->v_full[ve % VS], (ve / VS) & 1)) ok = false;
-      if (ok && pend) {
-        if (!wait_all(&bar->p_full[s], pcount & 1)) {
-          ok = false;
-        } else {
-          ++pcount;
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) issue_pv<D>(o_tm, s_tm, v4 + (ve % VS) * tile4, !pend_first);
-          __syncwarp();
-          ptx::mma_commit_elect(&bar->o_full[s]);
-        }
-      }
-      if (ok) ptx::mma_commit_elect(&bar->v_empty[ve % VS]);
     }
     if (!ok) {
       if (lane == 0) fail(p, bar, kErrMma);
@@ -608,7 +670,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         if (lane == 0) fail(p, bar, kErrSoftmax);
         break;
       }
-      if (it->h < 0) break;
+      if (it->h == kEnd) break;
+      if (it->h == kDrain) {
+        drop_item(bar, i);
+        continue;
+      }
       const int keys = it->keys, h = it->h;
       const bool valid = row < it->rows - 128 * s;
       const int pos = it->pos0 + 128 * s + row;
@@ -619,6 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       }
       if (!valid) hi = -1;
       const int first = it->first(s), last = it->last(s);
+      int whole_lo, whole_hi;
+      it->whole(p, s, &whole_lo, &whole_hi);
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain
       float l = 0.f;        // running sum of exp2(x - m)
       for (int kt = first < 0 ? last + 1 : first; kt <= last; ++kt) {
@@ -630,17 +698,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         }
         ++count;
         ptx::tc_fence_after();
+        bool sees = valid;  // this row sees a key of the tile
+        if (kt < whole_lo || kt > whole_hi) {
+          const int c_lo = max(lo - kt * kTile, 0), c_hi = min(hi - kt * kTile, 127);
+          mask_scores(s_tmem, c_lo, c_hi);
+          sees = c_lo <= c_hi;
+        }
         float x[128];
         ptx::tmem_ld32(s_tmem + 0, *reinterpret_cast<float(*)[32]>(&x[0]));
         ptx::tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
         ptx::tmem_ld32(s_tmem + 64, *reinterpret_cast<float(*)[32]>(&x[64]));
         ptx::tmem_ld32(s_tmem + 96, *reinterpret_cast<float(*)[32]>(&x[96]));
         ptx::tmem_wait_ld();
-        bool sees = valid;  // this row sees a key of the tile
-        if (it->partial(p, s, kt)) {
-          const int k0 = kt * kTile;
-          sees = mask_row(x, min(max(lo - k0, -1), 128), min(max(hi - k0, -1), 128), -1);
-        }
         // P = exp2(s * scale * log2e - m) into tensor memory, by the stale-max rule of
         // attention_fwd.cu; rows past the sequence's end (another's, or nothing) take
         // no part in it
@@ -691,7 +760,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         ++o_items;
         ptx::tc_fence_after();
       }
-      const bool odd = has_o && *reinterpret_cast<const volatile int*>(&it->odd);
+      // a row's output that is not finite may be a hidden key's values' doing (see above)
+      const bool part = has_o && (first < whole_lo || last > whole_hi) && !it->again;
+      float2 sum = make_float2(0.f, 0.f);
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (q_row * p.H + h) * D;
       const uint64_t o_policy = ptx::l2_policy_evict_first();
 #pragma unroll 1
@@ -706,21 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
 #pragma unroll
           for (int k = 0; k < 16; ++k) ov[k] = 0.f;
         }
-        if (odd && valid) {
-          // values that are not finite and were taken out of tiles seen in part: each
-          // has a positive weight in the rows that see it
-          for (int kt = it->lo; kt < it->lo + it->n; ++kt) {
-            if (!((it->uses(0, kt) && it->partial(p, 0, kt)) || (it->uses(1, kt) && it->partial(p, 1, kt)))) continue;
-            for (int j = max(lo, kt * kTile); j <= min(hi, kt * kTile + kTile - 1); ++j) {
-              const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + (it->k_row + (int64_t)j) * p.v_token +
-                                       (h / p.group) * p.v_head + c0;
+        if (part) {  // (a sum is finite only if its terms are)
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float y = __bfloat162float(v[k]);
-                if (!(fabsf(y) < INFINITY)) ov[k] += y;
-              }
-            }
-          }
+          for (int k = 0; k < 16; k += 2) sum = ptx::fadd2(sum, make_float2(ov[k], ov[k + 1]));
         }
         if (valid) {
           uint32_t pk[8];
@@ -731,6 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
         }
       }
+      if (__any_sync(0xffffffffu, part && valid && !(fabsf(sum.x + sum.y) < INFINITY)) && lane == 0 &&
+          atomicExch(&const_cast<Item*>(it)->marked, 1) == 0)
+        p.marked[it->id] = atomicExch(&bar->marked, it->id);
       drop_item(bar, i);
     }
   }
@@ -740,6 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x < 256 && !*abort_flag) {
+    for (int id = bar->marked; id >= 0; id = p.marked[id]) {
+      Item it;
+      it.set(p, id);
+      add_odd_values<D>(p, it, threadIdx.x);
+    }
   }
 }
 

@@ -167,7 +167,11 @@ int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dt
   return MATTN_OK;
 }
 
-size_t packed_bytes(int64_t T, int64_t B) { return sizeof(PackedPlan) + (size_t)packed_pairs(T, B) * sizeof(PackedPair); }
+// The plan, then the links of marked items.
+size_t packed_plan_bytes(int64_t T, int64_t B) {
+  return round256(sizeof(PackedPlan) + (size_t)packed_pairs(T, B) * sizeof(PackedPair));
+}
+size_t packed_bytes(int64_t T, int64_t B, int64_t H) { return packed_plan_bytes(T, B) + (size_t)(packed_pairs(T, B) * H) * 4; }
 
 int check_packed(int B, int T, int H) {
   if (B < 1 || H < 1 || T < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: B, H must be >= 1 and T >= 0");
@@ -295,7 +299,7 @@ int mattn_attention_packed_workspace(int B, int T, int H, size_t* bytes_out) {
   if (!bytes_out) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: bytes_out is NULL");
   const int rc = check_packed(B, T, H);
   if (rc) return rc;
-  *bytes_out = packed_bytes(T, B);
+  *bytes_out = packed_bytes(T, B, H);
   return MATTN_OK;
 }
 
@@ -335,7 +339,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
       return report_error(MATTN_ERR_UNSUPPORTED,
                           "attention_packed: strides must be positive multiples of 16 bytes below 2^40");
   }
-  if ((rc = check_workspace("attention_packed", workspace, workspace_bytes, packed_bytes(T, B)))) return rc;
+  if ((rc = check_workspace("attention_packed", workspace, workspace_bytes, packed_bytes(T, B, H)))) return rc;
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   if (T == 0) return MATTN_OK;
@@ -361,6 +365,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.cu_q = cu_seqlens_q;
   p.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q;
   p.plan = static_cast<PackedPlan*>(workspace);
+  p.marked = reinterpret_cast<int*>(static_cast<char*>(workspace) + packed_plan_bytes(T, B));
   p.err = err;
   p.timeout_ns = device_wait_timeout_ns();
   p.B = B; p.T = T; p.T_k = T_k; p.H = H; p.H_kv = H_kv;
