@@ -424,6 +424,13 @@ __device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, afte
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar->item_empty[i % kItems]);
 }
 
+// 32 bytes of an output row, written once and not read again here: first out of L2.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8], uint64_t policy) {
+  asm volatile("st.global.L1::no_allocate.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "l"(policy)
+               : "memory");
+}
+
 // This thread's row of a tile that it sees in part: the scores of columns outside [lo, hi]
 // (none inside where lo > hi) become -inf where they lie, in tensor memory.  In the pass
 // over the scores itself the same selects slow every tile, masked or not (its code is
@@ -785,9 +792,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
           uint32_t pk[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) pk[k] = ptx::pack_bf16x2(ov[2 * k], ov[2 * k + 1]);
-          uint4* to = reinterpret_cast<uint4*>(dst + c0);
-          ptx::st_global_v4_hint(to, make_uint4(pk[0], pk[1], pk[2], pk[3]), o_policy);
-          ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
+          if (p.wide) {
+            st_global_32(dst + c0, pk, o_policy);
+          } else {
+            uint4* to = reinterpret_cast<uint4*>(dst + c0);
+            ptx::st_global_v4_hint(to, make_uint4(pk[0], pk[1], pk[2], pk[3]), o_policy);
+            ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
+          }
         }
       }
       if (__any_sync(0xffffffffu, part && valid && !(fabsf(sum.x + sum.y) < INFINITY)) && lane == 0 &&

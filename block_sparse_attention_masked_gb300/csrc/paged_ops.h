@@ -86,6 +86,7 @@ struct PackedParams {
   unsigned long long timeout_ns;
   int B, T, T_k, H, H_kv, group;
   int causal, window;            // window 0: none
+  int wide;                      // o is 32-byte aligned
   int max_pairs, work_shift;
   float scale_log2;
   int selftest;                  // 1: the first K tile is left out, so that the wait for it runs out

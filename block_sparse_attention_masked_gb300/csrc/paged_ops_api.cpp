@@ -371,6 +371,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.B = B; p.T = T; p.T_k = T_k; p.H = H; p.H_kv = H_kv;
   p.group = H / H_kv;
   p.causal = causal ? 1 : 0;
+  p.wide = aligned(o, 32) ? 1 : 0;
   p.window = window < kMaxRows ? window : (int)kMaxRows;
   p.max_pairs = (int)packed_pairs(T, B);
   while (((2 * ((int64_t)T_k / 128 + 1)) >> p.work_shift) >= 1024) ++p.work_shift;
