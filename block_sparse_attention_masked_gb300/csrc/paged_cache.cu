@@ -8,8 +8,7 @@
 // tensor in eight bits, 4 d in bf16).
 //
 // d / 16 lanes take a row, two 16-byte pieces each, half a row apart, so that every
-// load and store of a warp covers whole 32-byte sectors; rows go to warps in memory
-// order of the packed side, U groups' loads together.
+// load and store of a warp covers whole 32-byte sectors.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -101,114 +100,119 @@ __device__ __forceinline__ uint4 values8(uint2 c, float f) {
                     values2(e4m3::to_half2_hi(c.y), f));
 }
 
+// A lane group takes a token, `heads` of its heads and k and v of each: one look-up of the
+// place, pointers moved from head to head, U heads' loads together.
 template <int D, bool E8, bool READ>
 __global__ void __launch_bounds__(kCacheThreads) cache_rows_kernel(const __grid_constant__ CacheRowsParams p) {
-  constexpr int LPR = D / 16, RW = 32 / LPR, U = 2;
+  constexpr int LPR = D / 16, GW = 32 / LPR, U = 2;
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t warp = (int64_t)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
-  const int64_t rows = (int64_t)p.T * p.H_kv;
-  int64_t r = warp * p.per_warp * RW + sub;  // this lane's first row
+  // (segments of a token's heads are neighbours, then tokens: GW tokens a warp and segment)
+  const int64_t block = warp / p.segs;
+  const int seg = (int)(warp - block * p.segs), t = (int)(block * GW) + sub;
+  const int h0 = seg * p.heads, h1 = min(h0 + p.heads, p.H_kv);
   after_previous();
-  if (r - sub >= rows) return;  // (whole warps)
-  int t = (int)(r / p.H_kv), h = (int)(r - (int64_t)t * p.H_kv);
-  int b = sequence_of(p, t);
-  for (int g = 0; g < p.per_warp; g += U) {
-    uint4 x[U][2][2];  // [..][tensor][half of the row]
-    Place at[U];
-    int ts[U], hs[U];
-    bool live[U];
-    uint32_t ex[U][2];
+  if (block * GW >= p.T) return;  // (whole warps)
+  int b = t < p.T ? sequence_of(p, t) : 0;
+  Place at;
+  at.page = -1;
+  const bool row = t < p.T && locate(p, t, b, at);  // (a row of some sequence)
+  const bool there = row && at.page >= 0;
+  // this lane's piece of the head's row and of its place, for k and v
+  const char* src[2];
+  char* dst[2];
+  int64_t src_step[2], dst_step[2], exp_step[2];
+  uint8_t* ex[2];
+  constexpr int kCell = E8 ? 1 : 2;  // bytes of a cached value
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      live[u] = r < rows && g + u < p.per_warp && locate(p, t, b, at[u]);
-      ts[u] = t;
-      hs[u] = h;
-      if (!READ) live[u] = live[u] && at[u].page >= 0;
-      const bool has = live[u] && at[u].page >= 0;
+  for (int i = 0; i < 2; ++i) {
+    char* r = static_cast<char*>(p.rows[i]) + 2 * (t * p.row_token[i] + h0 * p.row_head[i] + l * 8);
+    char* c = static_cast<char*>(p.pages[i]) +
+              kCell * ((there ? at.page * p.page_stride[i] + at.row * p.row_stride[i] : 0) + h0 * p.head_stride[i] + l * 8);
+    src[i] = READ ? c : r;
+    dst[i] = READ ? r : c;
+    src_step[i] = READ ? kCell * p.head_stride[i] : 2 * p.row_head[i];
+    dst_step[i] = READ ? 2 * p.row_head[i] : kCell * p.head_stride[i];
+    if (E8) {
+      ex[i] = p.exps[i] + (there ? at.page * p.exp_page[i] + at.row * p.exp_row[i] : 0) + h0 * p.exp_head[i];
+      exp_step[i] = p.exp_head[i];
+    }
+  }
+  for (int h = h0; h < h1; h += U) {
+    uint4 x[U][2][2];  // [..][tensor][half of the row]
+    uint32_t e[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         x[u][i][0] = x[u][i][1] = make_uint4(0, 0, 0, 0);
-        ex[u][i] = 0;
-        if (!has) continue;
-        if (READ && E8) {
-          const uint8_t* src = static_cast<const uint8_t*>(p.pages[i]) + at[u].page * p.page_stride[i] +
-                               h * p.head_stride[i] + at[u].row * p.row_stride[i] + l * 8;
-          const uint2 a = ld8(src), c = ld8(src + D / 2);
-          x[u][i][0] = make_uint4(a.x, a.y, c.x, c.y);
-          ex[u][i] = __ldg(p.exps[i] + at[u].page * p.exp_page[i] + h * p.exp_head[i] + at[u].row * p.exp_row[i]);
-        } else {
-          const __nv_bfloat16* src =
-              READ ? static_cast<const __nv_bfloat16*>(p.pages[i]) + at[u].page * p.page_stride[i] +
-                         h * p.head_stride[i] + at[u].row * p.row_stride[i]
-                   : static_cast<const __nv_bfloat16*>(p.rows[i]) + t * p.row_token[i] + h * p.row_head[i];
-          x[u][i][0] = ld16(src + l * 8);
-          x[u][i][1] = ld16(src + D / 2 + l * 8);
+        e[u][i] = 0;
+        if (there && h + u < h1) {
+          if (READ && E8) {
+            const uint2 a = ld8(src[i]), c = ld8(src[i] + D / 2);
+            x[u][i][0] = make_uint4(a.x, a.y, c.x, c.y);
+            e[u][i] = __ldg(ex[i]);
+          } else {
+            x[u][i][0] = ld16(src[i]);
+            x[u][i][1] = ld16(src[i] + D);
+          }
         }
+        src[i] += src_step[i];
+        if (READ && E8) ex[i] += exp_step[i];
       }
-      r += RW;
-      h += RW;
-      while (h >= p.H_kv) {
-        h -= p.H_kv;
-        ++t;
-      }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (READ) {
-          if (!live[u]) continue;
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.rows[i]) + ts[u] * p.row_token[i] + hs[u] * p.row_head[i] + l * 8;
           uint4 lo = x[u][i][0], hi = x[u][i][1];
           if (E8) {
-            const float f = e4m3::power((int)ex[u][i]);
+            const float f = e4m3::power((int)e[u][i]);
             hi = values8(make_uint2(lo.z, lo.w), f);
             lo = values8(make_uint2(lo.x, lo.y), f);
           }
-          *reinterpret_cast<uint4*>(dst) = lo;
-          *reinterpret_cast<uint4*>(dst + D / 2) = hi;
-          continue;
-        }
-        int e = 0;
-        if (E8) {  // (all lanes: rows of one warp end together)
+          if (row && h + u < h1) {
+            *reinterpret_cast<uint4*>(dst[i]) = lo;
+            *reinterpret_cast<uint4*>(dst[i] + D) = hi;
+          }
+        } else if (E8) {
           const uint4 a = x[u][i][0], c = x[u][i][1];
           uint32_t m = max_abs(max_abs(max_abs(max_abs(0, a.x), a.y), a.z), a.w);
           m = max_abs(max_abs(max_abs(max_abs(m, c.x), c.y), c.z), c.w);
 #pragma unroll
           for (int off = 1; off < LPR; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
           m = max(m >> 16, m & 0xffffu);
-          e = e4m3::row_exponent(m);
+          const int power = e4m3::row_exponent(m);
+          const float f = e4m3::inverse(power);
+          if (there && h + u < h1) {
+            *reinterpret_cast<uint2*>(dst[i]) = codes8(a, f);
+            *reinterpret_cast<uint2*>(dst[i] + D / 2) = codes8(c, f);
+            if (l == 0) *ex[i] = (uint8_t)power;
+          }
+          ex[i] += exp_step[i];
+        } else if (there && h + u < h1) {
+          *reinterpret_cast<uint4*>(dst[i]) = x[u][i][0];
+          *reinterpret_cast<uint4*>(dst[i] + D) = x[u][i][1];
         }
-        if (!live[u]) continue;
-        const int64_t to = at[u].page * p.page_stride[i] + hs[u] * p.head_stride[i] + at[u].row * p.row_stride[i] + l * 8;
-        if (E8) {
-          uint8_t* dst = static_cast<uint8_t*>(p.pages[i]) + to;
-          const float f = e4m3::inverse(e);
-          *reinterpret_cast<uint2*>(dst) = codes8(x[u][i][0], f);
-          *reinterpret_cast<uint2*>(dst + D / 2) = codes8(x[u][i][1], f);
-          if (l == 0)
-            p.exps[i][at[u].page * p.exp_page[i] + hs[u] * p.exp_head[i] + at[u].row * p.exp_row[i]] = (uint8_t)e;
-        } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.pages[i]) + to;
-          *reinterpret_cast<uint4*>(dst) = x[u][i][0];
-          *reinterpret_cast<uint4*>(dst + D / 2) = x[u][i][1];
-        }
+        dst[i] += dst_step[i];
       }
-    }
-    if (__all_sync(0xffffffffu, r >= rows)) break;
   }
 }
 
 template <int D, bool E8, bool READ>
 cudaError_t launch_d(const CacheRowsParams& p0, cudaStream_t stream) {
   CacheRowsParams p = p0;
-  constexpr int RW = 32 / (D / 16);
-  const int64_t groups = ((int64_t)p.T * p.H_kv + RW - 1) / RW;
-  // groups of a warp: more than one only where the machine has eight warps a
-  // scheduler without
-  const int64_t most = groups / (kPlanSms * 32);
-  p.per_warp = (int)(most < 2 ? (most < 1 ? 1 : 2) : (most > 8 ? 8 : (most & ~int64_t(1))));
-  const int64_t warps = (groups + p.per_warp - 1) / p.per_warp, ctas = (warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32);
+  constexpr int GW = 32 / (D / 16);
+  // Heads of a lane group: all of a token's, fewer where that leaves the machine without
+  // its 32 warps an SM.
+  const int64_t blocks = ((int64_t)p.T + GW - 1) / GW;
+  int64_t segs = (kPlanSms * 32 + blocks - 1) / blocks;
+  const int64_t most = (p.H_kv + 1) / 2;
+  segs = segs < 1 ? 1 : (segs > most ? most : segs);
+  p.heads = (int)((p.H_kv + segs - 1) / segs);
+  p.heads += p.heads & 1;
+  p.segs = (p.H_kv + p.heads - 1) / p.heads;
+  const int64_t warps = blocks * p.segs, ctas = (warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32);
   return launch_chained(cache_rows_kernel<D, E8, READ>, (unsigned)ctas, 1, kCacheThreads, 0, 1, p, stream);
 }
 

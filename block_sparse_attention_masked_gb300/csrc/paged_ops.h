@@ -25,7 +25,7 @@ struct CacheRowsParams {
   const int32_t* starts;     // [B] position of a sequence's first row, or null: 0
   int B, T, H_kv, d;
   int page, table_pages, n_pages;
-  int per_warp;              // groups of rows of a warp
+  int heads, segs;           // of a lane group; segs of them are a token (set by the launch)
 };
 cudaError_t launch_cache_write(const CacheRowsParams& p, bool e4m3, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsParams& p, bool e4m3, cudaStream_t stream);
