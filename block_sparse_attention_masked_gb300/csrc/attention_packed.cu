@@ -190,11 +190,10 @@ struct Item {
   int lo0, hi0, lo1, hi1;       // those of each query tile (hi < lo: none)
   int marked;                   // some row of its output is not finite
   int again;                    // the second time
-  __device__ __forceinline__ void set(const PackedParams& p, int item) {
-    const PackedPair* src = &p.plan->pair[item / p.H];
-    const int4 a = *reinterpret_cast<const int4*>(src);
+  __device__ __forceinline__ void set(const PackedParams& p, const PackedPair& pair, int item) {
+    const int4 a = *reinterpret_cast<const int4*>(&pair);
     q_row = a.x; rows = a.y; k_row = a.z; keys = a.w;
-    pos0 = src->pos0;
+    pos0 = pair.pos0;
     h = item % p.H;
     id = item;
     seen_tiles(p, pos0, min(rows, 128), keys, &lo0, &hi0);
@@ -235,7 +234,39 @@ struct Bar {
   uint32_t mma_turn;
   int marked;              // the CTA's last marked item, from which PackedParams::marked leads to the others; -1: none
   Item items[kItems];
+  PackedPair direct[kPackedDirect];  // the CTA's items' pairs, where there is no plan
+  int direct_total;                  // items of the grid
+  __device__ __forceinline__ const PackedPair& pair(const PackedParams& p, int item) const {
+    return p.direct ? direct[(item - blockIdx.x) / gridDim.x] : p.plan->pair[item / p.H];
+  }
 };
+
+// The pairs of this CTA's items (one warp), in the sequences' order: few items need no
+// order by length, and the plan kernel takes longer than the shortest of them (8 prompts
+// of 700 tokens: 12.8 us with it, .. so).
+__device__ __forceinline__ void plan_direct(const PackedParams& p, Bar* bar) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Sequence s = {0, 0, 0, 0};
+    if (b0 + lane < p.B) s = sequence(p, b0 + lane);
+    const int n = (s.nq + 255) / 256;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+#pragma unroll
+    for (int k = 0; k < kPackedDirect; ++k) {
+      const int i = ((int)blockIdx.x + k * (int)gridDim.x) / p.H - (before + incl - n);
+      if (i >= 0 && i < n) bar->direct[k] = {s.q0 + i * 256, s.nq - i * 256, s.k0, s.nk, s.nk - s.nq + i * 256, {0, 0, 0}};
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) bar->direct_total = min(before, p.max_pairs) * p.H;
+  __syncwarp();
+}
 
 __device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t bit) {
   *reinterpret_cast<volatile int*>(&bar->abort_flag) = 1;
@@ -266,7 +297,7 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
                                               volatile int* abort_flag) {
   using G = Geo<D>;
   const uint64_t keep = ptx::l2_policy_evict_last(), once = ptx::l2_policy_evict_first();
-  const int total = p.plan->pairs * p.H;
+  const int total = p.direct ? bar->direct_total : p.plan->pairs * p.H;
   int id = blockIdx.x;
   int pub = 0;        // items published
   bool done = false;  // the last of them is the end
@@ -289,10 +320,10 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
       }
       Item& it = bar->items[pub % kItems];
       if (again ? id >= 0 : id < total) {
-        it.set(p, id);
+        it.set(p, bar->pair(p, id), id);
         it.marked = 0;
         it.again = again ? 1 : 0;
-        id = again ? p.marked[id] : gridDim.x + atomicAdd(&p.plan->next, 1);
+        id = again ? p.marked[id] : (p.direct ? id + gridDim.x : gridDim.x + atomicAdd(&p.plan->next, 1));
       } else {
         it.h = again ? kEnd : kDrain;
         it.n = 0;
@@ -504,6 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   ptx::tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   after_previous();  // the plan, and whatever the inputs come from
+  if (p.direct) {
+    if (warp == 0) plan_direct(p, bar);
+    __syncthreads();
+  }
 
   if (warp == 0) {
     ptx::setmaxnreg_dec<kRegsControl>();
@@ -817,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   if (threadIdx.x < 256 && !*abort_flag) {
     for (int id = bar->marked; id >= 0; id = p.marked[id]) {
       Item it;
-      it.set(p, id);
+      it.set(p, bar->pair(p, id), id);
       add_odd_values<D>(p, it, threadIdx.x);
     }
   }
@@ -834,7 +869,7 @@ cudaError_t launch_d(const PackedParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  if ((e = launch_chained(packed_plan_kernel, 1, 1, kPlanThreads, 0, 1, p, stream)) != cudaSuccess) return e;
+  if (!p.direct && (e = launch_chained(packed_plan_kernel, 1, 1, kPlanThreads, 0, 1, p, stream)) != cudaSuccess) return e;
   const int64_t items = (int64_t)p.max_pairs * p.H;
   return launch_chained(kern, (unsigned)(items < kPlanSms ? items : kPlanSms), 1, kThreads, smem, 1, p, stream);
 }

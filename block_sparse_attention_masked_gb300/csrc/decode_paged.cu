@@ -67,9 +67,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 }
 
 // Tiles of a warp's ring.
-template <int D, bool E8>
+template <int D, int NT, bool E8>
 struct Tile {
-  static constexpr int TK = paged_tile(D, E8), MT = TK / 16, kShift = TK == 32 ? 5 : 4;
+  static constexpr int TK = paged_tile(D, E8, 8 * NT), MT = TK / 16, kShift = paged_shift(D, E8, 8 * NT);
+  static constexpr int kLanes = TK < 32 ? TK : 32, kRows = TK / kLanes;  // rows lane, lane + 32 of a tile are a lane's
   static constexpr int kRow = E8 && D == 64 ? 64 : 128;    // bytes of a box's row
   static constexpr int kCols = D * (E8 ? 1 : 2) / kRow;    // box columns of a tile
   static constexpr int kBox = 16 * kRow;                   // bytes of a box
@@ -78,13 +79,14 @@ struct Tile {
   static constexpr int kStage = 2 * kTensor;
   static constexpr int NS = 2;
   static constexpr int kRing = NS * kStage;
-  static constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : 0xffffu;
+  using Mask = typename std::conditional<TK == 64, uint64_t, uint32_t>::type;  // of a tile's rows
+  static constexpr Mask kAll = TK == 16 ? Mask(0xffff) : ~Mask(0);
 };
 
 // One warp's running state of one group's query heads over e4m3 tiles.
 template <int D, int NT>
 struct State8 {
-  using T = Tile<D, true>;
+  using T = Tile<D, NT, true>;
   float m[NT][2], l[NT][2], mo[NT][2], o[NT][D / 16][4];  // m: of the scores; mo: of score + value power
   uint32_t qf[NT][D / 16][2];
   float qs[NT][2];  // takes a product to the score in the log2 domain, without the key's power
@@ -139,8 +141,9 @@ struct State8 {
   }
 
   // Adds a landed tile at `tile` (K, then V); mask (not 0): its rows that hold a key;
-  // kx, vx: the exponent bytes of row `lane`.
-  __device__ __forceinline__ void step(uint8_t* tile, uint32_t mask, uint32_t kx, uint32_t vx) {
+  // kx, vx: the exponent bytes of the lane's rows.
+  __device__ __forceinline__ void step(uint8_t* tile, typename T::Mask mask, const uint32_t (&kx)[T::kRows],
+                                       const uint32_t (&vx)[T::kRows]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int MT = T::MT;
     if (mask != T::kAll) {
@@ -187,15 +190,20 @@ struct State8 {
           s[nt][mt][j] = ((acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][2][j] + acc[nt][3][j])) * qs[nt][j & 1];
     }
     // the rows' powers, from the lane that loaded them
-    const float kp = e4m3::power((int)kx), vp = vx == 255u ? __uint_as_float(0x7fffffffu) : (float)((int)vx - 127);
+    float kp[T::kRows], vp[T::kRows];
+#pragma unroll
+    for (int i = 0; i < T::kRows; ++i) {
+      kp[i] = e4m3::power((int)kx[i]);
+      vp[i] = vx[i] == 255u ? __uint_as_float(0x7fffffffu) : (float)((int)vx[i] - 127);
+    }
     float ve[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = mt * 16 + r * 8 + kr;
-        const float k2 = __shfl_sync(0xffffffffu, kp, row);
-        ve[mt][r] = __shfl_sync(0xffffffffu, vp, row);
+        const float k2 = __shfl_sync(0xffffffffu, kp[mt / 2 % T::kRows], row & 31);
+        ve[mt][r] = __shfl_sync(0xffffffffu, vp[mt / 2 % T::kRows], row & 31);
         const bool there = (mask >> row) & 1u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -357,7 +365,7 @@ struct Cursor {
 template <int D, int NT, bool E8>
 __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, int W, uint8_t* ring, uint64_t* full,
                                            volatile int* abort_flag) {
-  using T = Tile<D, E8>;
+  using T = Tile<D, NT, E8>;
   constexpr int MT = T::MT, NS = T::NS;
   static_assert(NS == 2, "the masks of the stages are two registers");
   const int lane = threadIdx.x & 31;
@@ -407,21 +415,26 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
     while (k.b < p.B && k.s.tiles == 0);
   };
   // Loads the cursor's tile into `stage`, a lane per copy; returns its rows that hold
-  // a visible key, and (eight bits) the exponent bytes of row `lane`.
-  auto issue = [&](const Cursor& f, int stage, uint32_t* kx, uint32_t* vx) -> uint32_t {
+  // a visible key, and (eight bits) the exponent bytes of rows lane, lane + 32.
+  auto issue = [&](const Cursor& f, int stage, uint32_t (&kx)[T::kRows], uint32_t (&vx)[T::kRows]) -> typename T::Mask {
     const int at = (f.t < f.s.head ? f.t : f.s.t0 + f.t - f.s.head) << T::kShift;  // position of its first key
-    // (lane x: row x of the tile)
-    const int pos = at + lane;
-    bool seen = lane < T::TK && pos < f.s.len && (pos >= f.s.w0 || pos < p.first);
-    const int j = (uint32_t)pos / (uint32_t)p.page, r = pos - j * p.page;
-    int id = seen ? __ldg(p.table + (int64_t)f.b * p.table_pages + j) : -1;
-    seen = seen && (uint32_t)id < (uint32_t)p.n_pages;
-    const uint32_t mask = __ballot_sync(0xffffffffu, seen);
-    if (E8) {
-      *kx = *vx = 0;
-      if (seen) {
-        *kx = __ldg(p.exps[0] + id * p.exp_page[0] + f.h * p.exp_head[0] + r * p.exp_row[0]);
-        *vx = __ldg(p.exps[1] + id * p.exp_page[1] + f.h * p.exp_head[1] + r * p.exp_row[1]);
+    uint32_t half[2] = {0, 0};
+    int id[T::kRows], r[T::kRows];
+#pragma unroll
+    for (int i = 0; i < T::kRows; ++i) {
+      const int pos = at + lane + 32 * i;
+      bool seen = lane < T::kLanes && pos < f.s.len && (pos >= f.s.w0 || pos < p.first);
+      const int j = (uint32_t)pos / (uint32_t)p.page;
+      r[i] = pos - j * p.page;
+      id[i] = seen ? __ldg(p.table + (int64_t)f.b * p.table_pages + j) : -1;
+      seen = seen && (uint32_t)id[i] < (uint32_t)p.n_pages;
+      half[i] = __ballot_sync(0xffffffffu, seen);
+      if (E8) {
+        kx[i] = vx[i] = 0;
+        if (seen) {
+          kx[i] = __ldg(p.exps[0] + id[i] * p.exp_page[0] + f.h * p.exp_head[0] + r[i] * p.exp_row[0]);
+          vx[i] = __ldg(p.exps[1] + id[i] * p.exp_page[1] + f.h * p.exp_head[1] + r[i] * p.exp_row[1]);
+        }
       }
     }
     // a list's queries into L1, for the state that begins two tiles later
@@ -431,18 +444,24 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
     const int x = lane / kPer, col = (lane >> 1) % T::kCols, tensor = lane & 1;
     uint32_t bytes = 0;
 #pragma unroll
-    for (int y = 0; y < MT; ++y) bytes += (mask >> (16 * y)) & 0xffffu ? kPer * (uint32_t)T::kBox : 0u;
+    for (int y = 0; y < MT; ++y) bytes += (half[y >> 1] >> (16 * (y & 1))) & 0xffffu ? kPer * (uint32_t)T::kBox : 0u;
     if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
     __syncwarp();
     // the box's page and row from the lane of a visible key of it
-    const uint32_t box = x < MT ? (mask >> (16 * x)) & 0xffffu : 0u;
-    const int from = 16 * (x < MT ? x : 0) + (box ? __ffs(box) - 1 : 0);
-    const int page = __shfl_sync(0xffffffffu, id, from), row = __shfl_sync(0xffffffffu, r, from) & ~15;
+    const uint32_t box = x < MT ? (half[MT > 2 ? x >> 1 : 0] >> (16 * (x & 1))) & 0xffffu : 0u;
+    const int from = 16 * (x & 1) + (box ? __ffs(box) - 1 : 0);
+    int page = __shfl_sync(0xffffffffu, id[0], from), row = __shfl_sync(0xffffffffu, r[0], from);
+    if (T::kRows == 2) {
+      const int id1 = __shfl_sync(0xffffffffu, id[T::kRows - 1], from), r1 = __shfl_sync(0xffffffffu, r[T::kRows - 1], from);
+      if (x >= 2) page = id1, row = r1;
+    }
+    row &= ~15;
     if (box && debug_check(p.err, page >= 0 && page < p.n_pages && row >= 0 && row < p.page && f.h < p.H_kv && stage < NS,
                            kSiteLoad))
       ptx::tma_load_4d(ring + stage * T::kStage + tensor * T::kTensor + col * T::kChunk + x * T::kBox,
                        tensor ? &p.tv : &p.tk, full + stage, col * (E8 ? 128 : 64), row, f.h, page);
-    return mask;
+    if constexpr (T::TK == 64) return (uint64_t)half[1] << 32 | half[0];
+    else return half[0];
   };
   auto give_up = [&]() {
     if (lane == 0) {
@@ -456,12 +475,13 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
 
   typename std::conditional<E8, State8<D, NT>, rows::State<D, NT>>::type st;
   Cursor f = c;  // the last tile loaded
-  uint32_t masks[2] = {0, 0}, kx[2] = {0, 0}, vx[2] = {0, 0};
+  typename T::Mask masks[2] = {0, 0};
+  uint32_t kx[2][T::kRows] = {}, vx[2][T::kRows] = {};
 #pragma unroll
   for (int n = 0; n < NS; ++n)
     if (n < n_mine) {
       if (n) advance(f);
-      if (n || p.selftest != 1) masks[n] = issue(f, n, &kx[n], &vx[n]);
+      if (n || p.selftest != 1) masks[n] = issue(f, n, kx[n], vx[n]);
     }
   uint32_t at_k = 0, at_v = 0;
   if constexpr (!E8) {
@@ -475,13 +495,21 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
       else st.begin(p.q, (int64_t)c.b * p.H + c.h * G, G);
     }
     const int stage = n & 1;
-    const uint32_t mask = stage ? masks[1] : masks[0];
+    const typename T::Mask mask = stage ? masks[1] : masks[0];
     const bool got = ptx::mbar_wait(full + stage, (n >> 1) & 1, p.timeout_ns, abort_flag);
     if (!__all_sync(0xffffffffu, got)) return give_up();
     if (mask) {  // warp-uniform
-      if constexpr (E8) st.step(ring + stage * T::kStage, mask, stage ? kx[1] : kx[0], stage ? vx[1] : vx[0]);
+      if constexpr (E8) {
+        uint32_t k[T::kRows], v[T::kRows];
+#pragma unroll
+        for (int i = 0; i < T::kRows; ++i) {
+          k[i] = stage ? kx[1][i] : kx[0][i];
+          v[i] = stage ? vx[1][i] : vx[0][i];
+        }
+        st.step(ring + stage * T::kStage, mask, k, v);
+      }
       else
-        st.step(at_k + stage * T::kStage, at_v + stage * T::kStage, ring + stage * T::kStage + T::kTensor, mask,
+        st.step(at_k + stage * T::kStage, at_v + stage * T::kStage, ring + stage * T::kStage + T::kTensor, (uint32_t)mask,
                 p.scale_log2);
     }
     __syncwarp();
@@ -489,10 +517,17 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
       if (mask != T::kAll) ptx::fence_proxy_async_shared();  // the zeros of step before the copy that overwrites them
       __syncwarp();
       advance(f);
-      uint32_t k = 0, v = 0;
-      const uint32_t x = issue(f, stage, &k, &v);
-      if (stage) masks[1] = x, kx[1] = k, vx[1] = v;
-      else masks[0] = x, kx[0] = k, vx[0] = v;
+      uint32_t k[T::kRows], v[T::kRows];
+      const typename T::Mask x = issue(f, stage, k, v);
+      masks[0] = stage ? masks[0] : x;
+      masks[1] = stage ? x : masks[1];
+#pragma unroll
+      for (int i = 0; i < T::kRows && E8; ++i) {
+        kx[0][i] = stage ? kx[0][i] : k[i];
+        kx[1][i] = stage ? k[i] : kx[1][i];
+        vx[0][i] = stage ? vx[0][i] : v[i];
+        vx[1][i] = stage ? v[i] : vx[1][i];
+      }
     }
     const int g = c.b * p.H_kv + c.h;
     const bool last = n + 1 == n_mine;
@@ -523,9 +558,9 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
   }
 }
 
-template <int D, bool E8>
+template <class T>
 constexpr size_t paged_smem(int warps) {
-  return 1024 + (size_t)warps * (Tile<D, E8>::kRing + Tile<D, E8>::NS * 8) + 16;
+  return 1024 + (size_t)warps * (T::kRing + T::NS * 8) + 16;
 }
 
 // One CTA per SM, of p.warps warps; warp w of the grid is warp w / grid of CTA w % grid,
@@ -533,7 +568,7 @@ constexpr size_t paged_smem(int warps) {
 template <int D, int NT, bool E8>
 __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
     decode_paged_kernel(const __grid_constant__ DecodePagedParams p) {
-  using T = Tile<D, E8>;
+  using T = Tile<D, NT, E8>;
   const int warps = blockDim.x >> 5;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -551,14 +586,15 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
 
 template <int D, int NT, bool E8>
 cudaError_t launch_nt(const DecodePagedParams& p, cudaStream_t stream) {
-  constexpr size_t most = paged_smem<D, E8>(decode_rows_warps(D));
+  using T = Tile<D, NT, E8>;
+  constexpr size_t most = paged_smem<T>(decode_rows_warps(D));
   static_assert(most <= 227 * 1024, "shared memory");
   if (p.warps < 1 || p.warps > decode_rows_warps(D)) return cudaErrorInvalidValue;
   auto kern = decode_paged_kernel<D, NT, E8>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, most, &done);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, (unsigned)p.ctas, 1, 32 * p.warps, paged_smem<D, E8>(p.warps), 1, p, stream);
+  return launch_chained(kern, (unsigned)p.ctas, 1, 32 * p.warps, paged_smem<T>(p.warps), 1, p, stream);
 }
 
 }  // namespace

@@ -31,9 +31,16 @@ cudaError_t launch_cache_write(const CacheRowsParams& p, bool e4m3, cudaStream_t
 cudaError_t launch_cache_read(const CacheRowsParams& p, bool e4m3, cudaStream_t stream);
 
 // ------------------------------------------------------------ decode_paged.cu
-// Keys per tile: as the row workers' of decode_rows.cuh in bf16, 32 in eight bits
-// (8 KB of K and V, 16 KB at d = 256, 4 KB at 64).
-constexpr int paged_tile(int d, bool e4m3) { return e4m3 ? 32 : decode_rows_tile(d); }
+// Keys per tile: as the row workers' of decode_rows.cuh in bf16; in eight bits 32, 64 at
+// d = 64 (8 KB of K and V; half of it took 64 sequences of 6,144 keys 101 us, so 86), 16 for
+// more than eight query heads of 256, whose states leave few registers (16 sequences:
+// 82 us with 32, 55 so).
+constexpr int paged_tile(int d, bool e4m3, int group) {
+  return !e4m3 ? decode_rows_tile(d) : (d == 64 ? 64 : (d == 256 && group > 8 ? 16 : 32));
+}
+constexpr int paged_shift(int d, bool e4m3, int group) {
+  return paged_tile(d, e4m3, group) == 64 ? 6 : (paged_tile(d, e4m3, group) == 32 ? 5 : 4);
+}
 
 struct DecodePagedParams {
   CUtensorMap tk, tv;        // [n_pages][H_kv][page][d] views, boxes of 16 keys x 128 bytes (or a row of 64)
@@ -63,6 +70,7 @@ cudaError_t launch_decode_paged(const DecodePagedParams& p, int d, bool e4m3, cu
 struct __align__(16) PackedPair {
   int q_row, rows, k_row, keys, pos0, pad[3];
 };
+constexpr int kPackedDirect = 2;
 struct PackedPlan {        // in the workspace
   int next;                // the next item that no CTA has
   int pairs;
@@ -88,6 +96,7 @@ struct PackedParams {
   int causal, window;            // window 0: none
   int wide;                      // o is 32-byte aligned
   int max_pairs, work_shift;
+  int direct;                    // no plan: at most kPackedDirect items a CTA, in the sequences' order
   float scale_log2;
   int selftest;                  // 1: the first K tile is left out, so that the wait for it runs out
 };

@@ -150,8 +150,6 @@ int fill_rows(const char* what, const void* k, const void* v, const int64_t* tok
   return check_device();
 }
 
-int paged_shift(int d, bool e8) { return paged_tile(d, e8) == 32 ? 5 : 4; }
-
 // The tiles of all lists at most, and the warps of a CTA that share them.
 int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dtype, int64_t* tiles) {
   const int rc = check_heads("decode_paged", B, H, H_kv, d, MATTN_BF16);
@@ -161,7 +159,7 @@ int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dt
     return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: table_pages and page must be >= 1");
   const int64_t L = (int64_t)table_pages * page;
   if (L > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: table_pages * page exceeds 2^30");
-  const int tk = paged_tile(d, dtype == MATTN_E4M3);
+  const int tk = paged_tile(d, dtype == MATTN_E4M3, H / H_kv);
   *tiles = (int64_t)B * H_kv * ((L + tk - 1) / tk + 1);  // (a window's first tile and the first tokens' last one are parts)
   if (*tiles > INT32_MAX) return report_error(MATTN_ERR_UNSUPPORTED, "decode_paged: more than 2^31 - 1 tiles of keys");
   return MATTN_OK;
@@ -284,7 +282,7 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   m.warps = lay.warps;
   m.seq_lens = seq_lens;
   m.L = p.L;
-  m.tile_shift = paged_shift(d, e8);
+  m.tile_shift = paged_shift(d, e8, H / H_kv);
   m.window = p.window;
   m.first = p.first;
   m.sink = sink;
@@ -375,6 +373,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.window = window < kMaxRows ? window : (int)kMaxRows;
   p.max_pairs = (int)packed_pairs(T, B);
   while (((2 * ((int64_t)T_k / 128 + 1)) >> p.work_shift) >= 1024) ++p.work_shift;
+  p.direct = (int64_t)p.max_pairs * H <= kPackedDirect * kPlanSms ? 1 : 0;
   p.scale_log2 = scale_log2(softmax_scale, d);
   p.selftest = g_wait_selftest.load();
   return launched(launch_attention_packed(p, d, stream), "attention_packed launch");
