@@ -237,13 +237,18 @@ struct Bar {
   PackedPair direct[kPackedDirect];  // the CTA's items' pairs, where there is no plan
   int direct_total;                  // items of the grid
   __device__ __forceinline__ const PackedPair& pair(const PackedParams& p, int item) const {
-    return p.direct ? direct[(item - blockIdx.x) / gridDim.x] : p.plan->pair[item / p.H];
+    return p.direct ? direct[item / (int)gridDim.x] : p.plan->pair[item / p.H];
   }
 };
 
+// Without a plan, a CTA's k-th item: there and back through the CTAs, so that those with
+// the first, longest ones of a sequence get the last ones too.
+__device__ __forceinline__ int direct_item(int k) {
+  return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
 // The pairs of this CTA's items (one warp), in the sequences' order: few items need no
-// order by length, and the plan kernel takes longer than the shortest of them (8 prompts
-// of 700 tokens: 12.8 us with it, .. so).
+// order by length, and the plan kernel takes 3 us (8 prompts of 700 tokens 13.8 us with
+// it, 10.7 so; 9 of 64 with 32 heads 16.0 and 12.3; 4 of 500 23.2 and 22.3).
 __device__ __forceinline__ void plan_direct(const PackedParams& p, Bar* bar) {
   const int lane = threadIdx.x & 31;
   int before = 0;
@@ -259,7 +264,8 @@ __device__ __forceinline__ void plan_direct(const PackedParams& p, Bar* bar) {
     }
 #pragma unroll
     for (int k = 0; k < kPackedDirect; ++k) {
-      const int i = ((int)blockIdx.x + k * (int)gridDim.x) / p.H - (before + incl - n);
+      // (a sequence's last rows, which see most keys, first)
+      const int i = before + incl - 1 - direct_item(k) / p.H;
       if (i >= 0 && i < n) bar->direct[k] = {s.q0 + i * 256, s.nq - i * 256, s.k0, s.nk, s.nk - s.nq + i * 256, {0, 0, 0}};
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -323,7 +329,7 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
         it.set(p, bar->pair(p, id), id);
         it.marked = 0;
         it.again = again ? 1 : 0;
-        id = again ? p.marked[id] : (p.direct ? id + gridDim.x : gridDim.x + atomicAdd(&p.plan->next, 1));
+        id = again ? p.marked[id] : (p.direct ? direct_item(id / (int)gridDim.x + 1) : gridDim.x + atomicAdd(&p.plan->next, 1));
       } else {
         it.h = again ? kEnd : kDrain;
         it.n = 0;

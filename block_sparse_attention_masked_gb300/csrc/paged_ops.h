@@ -70,7 +70,7 @@ cudaError_t launch_decode_paged(const DecodePagedParams& p, int d, bool e4m3, cu
 struct __align__(16) PackedPair {
   int q_row, rows, k_row, keys, pos0, pad[3];
 };
-constexpr int kPackedDirect = 2;
+constexpr int kPackedDirect = 4;
 struct PackedPlan {        // in the workspace
   int next;                // the next item that no CTA has
   int pairs;
