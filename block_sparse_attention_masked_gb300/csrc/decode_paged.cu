@@ -69,6 +69,7 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // Tiles of a warp's ring.
 template <int D, int NT, bool E8>
 struct Tile {
+  static constexpr int kHeads = 8 * NT;  // rows of a state
   static constexpr int TK = paged_tile(D, E8, 8 * NT), MT = TK / 16, kShift = paged_shift(D, E8, 8 * NT);
   static constexpr int kLanes = TK < 32 ? TK : 32, kRows = TK / kLanes;  // rows lane, lane + 32 of a tile are a lane's
   static constexpr int kRow = E8 && D == 64 ? 64 : 128;    // bytes of a box's row
@@ -328,8 +329,8 @@ struct State8 {
     }
   }
 
-  // The piece's state: head `head`'s O against the softmax's reference m.
-  __device__ __forceinline__ void store(float* part_o, float* part_ml, int64_t slot, int G) {
+  // The state: O [G][D] against the softmax's reference m, and (m, sum) [G][2].
+  __device__ __forceinline__ void store(float* to_o, float* to_ml, int G) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -338,9 +339,9 @@ struct State8 {
         const float z = sum(nt, e);
         const int head = nt * 8 + (lane & 3) * 2 + e;
         if (head >= G) continue;
-        if (lane < 4) *reinterpret_cast<float2*>(part_ml + (slot * G + head) * 2) = make_float2(m[nt][e], z);
+        if (lane < 4) *reinterpret_cast<float2*>(to_ml + head * 2) = make_float2(m[nt][e], z);
         const float f = m[nt][e] == -INFINITY ? 1.f : ptx::ex2(mo[nt][e] - 14.f - m[nt][e]);
-        float* dst = part_o + (slot * G + head) * D + rot(lane >> 2) * (D == 64 ? 8 : 16);
+        float* dst = to_o + head * D + rot(lane >> 2) * (D == 64 ? 8 : 16);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2) {
           float* to = dst + (D == 64 ? 2 * i : (i >> 3) * 128 + 2 * (i & 7));
@@ -350,6 +351,57 @@ struct State8 {
       }
   }
 };
+
+// The same of a bf16 state.
+template <int D, int NT>
+__device__ __forceinline__ void store(const rows::State<D, NT>& st, float* to_o, float* to_ml, int G) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float s = st.sum(nt, e);
+      const int head = nt * 8 + (lane & 3) * 2 + e;
+      if (head >= G) continue;
+      if (lane < 4) *reinterpret_cast<float2*>(to_ml + head * 2) = make_float2(st.m[nt][e], s);
+      float* dst = to_o + head * D + (lane >> 2);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        dst[i * 16] = st.o[nt][i][e];
+        dst[i * 16 + 8] = st.o[nt][i][e + 2];
+      }
+    }
+}
+template <int D, int NT>
+__device__ __forceinline__ void store(State8<D, NT>& st, float* to_o, float* to_ml, int G) {
+  st.store(to_o, to_ml, G);
+}
+
+template <int D, int NT, bool E8>
+using StateOf = typename std::conditional<E8, State8<D, NT>, rows::State<D, NT>>::type;
+
+// Begins a group's state, with its queries.
+template <int D, int NT>
+__device__ __forceinline__ void begin(State8<D, NT>& st, const DecodePagedParams& p, int64_t bh0, int G) {
+  st.begin(p.q, bh0, G, p.scale_log2);
+}
+template <int D, int NT>
+__device__ __forceinline__ void begin(rows::State<D, NT>& st, const DecodePagedParams& p, int64_t bh0, int G) {
+  st.begin(p.q, bh0, G);
+}
+// Adds a landed tile (mask: not 0).
+template <int D, int NT, class T = Tile<D, NT, true>>
+__device__ __forceinline__ void add_tile(State8<D, NT>& st, const DecodePagedParams& p, uint8_t* tile,
+                                         typename T::Mask mask, const uint32_t (&kx)[T::kRows],
+                                         const uint32_t (&vx)[T::kRows]) {
+  st.step(tile, mask, kx, vx);
+}
+template <int D, int NT, class T = Tile<D, NT, false>>
+__device__ __forceinline__ void add_tile(rows::State<D, NT>& st, const DecodePagedParams& p, uint8_t* tile, uint32_t mask,
+                                         const uint32_t (&)[T::kRows], const uint32_t (&)[T::kRows]) {
+  st.step(rows::lane_k(ptx::smem_addr(tile)), rows::lane_v(ptx::smem_addr(tile) + T::kTensor), tile + T::kTensor, mask,
+          p.scale_log2);
+}
 
 __device__ __forceinline__ int cached_keys(const DecodePagedParams& p, int b) {
   const int len = p.seq_lens ? __ldg(p.seq_lens + b) : p.L;
@@ -362,11 +414,77 @@ struct Cursor {
   KeySpan s;
 };
 
+// Loads the cursor's tile into `stage` of a warp's ring, a lane per copy; returns its rows
+// that hold a visible key, and (eight bits) the exponent bytes of rows lane, lane + 32.
+template <int D, int NT, bool E8, class T = Tile<D, NT, E8>>
+__device__ __forceinline__ typename T::Mask issue_tile(const DecodePagedParams& p, uint8_t* ring, uint64_t* full,
+                                                       const Cursor& f, int stage, uint32_t (&kx)[T::kRows],
+                                                       uint32_t (&vx)[T::kRows]) {
+  constexpr int MT = T::MT, NS = T::NS;
+  const int lane = threadIdx.x & 31, G = p.H / p.H_kv;
+  const int at = (f.t < f.s.head ? f.t : f.s.t0 + f.t - f.s.head) << T::kShift;  // position of its first key
+  uint32_t half[2] = {0, 0};
+  int id[T::kRows], r[T::kRows];
+#pragma unroll
+  for (int i = 0; i < T::kRows; ++i) {
+    const int pos = at + lane + 32 * i;
+    bool seen = lane < T::kLanes && pos < f.s.len && (pos >= f.s.w0 || pos < p.first);
+    const int j = (uint32_t)pos / (uint32_t)p.page;
+    r[i] = pos - j * p.page;
+    id[i] = seen ? __ldg(p.table + (int64_t)f.b * p.table_pages + j) : -1;
+    seen = seen && (uint32_t)id[i] < (uint32_t)p.n_pages;
+    half[i] = __ballot_sync(0xffffffffu, seen);
+    if (E8) {
+      kx[i] = vx[i] = 0;
+      if (seen) {
+        kx[i] = __ldg(p.exps[0] + id[i] * p.exp_page[0] + f.h * p.exp_head[0] + r[i] * p.exp_row[0]);
+        vx[i] = __ldg(p.exps[1] + id[i] * p.exp_page[1] + f.h * p.exp_head[1] + r[i] * p.exp_row[1]);
+      }
+    }
+  }
+  // a list's queries into L1, for the state that begins two tiles later
+  if (f.t == 0 && lane * 64 < G * D)
+    ptx::prefetch_l1(reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)(f.b * p.H_kv + f.h) * G * D + lane * 64);
+  constexpr int kPer = T::kCols * 2;  // copies per box of 16 keys (of one page)
+  const int x = lane / kPer, col = (lane >> 1) % T::kCols, tensor = lane & 1;
+  uint32_t bytes = 0;
+#pragma unroll
+  for (int y = 0; y < MT; ++y) bytes += (half[y >> 1] >> (16 * (y & 1))) & 0xffffu ? kPer * (uint32_t)T::kBox : 0u;
+  if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
+  __syncwarp();
+  // the box's page and row from the lane of a visible key of it
+  const uint32_t box = x < MT ? (half[MT > 2 ? x >> 1 : 0] >> (16 * (x & 1))) & 0xffffu : 0u;
+  const int from = 16 * (x & 1) + (box ? __ffs(box) - 1 : 0);
+  int page = __shfl_sync(0xffffffffu, id[0], from), row = __shfl_sync(0xffffffffu, r[0], from);
+  if (T::kRows == 2) {
+    const int id1 = __shfl_sync(0xffffffffu, id[T::kRows - 1], from), r1 = __shfl_sync(0xffffffffu, r[T::kRows - 1], from);
+    if (x >= 2) page = id1, row = r1;
+  }
+  row &= ~15;
+  if (box && debug_check(p.err, page >= 0 && page < p.n_pages && row >= 0 && row < p.page && f.h < p.H_kv && stage < NS,
+                         kSiteLoad))
+    ptx::tma_load_4d(ring + stage * T::kStage + tensor * T::kTensor + col * T::kChunk + x * T::kBox,
+                     tensor ? &p.tv : &p.tk, full + stage, col * (E8 ? 128 : 64), row, f.h, page);
+  if constexpr (T::TK == 64) return (uint64_t)half[1] << 32 | half[0];
+  else return half[0];
+}
+
+// After a wait that gave up: the abort flag, the error word, and time for the copies in
+// flight to land before the shared memory goes.
+__device__ __forceinline__ void give_up(const DecodePagedParams& p, volatile int* abort_flag) {
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    atomicOr(p.err, kErrProducer);
+  }
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
+}
+
 template <int D, int NT, bool E8>
 __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, int W, uint8_t* ring, uint64_t* full,
                                            volatile int* abort_flag) {
   using T = Tile<D, NT, E8>;
-  constexpr int MT = T::MT, NS = T::NS;
+  constexpr int NS = T::NS;
   static_assert(NS == 2, "the masks of the stages are two registers");
   const int lane = threadIdx.x & 31;
   const int G = p.H / p.H_kv;
@@ -414,66 +532,7 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
     do k.s = span(++k.b);
     while (k.b < p.B && k.s.tiles == 0);
   };
-  // Loads the cursor's tile into `stage`, a lane per copy; returns its rows that hold
-  // a visible key, and (eight bits) the exponent bytes of rows lane, lane + 32.
-  auto issue = [&](const Cursor& f, int stage, uint32_t (&kx)[T::kRows], uint32_t (&vx)[T::kRows]) -> typename T::Mask {
-    const int at = (f.t < f.s.head ? f.t : f.s.t0 + f.t - f.s.head) << T::kShift;  // position of its first key
-    uint32_t half[2] = {0, 0};
-    int id[T::kRows], r[T::kRows];
-#pragma unroll
-    for (int i = 0; i < T::kRows; ++i) {
-      const int pos = at + lane + 32 * i;
-      bool seen = lane < T::kLanes && pos < f.s.len && (pos >= f.s.w0 || pos < p.first);
-      const int j = (uint32_t)pos / (uint32_t)p.page;
-      r[i] = pos - j * p.page;
-      id[i] = seen ? __ldg(p.table + (int64_t)f.b * p.table_pages + j) : -1;
-      seen = seen && (uint32_t)id[i] < (uint32_t)p.n_pages;
-      half[i] = __ballot_sync(0xffffffffu, seen);
-      if (E8) {
-        kx[i] = vx[i] = 0;
-        if (seen) {
-          kx[i] = __ldg(p.exps[0] + id[i] * p.exp_page[0] + f.h * p.exp_head[0] + r[i] * p.exp_row[0]);
-          vx[i] = __ldg(p.exps[1] + id[i] * p.exp_page[1] + f.h * p.exp_head[1] + r[i] * p.exp_row[1]);
-        }
-      }
-    }
-    // a list's queries into L1, for the state that begins two tiles later
-    if (f.t == 0 && lane * 64 < G * D)
-      ptx::prefetch_l1(reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)(f.b * p.H_kv + f.h) * G * D + lane * 64);
-    constexpr int kPer = T::kCols * 2;  // copies per box of 16 keys (of one page)
-    const int x = lane / kPer, col = (lane >> 1) % T::kCols, tensor = lane & 1;
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int y = 0; y < MT; ++y) bytes += (half[y >> 1] >> (16 * (y & 1))) & 0xffffu ? kPer * (uint32_t)T::kBox : 0u;
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
-    __syncwarp();
-    // the box's page and row from the lane of a visible key of it
-    const uint32_t box = x < MT ? (half[MT > 2 ? x >> 1 : 0] >> (16 * (x & 1))) & 0xffffu : 0u;
-    const int from = 16 * (x & 1) + (box ? __ffs(box) - 1 : 0);
-    int page = __shfl_sync(0xffffffffu, id[0], from), row = __shfl_sync(0xffffffffu, r[0], from);
-    if (T::kRows == 2) {
-      const int id1 = __shfl_sync(0xffffffffu, id[T::kRows - 1], from), r1 = __shfl_sync(0xffffffffu, r[T::kRows - 1], from);
-      if (x >= 2) page = id1, row = r1;
-    }
-    row &= ~15;
-    if (box && debug_check(p.err, page >= 0 && page < p.n_pages && row >= 0 && row < p.page && f.h < p.H_kv && stage < NS,
-                           kSiteLoad))
-      ptx::tma_load_4d(ring + stage * T::kStage + tensor * T::kTensor + col * T::kChunk + x * T::kBox,
-                       tensor ? &p.tv : &p.tk, full + stage, col * (E8 ? 128 : 64), row, f.h, page);
-    if constexpr (T::TK == 64) return (uint64_t)half[1] << 32 | half[0];
-    else return half[0];
-  };
-  auto give_up = [&]() {
-    if (lane == 0) {
-      *abort_flag = 1;
-      atomicOr(p.err, kErrProducer);
-    }
-    // copies in flight land before the shared memory goes
-    const uint64_t t0 = ptx::globaltimer_ns();
-    for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
-  };
-
-  typename std::conditional<E8, State8<D, NT>, rows::State<D, NT>>::type st;
+  StateOf<D, NT, E8> st;
   Cursor f = c;  // the last tile loaded
   typename T::Mask masks[2] = {0, 0};
   uint32_t kx[2][T::kRows] = {}, vx[2][T::kRows] = {};
@@ -481,36 +540,25 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
   for (int n = 0; n < NS; ++n)
     if (n < n_mine) {
       if (n) advance(f);
-      if (n || p.selftest != 1) masks[n] = issue(f, n, kx[n], vx[n]);
+      if (n || p.selftest != 1) masks[n] = issue_tile<D, NT, E8>(p, ring, full, f, n, kx[n], vx[n]);
     }
-  uint32_t at_k = 0, at_v = 0;
-  if constexpr (!E8) {
-    at_k = rows::lane_k(ptx::smem_addr(ring));
-    at_v = rows::lane_v(ptx::smem_addr(ring) + T::kTensor);
-  }
   for (int n = 0; n < n_mine; ++n) {
     if (n == 0 || c.t == 0) {
       if (c.t == 0 && lane == 0) p.group_start[c.b * p.H_kv + c.h] = x0 + n;
-      if constexpr (E8) st.begin(p.q, (int64_t)c.b * p.H + c.h * G, G, p.scale_log2);
-      else st.begin(p.q, (int64_t)c.b * p.H + c.h * G, G);
+      begin(st, p, (int64_t)c.b * p.H + c.h * G, G);
     }
     const int stage = n & 1;
     const typename T::Mask mask = stage ? masks[1] : masks[0];
     const bool got = ptx::mbar_wait(full + stage, (n >> 1) & 1, p.timeout_ns, abort_flag);
-    if (!__all_sync(0xffffffffu, got)) return give_up();
+    if (!__all_sync(0xffffffffu, got)) return give_up(p, abort_flag);
     if (mask) {  // warp-uniform
-      if constexpr (E8) {
-        uint32_t k[T::kRows], v[T::kRows];
+      uint32_t k[T::kRows], v[T::kRows];
 #pragma unroll
-        for (int i = 0; i < T::kRows; ++i) {
-          k[i] = stage ? kx[1][i] : kx[0][i];
-          v[i] = stage ? vx[1][i] : vx[0][i];
-        }
-        st.step(ring + stage * T::kStage, mask, k, v);
+      for (int i = 0; i < T::kRows; ++i) {
+        k[i] = stage ? kx[1][i] : kx[0][i];
+        v[i] = stage ? vx[1][i] : vx[0][i];
       }
-      else
-        st.step(at_k + stage * T::kStage, at_v + stage * T::kStage, ring + stage * T::kStage + T::kTensor, (uint32_t)mask,
-                p.scale_log2);
+      add_tile(st, p, ring + stage * T::kStage, mask, k, v);
     }
     __syncwarp();
     if (n + NS < n_mine) {
@@ -518,7 +566,7 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
       __syncwarp();
       advance(f);
       uint32_t k[T::kRows], v[T::kRows];
-      const typename T::Mask x = issue(f, stage, k, v);
+      const typename T::Mask x = issue_tile<D, NT, E8>(p, ring, full, f, stage, k, v);
       masks[0] = stage ? masks[0] : x;
       masks[1] = stage ? x : masks[1];
 #pragma unroll
@@ -532,27 +580,8 @@ __device__ __forceinline__ void paged_work(const DecodePagedParams& p, int w, in
     const int g = c.b * p.H_kv + c.h;
     const bool last = n + 1 == n_mine;
     if (last || c.t + 1 == c.s.tiles) {
-      if constexpr (E8) {
-        st.store(p.part_o, p.part_ml, (int64_t)w + g, G);
-      } else {
-        const int64_t slot = (int64_t)w + g;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = st.sum(nt, e);
-            const int head = nt * 8 + (lane & 3) * 2 + e;
-            if (head < G) {
-              if (lane < 4) *reinterpret_cast<float2*>(p.part_ml + (slot * G + head) * 2) = make_float2(st.m[nt][e], s);
-              float* dst = p.part_o + (slot * G + head) * D + (lane >> 2);
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                dst[i * 16] = st.o[nt][i][e];
-                dst[i * 16 + 8] = st.o[nt][i][e + 2];
-              }
-            }
-          }
-      }
+      const int64_t at = ((int64_t)w + g) * G;
+      store(st, p.part_o + at * D, p.part_ml + at * 2, G);
     }
     if (!last) advance(c);
   }
@@ -584,8 +613,146 @@ __global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
                         abort_flag);
 }
 
+// Few groups with short lists: a cluster of CTAs a group, warps in turn with a tile each, no
+// states in memory and no second launch.  The warps of a CTA meet in its shared memory, the
+// CTAs of the cluster in each other's, each CTA finishing a share of the G x D outputs.
+template <class T, int D>
+struct ClusterSmem {
+  static constexpr int kWarps = decode_rows_warps(D), kUnits = kWarps + 1;  // the warps' states and the CTA's
+  static constexpr size_t kRing = (size_t)kWarps * T::kRing, kStates = (size_t)kUnits * T::kHeads * (D + 2) * 4;
+  static constexpr size_t kBytes = 1024 + (kRing > kStates ? kRing : kStates) + kWarps * T::NS * 8 + 16;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+template <int D, int NT, bool E8>
+__global__ void __launch_bounds__(32 * decode_rows_warps(D), 1)
+    decode_paged_cluster_kernel(const __grid_constant__ DecodePagedParams p) {
+  using T = Tile<D, NT, E8>;
+  using Mem = ClusterSmem<T, D>;
+  constexpr int W = Mem::kWarps, HP = T::kHeads, NS = T::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Mem::kBytes - 1024 - W * NS * 8 - 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + W * NS);
+  const int warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x % p.cluster, bkv = blockIdx.x / p.cluster, G = p.H / p.H_kv;
+  const int64_t bh0 = (int64_t)bkv * G;
+  if (threadIdx.x < W * NS) ptx::mbar_init(bars + threadIdx.x, 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  ptx::fence_barrier_init();
+  __syncthreads();
+  after_previous();
+
+  uint8_t* ring = base + warp * T::kRing;
+  uint64_t* full = bars + warp * NS;
+  Cursor c;
+  c.b = bkv / p.H_kv;
+  c.h = bkv - c.b * p.H_kv;
+  c.s = key_span(cached_keys(p, c.b), p.window, p.first, T::kShift);
+  const int first = rank + warp * p.cluster, step = p.cluster * W;  // this warp's tiles: first, first + step, ..
+  const int mine = first < c.s.tiles ? (c.s.tiles - first + step - 1) / step : 0;
+  typename T::Mask mask = 0, mask1 = 0;  // of the tile at hand and the one behind it
+  uint32_t kx[T::kRows] = {}, vx[T::kRows] = {}, kx1[T::kRows] = {}, vx1[T::kRows] = {};
+  c.t = first;
+  if (mine > 0 && p.selftest != 1) mask = issue_tile<D, NT, E8>(p, ring, full, c, 0, kx, vx);
+  c.t += step;
+  if (mine > 1) mask1 = issue_tile<D, NT, E8>(p, ring, full, c, 1, kx1, vx1);
+  StateOf<D, NT, E8> st;
+  begin(st, p, bh0, G);
+  for (int n = 0; n < mine; ++n) {
+    const int stage = n & 1;
+    const bool got = ptx::mbar_wait(full + stage, (n >> 1) & 1, p.timeout_ns, abort_flag);
+    if (!__all_sync(0xffffffffu, got)) {
+      give_up(p, abort_flag);
+      break;
+    }
+    if (mask) add_tile(st, p, ring + stage * T::kStage, mask, kx, vx);  // warp-uniform
+    __syncwarp();
+    if (mask != T::kAll) ptx::fence_proxy_async_shared();  // the zeros of a step before the copy that overwrites them
+    __syncwarp();
+    mask = mask1;
+#pragma unroll
+    for (int i = 0; i < T::kRows; ++i) kx[i] = kx1[i], vx[i] = vx1[i];
+    if (n + NS < mine) {
+      c.t += step;
+      mask1 = issue_tile<D, NT, E8>(p, ring, full, c, stage, kx1, vx1);
+    }
+  }
+  __syncthreads();  // every tile of every warp is read
+  // over the rings: O [W + 1][HP][D], then reference and sum [W + 1][HP][2]
+  float* so = reinterpret_cast<float*>(base);
+  float* sml = so + Mem::kUnits * HP * D;
+  store(st, so + warp * HP * D, sml + warp * HP * 2, G);
+  __syncthreads();
+  for (int x = threadIdx.x; x < G * D; x += 32 * W) {  // the CTA's state
+    const int g = x / D;
+    float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, sml[(w * HP + g) * 2]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float mw = sml[(w * HP + g) * 2], e = mw == M ? 1.f : ptx::ex2(mw - M);
+      L = fmaf(sml[(w * HP + g) * 2 + 1], e, L);
+      O = fmaf(so[w * HP * D + x], e, O);
+    }
+    so[W * HP * D + x] = O;
+    if (x % D == 0) {
+      sml[(W * HP + g) * 2] = M;
+      sml[(W * HP + g) * 2 + 1] = L;
+    }
+  }
+  auto all = [&]() {
+    if (p.cluster > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
+  all();
+  // this CTA's share of the outputs (a CTA that gave up leaves no number behind: its
+  // cluster's outputs are then undefined, and the error word says so)
+  const int share = (G * D + p.cluster - 1) / p.cluster;
+  const int end = (rank + 1) * share < G * D ? (rank + 1) * share : G * D;
+  for (int x = rank * share + threadIdx.x; x < end; x += 32 * W) {
+    const int g = x / D;
+    const float* ml = sml + (W * HP + g) * 2;
+    const float* o = so + W * HP * D + x;
+    const float b2 = p.sink ? p.sink[c.h * G + g] * 1.4426950408889634f : -INFINITY;
+    float mr[8], lr[8], ors[8], M = b2;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      mr[r] = r < p.cluster ? rows::cluster_ld(ml, r) : -INFINITY;
+      lr[r] = r < p.cluster ? rows::cluster_ld(ml + 1, r) : 0.f;
+      ors[r] = r < p.cluster ? rows::cluster_ld(o, r) : 0.f;
+      M = fmaxf(M, mr[r]);
+    }
+    float z = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - M), O = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float e = mr[r] == M ? 1.f : ptx::ex2(mr[r] - M);
+      z = fmaf(lr[r], e, z);
+      O = fmaf(ors[r], e, O);
+    }
+    reinterpret_cast<__nv_bfloat16*>(p.o)[bh0 * D + x] = __float2bfloat16_rn(z == 0.f ? 0.f : O / z);
+    if (x % D == 0 && p.lse) p.lse[bh0 + g] = z == 0.f ? -INFINITY : (M + __log2f(z)) * 0.6931471805599453f;
+  }
+  if (p.cluster > 1) all();  // no CTA leaves while another reads its shared memory
+}
+
+template <int D, int NT, bool E8>
+cudaError_t launch_cluster(const DecodePagedParams& p, cudaStream_t stream) {
+  constexpr size_t smem = ClusterSmem<Tile<D, NT, E8>, D>::kBytes;
+  auto kern = decode_paged_cluster_kernel<D, NT, E8>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kern, smem, &done);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, (unsigned)(p.B * p.H_kv * p.cluster), 1, 32 * decode_rows_warps(D), smem, p.cluster, p, stream);
+}
+
 template <int D, int NT, bool E8>
 cudaError_t launch_nt(const DecodePagedParams& p, cudaStream_t stream) {
+  if (p.cluster) return launch_cluster<D, NT, E8>(p, stream);
   using T = Tile<D, NT, E8>;
   constexpr size_t most = paged_smem<T>(decode_rows_warps(D));
   static_assert(most <= 227 * 1024, "shared memory");

@@ -71,14 +71,6 @@ struct ListSmem {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
-  uint32_t a;
-  float x;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-  return x;
-}
-
 template <int D, int NT, int W>
 __global__ void __launch_bounds__(32 * W, 1)
     decode_lists_kernel(const __grid_constant__ DecodeRowsParams p) {
@@ -199,7 +191,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     float mr[8], M = b2;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      mr[r] = r < p.cluster ? cluster_ld(ml, r) : -INFINITY;
+      mr[r] = r < p.cluster ? rows::cluster_ld(ml, r) : -INFINITY;
       M = fmaxf(M, mr[r]);
     }
     float z = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - M), O = 0.f;
@@ -207,8 +199,8 @@ __global__ void __launch_bounds__(32 * W, 1)
     for (int r = 0; r < 8; ++r)
       if (r < p.cluster) {
         const float e = mr[r] == M ? 1.f : ptx::ex2(mr[r] - M);
-        z = fmaf(cluster_ld(ml + 1, r), e, z);
-        O = fmaf(cluster_ld(o, r), e, O);
+        z = fmaf(rows::cluster_ld(ml + 1, r), e, z);
+        O = fmaf(rows::cluster_ld(o, r), e, O);
       }
     reinterpret_cast<__nv_bfloat16*>(p.o)[(bh0 + g) * D + c] = __float2bfloat16_rn(z == 0.f ? 0.f : O / z);
     if (c == 0 && p.lse) p.lse[bh0 + g] = z == 0.f ? -INFINITY : (M + __log2f(z)) * kLn2R;

@@ -77,6 +77,15 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// A word of a CTA of this cluster, at this CTA's address p.
+__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+  uint32_t a;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+
 __device__ __forceinline__ int cached_keys(const DecodeRowsParams& p, int b) {
   const int len = p.seq_lens ? __ldg(p.seq_lens + b) : p.L;
   return len < 0 ? 0 : (len > p.L ? p.L : len);

@@ -58,6 +58,10 @@ struct DecodePagedParams {
   int page, table_pages, n_pages, L;  // L = table_pages * page
   int window, first;         // keys [len - window, len) and [0, first); window 0: all
   int ctas, warps;
+  int cluster;               // CTAs of a group (decode_paged_cluster_kernel writes o itself), or 0: equal shares and states
+  const float* sink;
+  void* o;                   // [B][H][d] bf16
+  float* lse;                // [B][H] or null
   float scale_log2;
   int selftest;              // 1: every worker's first copies are left out, so that its wait runs out
 };

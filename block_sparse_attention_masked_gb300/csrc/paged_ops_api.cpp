@@ -150,6 +150,36 @@ int fill_rows(const char* what, const void* k, const void* v, const int64_t* tok
   return check_device();
 }
 
+// CTAs of a group's cluster for lists of `tiles` tiles at most, or 0: equal shares of all
+// lists.  A cluster saves the states, their merge and a launch (about 3 us), and costs the
+// rounds of a tile for every warp by which its CTAs take longer than all SMs would: up to
+// two and a half, or five of bf16's half as many keys, it is the faster (32 / 8 heads of 128, lengths
+// between L / 2 and L, clusters and shares, us: in e4m3 16 sequences of L = 1,024 10.5 and 16.3, of
+// 4,096 28.3 and 33.9, of 16,384 89.6 and 73.9, one of 8,192 11.0 and 14.2, of 32,768 28.0 and 25.0;
+// in bf16 16 of 1,024 14.3 and 17.0, of 4,096 38.2 and 42.5, one of 32,768 33.2 and 31.0).  Eight
+// CTAs only where eight clusters of them do: sixteen do not find their places at once
+// (two sequences of 8,192: 16.6 and 13.7).
+int paged_cluster(int64_t groups, int64_t tiles, int d, bool e4m3) {
+  if (groups > kPlanSms) return 0;
+  const int warps = decode_rows_warps(d);
+  int64_t cluster = 1;
+  while (cluster < (groups <= 8 ? 8 : 4) && groups * cluster * 2 <= kPlanSms && cluster * warps < tiles) cluster *= 2;
+  const int64_t rounds = (tiles + cluster * warps - 1) / (cluster * warps);
+  // (in 152 * warps-ths of a round)
+  const int64_t over = rounds * kPlanSms * warps - groups * tiles;
+  return over * 2 <= (e4m3 ? 5 : 10) * kPlanSms * warps ? (int)cluster : 0;
+}
+
+// Tiles of a list at most: the window's (which may begin and end inside one) and the
+// first tokens', or all.
+int64_t list_tiles_at_most(int64_t L, int window, int first, int d, bool e4m3, int group) {
+  const int tk = paged_tile(d, e4m3, group);
+  const int64_t all = (L + tk - 1) / tk;
+  if (!window) return all;
+  const int64_t seen = ((int64_t)window + tk - 1) / tk + 1 + (first + tk - 1) / tk;
+  return all < seen ? all : seen;
+}
+
 // The tiles of all lists at most, and the warps of a CTA that share them.
 int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dtype, int64_t* tiles) {
   const int rc = check_heads("decode_paged", B, H, H_kv, d, MATTN_BF16);
@@ -273,7 +303,11 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   p.warps = warps;
   p.selftest = g_wait_selftest.load();
   p.scale_log2 = scale_log2(softmax_scale, d);
-  if ((rc = launched(launch_decode_paged(p, d, e8, stream), "paged launch"))) return rc;
+  p.sink = sink;
+  p.o = o;
+  p.lse = lse;
+  p.cluster = paged_cluster((int64_t)B * H_kv, list_tiles_at_most(p.L, window, p.first, d, e8, H / H_kv), d, e8);
+  if ((rc = launched(launch_decode_paged(p, d, e8, stream), "paged launch")) || p.cluster) return rc;
   MergeParams m;
   memset(&m, 0, sizeof(m));
   m.b_o = p.part_o;
@@ -377,6 +411,21 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.scale_log2 = scale_log2(softmax_scale, d);
   p.selftest = g_wait_selftest.load();
   return launched(launch_attention_packed(p, d, stream), "attention_packed launch");
+}
+
+// Test hook (not in the public header), host only: how decode_paged reads its lists:
+// {CTAs of a group's cluster or 0 for equal shares, warps of a CTA then, keys of a tile}.
+int mattn_internal_paged_plan(int B, int H, int H_kv, int table_pages, int page, int d, int dtype, int window,
+                              int sink_tokens, int* out) {
+  int64_t tiles = 0;
+  const int rc = check_paged(B, H, H_kv, table_pages, page, d, dtype, &tiles);
+  if (rc) return rc;
+  const bool e8 = dtype == MATTN_E4M3;
+  out[0] = paged_cluster((int64_t)B * H_kv, list_tiles_at_most((int64_t)table_pages * page, window, sink_tokens, d, e8, H / H_kv),
+                         d, e8);
+  out[1] = decode_share_warps(tiles, d);
+  out[2] = paged_tile(d, e8, H / H_kv);
+  return MATTN_OK;
 }
 
 // Test hook (not in the public header): the launches of decode_paged and

@@ -279,6 +279,26 @@ def test_decode_paged_many_sequences(e4m3):
     decode_case(B, 2, 1, 64, 16, 3, lens, e4m3, seed=9)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("what", ["plain", "window", "holes", "rows", "group"])
+def test_decode_paged_in_equal_shares(d, what, e4m3):
+    """More groups than SMs: warps' shares end anywhere in the lists."""
+    B, Hkv, slots = 80, 2, 9
+    lens = [(37 * b) % 150 for b in range(B)]
+    kw = {"plain": dict(), "window": dict(window=50, first=5, sink=True), "rows": dict(layout="rows", scale=0.2),
+          "holes": dict(holes=[(b, (3 * b) % slots, -1) for b in range(0, B, 2)] + [(7, j, 1 << 20) for j in range(slots)]),
+          "group": dict(sink=True)}[what]
+    decode_case(B, 24 if what == "group" else 4, Hkv, d, 16, slots, lens, e4m3, seed=12, **kw)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,slots,lens", [(1, 40, [640]), (2, 40, [600, 333]), (9, 8, [128] * 9), (1, 3, [1]), (30, 4, [0] * 15 + [64] * 15)])
+def test_decode_paged_in_clusters(B, slots, lens, e4m3):
+    """Clusters of 8, 4, 2 and 1 CTAs; more warps than tiles, and CTAs without any."""
+    decode_case(B, 8, 4, 128, 16, slots, lens, e4m3, seed=B, sink=B == 2)
+
+
 def test_decode_paged_powers_far_apart():
     """Rows whose powers lie 2^80 apart, queries from 2^-60 on: weights and their powers meet in range."""
     for q_scale in (2.0 ** -60, 1.0):
@@ -485,11 +505,13 @@ def test_cache_write_of_one_token_each():
 # ------------------------------------------------------------------ waits that run out
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_decode_paged_waits_run_out(d, e4m3):
-    B, H, Hkv = 3, 8, 2
+@pytest.mark.parametrize("B", [3, 90])
+def test_decode_paged_waits_run_out(d, e4m3, B):
+    """In clusters (3 sequences) and in equal shares with the merge (90)."""
+    H, Hkv = 8, 2
     c = Cache(B, Hkv, d, 16, 12, e4m3, seed=1)
     q = _randn(_gen(2), B, H, d)
-    lens = _i32([190, 3, 100])
+    lens = _i32(([190, 3, 100] * B)[:B])
     ws = mattn.decode_paged_workspace(B, H, Hkv, 12, 16, d, e4m3)
     run = lambda: mattn.decode_paged(q, c.k, c.v, c.table, lens, workspace=ws, **c.kw())  # noqa: E731
     want = [x.clone() for x in run()]

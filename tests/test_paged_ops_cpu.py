@@ -183,6 +183,27 @@ def test_decode_paged_workspace(L):
     assert f(4096, 8, 8, 1 << 24, 64, 128, E4M3, ctypes.byref(n)) == -2  # 2^35 tiles
 
 
+def _plan(L, B, H, Hkv, pages, page=64, d=128, dtype=E4M3, window=0, first=0):
+    out = (ctypes.c_int * 3)()
+    assert L.mattn_internal_paged_plan(B, H, Hkv, pages, page, d, dtype, window, first, out) == 0
+    return tuple(out)
+
+
+def test_decode_paged_plan(L):
+    """Clusters for few groups with short lists, equal shares for the others; the tile by type, head dim and group."""
+    assert _plan(L, 4, 16, 4, 63, 16, dtype=BF16) == (4, 6, 16)  # 1,008 keys
+    assert _plan(L, 1, 32, 8, 128)[0] == 8  # 8,192 keys of eight groups
+    assert _plan(L, 1, 32, 8, 512)[0] == 0  # 32,768: eleven rounds against four and a half
+    assert _plan(L, 2, 32, 8, 128)[0] == 0  # sixteen groups: four CTAs each, six rounds
+    assert _plan(L, 16, 32, 8, 64)[0] == 1 and _plan(L, 16, 32, 8, 256)[0] == 0
+    assert _plan(L, 20, 32, 8, 1)[0] == 0  # 160 groups
+    assert _plan(L, 64, 32, 8, 128) == (0, 12, 32)
+    assert _plan(L, 1, 32, 8, 512, window=1024)[0] == 4 and _plan(L, 1, 32, 8, 512, window=1024, first=20000)[0] == 0
+    for d, group, dtype, tile in ((64, 4, E4M3, 64), (128, 16, E4M3, 32), (256, 8, E4M3, 32), (256, 9, E4M3, 16), (64, 1, BF16, 32),
+                                  (128, 1, BF16, 16), (256, 16, BF16, 16)):
+        assert _plan(L, 200, group, 1, 10, d=d, dtype=dtype)[2] == tile
+
+
 def test_a_null_size_and_the_binding(L):
     import torch
 
