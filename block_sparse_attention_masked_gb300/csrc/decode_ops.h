@@ -222,6 +222,7 @@ struct MergeParams {
   int na;
   int warps;                 // row workers of the own lists
   int states;                // of a row, about
+  int many;                  // sixteen states in flight a lane group where there are few rows, not four
   int L, list_tiles;
   int tile_shift;            // 1 << tile_shift keys a tile of the own lists
   int window, first;         // KeySpan's

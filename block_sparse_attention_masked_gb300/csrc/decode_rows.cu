@@ -239,7 +239,6 @@ cudaError_t launch_lists_nt(const DecodeRowsParams& p, cudaStream_t stream) {
 // their references and values loaded together, pointers moved and not formed
 // anew (2,048 rows of 18 states: 7.6 us with 16 states in flight a warp and a
 // warp a row).
-constexpr int kMergeBatch = 4;
 
 struct Running {
   float m, l;
@@ -248,6 +247,7 @@ struct Running {
 
 // Adds n states, `step` apart: reference and sum at `ml`, the lane's dims at `o`
 // (ml_step and o_step floats from one to the next).
+template <int kMergeBatch>
 __device__ __forceinline__ void add_states(Running& r, const float* ml, const float* o, int n, int64_t ml_step,
                                            int64_t o_step) {
   for (; n > 0; n -= kMergeBatch) {
@@ -283,7 +283,7 @@ __device__ __forceinline__ void add_states(Running& r, const float* ml, const fl
   }
 }
 
-template <int D, int SL, int WPR>
+template <int D, int SL, int WPR, int NB>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int LPS = SL / 4, SPW = 32 / LPS, U = WPR * SPW;
   static_assert(SL <= 128, "a warp's lanes hold four dims each");
@@ -316,12 +316,12 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const float b2 = p.sink ? p.sink[h] * kLog2eR : -INFINITY;
   Running r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   // this unit's states: unit, unit + U, ..
-  add_states(r, p.a_ml + (ra + unit) * 2, p.a_o + (ra + unit) * D + c0 + part * 4, (p.na - unit + U - 1) / U, U * 2, U * D);
+  add_states<NB>(r, p.a_ml + (ra + unit) * 2, p.a_o + (ra + unit) * D + c0 + part * 4, (p.na - unit + U - 1) / U, U * 2, U * D);
   if (tiles) {
     // state s of the own list: slot w0 + s + g, head h % G of the group
     const ListPieces own = list_pieces(start, tiles, per, p.warps);
     const int64_t at = ((int64_t)own.w0 + g + unit) * G + h % G;
-    add_states(r, p.b_ml + at * 2, p.b_o + at * D + c0 + part * 4, (own.n - unit + U - 1) / U, (int64_t)U * G * 2,
+    add_states<NB>(r, p.b_ml + at * 2, p.b_o + at * D + c0 + part * 4, (own.n - unit + U - 1) / U, (int64_t)U * G * 2,
                (int64_t)U * G * D);
   }
   if (part == 0) {
@@ -350,10 +350,10 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   if (lane == 0 && warp == 0 && blockIdx.y == 0 && p.lse) p.lse[bh] = z == 0.f ? -INFINITY : (M + __log2f(z)) * kLn2R;
 }
 
-template <int D, int SL, int WPR>
+template <int D, int SL, int WPR, int NB = 4>
 cudaError_t launch_merge_sl(const MergeParams& p, cudaStream_t stream) {
   const int rows = p.B * p.H;
-  return launch_chained(decode_merge_kernel<D, SL, WPR>,
+  return launch_chained(decode_merge_kernel<D, SL, WPR, NB>,
                         (unsigned)((rows + 4 / WPR - 1) / (4 / WPR)), D / SL, 128, 0, 1, p, stream);
 }
 
@@ -365,6 +365,7 @@ cudaError_t launch_merge_d(const MergeParams& p, cudaStream_t stream) {
   // 84.4, 80.1; 8,192 166.9, 168.4, 158.7).
   constexpr int SL = D < 128 ? D : 128;
   const int64_t warps = (int64_t)p.B * p.H * (D / SL), most = kPlanSms * 36;
+  if (p.many && p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4, 16>(p, stream);
   if (p.B * p.H <= kPlanSms) return launch_merge_sl<D, 32, 4>(p, stream);
   if (warps * 4 <= (p.states >= 8 ? 2 * most : most)) return launch_merge_sl<D, SL, 4>(p, stream);
   if (warps * 2 <= most) return launch_merge_sl<D, SL, 2>(p, stream);

@@ -326,3 +326,25 @@ def test_packed_rows_past_four_gigabytes():
     c = [0, 300, 600, 900]
     packed.check(o[at:, :4], lse[:4, at:], q[at:, :4], k[at:], v[at:], c, c, True, None, None, d ** -0.5)
     assert not o[:at].any() and math.isfinite(float(lse[:, :at].sum()))
+
+
+# ------------------------------------------------------------------ the debug library
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B", [3, 90])
+def test_debug_library_gives_the_same(e4m3, B):
+    """Bounds checks before every copy: none fails, and the results are the product library's bit for bit."""
+    want, got = Calls(1, e4m3, B), Calls(1, e4m3, B)
+    want.run()
+    torch.cuda.synchronize()
+    mattn.use_debug_library(True)
+    try:
+        if not os.path.exists(mattn.DEBUG_LIB_PATH):
+            pytest.skip("the debug library is not built")
+        got.run()
+        torch.cuda.synchronize()
+        rc, word = mattn.device_status()
+        assert mattn.lib().mattn_debug_checks() == 1 and rc == 0, hex(word)
+    finally:
+        mattn.use_debug_library(False)
+    for a, b in zip(got.outputs(), want.outputs()):
+        assert torch.equal(a, b)
