@@ -162,11 +162,12 @@ struct State8 {
     float s[NT][MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float acc[NT][4][4];
+      constexpr int A = NT == 2 && D >= 128 ? 2 : 4;  // sums that do not wait on each other, by the registers left
+      float acc[NT][A][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < A; ++a)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[nt][a][j] = 0.f;
 #pragma unroll
@@ -181,14 +182,15 @@ struct State8 {
           const uint32_t f[4] = {e4m3::to_half2(wa[w]), e4m3::to_half2(wb[w]), e4m3::to_half2_hi(wa[w]),
                                  e4m3::to_half2_hi(wb[w])};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816_f16(acc[nt][w], f, qf[nt][i0 + w][0], qf[nt][i0 + w][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816_f16(acc[nt][w % A], f, qf[nt][i0 + w][0], qf[nt][i0 + w][1]);
         }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[nt][mt][j] = ((acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][2][j] + acc[nt][3][j])) * qs[nt][j & 1];
+          s[nt][mt][j] = (A == 4 ? (acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][A - 2][j] + acc[nt][A - 1][j])
+                                 : acc[nt][0][j] + acc[nt][1][j]) * qs[nt][j & 1];
     }
     // the rows' powers, from the lane that loaded them
     float kp[T::kRows], vp[T::kRows];
