@@ -28,6 +28,14 @@
 //
 // Roles (384 threads) and tensor memory: as attention_persist.cu; every wait is bounded
 // in time and gives up by raising a CTA-wide abort flag and a device error bit.
+//
+// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads of 128, 349 us = 1,576
+// (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads, 306-317 us =
+// 1,200-1,240, the same tokens as 64 prompts of 256 89 us = 389, 12 images of 1 to 3,038 patches, 16 heads of 80,
+// 186 us = 929.  Long lists run at the forward's own rate; an item costs 2.5 to 5 us beside its
+// tiles (its first S, its last P V and its output, which only the other query tile's work hides).
+// Tried without gain: the output staged in shared memory (d = 80 and 64 2% slower), O read from tensor memory 32 or
+// 64 columns at a time, a warp for K tiles alone, the scheduler's next pair fetched ahead.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const __grid_
       const PackedPair x = pair_at(b0, j);
       const int at = atomicAdd(&bins[bin_of(x)], 1);
       // (sequences that overlap could have more pairs than there is room for)
-      if (at < p.max_pairs) p.plan->pair[at] = x;
+      if (at >= 0 && at < p.max_pairs) p.plan->pair[at] = x;
     }
     __syncthreads();
   }
@@ -194,6 +202,10 @@ struct Item {
     const int4 a = *reinterpret_cast<const int4*>(&pair);
     q_row = a.x; rows = a.y; k_row = a.z; keys = a.w;
     pos0 = pair.pos0;
+    // (a pair that the plan left unwritten, as for sequences that overlap, may hold anything: no rows then)
+    if (q_row < 0 || q_row > p.T || rows > p.T - q_row || k_row < 0 || k_row > p.T_k || keys < 0 || keys > p.T_k - k_row ||
+        pos0 < -p.T || pos0 > p.T_k)
+      rows = 0;
     h = item % p.H;
     id = item;
     seen_tiles(p, pos0, min(rows, 128), keys, &lo0, &hi0);
@@ -222,6 +234,12 @@ struct Item {
     return false;
   }
 };
+
+// The item marked before `id` in its CTA, or -1.
+__device__ __forceinline__ int next_marked(const PackedParams& p, int id) {
+  const int x = p.marked[id];
+  return x < p.max_pairs * p.H ? x : -1;
+}
 
 struct Bar {
   uint64_t q_full[kQSlots], q_empty[kQSlots];
@@ -329,7 +347,7 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
         it.set(p, bar->pair(p, id), id);
         it.marked = 0;
         it.again = again ? 1 : 0;
-        id = again ? p.marked[id] : (p.direct ? direct_item(id / (int)gridDim.x + 1) : gridDim.x + atomicAdd(&p.plan->next, 1));
+        id = again ? next_marked(p, id) : (p.direct ? direct_item(id / (int)gridDim.x + 1) : gridDim.x + atomicAdd(&p.plan->next, 1));
       } else {
         it.h = again ? kEnd : kDrain;
         it.n = 0;
@@ -470,9 +488,9 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8], ui
 
 // This thread's row of a tile that it sees in part: the scores of columns outside [lo, hi]
 // (none inside where lo > hi) become -inf where they lie, in tensor memory.  In the pass
-// over the scores itself the same selects slow every tile, masked or not (its code is
-// fetched and its registers are held: one sequence of 16,384 363 us,
-// 359 with the tiles' bounds read each time, 348 so).
+// over the scores itself the same selects slow every tile, masked or not, as its code is
+// fetched and its registers are held (one sequence of 16,384, 8 heads of 128: 369 us, so 359, and
+// 348 with the bounds of the tiles seen whole kept in registers).
 __device__ __forceinline__ void mask_scores(uint32_t s_tmem, int lo, int hi) {
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {
@@ -856,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     ptx::tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x < 256 && !*abort_flag) {
-    for (int id = bar->marked; id >= 0; id = p.marked[id]) {
+    for (int id = bar->marked; id >= 0; id = next_marked(p, id)) {
       Item it;
       it.set(p, bar->pair(p, id), id);
       add_odd_values<D>(p, it, threadIdx.x);

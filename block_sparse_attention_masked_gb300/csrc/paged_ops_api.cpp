@@ -97,7 +97,7 @@ int fill_rows(const char* what, const void* k, const void* v, const int64_t* tok
   int rc = check_cache(what, c, B, H_kv, d);
   if (rc) return rc;
   if (dtype != MATTN_BF16) return report_error(MATTN_ERR_UNSUPPORTED, "%s takes bf16 rows", what);
-  if (!k || !v || !token_stride || !head_stride)
+  if ((T != 0 && (!k || !v)) || !token_stride || !head_stride)
     return report_error(MATTN_ERR_INVALID_ARG, "%s: k, v and their strides must be non-NULL", what);
   if (T < 0) return report_error(MATTN_ERR_INVALID_ARG, "%s: T must be >= 0", what);
   if (!cu && T != B) return report_error(MATTN_ERR_INVALID_ARG, "%s: without cu_seqlens there is one token for each sequence", what);
@@ -134,11 +134,11 @@ int fill_rows(const char* what, const void* k, const void* v, const int64_t* tok
   // rows are read and written in no order.  (Interleaved views, as k and v of one
   // projection or of one pool, share an extent without sharing a byte: the two
   // tensors of a side may; whole sides may not.)
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2 && T > 0; ++i)
     for (int j = 0; j < 2; ++j)
       if (at[i].meets(pages_extent(c, j, H_kv, d)))
         return report_error(MATTN_ERR_INVALID_ARG, "%s: the rows overlap the cache", what);
-  if ((reads && rows[0] == rows[1]) || (!reads && (pages[0] == pages[1] || (exps[0] && exps[0] == exps[1]))))
+  if ((reads && T > 0 && rows[0] == rows[1]) || (!reads && (pages[0] == pages[1] || (exps[0] && exps[0] == exps[1]))))
     return report_error(MATTN_ERR_INVALID_ARG, "%s: k and v are written to one place", what);
   p->table = c->page_table;
   p->cu = cu;

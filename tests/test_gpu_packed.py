@@ -267,6 +267,24 @@ def test_packed_outputs_made_by_the_call():
     assert empty[0].shape == (0, 4, 64) and empty[1].shape == (4, 0)
 
 
+@pytest.mark.parametrize("T,B", [(300, 3), (9000, 3), (9000, 2000)])
+def test_packed_sequences_that_are_none(T, B):
+    """Ends that do not ascend, overlap or lie outside the rows: clamped, nothing outside the outputs
+    is written, and the next call is right."""
+    q, k, v = inputs(T, T, 4, 2, 64, 9)
+    g = torch.Generator().manual_seed(3)
+    for low, high in ((-50, T + 50), (-(1 << 31), (1 << 31) - 1)):
+        cu = torch.randint(low, high, (B + 1,), generator=g).to(torch.int32).cuda()
+        guard = torch.full((T + 64, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((4, T), 7.0, device="cuda")
+        mattn.attention_packed(q, k, v, cu, cu.flip(0), out=guard[32 : 32 + T], lse=lse)
+        torch.cuda.synchronize()
+        assert bool((guard[:32] == 7).all()) and bool((guard[32 + T:] == 7).all())
+    c = _cu([100, 77, T - 177])
+    o, lse = mattn.attention_packed(q, k, v, _i32(c))
+    check(o, lse, q, k, v, c, c, True, None, None, 64 ** -0.5)
+
+
 @pytest.mark.parametrize("d", [64, 80, 96, 128])
 def test_packed_waits_run_out(d):
     q, k, v = inputs(700, 700, 4, 2, d, 7)

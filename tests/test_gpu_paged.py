@@ -502,6 +502,26 @@ def test_cache_write_of_one_token_each():
             assert torch.equal(a[0], k) and torch.equal(a[1], v)
 
 
+def test_cache_calls_without_rows():
+    """A step with nothing to write or read back."""
+    c = Cache(2, 2, 64, 16, 3, True)
+    before = c.held("k")
+    none = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    mattn.cache_write(none, none, c.k, c.v, c.table, _i32([0, 0, 0]), **c.kw())
+    k, v = mattn.cache_read(c.k, c.v, c.table, _i32([0, 0, 0]), 0, **c.kw())
+    assert k.shape == v.shape == (0, 2, 64) and torch.equal(c.held("k"), before)
+
+
+@pytest.mark.parametrize("bad", [[5, 3, 40], [-7, 2000000000, 3], [2147483647, -2147483648, 0], [40, 40, 40]])
+def test_cache_calls_with_sequences_that_are_none(bad):
+    """Ends that do not ascend or lie outside the rows: every row stays inside its tensors."""
+    c = Cache(2, 2, 64, 16, 3, True, spare=0)
+    k, v = rows_of(1, 40, 2, 64)
+    mattn.cache_write(k, v, c.k, c.v, c.table, _i32(bad), _i32([2147483647, -5]), **c.kw())
+    mattn.cache_read(c.k, c.v, c.table, _i32(bad), 40, _i32([-2147483648, 7]), **c.kw())
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ waits that run out
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128, 256])
