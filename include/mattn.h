@@ -584,8 +584,8 @@ int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int6
  *               0 .. table_pages * page are clamped.  Positions without a page are
  *               no keys.  What rows hold that no query sees is not used.
  *   window      0: every key; sink_tokens >= 0, 0 without a window
- *   At most 2^31 - 1 tiles of keys (of 32 keys in e4m3 or at d = 64, else 16) in
- *   all of B tables.
+ *   At most 2^31 - 1 tiles of keys in all of B tables (16 keys; 32 in e4m3 or at
+ *   d = 64, 64 where both; 16 in e4m3 at d = 256 with H / H_kv > 8).
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Sums,
  * statistics and states are fp32.  Softmax weights meet the values as two bf16
  * parts, 2^-16 of a weight off at most; in e4m3 as one f16 value, 2^-11 off, with
