@@ -30,7 +30,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["attention_fwd.cu", "attention_persist.cu", "attention_sp.cu", "rr_select.cu", "received.cu", "decode.cu", "mattn_api.cpp",
            "mattn_noalloc.cu", "qk_rope.cu", "decode_shared.cu", "decode_rows.cu", "block_select.cu",
-           "decode_ops_api.cpp", "paged_cache.cu", "decode_paged.cu", "attention_packed.cu",
+           "decode_ops_api.cpp", "paged_cache.cu", "decode_paged.cu", "attention_packed.cu", "attention_packed_256.cu",
            "paged_ops_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

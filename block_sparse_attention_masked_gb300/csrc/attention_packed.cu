@@ -41,6 +41,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "attention_packed.cuh"
 #include "attention_tiles.cuh"
 #include "kernel_params.h"
 #include "paged_ops.h"
@@ -55,40 +56,12 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
 
-// Sequence b's rows and keys, inside the packed rows whatever the arrays hold.
-struct Sequence {
-  int q0, nq, k0, nk;
-};
-__device__ __forceinline__ Sequence sequence(const PackedParams& p, int b) {
-  auto in = [](int x, int n) { return x < 0 ? 0 : (x > n ? n : x); };
-  Sequence s;
-  s.q0 = in(__ldg(p.cu_q + b), p.T);
-  s.nq = in(__ldg(p.cu_q + b + 1), p.T) - s.q0;
-  s.k0 = in(__ldg(p.cu_k + b), p.T_k);
-  s.nk = in(__ldg(p.cu_k + b + 1), p.T_k) - s.k0;
-  if (s.nq < 0) s.nq = 0;
-  if (s.nk < 0) s.nk = 0;
-  return s;
-}
-
-// The key tiles [lo, hi] that rows r0 .. r0 + n - 1 of a pair see (n < 1 or lo > hi: none).
-__device__ __forceinline__ void seen_tiles(const PackedParams& p, int pos, int n, int keys, int* lo, int* hi) {
-  int last = keys - 1, first = 0;
-  if (p.causal) {
-    last = min(last, pos + n - 1);
-    if (p.window) first = max(0, pos - p.window + 1);
-  }
-  *lo = first >> 7;
-  *hi = n > 0 && last >= first ? last >> 7 : -1;
-  if (*hi < 0) *lo = 0;
-}
-
 __device__ __forceinline__ int pair_work(const PackedParams& p, const PackedPair& x) {
   int w = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     int lo, hi;
-    seen_tiles(p, x.pos0 + 128 * s, min(x.rows - 128 * s, 128), x.keys, &lo, &hi);
+    seen_tiles<7>(p, x.pos0 + 128 * s, min(x.rows - 128 * s, 128), x.keys, &lo, &hi);
     w += hi - lo + 1;
   }
   return w;
@@ -203,13 +176,11 @@ struct Item {
     q_row = a.x; rows = a.y; k_row = a.z; keys = a.w;
     pos0 = pair.pos0;
     // (a pair that the plan left unwritten, as for sequences that overlap, may hold anything: no rows then)
-    if (q_row < 0 || q_row > p.T || rows > p.T - q_row || k_row < 0 || k_row > p.T_k || keys < 0 || keys > p.T_k - k_row ||
-        pos0 < -p.T || pos0 > p.T_k)
-      rows = 0;
+    if (!in_bounds(p, pair)) rows = 0;
     h = item % p.H;
     id = item;
-    seen_tiles(p, pos0, min(rows, 128), keys, &lo0, &hi0);
-    seen_tiles(p, pos0 + 128, min(rows - 128, 128), keys, &lo1, &hi1);
+    seen_tiles<7>(p, pos0, min(rows, 128), keys, &lo0, &hi0);
+    seen_tiles<7>(p, pos0 + 128, min(rows - 128, 128), keys, &lo1, &hi1);
     lo = hi0 < lo0 ? lo1 : (hi1 < lo1 ? lo0 : min(lo0, lo1));
     const int end = max(hi0, hi1);
     n = end < lo ? 0 : end - lo + 1;
@@ -296,12 +267,6 @@ __device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t b
   *reinterpret_cast<volatile int*>(&bar->abort_flag) = 1;
   atomicOr(p.err, bit);
 }
-__device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
-  if (!*abort_flag) return;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
-}
-
 // 128 rows of one head from packed row `row` on, laid out as tile_mma.cuh has them.
 template <int D>
 __device__ __forceinline__ void load_rows(const CUtensorMap* maps, uint8_t* dst, uint64_t* bar, int h, int row,
@@ -418,9 +383,6 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
   let_copies_land(abort_flag);
 }
 
-// The 16-bit halves of x that are no infinity or NaN, and zeros for those that are.
-__device__ __forceinline__ uint32_t clean(uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
-
 // A landed V tile: rows from `rows` on and values that are not finite become zeros.  One
 // warp; the layout does not matter, as a row's columns lie in rows of every chunk.
 template <int D>
@@ -477,13 +439,6 @@ __device__ __forceinline__ const Item* take_item(const PackedParams& p, Bar* bar
 __device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, after its last read)
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar->item_empty[i % kItems]);
-}
-
-// 32 bytes of an output row, written once and not read again here: first out of L2.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8], uint64_t policy) {
-  asm volatile("st.global.L1::no_allocate.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
-               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "l"(policy)
-               : "memory");
 }
 
 // This thread's row of a tile that it sees in part: the scores of columns outside [lo, hi]
@@ -882,6 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
   }
 }
 
+cudaError_t launch_plan(const PackedParams& p, cudaStream_t stream) {
+  return launch_chained(packed_plan_kernel, 1, 1, kPlanThreads, 0, 1, p, stream);
+}
+
 template <int D>
 cudaError_t launch_d(const PackedParams& p, cudaStream_t stream) {
   using G = Geo<D>;
@@ -893,7 +852,7 @@ cudaError_t launch_d(const PackedParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_shared(kern, smem, &done);
   if (e != cudaSuccess) return e;
-  if (!p.direct && (e = launch_chained(packed_plan_kernel, 1, 1, kPlanThreads, 0, 1, p, stream)) != cudaSuccess) return e;
+  if (!p.direct && (e = launch_plan(p, stream)) != cudaSuccess) return e;
   const int64_t items = (int64_t)p.max_pairs * p.H;
   return launch_chained(kern, (unsigned)(items < kPlanSms ? items : kPlanSms), 1, kThreads, smem, 1, p, stream);
 }
@@ -906,6 +865,10 @@ cudaError_t launch_attention_packed(const PackedParams& p, int d, cudaStream_t s
     case 80: return launch_d<80>(p, stream);
     case 96: return launch_d<96>(p, stream);
     case 128: return launch_d<128>(p, stream);
+    case 256: {
+      const cudaError_t e = launch_plan(p, stream);
+      return e == cudaSuccess ? launch_attention_packed_256(p, stream) : e;
+    }
     default: return cudaErrorInvalidValue;
   }
 }

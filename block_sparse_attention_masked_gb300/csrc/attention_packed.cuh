@@ -1,0 +1,67 @@
+// Device pieces that the packed forwards (attention_packed.cu, attention_packed_256.cu)
+// share: their sequences and key tiles, values that are not finite, output rows.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "paged_ops.h"
+#include "ptx.cuh"
+
+namespace mattn {
+namespace {
+
+// Sequence b's rows and keys, inside the packed rows whatever the arrays hold.
+struct Sequence {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Sequence sequence(const PackedParams& p, int b) {
+  auto in = [](int x, int n) { return x < 0 ? 0 : (x > n ? n : x); };
+  Sequence s;
+  s.q0 = in(__ldg(p.cu_q + b), p.T);
+  s.nq = in(__ldg(p.cu_q + b + 1), p.T) - s.q0;
+  s.k0 = in(__ldg(p.cu_k + b), p.T_k);
+  s.nk = in(__ldg(p.cu_k + b + 1), p.T_k) - s.k0;
+  if (s.nq < 0) s.nq = 0;
+  if (s.nk < 0) s.nk = 0;
+  return s;
+}
+
+// The key tiles [lo, hi] of 2^SHIFT keys that the n rows at positions pos, pos + 1, .. see
+// (n < 1 or lo > hi: none).
+template <int SHIFT>
+__device__ __forceinline__ void seen_tiles(const PackedParams& p, int pos, int n, int keys, int* lo, int* hi) {
+  int last = keys - 1, first = 0;
+  if (p.causal) {
+    last = min(last, pos + n - 1);
+    if (p.window) first = max(0, pos - p.window + 1);
+  }
+  *lo = first >> SHIFT;
+  *hi = n > 0 && last >= first ? last >> SHIFT : -1;
+  if (*hi < 0) *lo = 0;
+}
+
+// Whether a pair's rows and keys lie in the packed rows.
+__device__ __forceinline__ bool in_bounds(const PackedParams& p, const PackedPair& x) {
+  return !(x.q_row < 0 || x.q_row > p.T || x.rows > p.T - x.q_row || x.k_row < 0 || x.k_row > p.T_k || x.keys < 0 ||
+           x.keys > p.T_k - x.k_row || x.pos0 < -p.T || x.pos0 > p.T_k);
+}
+
+// The 16-bit halves of x that are no infinity or NaN, and zeros for those that are.
+__device__ __forceinline__ uint32_t clean(uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
+
+__device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
+  if (!*abort_flag) return;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 0; it < 0x10000000u && ptx::globaltimer_ns() - t0 < 2000000ull; ++it) { }
+}
+
+// 32 bytes of an output row, written once and not read again here: first out of L2.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8], uint64_t policy) {
+  asm volatile("st.global.L1::no_allocate.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "l"(policy)
+               : "memory");
+}
+
+}  // namespace
+}  // namespace mattn

@@ -69,8 +69,8 @@ int make_state_map(CUtensorMap* map, const void* base, int d, int64_t splits, in
 int make_pages_map(CUtensorMap* map, const void* base, bool e4m3, int d, int64_t rows, int64_t heads, int64_t n_pages,
                    int64_t row_stride, int64_t head_stride, int64_t page_stride);
 // View of packed rows [rows][heads][cols] of bf16 with the given strides (in elements):
-// boxes of box_cols columns (64, 32 or 16: swizzled by their bytes) x 128 rows of a head.
-int make_packed_map(CUtensorMap* map, const void* base, int cols, int box_cols, int64_t rows, int64_t heads,
-                    int64_t row_stride, int64_t head_stride);
+// boxes of box_cols columns (64, 32 or 16: swizzled by their bytes) x box_rows rows of a head.
+int make_packed_map(CUtensorMap* map, const void* base, int cols, int box_cols, int box_rows, int64_t rows,
+                    int64_t heads, int64_t row_stride, int64_t head_stride);
 
 }  // namespace mattn

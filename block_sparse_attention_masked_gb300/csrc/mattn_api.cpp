@@ -1047,13 +1047,13 @@ int make_pages_map(CUtensorMap* map, const void* base, bool e4m3, int d, int64_t
                 e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
-int make_packed_map(CUtensorMap* map, const void* base, int cols, int box_cols, int64_t rows, int64_t heads,
-                    int64_t row_stride, int64_t head_stride) {
+int make_packed_map(CUtensorMap* map, const void* base, int cols, int box_cols, int box_rows, int64_t rows,
+                    int64_t heads, int64_t row_stride, int64_t head_stride) {
   const int rc = get_encoder();
   if (rc) return rc;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, (cuuint32_t)kTile};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows};
   return encode(map, base, 3, dims, strides, box,
                 box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
                                : (box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B));

@@ -14,6 +14,7 @@
 #include "mattn.h"
 #include "op_checks.h"
 #include "paged_ops.h"
+#include "plan_rules.h"
 
 namespace mattn {
 namespace {
@@ -346,8 +347,8 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   if (rc) return rc;
   if (H_kv < 1 || H % H_kv)
     return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: H = %d is not a multiple of H_kv = %d", H, H_kv);
-  if (d != 64 && d != 80 && d != 96 && d != 128)
-    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: head dim %d (64, 80, 96, 128)", d);
+  if (d != 64 && d != 80 && d != 96 && d != 128 && d != 256)
+    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: head dim %d (64, 80, 96, 128, 256)", d);
   if (dtype != MATTN_BF16) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed takes bf16");
   if (T_k < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: T_k must be >= 0");
   if (T_k > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: T_k exceeds 2^30");
@@ -378,16 +379,16 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   if (T == 0) return MATTN_OK;
   PackedParams p;
   memset(&p, 0, sizeof(p));
-  const int rem = d % 64, vw = d % 64 == 0 ? 64 : (d % 32 == 0 ? 32 : 16);
+  const int rem = d % 64, vw = d % 64 == 0 ? 64 : (d % 32 == 0 ? 32 : 16), kt = d == 256 ? kPackedKeys256 : kTile;
   auto maps = [&](CUtensorMap* m, const void* x, int64_t rows, int heads, int i) {  // 64-column chunks and the rest
-    const int e = make_packed_map(&m[0], x, d, 64, rows, heads, ts[i], hs[i]);
+    const int n = i ? kt : kTile, e = make_packed_map(&m[0], x, d, 64, n, rows, heads, ts[i], hs[i]);
     if (e || !rem) return e;
-    return make_packed_map(&m[1], static_cast<const char*>(x) + (d - rem) * 2, rem, rem, rows, heads, ts[i], hs[i]);
+    return make_packed_map(&m[1], static_cast<const char*>(x) + (d - rem) * 2, rem, rem, n, rows, heads, ts[i], hs[i]);
   };
   if ((rc = maps(p.tq, q, T, H, 0))) return rc;
   if (T_k > 0) {  // (else no tile is loaded)
     if ((rc = maps(p.tk, k, T_k, H_kv, 1))) return rc;
-    if ((rc = make_packed_map(&p.tv, v, d, vw, T_k, H_kv, ts[2], hs[2]))) return rc;
+    if ((rc = make_packed_map(&p.tv, v, d, vw, kt, T_k, H_kv, ts[2], hs[2]))) return rc;
   }
   p.o = o;
   p.lse = lse;
@@ -408,7 +409,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.window = window < kMaxRows ? window : (int)kMaxRows;
   p.max_pairs = (int)packed_pairs(T, B);
   while (((2 * ((int64_t)T_k / 128 + 1)) >> p.work_shift) >= 1024) ++p.work_shift;
-  p.direct = (int64_t)p.max_pairs * H <= kPackedDirect * kPlanSms ? 1 : 0;
+  p.direct = d != 256 && (int64_t)p.max_pairs * H <= kPackedDirect * kPlanSms ? 1 : 0;
   p.scale_log2 = scale_log2(softmax_scale, d);
   p.selftest = g_wait_selftest.load();
   return launched(launch_attention_packed(p, d, stream), "attention_packed launch");

@@ -129,7 +129,7 @@ def packed_case(nq, H, Hkv, d, nk=None, causal=True, window=None, sink=False, sc
     return out, lse
 
 
-@pytest.mark.parametrize("d", [64, 80, 96, 128])
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("heads", [(1, 1), (4, 4), (8, 2), (6, 1)])
 def test_packed_heads(heads, causal, d):
@@ -142,7 +142,7 @@ def test_packed_lengths(nq, causal):
     packed_case(nq, 4, 2, 128, causal=causal, seed=len(nq) + nq[0], sink=nq[0] == 127)
 
 
-@pytest.mark.parametrize("d", [80, 128])
+@pytest.mark.parametrize("d", [80, 128, 256])
 @pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 500, 100000])
 def test_packed_windows(window, d):
     packed_case([700, 33, 260], 4, 1, d, window=window, seed=window, sink=window == 100)
@@ -150,7 +150,7 @@ def test_packed_windows(window, d):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("d", [64, 80, 96, 128])
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
 def test_packed_with_cached_rows(d, causal):
     """More keys than queries, none, fewer (rows that see nothing under causality)."""
     nq, nk = [100, 1, 64, 300, 7, 140], [612, 900, 0, 120, 0, 139]
@@ -160,13 +160,13 @@ def test_packed_with_cached_rows(d, causal):
 
 
 @pytest.mark.parametrize("layout", ["fused", "heads"])
-@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("d", [64, 80, 128, 256])
 def test_packed_layouts(d, layout):
     packed_case([100, 300, 29], 6, 2, d, layout=layout, seed=1)
     packed_case([100, 300], 4, 1, d, nk=[150, 300], layout=layout, seed=2, causal=False)
 
 
-@pytest.mark.parametrize("d", [64, 80, 96, 128])
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
 def test_packed_padding(d):
     """Rows of no sequence, NaN: unused, and left as they are."""
     packed_case([100, 0, 257], 4, 2, d, pad=(3, 40), seed=3)
@@ -180,6 +180,35 @@ def test_packed_score_ranges(q_scale):
     packed_case([300, 20, 515], 4, 2, 80, q_scale=q_scale, seed=6, causal=False, sink=True, scale=0.1)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq", [[1], [63, 64, 65], [127, 128, 129], [255, 256, 257], [0, 3, 0, 0, 511, 0], [1] * 70, [1025], [640, 1, 640]])
+def test_packed_256_lengths(nq, causal):
+    packed_case(nq, 4, 2, 256, causal=causal, seed=len(nq) + nq[0], sink=nq[0] == 127)
+    packed_case(nq, 12, 1, 256, nk=[2 * n + 1 for n in nq], causal=causal, seed=len(nq))
+
+
+@pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -20, 40.0, 400.0])
+def test_packed_256_score_ranges(q_scale):
+    packed_case([300, 20, 515], 4, 2, 256, q_scale=q_scale, seed=5, scale=0.1)
+    packed_case([300, 20, 515], 4, 2, 256, q_scale=q_scale, seed=6, causal=False, sink=True, scale=0.1)
+
+
+def test_packed_256_more_items_than_sms():
+    """Items behind one another in a CTA, marked ones among them."""
+    nq = [2000, 5, 700, 1300, 64, 900]
+    packed_case(nq, 16, 4, 256, seed=11)
+    cq = _cu(nq)
+    q, k, v = inputs(cq[-1], cq[-1], 16, 4, 256, 12)
+    want, lse = mattn.attention_packed(q, k, v, _i32(cq))
+    for b in (0, 2, 3, 5):
+        v[cq[b + 1] - 1] = NAN  # the last query's alone
+    for _ in range(3):
+        o, l = mattn.attention_packed(q, k, v, _i32(cq))
+        hit = torch.zeros(cq[-1], dtype=torch.bool, device="cuda")
+        hit[[cq[b + 1] - 1 for b in (0, 2, 3, 5)]] = True
+        assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], want[~hit]) and torch.equal(l, lse)
+
+
 def test_packed_many_sequences():
     """More sequences than the plan takes at a time."""
     g = torch.Generator().manual_seed(1)
@@ -191,9 +220,10 @@ def test_packed_many_sequences():
 def test_packed_long():
     packed_case([5000, 300, 9000, 1], 2, 1, 128, seed=8)
     packed_case([40, 9], 2, 2, 64, nk=[70000, 20], seed=9)
+    packed_case([3000, 200, 40, 1], 2, 1, 256, nk=[3000, 9000, 70000, 2], seed=10)
 
 
-@pytest.mark.parametrize("d", [64, 80, 96, 128])
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
 @pytest.mark.parametrize("causal", [True, False])
 def test_packed_values_that_are_not_finite(d, causal):
     """Infinite and NaN values reach the rows that see them, in their columns, and no other;
@@ -267,25 +297,26 @@ def test_packed_outputs_made_by_the_call():
     assert empty[0].shape == (0, 4, 64) and empty[1].shape == (4, 0)
 
 
+@pytest.mark.parametrize("d", [64, 256])
 @pytest.mark.parametrize("T,B", [(300, 3), (9000, 3), (9000, 2000)])
-def test_packed_sequences_that_are_none(T, B):
+def test_packed_sequences_that_are_none(T, B, d):
     """Ends that do not ascend, overlap or lie outside the rows: clamped, nothing outside the outputs
     is written, and the next call is right."""
-    q, k, v = inputs(T, T, 4, 2, 64, 9)
+    q, k, v = inputs(T, T, 4, 2, d, 9)
     g = torch.Generator().manual_seed(3)
     for low, high in ((-50, T + 50), (-(1 << 31), (1 << 31) - 1)):
         cu = torch.randint(low, high, (B + 1,), generator=g).to(torch.int32).cuda()
-        guard = torch.full((T + 64, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        guard = torch.full((T + 64, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
         lse = torch.full((4, T), 7.0, device="cuda")
         mattn.attention_packed(q, k, v, cu, cu.flip(0), out=guard[32 : 32 + T], lse=lse)
         torch.cuda.synchronize()
         assert bool((guard[:32] == 7).all()) and bool((guard[32 + T:] == 7).all())
     c = _cu([100, 77, T - 177])
     o, lse = mattn.attention_packed(q, k, v, _i32(c))
-    check(o, lse, q, k, v, c, c, True, None, None, 64 ** -0.5)
+    check(o, lse, q, k, v, c, c, True, None, None, d ** -0.5)
 
 
-@pytest.mark.parametrize("d", [64, 80, 96, 128])
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
 def test_packed_waits_run_out(d):
     q, k, v = inputs(700, 700, 4, 2, d, 7)
     cu = _i32([0, 300, 700])

@@ -245,7 +245,7 @@ def _packed(L, **kw):
     ("other keys than queries and no cu_seqlens_k", {"T_k": 99}, -1),
     ("more than 2^30 rows", {"T": (1 << 30) + 1, "T_k": (1 << 30) + 1}, -2),
     ("2^31 items", {"T": 1 << 30, "T_k": 1 << 30, "H": 512}, -2),
-    ("head dim 256", {"d": 256}, -2),
+    ("head dim 112", {"d": 112}, -2),
     ("head dim 72", {"d": 72}, -2),
     ("fp32", {"dtype": F32}, -2),
     ("a negative window", {"window": -4}, -1),
