@@ -1,22 +1,29 @@
 // attention_packed.cu's attention for heads of 256, for sm_103a, where two query tiles'
 // accumulators would take all of tensor memory: one 128-row query tile at a time against
-// key tiles of 64, S double-buffered, as attention_sp.cu has it:
-//   S_t = Q K_t^T     M128 N64 K256, into S buffer t % 2
-//   P_t = exp2(S_t scale log2e - m)    one row a thread, P over its S
-//   O  += P_t V_t     M128 N256 K64
+// key tiles of 128, S double-buffered,
+//   S_g = Q K_g^T     M128 N128 K256, into S buffer g % 2
+//   P_g = exp2(S_g scale log2e - m)    two threads a row, 64 keys each, P over its S
+//   O  += P_g V_g     M128 N256 K128
 //   issue order  S_0, S_1, [P_0] PV_0, S_2, [P_1] PV_1, S_3, ...
-// 4 d FLOPs a visible (head, pair): bound by the tensor cores.  Tensor memory: S_0 [0, 64),
-// S_1 [64, 128), O [256, 512).  Shared memory: Q (64 KB), rings of two K and two V tiles
-// (32 KB each).
+// 4 d FLOPs a visible (head, pair): bound by the tensor cores.  Tensor memory: S [0, 256),
+// O [256, 512).  Shared memory: Q (64 KB) and rings of 16 KB pieces, five of K (64 columns
+// of a tile) and five of V (32 rows of it), as two whole tiles of each do not fit.
 //
 // A CTA per SM takes items, the query tiles of packed_plan_kernel's pairs head by head,
 // longest first, from a counter, one after another: an item begins when the last one is
 // written.  What a row does not see is treated as there, but that an item whose output
 // may have been spoilt by hidden values is done again at once.
 //
-// Roles (256 threads): warp 0 the items and the TMA copies; warp 1 tensor memory and the
-// products; warps 4..7 softmax and output.  Every wait is bounded in time and gives up by
-// raising a CTA-wide abort flag and a device error bit.
+// Roles (352 threads): warp 0 the items, Q and K; warp 1 tensor memory and the products;
+// warp 2 V; warps 3..10 softmax and output: warps w and w + 4 the same 32 rows, half of a
+// tile's keys and of the output's columns each.  Every wait is bounded in time and gives up
+// by raising a CTA-wide abort flag and a device error bit.
+//
+// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 675 us = 1,628,
+// eight prompts of 1 to 3,352 tokens, 32 heads, 609-621 us = 1,222-1,247, 64 prompts of 256
+// 193 us = 357; an item costs about 3.5 us beside its tiles.  Key tiles of 64, as in
+// attention_sp.cu, took 882 us for the first: a product of 64 columns takes as long as one of
+// 128.  Two groups of softmax warps taking such tiles in turn 910.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,11 +39,13 @@
 namespace mattn {
 namespace {
 
-constexpr int kD = 256, kKT = kPackedKeys256;
-static_assert(kKT == 64, "a key tile's scores are two groups of 32 columns");
-constexpr int kThreads = 256, kStages = 2;
+constexpr int kD = 256;
+constexpr int kThreads = 352;
+constexpr int kPieces = 4, kRing = 5;  // pieces of a K or V tile; in each ring
 constexpr int kQChunk = kTile * 128, kQBytes = kD / 64 * kQChunk;  // chunks of 64 columns, 128-byte swizzle
-constexpr int kKVChunk = kKT * 128, kKVBytes = kD / 64 * kKVChunk;
+constexpr int kPiece = kQChunk;                                    // of K: such a chunk
+constexpr int kVRows = kPackedValues256, kVChunk = kVRows * 128;   // of V: four chunks of 32 rows
+static_assert(kVRows * kPieces == kTile && kVChunk * (kD / 64) == kPiece, "pieces");
 
 // An item: a query tile of a pair, and its key tiles lo .. lo + n - 1.
 struct Item {
@@ -51,17 +60,17 @@ struct Item {
     pos = x.pos0 + 128 * s;
     h = head;
     int hi;
-    seen_tiles<6>(p, pos, rows, keys, &lo, &hi);
+    seen_tiles<7>(p, pos, rows, keys, &lo, &hi);
     n = hi < lo ? 0 : hi - lo + 1;
-    whole_hi = ((p.causal ? min(keys, pos + 1) : keys) >> 6) - 1;
-    whole_lo = p.window ? (max(0, pos + rows - p.window) + 63) >> 6 : 0;
+    whole_hi = ((p.causal ? min(keys, pos + 1) : keys) >> 7) - 1;
+    whole_lo = p.window ? (max(0, pos + rows - p.window) + 127) >> 7 : 0;
   }
   __device__ __forceinline__ bool partial(int kt) const { return kt < whole_lo || kt > whole_hi; }
 };
 
 struct Bar {
   uint64_t q_full;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
   uint64_t v_land;
   uint64_t s_full[2], p_full[2];
   uint64_t pv_done;  // one phase per P V product
@@ -71,6 +80,8 @@ struct Bar {
   int abort_flag;
   int marked[3];     // of item i in [i % 3]: some row of its output is not finite
   Item items[2];
+  uint32_t redo[2][4];   // rows of each half and 32 rows whose tile is done again
+  float half[2][kTile];  // a row's maximum over half a tile, at last half its sum
 };
 
 __device__ __forceinline__ uint64_t dsc(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
@@ -94,12 +105,12 @@ __device__ __forceinline__ void next_item(const PackedParams& p, int64_t total, 
   }
 }
 
-// A landed V tile: rows from `rows` on and values that are not finite become zeros (one warp).
-__device__ __forceinline__ void clean_tile(uint8_t* tile, int rows) {
+// A landed piece of V: rows from `rows` on and values that are not finite become zeros (one warp).
+__device__ __forceinline__ void clean_piece(uint8_t* piece, int rows) {
   const int lane = threadIdx.x & 31;
   for (int c = 0; c < kD / 64; ++c) {
-    uint4* x = reinterpret_cast<uint4*>(tile + c * kKVChunk);
-    for (int i = lane; i < kKVChunk / 16; i += 32) {
+    uint4* x = reinterpret_cast<uint4*>(piece + c * kVChunk);
+    for (int i = lane; i < kVChunk / 16; i += 32) {
       const uint4 v = x[i];
       x[i] = i < rows * 8 ? make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w)) : make_uint4(0, 0, 0, 0);
     }
@@ -108,18 +119,29 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int rows) {
   __syncwarp();
 }
 
-// The values that clean_tile took out, added to the output of the row (a thread's) that
-// sees them.
-__device__ __forceinline__ void add_odd_values(const PackedParams& p, const Item& it, int row, int lo, int hi) {
+// A barrier of the two warps of 32 rows; whether x holds in any of their threads.
+__device__ __forceinline__ bool pair_any(int quarter, bool x) {
+  int r;
+  asm volatile(
+      "{\n.reg .pred a, b;\nsetp.ne.s32 a, %1, 0;\nbarrier.cta.red.or.pred b, %2, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
+      : "=r"(r)
+      : "r"((int)x), "r"(1 + quarter)
+      : "memory");
+  return r;
+}
+
+// The values that clean_piece took out, added to the output of the row (a thread's, half of
+// the columns from `col` on) that sees them.
+__device__ __forceinline__ void add_odd_values(const PackedParams& p, const Item& it, int row, int col, int lo, int hi) {
   if (row >= it.rows) return;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.o) + (((int64_t)it.q_row + row) * p.H + it.h) * kD;
   for (int kt = it.lo; kt < it.lo + it.n; ++kt) {
     if (!it.partial(kt)) continue;
-    for (int j = max(lo, kt * kKT); j <= min(hi, kt * kKT + kKT - 1); ++j) {
+    for (int j = max(lo, kt * kTile); j <= min(hi, kt * kTile + kTile - 1); ++j) {
       const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + (it.k_row + (int64_t)j) * p.v_token +
                                (it.h / p.group) * p.v_head;
 #pragma unroll 4
-      for (int c = 0; c < kD; c += 2) {
+      for (int c = col; c < col + kD / 2; c += 2) {
         const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(v + c)), odd = x ^ clean(x);
         if (!odd) continue;
         __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(o + c);
@@ -135,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = base;
   uint8_t* sk = sq + kQBytes;
-  uint8_t* sv = sk + kStages * kKVBytes;
-  Bar* bar = reinterpret_cast<Bar*>(sv + kStages * kKVBytes);
+  uint8_t* sv = sk + kRing * kPiece;
+  Bar* bar = reinterpret_cast<Bar*>(sv + kRing * kPiece);
   volatile int* abort_flag = &bar->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -145,16 +167,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
     ptx::prefetch_tmap(&p.tk[0]);
     ptx::prefetch_tmap(&p.tv);
     ptx::mbar_init(&bar->q_full, 1);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(&bar->k_full[i], 1);
       ptx::mbar_init(&bar->k_empty[i], 1);
       ptx::mbar_init(&bar->v_full[i], 1);
       ptx::mbar_init(&bar->v_empty[i], 1);
-      ptx::mbar_init(&bar->s_full[i], 1);
-      ptx::mbar_init(&bar->p_full[i], kTile);
     }
-    ptx::mbar_init(&bar->v_land, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bar->s_full[i], 1);
+      ptx::mbar_init(&bar->p_full[i], 2 * kTile);
+    }
     ptx::mbar_init(&bar->pv_done, 1);
+    ptx::mbar_init(&bar->v_land, 1);
     ptx::mbar_init(&bar->o_full, 1);
     ptx::mbar_init(&bar->drain, 1);
     bar->abort_flag = 0;
@@ -184,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
     if (it.h < 0) break;
     const int n = it.n;
     if (warp == 0) {
-      // ---------------------------------------------------------- items and copies
+      // ---------------------------------------------------------- items, Q and K
       const uint64_t keep = ptx::l2_policy_evict_last(), once = ptx::l2_policy_evict_first();
       const int h_kv = it.h / p.group;
       bool ok = true;
@@ -196,44 +220,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
             ptx::tma_load_3d_hint(sq + c * kQChunk, &p.tq[0], &bar->q_full, c * 64, it.h, it.q_row, once);
         }
       }
-      for (int t = 0; t < n; ++t) {
-        const int slot = (e + t) % kStages, kt = it.lo + t, row = it.k_row + kt * kKT;
-        const uint32_t par = (((e + t) / kStages) & 1) ^ 1;
-        if (!debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad) ||
-            !__all_sync(0xffffffffu, ptx::mbar_wait(&bar->k_empty[slot], par, p.timeout_ns, abort_flag))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&bar->k_full[slot], kKVBytes);
-          if (!(p.selftest == 1 && e + t == 0)) {
-#pragma unroll
-            for (int c = 0; c < kD / 64; ++c)
-              ptx::tma_load_3d_hint(sk + slot * kKVBytes + c * kKVChunk, &p.tk[0], &bar->k_full[slot], c * 64, h_kv, row, keep);
-          }
-        }
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_empty[slot], par, p.timeout_ns, abort_flag))) {
-          ok = false;
-          break;
-        }
-        const bool look = again && it.partial(kt);
-        uint8_t* tile = sv + slot * kKVBytes;
-        uint64_t* landing = look ? &bar->v_land : &bar->v_full[slot];
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(landing, kKVBytes);
-#pragma unroll
-          for (int c = 0; c < kD / 64; ++c)
-            ptx::tma_load_3d_hint(tile + c * kKVChunk, &p.tv, landing, c * 64, h_kv, row, keep);
-        }
-        __syncwarp();
-        if (look) {
-          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_land, lands & 1, p.timeout_ns, abort_flag))) {
+      for (int t = 0; ok && t < n; ++t) {
+        const int row = it.k_row + (it.lo + t) * kTile;
+        if (!debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad)) ok = false;
+        for (int c = 0; ok && c < kPieces; ++c) {
+          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->k_empty[slot], ((g / kRing) & 1) ^ 1, p.timeout_ns, abort_flag))) {
             ok = false;
             break;
           }
-          ++lands;
-          clean_tile(tile, min(it.keys - kt * kKT, kKT));
-          if (lane == 0) ptx::mbar_arrive(&bar->v_full[slot]);
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(&bar->k_full[slot], kPiece);
+            if (!(p.selftest == 1 && g == 0))
+              ptx::tma_load_3d_hint(sk + slot * kPiece, &p.tk[0], &bar->k_full[slot], c * 64, h_kv, row, keep);
+          }
+          __syncwarp();
         }
       }
       if (!ok && lane == 0) fail(p, bar, kErrProducer);
@@ -241,6 +242,43 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         next_item(p, total, (int64_t)gridDim.x + atomicAdd(&p.plan->next, 1), &bar->items[(i + 1) & 1]);
         bar->marked[(i + 1) % 3] = 0;
       }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- V
+      const uint64_t keep = ptx::l2_policy_evict_last();
+      const int h_kv = it.h / p.group;
+      bool ok = true;
+      for (int t = 0; ok && t < n; ++t) {
+        const int kt = it.lo + t, row = it.k_row + kt * kTile;
+        if (!debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad)) ok = false;
+        const bool look = again && it.partial(kt);
+        for (int c = 0; ok && c < kPieces; ++c) {
+          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_empty[slot], ((g / kRing) & 1) ^ 1, p.timeout_ns, abort_flag))) {
+            ok = false;
+            break;
+          }
+          uint8_t* piece = sv + slot * kPiece;
+          uint64_t* landing = look ? &bar->v_land : &bar->v_full[slot];
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(landing, kPiece);
+#pragma unroll
+            for (int i = 0; i < kD / 64; ++i)
+              ptx::tma_load_3d_hint(piece + i * kVChunk, &p.tv, landing, i * 64, h_kv, row + c * kVRows, keep);
+          }
+          __syncwarp();
+          if (look) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_land, lands & 1, p.timeout_ns, abort_flag))) {
+              ok = false;
+              break;
+            }
+            ++lands;
+            clean_piece(piece, max(min(it.keys - kt * kTile - c * kVRows, kVRows), 0));
+            if (lane == 0) ptx::mbar_arrive(&bar->v_full[slot]);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail(p, bar, kErrProducer);
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------- products
@@ -252,52 +290,59 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
       const uint32_t v4 = ptx::smem_addr(sv) >> 4;
       constexpr uint32_t hi128 = ptx::smem_desc_hi(1024, ptx::kSw128);
       constexpr uint32_t lbo_k = 1u << 16;  // unused for swizzled K-major operands
-      constexpr uint32_t lbo_v = (uint32_t)(kKVChunk >> 4) << 16;  // V's atoms of 64 columns lie a chunk apart
-      constexpr uint32_t idesc_qk = ptx::idesc_bf16(128, kKT, 0);
+      constexpr uint32_t lbo_v = (uint32_t)(kVChunk >> 4) << 16;  // V's atoms of 64 columns lie a chunk apart
+      constexpr uint32_t idesc_qk = ptx::idesc_bf16(128, kTile, 0);
       constexpr uint32_t idesc_pv = ptx::idesc_bf16(128, kD, 1);
       bool ok = true, issued = false;
-      auto issue_s = [&](int t) {  // K_t landed: S = Q K_t^T
-        const int slot = (e + t) % kStages;
-        if (!wait_all(&bar->k_full[slot], ((e + t) / kStages) & 1)) return false;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          uint32_t acc = 0;
-#pragma unroll 1
-          for (int step = 0; step < kD / 16; ++step) {
-            const uint32_t qo = (uint32_t)(((step >> 2) * kQChunk + (step & 3) * 32) >> 4) + lbo_k;
-            const uint32_t ko = (uint32_t)((slot * kKVBytes + (step >> 2) * kKVChunk + (step & 3) * 32) >> 4) + lbo_k;
-            ptx::mma_ss(tmem + slot * kKT, dsc(q4 + qo, hi128), dsc(k4 + ko, hi128), idesc_qk, acc);
-            acc = 1;
+      auto issue_s = [&](int t) {  // S = Q K^T, piece after piece as they land
+        const int sb = (e + t) & 1;
+        for (int c = 0; c < kPieces; ++c) {
+          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+          if (!wait_all(&bar->k_full[slot], (g / kRing) & 1)) return false;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t qo = (uint32_t)((c * kQChunk + k * 32) >> 4) + lbo_k;
+              const uint32_t ko = (uint32_t)((slot * kPiece + k * 32) >> 4) + lbo_k;
+              ptx::mma_ss(tmem + sb * kTile, dsc(q4 + qo, hi128), dsc(k4 + ko, hi128), idesc_qk, (c > 0 || k > 0) ? 1u : 0u);
+            }
           }
+          __syncwarp();
+          ptx::mma_commit_elect(&bar->k_empty[slot]);
+          issued = true;
         }
-        __syncwarp();
-        ptx::mma_commit_elect(&bar->s_full[slot]);
-        ptx::mma_commit_elect(&bar->k_empty[slot]);
-        issued = true;
+        ptx::mma_commit_elect(&bar->s_full[sb]);
         return true;
       };
       if (n > 0) ok = wait_all(&bar->q_full, passes & 1);
       for (int t = 0; ok && t < 2 && t < n; ++t) ok = issue_s(t);
       for (int t = 0; ok && t < n; ++t) {
-        // P_t and V_t there: O += P_t V_t, then the next scores over P_t
-        const int slot = (e + t) % kStages;
-        if (!wait_all(&bar->p_full[slot], ((e + t) / kStages) & 1) ||
-            !wait_all(&bar->v_full[slot], ((e + t) / kStages) & 1)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-#pragma unroll 1
-          for (int k = 0; k < kKT / 16; ++k) {
-            // 16 keys: 8 tensor-memory columns of P, 16 rows (2 KB) of V
-            const uint32_t vo = (uint32_t)((slot * kKVBytes + k * 16 * 128) >> 4) + lbo_v;
-            ptx::mma_ts(tmem + 256, tmem + slot * kKT + k * 8, dsc(v4 + vo, hi128), idesc_pv, (t > 0 || k > 0) ? 1u : 0u);
+        // P there: O += P V, piece after piece, then the next scores over P
+        const int sb = (e + t) & 1;
+        ok = wait_all(&bar->p_full[sb], ((e + t) >> 1) & 1);
+        for (int c = 0; ok && c < kPieces; ++c) {
+          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+          if (!wait_all(&bar->v_full[slot], (g / kRing) & 1)) {
+            ok = false;
+            break;
           }
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kVRows / 16; ++k) {
+              // 16 keys: 8 tensor-memory columns of P, those of a half 64 on, 16 rows (2 KB) of V
+              const int step = c * (kVRows / 16) + k;
+              const uint32_t vo = (uint32_t)((slot * kPiece + k * 16 * 128) >> 4) + lbo_v;
+              ptx::mma_ts(tmem + 256, tmem + sb * kTile + (step >> 2) * 64 + (step & 3) * 8, dsc(v4 + vo, hi128), idesc_pv,
+                          (t > 0 || step > 0) ? 1u : 0u);
+            }
+          }
+          __syncwarp();
+          ptx::mma_commit_elect(&bar->v_empty[slot]);
         }
-        __syncwarp();
+        if (!ok) break;
         ptx::mma_commit_elect(&bar->pv_done);
-        ptx::mma_commit_elect(&bar->v_empty[slot]);
         if (t + 2 < n) ok = issue_s(t + 2);
       }
       if (ok && n > 0) ptx::mma_commit_elect(&bar->o_full);
@@ -309,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           ptx::mbar_wait_time_only(&bar->drain, 0, p.timeout_ns);
         }
       }
-    } else if (warp >= 4) {
+    } else {
       // ---------------------------------------------------------- softmax and output
+      const int half = (warp - 3) >> 2;
       const int quarter = warp & 3;  // tensor-memory lane quarter this warp may access
       const int row = quarter * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
@@ -324,74 +370,87 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
       }
       if (!valid) hi = -1;
       bool ok = true;
-      float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain
-      float l = 0.f;        // running sum of exp2(x - m)
+      float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain; both halves have the same
+      float l = 0.f;        // running sum of exp2(x - m) of this half's keys
       for (int t = 0; t < n; ++t) {
-        const int slot = (e + t) % kStages, kt = it.lo + t;
-        const uint32_t s_tmem = tmem + lane_off + slot * kKT;
-        const bool got = ptx::mbar_wait(&bar->s_full[slot], ((e + t) / kStages) & 1, p.timeout_ns, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
+        const int g = e + t, sb = g & 1, kt = it.lo + t;
+        const uint32_t s_tmem = tmem + lane_off + sb * kTile + half * 64;
+        const bool got = ptx::mbar_wait(&bar->s_full[sb], (g >> 1) & 1, p.timeout_ns, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) ok = false;  // (and on to the barrier that the other warp may be at)
         ptx::tc_fence_after();
-        float x[kKT];
-        ptx::tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(&x[0]));
-        ptx::tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
-        ptx::tmem_wait_ld();
-        bool sees = valid;  // this row sees a key of the tile
-        if (it.partial(kt)) {
-          const int c_lo = max(lo - kt * kKT, 0), c_hi = min(hi - kt * kKT, kKT - 1);
-          sees = c_lo <= c_hi;
+        float x[64];
+        bool sees = valid, sees_half = valid;  // this row sees a key of the tile, of this half
+        float ts = 0.f;
+        if (ok) {
+          ptx::tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(&x[0]));
+          ptx::tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+          ptx::tmem_wait_ld();
+          if (it.partial(kt)) {
+            const int c_lo = max(lo - kt * kTile, 0), c_hi = min(hi - kt * kTile, kTile - 1);
+            sees = c_lo <= c_hi;
+            sees_half = max(c_lo, 64 * half) <= min(c_hi, 64 * half + 63);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint32_t vis = range_bits(g, c_lo, c_hi);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t vis = range_bits(2 * half + j, c_lo, c_hi);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[32 * g + j] = ((vis >> j) & 1u) ? x[32 * g + j] : -INFINITY;
+              for (int k = 0; k < 32; ++k) x[32 * j + k] = ((vis >> k) & 1u) ? x[32 * j + k] : -INFINITY;
+            }
           }
+          ts = exp_to_tmem(x, sl2, m == -INFINITY ? 0.f : m, s_tmem);
         }
-        // (the stale-max rule, and rows that keep their reference while another's is redone,
-        // as in attention_packed.cu)
+        // (the stale-max rule, for half a tile each, and rows that keep their reference while
+        // another's is redone, as in attention_packed.cu)
         const bool fresh = m == -INFINITY;
-        float ts = exp_to_tmem(x, sl2, fresh ? 0.f : m, s_tmem);
-        const bool redo = valid && (!(ts <= kMaxTileSum) || (fresh && sees && !(ts >= kMinTileSum)));
-        if (fresh && sees && !redo) m = 0.f;  // the row's reference from here on
-        if (__any_sync(0xffffffffu, redo)) {
-          ptx::tmem_wait_st();  // let these stores land before they are overwritten
-          const float m_new = redo ? fmaxf(m, row_max(x) * sl2) : m;
+        const bool mine = valid && (!(ts <= kMaxTileSum) || (fresh && sees_half && !(ts >= kMinTileSum)));
+        const bool slow = pair_any(quarter, mine || !ok);
+        if (!slow) {
+          if (fresh && sees) m = 0.f;  // the row's reference from here on
+        } else {
+          if (ok) ptx::tmem_wait_st();  // let these stores land before they are overwritten
+          const uint32_t rows = __ballot_sync(0xffffffffu, mine);
+          bar->half[half][row] = ok ? row_max(x) : 0.f;
+          if (lane == 0) bar->redo[half][quarter] = rows;
+          if (pair_any(quarter, !ok)) {
+            ok = false;
+            break;
+          }
+          const bool redo = ((rows | bar->redo[half ^ 1][quarter]) >> lane) & 1u;
+          const float m_new = redo ? fmaxf(m, fmaxf(bar->half[0][row], bar->half[1][row]) * sl2) : (fresh && sees ? 0.f : m);
           const bool need_rescale = !fresh && m_new > m;
           if (fresh) m = m_new;
           if (__any_sync(0xffffffffu, need_rescale)) {
             // the last product adds into O: wait for it (S_t there means that the one before
             // it is done, so the barrier is one phase behind at most)
-            const bool pv = ptx::mbar_wait(&bar->pv_done, (e + t - 1) & 1, p.timeout_ns, abort_flag);
-            if (!__all_sync(0xffffffffu, pv)) {
-              ok = false;
-              break;
-            }
+            const bool pv = ptx::mbar_wait(&bar->pv_done, (g - 1) & 1, p.timeout_ns, abort_flag);
+            ok = __all_sync(0xffffffffu, pv);
             ptx::tc_fence_after();
-            const float alpha = need_rescale ? ptx::ex2(m - m_new) : 1.f;
-            rescale_o<kD>(o_tmem, alpha);
+            if (ok) rescale_o<kD>(o_tmem, need_rescale ? ptx::ex2(m - m_new) : 1.f, half * (kD / 2), (half + 1) * (kD / 2));
             if (need_rescale) {
-              l *= alpha;
+              l *= ptx::ex2(m - m_new);
               m = m_new;
             }
           }
-          ts = exp_to_tmem(x, sl2, (m == -INFINITY) ? 0.f : m, s_tmem);
+          if (ok) ts = exp_to_tmem(x, sl2, (m == -INFINITY) ? 0.f : m, s_tmem);
+          if (pair_any(quarter, !ok)) {  // (and the maxima are read)
+            ok = false;
+            break;
+          }
         }
         l += ts;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&bar->p_full[slot]);
+        ptx::mbar_arrive(&bar->p_full[sb]);
       }
       if (ok && n > 0) {
         const bool got = ptx::mbar_wait(&bar->o_full, passes & 1, p.timeout_ns, abort_flag);
         ok = __all_sync(0xffffffffu, got);
         ptx::tc_fence_after();
       }
-      if (!ok) {
-        if (lane == 0) fail(p, bar, kErrSoftmax);
-      } else {
+      if (!ok && lane == 0) fail(p, bar, kErrSoftmax);
+      bar->half[half][row] = l;
+      pair_any(quarter, false);
+      if (ok) {
+        l = bar->half[0][row] + bar->half[1][row];
         const float b2 = p.sink ? __ldg(p.sink + it.h) * kLog2e : -INFINITY;
         const float M = fmaxf(m, b2);
         const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
@@ -399,14 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
         const float o_scale = z == 0.f ? 0.f : em / z;
         const int64_t q_row = (int64_t)it.q_row + row;
-        if (valid && p.lse) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
+        if (valid && p.lse && half == 0) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
         // a row's output that is not finite may be a hidden key's values' doing
         const bool part = n > 0 && (it.partial(it.lo) || it.partial(it.lo + n - 1)) && !again;
         float2 sum = make_float2(0.f, 0.f);
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (q_row * p.H + it.h) * kD;
         const uint64_t o_policy = ptx::l2_policy_evict_first();
 #pragma unroll 1
-        for (int c0 = 0; c0 < kD; c0 += 16) {
+        for (int c0 = half * (kD / 2); c0 < (half + 1) * (kD / 2); c0 += 16) {
           float ov[16];
           if (n > 0) {
             ptx::tmem_ld16(o_tmem + c0, ov);
@@ -435,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           }
         }
         if (part && valid && !(fabsf(sum.x + sum.y) < INFINITY)) *reinterpret_cast<volatile int*>(&bar->marked[i % 3]) = 1;
-        if (again) add_odd_values(p, it, row, lo, hi);
+        if (again) add_odd_values(p, it, row, half * (kD / 2), lo, hi);
         ptx::tc_fence_before();  // (O is read: the next item's first product may overwrite it)
       }
     }
@@ -463,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
 }  // namespace
 
 cudaError_t launch_attention_packed_256(const PackedParams& p, cudaStream_t stream) {
-  constexpr size_t smem = 1024 + kQBytes + 2 * kStages * kKVBytes + sizeof(Bar);
+  constexpr size_t smem = 1024 + kQBytes + 2 * kRing * kPiece + sizeof(Bar);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(attention_packed_256_kernel, smem, &done);

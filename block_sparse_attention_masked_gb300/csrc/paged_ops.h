@@ -85,7 +85,7 @@ struct PackedPlan {        // in the workspace
 inline int64_t packed_pairs(int64_t T, int64_t B) { return T / 256 + (B < T ? B : T); }
 
 struct PackedParams {
-  CUtensorMap tq[2], tk[2], tv;  // [T][heads][d] views: boxes of 128 rows of one head (tile_mma.cuh; d = 256, k and v: 64)
+  CUtensorMap tq[2], tk[2], tv;  // [T][heads][d] views: boxes of 128 rows of one head (tile_mma.cuh; d = 256, v: 32)
   void* o;                       // [T][H][d] bf16
   float* lse;                    // [H][T] or null
   const float* sink;             // [H] or null
@@ -105,9 +105,9 @@ struct PackedParams {
   int selftest;                  // 1: the first K tile is left out, so that the wait for it runs out
 };
 cudaError_t launch_attention_packed(const PackedParams& p, int d, cudaStream_t stream);
-// Behind the plan, for heads of 256 (attention_packed_256.cu), whose boxes of k and v are
-// of this many rows.
-constexpr int kPackedKeys256 = 64;
+// Behind the plan, for heads of 256 (attention_packed_256.cu), whose boxes of v are of
+// this many rows.
+constexpr int kPackedValues256 = 32;
 cudaError_t launch_attention_packed_256(const PackedParams& p, cudaStream_t stream);
 
 }  // namespace mattn

@@ -379,16 +379,16 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   if (T == 0) return MATTN_OK;
   PackedParams p;
   memset(&p, 0, sizeof(p));
-  const int rem = d % 64, vw = d % 64 == 0 ? 64 : (d % 32 == 0 ? 32 : 16), kt = d == 256 ? kPackedKeys256 : kTile;
+  const int rem = d % 64, vw = d % 64 == 0 ? 64 : (d % 32 == 0 ? 32 : 16);
   auto maps = [&](CUtensorMap* m, const void* x, int64_t rows, int heads, int i) {  // 64-column chunks and the rest
-    const int n = i ? kt : kTile, e = make_packed_map(&m[0], x, d, 64, n, rows, heads, ts[i], hs[i]);
+    const int e = make_packed_map(&m[0], x, d, 64, kTile, rows, heads, ts[i], hs[i]);
     if (e || !rem) return e;
-    return make_packed_map(&m[1], static_cast<const char*>(x) + (d - rem) * 2, rem, rem, n, rows, heads, ts[i], hs[i]);
+    return make_packed_map(&m[1], static_cast<const char*>(x) + (d - rem) * 2, rem, rem, kTile, rows, heads, ts[i], hs[i]);
   };
   if ((rc = maps(p.tq, q, T, H, 0))) return rc;
   if (T_k > 0) {  // (else no tile is loaded)
     if ((rc = maps(p.tk, k, T_k, H_kv, 1))) return rc;
-    if ((rc = make_packed_map(&p.tv, v, d, vw, kt, T_k, H_kv, ts[2], hs[2]))) return rc;
+    if ((rc = make_packed_map(&p.tv, v, d, vw, d == 256 ? kPackedValues256 : kTile, T_k, H_kv, ts[2], hs[2]))) return rc;
   }
   p.o = o;
   p.lse = lse;
