@@ -96,5 +96,9 @@ struct Extent {
   uintptr_t lo, hi;
   bool meets(const Extent& x) const { return lo < x.hi && x.lo < hi; }
 };
+inline Extent extent_of(const void* p, uint64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + (p ? bytes : 0)};
+}
 
 }  // namespace mattn

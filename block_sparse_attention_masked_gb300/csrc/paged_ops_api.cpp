@@ -265,6 +265,11 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   if ((rc = check_small("decode_paged", lse, seq_lens, sink))) return rc;
   if ((rc = check_scale("decode_paged", softmax_scale))) return rc;
   const bool e8 = cache->dtype == MATTN_E4M3;
+  const Extent ins[3] = {extent_of(q, (uint64_t)B * H * d * 2), pages_extent(cache, 0, H_kv, d), pages_extent(cache, 1, H_kv, d)};
+  const Extent to = extent_of(o, (uint64_t)B * H * d * 2), to_lse = extent_of(lse, (uint64_t)B * H * 4);
+  for (const Extent& x : ins)
+    if (to.meets(x) || to_lse.meets(x) || to.meets(to_lse))
+      return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: an output overlaps q, the cache or the other output");
   const int warps = decode_share_warps(tiles, d);
   const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * warps, d);
   if ((rc = check_workspace("decode_paged", workspace, workspace_bytes, lay.all()))) return rc;
@@ -372,6 +377,15 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
     if (ts[i] <= 0 || hs[i] <= 0 || ts[i] % 8 || hs[i] % 8 || ts[i] >= int64_t(1) << 39 || hs[i] >= int64_t(1) << 39)
       return report_error(MATTN_ERR_UNSUPPORTED,
                           "attention_packed: strides must be positive multiples of 16 bytes below 2^40");
+  }
+  // (items are read and written in no order, some twice)
+  const void* from[3] = {q, k, v};
+  const Extent to = extent_of(o, (uint64_t)T * H * d * 2), to_lse = extent_of(lse, (uint64_t)T * H * 4);
+  for (int i = 0; i < 3; ++i) {
+    const int64_t rows = i ? T_k : T, heads = i ? H_kv : H;
+    const Extent x = extent_of(from[i], rows > 0 ? ((uint64_t)(rows - 1) * ts[i] + (uint64_t)(heads - 1) * hs[i] + d) * 2 : 0);
+    if (to.meets(x) || to_lse.meets(x) || to.meets(to_lse))
+      return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: an output overlaps an input or the other output");
   }
   if ((rc = check_workspace("attention_packed", workspace, workspace_bytes, packed_bytes(T, B, H)))) return rc;
   uint32_t* err = nullptr;

@@ -384,9 +384,10 @@ int mattn_rr_select(const void* q, const void* k, int B, int H, int N, int d, in
  * (host only, no device needed; 0 = may be NULL; other sizes, smaller ones
  * too, may need more).  Calls that may overlap on
  * the GPU need workspaces of their own; a captured graph keeps its own
- * alive.  A first call of mattn_decode_shared or mattn_decode_blocks on a
- * device makes the library's error word and must not be under stream capture
- * (MATTN_ERR_UNSUPPORTED); every other call can be captured.  All are asynchronous on `stream`; errors as for mattn_fwd,
+ * alive.  A first call of mattn_decode_shared, mattn_decode_blocks,
+ * mattn_decode_paged or mattn_attention_packed on a device makes the library's
+ * error word and must not be under stream capture (MATTN_ERR_UNSUPPORTED); every
+ * other call can be captured.  All are asynchronous on `stream`; errors as for mattn_fwd,
  * MATTN_ERR_CAPACITY for a workspace that is too small.
  */
 
@@ -584,6 +585,7 @@ int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int6
  *               0 .. table_pages * page are clamped.  Positions without a page are
  *               no keys.  What rows hold that no query sees is not used.
  *   window      0: every key; sink_tokens >= 0, 0 without a window
+ *   o and lse must not overlap q, the pages or each other.
  *   At most 2^31 - 1 tiles of keys in all of B tables (16 keys; 32 in e4m3 or at
  *   d = 64, 64 where both; 16 in e4m3 at d = 256 with H / H_kv > 8).
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Sums,
@@ -607,7 +609,8 @@ int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int pa
  *   q, k, v    DEVICE bf16: element (t, h, c) at t * token_stride + h * head_stride +
  *              c ([0] q, [1] k, [2] v), 16-byte aligned, strides positive multiples
  *              of 8 (of a dimension of one entry: any)
- *   o          DEVICE bf16 [T][H][d];  lse  DEVICE fp32 [H][T] or NULL
+ *   o          DEVICE bf16 [T][H][d];  lse  DEVICE fp32 [H][T] or NULL; neither overlaps
+ *              q, k, v or the other
  *   cu_seqlens_q, cu_seqlens_k  DEVICE int32 [B + 1], ascending, inside 0..T and
  *              0..T_k (values outside are clamped); cu_seqlens_k NULL: cu_seqlens_q
  *              (T_k = T).  Rows of no sequence are not used, and o and lse left as

@@ -54,7 +54,7 @@ def _i32(x):
 
 # ------------------------------------------------------------------ a request's life
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_prefill_chunk_and_decode(d, e4m3):
     """Two chunks of packed prompts and three single tokens: norms and rotation, rows into the
     cache, attention over the chunk with the cached rows in front of it, attention over the
@@ -96,19 +96,19 @@ def test_prefill_chunk_and_decode(d, e4m3):
 class Calls:
     """One call of each operator on tensors that stay, of `seed`'s values."""
 
-    def __init__(self, seed, e4m3=True, B=3):
+    def __init__(self, seed, e4m3=True, B=3, d=128):
         g = _gen(seed)
         self.B = B
-        self.c = paged.Cache(B, 2, 128, 32, 5, e4m3, seed=seed)
+        self.c = paged.Cache(B, 2, d, 32, 5, e4m3, seed=seed)
         n = ([50, 0, 31] * B)[:B]
         self.cu, self.starts, self.lens = paged._lens_to_cu(n), _i32([3] * B), _i32(([160, 3, 77] * B)[:B])
         T = sum(n)
-        self.q, self.k, self.v = _randn(g, T, 8, 128), _randn(g, T, 2, 128), _randn(g, T, 2, 128)
-        self.qd = _randn(g, B, 8, 128)
+        self.q, self.k, self.v = _randn(g, T, 8, d), _randn(g, T, 2, d), _randn(g, T, 2, d)
+        self.qd = _randn(g, B, 8, d)
         self.ko, self.vo = torch.zeros_like(self.k), torch.zeros_like(self.v)
         self.od, self.ld = torch.zeros_like(self.qd), torch.zeros((B, 8), device="cuda")
         self.op, self.lp = torch.zeros_like(self.q), torch.zeros((8, T), device="cuda")
-        self.wd = mattn.decode_paged_workspace(B, 8, 2, 5, 32, 128, e4m3)
+        self.wd = mattn.decode_paged_workspace(B, 8, 2, 5, 32, d, e4m3)
         self.wp = mattn.attention_packed_workspace(T, B, 8)
 
     def inputs(self):
@@ -125,18 +125,19 @@ class Calls:
         mattn.attention_packed(self.q, self.ko, self.vo, self.cu, out=self.op, lse=self.lp, workspace=self.wp, stream=stream)
 
 
+@pytest.mark.parametrize("d", [128, 256])
 @pytest.mark.parametrize("B", [3, 90])
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_captured_chain_replays_on_new_values(e4m3, B):
+def test_captured_chain_replays_on_new_values(e4m3, B, d):
     """A graph of the four, replayed twice on other inputs, between eager calls of other tensors."""
-    x, other = Calls(1, e4m3, B), Calls(2, e4m3, B)
+    x, other = Calls(1, e4m3, B, d), Calls(2, e4m3, B, d)
     x.run()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         x.run()
     for seed in (3, 4):
-        want = Calls(seed, e4m3, B)
+        want = Calls(seed, e4m3, B, d)
         for a, b in zip((paged.Cache._bytes(x.c.k), paged.Cache._bytes(x.c.v), x.c.table), (paged.Cache._bytes(want.c.k), paged.Cache._bytes(want.c.v), want.c.table)):
             a.copy_(b)
         if e4m3:
@@ -155,7 +156,7 @@ def test_captured_chain_replays_on_new_values(e4m3, B):
 
 def test_two_graphs_replayed_side_by_side():
     """Graphs with workspaces of their own, replayed on two streams at once."""
-    xs = [Calls(s, B=b) for s, b in ((1, 3), (2, 40))]
+    xs = [Calls(s, B=b, d=d) for s, b, d in ((1, 3, 128), (2, 40, 128), (3, 40, 256))]
     graphs, want = [], []
     for x in xs:
         x.run()
@@ -331,9 +332,10 @@ def test_packed_rows_past_four_gigabytes():
 # ------------------------------------------------------------------ the debug library
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("B", [3, 90])
-def test_debug_library_gives_the_same(e4m3, B):
+@pytest.mark.parametrize("d", [128, 256])
+def test_debug_library_gives_the_same(e4m3, B, d):
     """Bounds checks before every copy: none fails, and the results are the product library's bit for bit."""
-    want, got = Calls(1, e4m3, B), Calls(1, e4m3, B)
+    want, got = Calls(1, e4m3, B, d), Calls(1, e4m3, B, d)
     want.run()
     torch.cuda.synchronize()
     mattn.use_debug_library(True)

@@ -162,6 +162,11 @@ def test_decode_paged_refuses_the_cache(L, why, kw, code):
     ("no workspace", {"ws": None}, -6),
     ("a small workspace", {"ws_bytes": 1000}, -6),
     ("a workspace off a 256-byte boundary", {"ws": MB + 16}, -1),
+    ("an output over the queries", {"q": 5 * MB, "o": 5 * MB + 512}, -1),
+    ("an output over the keys", {"o": 256 * MB + 4096}, -1),
+    ("an output that ends in the values", {"o": 512 * MB - 256}, -1),
+    ("an lse over the keys", {"lse": 256 * MB + 4096}, -1),
+    ("an lse over the output", {"o": 5 * MB, "lse": 5 * MB + 64}, -1),
 ])
 def test_decode_paged_refuses(L, why, kw, code):
     kw = dict(kw)
@@ -262,6 +267,11 @@ def _packed(L, **kw):
     ("no workspace", {"ws": None}, -6),
     ("a small workspace", {"ws_bytes": 64}, -6),
     ("a workspace off a 256-byte boundary", {"ws": MB + 16}, -1),
+    ("an output over the queries", {"o": MB}, -1),
+    ("an output that ends in the keys", {"o": 2 * MB - 512}, -1),
+    ("an output over the values' last row", {"o": 3 * MB + 99 * 512}, -1),
+    ("an lse over the queries", {"lse": MB + 4096}, -1),
+    ("an lse over the output", {"lse": 4 * MB + 4096}, -1),
 ])
 def test_attention_packed_refuses(L, why, kw, code):
     assert _packed(L, **kw) == code, why
@@ -276,6 +286,8 @@ def test_attention_packed_accepts(L):
     assert f(3, 100, 8, ctypes.byref(n)) == 0
     assert _packed(L, ws_bytes=n.value) in ok and _packed(L, ws_bytes=n.value - 1) == mattn.ERR_CAPACITY
     assert _packed(L, H_kv=1, head=(128, 0, -5)) in ok
+    assert _packed(L, d=256, token=(2048, 512, 512), head=(256, 256, 256)) in ok
+    assert _packed(L, o=MB + 99 * 2048 + 2048, lse=2 * MB - 3200) in ok  # behind the queries, before the keys
     assert _packed(L, T=1, T_k=1, token=(0, 0, 0)) in ok
     assert _packed(L, T_k=0, k=None, v=None, cu_k=MB) in ok
     assert f(0, 100, 8, ctypes.byref(n)) == -1 and f(3, -1, 8, ctypes.byref(n)) == -1 and f(3, 100, 8, None) == -1
