@@ -623,6 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       const int first_use = it->first(s), last_use = it->last(s);
       const int has0 = it->first(0) >= 0, has1 = it->first(1) >= 0;
       drop_item(bar, i);
+      if (n == 0) {
+        // (no entry carries the last P V along, and the ring's slots wait for its output)
+        ok = finish();
+        continue;
+      }
       const int tq = t + (s ? has0 : 0);  // this query tile's Q
       t += has0 + has1;
       const int qslot = tq % kQSlots;

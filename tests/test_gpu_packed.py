@@ -193,6 +193,15 @@ def test_packed_256_score_ranges(q_scale):
     packed_case([300, 20, 515], 4, 2, 256, q_scale=q_scale, seed=6, causal=False, sink=True, scale=0.1)
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_packed_many_sequences_without_keys(d):
+    """A few with keys, hundreds without behind them: zeros, or the sink's part."""
+    nq = [300] + [3] * 400 + [200, 64]
+    nk = [300] + [0] * 400 + [500, 64]
+    packed_case(nq, 8, 2, d, nk=nk, seed=13)
+    packed_case(nq, 8, 8, d, nk=nk, seed=14, sink=True, causal=False)
+
+
 def test_packed_256_more_items_than_sms():
     """Items behind one another in a CTA, marked ones among them."""
     nq = [2000, 5, 700, 1300, 64, 900]
