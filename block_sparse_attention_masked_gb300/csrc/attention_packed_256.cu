@@ -10,20 +10,23 @@
 // of a tile) and five of V (32 rows of it), as two whole tiles of each do not fit.
 //
 // A CTA per SM takes items, the query tiles of packed_plan_kernel's pairs head by head,
-// longest first, from a counter, one after another: an item begins when the last one is
-// written.  What a row does not see is treated as there, but that an item whose output
-// may have been spoilt by hidden values is done again at once.
+// longest first, from a counter; copies run ahead into the next item, and its first scores are
+// made while the last output is read.  What a row does not
+// see is treated as there: items whose output hidden values may have spoilt are marked,
+// and done again after the others.
 //
-// Roles (352 threads): warp 0 the items, Q and K; warp 1 tensor memory and the products;
-// warp 2 V; warps 3..10 softmax and output: warps w and w + 4 the same 32 rows, half of a
-// tile's keys and of the output's columns each.  Every wait is bounded in time and gives up
-// by raising a CTA-wide abort flag and a device error bit.
+// Roles (384 threads): warp 0 Q and K; warp 1 tensor memory and the products; warp 2 V;
+// warp 3 the items; warps 4..11 softmax and output: warps w and w + 4 the same 32 rows, half
+// of a tile's keys and of the output's columns each.  Every wait is bounded in time and
+// gives up by raising a CTA-wide abort flag and a device error bit; the two warps of a
+// pair, which meet at barriers, give up together.
 //
-// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 675 us = 1,628,
-// eight prompts of 1 to 3,352 tokens, 32 heads, 609-621 us = 1,222-1,247, 64 prompts of 256
-// 193 us = 357; an item costs about 3.5 us beside its tiles.  Key tiles of 64, as in
-// attention_sp.cu, took 882 us for the first: a product of 64 columns takes as long as one of
-// 128.  Two groups of softmax warps taking such tiles in turn 910.
+// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 700 us = 1,571,
+// eight prompts of 1 to 3,352 tokens, 32 heads, 595 us = 1,277, 16 of 1,024 not causal 398 us =
+// 1,381, 64 of 256 150 us = 459.  Key tiles of 64, as in attention_sp.cu, took 882 us for the
+// first: a product of 64 columns takes as long as one of 128.  Items that begin when the last
+// one is written took 677, 617, 444 and 191.  The next item's first scores before the last P V
+// of this one gained nothing: they wait for its Q.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,48 +43,63 @@ namespace mattn {
 namespace {
 
 constexpr int kD = 256;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+constexpr int kItems = 3, kReaders = 11;  // of the ring; of an item: the warps but the scheduler's
 constexpr int kPieces = 4, kRing = 5;  // pieces of a K or V tile; in each ring
 constexpr int kQChunk = kTile * 128, kQBytes = kD / 64 * kQChunk;  // chunks of 64 columns, 128-byte swizzle
 constexpr int kPiece = kQChunk;                                    // of K: such a chunk
 constexpr int kVRows = kPackedValues256, kVChunk = kVRows * 128;   // of V: four chunks of 32 rows
 static_assert(kVRows * kPieces == kTile && kVChunk * (kD / 64) == kPiece, "pieces");
 
-// An item: a query tile of a pair, and its key tiles lo .. lo + n - 1.
+// An item: a query tile of a pair, and its key tiles lo .. lo + n - 1; or (h < 0) the word to
+// finish what is under way, after which there is nothing more (kEnd) or may be (kDrain).
+constexpr int kDrain = -2, kEnd = -1;
 struct Item {
-  int q_row, rows, k_row, keys, pos, h;  // h < 0: there are no more
+  int q_row, rows, k_row, keys, pos, h, id;
   int lo, n;
   int whole_lo, whole_hi;  // the key tiles that every row sees whole
-  __device__ __forceinline__ void set(const PackedParams& p, const PackedPair& x, int s, int head) {
+  int marked;              // some row of its output is not finite
+  int again;               // the second time
+  __device__ __forceinline__ void set(const PackedParams& p, int item) {
+    const int pair = item / (2 * p.H), i = item - pair * 2 * p.H;
+    const int s = i < p.H ? 1 : 0;  // (the second query tile, which sees most keys, first)
+    const PackedPair& x = p.plan->pair[pair];
     q_row = x.q_row + 128 * s;
     rows = in_bounds(p, x) ? min(x.rows - 128 * s, 128) : 0;
     k_row = x.k_row;
     keys = x.keys;
     pos = x.pos0 + 128 * s;
-    h = head;
+    h = i < p.H ? i : i - p.H;
+    id = item;
     int hi;
     seen_tiles<7>(p, pos, rows, keys, &lo, &hi);
     n = hi < lo ? 0 : hi - lo + 1;
     whole_hi = ((p.causal ? min(keys, pos + 1) : keys) >> 7) - 1;
     whole_lo = p.window ? (max(0, pos + rows - p.window) + 127) >> 7 : 0;
+    marked = 0;
+  }
+  __device__ __forceinline__ void say(int what) {
+    h = what;
+    n = 0;
   }
   __device__ __forceinline__ bool partial(int kt) const { return kt < whole_lo || kt > whole_hi; }
 };
 
 struct Bar {
-  uint64_t q_full;
+  uint64_t q_full, q_empty;
   uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
   uint64_t v_land;
   uint64_t s_full[2], p_full[2];
-  uint64_t pv_done;  // one phase per P V product
-  uint64_t o_full;   // one per item with keys, after its last
+  uint64_t pv_done;          // one phase per P V product
+  uint64_t o_full, o_empty;  // one per item with keys: after its last product, once its output is read
   uint64_t drain;
+  uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem_base;
   int abort_flag;
-  int marked[3];     // of item i in [i % 3]: some row of its output is not finite
-  Item items[2];
-  uint32_t redo[2][4];   // rows of each half and 32 rows whose tile is done again
-  float half[2][kTile];  // a row's maximum over half a tile, at last half its sum
+  int marked;                // the CTA's last marked item, from which PackedParams::marked leads to the others; -1: none
+  Item items[kItems];
+  uint32_t redo[2][4];       // rows of each half and 32 rows whose tile is done again
+  float half[2][kTile];      // a row's maximum over half a tile, at last half its sum
 };
 
 __device__ __forceinline__ uint64_t dsc(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
@@ -91,18 +109,55 @@ __device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t b
   atomicOr(p.err, bit);
 }
 
-// The next item from number `id` on that has rows (one thread).  The heads of a pair run
-// side by side, its second query tile, which sees most keys, first.
-__device__ __forceinline__ void next_item(const PackedParams& p, int64_t total, int64_t id, Item* it) {
-  for (;; id = (int64_t)gridDim.x + atomicAdd(&p.plan->next, 1)) {
-    if (id >= total) {
-      it->h = -1;
+// The items, in order (one thread).
+__device__ __forceinline__ void schedule(const PackedParams& p, Bar* bar, volatile int* abort_flag) {
+  const int total = p.plan->pairs * 2 * p.H;
+  int id = blockIdx.x;
+  for (int i = 0, again = 0;; ++i) {
+    const int slot = i % kItems;
+    const uint32_t phase = (i / kItems) & 1;
+    if (!ptx::mbar_wait_backoff(&bar->item_empty[slot], phase ^ 1, p.timeout_ns, abort_flag, 200)) break;
+    Item& it = bar->items[slot];
+    if (!again) {
+      for (; id < total; id = (int)gridDim.x + atomicAdd(&p.plan->next, 1)) {
+        it.set(p, id);
+        if (it.rows > 0) break;
+      }
+      it.again = 0;
+      if (id < total) {
+        ptx::mbar_arrive(&bar->item_full[slot]);
+        id = (int)gridDim.x + atomicAdd(&p.plan->next, 1);
+        continue;
+      }
+      // every item so far written: then the marked ones
+      it.say(kDrain);
+      ptx::mbar_arrive(&bar->item_full[slot]);
+      if (!ptx::mbar_wait_backoff(&bar->item_empty[slot], phase, p.timeout_ns, abort_flag, 200)) break;
+      again = 1;
+      id = *reinterpret_cast<volatile int*>(&bar->marked);
+      continue;
+    }
+    if (id < 0 || id >= p.max_pairs * 2 * p.H) {
+      it.say(kEnd);
+      ptx::mbar_arrive(&bar->item_full[slot]);
       return;
     }
-    const int pair = (int)(id / (2 * p.H)), i = (int)(id - (int64_t)pair * 2 * p.H);
-    it->set(p, p.plan->pair[pair], i < p.H ? 1 : 0, i < p.H ? i : i - p.H);
-    if (it->rows > 0) return;
+    it.set(p, id);
+    it.again = 1;
+    ptx::mbar_arrive(&bar->item_full[slot]);
+    id = p.marked[id];
   }
+  fail(p, bar, kErrProducer);
+}
+
+// Waits for the CTA's item i (a warp); null if the wait gave up.
+__device__ __forceinline__ const Item* take_item(const PackedParams& p, Bar* bar, int i, volatile int* abort_flag) {
+  const bool got = ptx::mbar_wait(&bar->item_full[i % kItems], (i / kItems) & 1, p.timeout_ns, abort_flag);
+  return __all_sync(0xffffffffu, got) ? &bar->items[i % kItems] : nullptr;
+}
+__device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, after its last read)
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar->item_empty[i % kItems]);
 }
 
 // A landed piece of V: rows from `rows` on and values that are not finite become zeros (one warp).
@@ -167,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
     ptx::prefetch_tmap(&p.tk[0]);
     ptx::prefetch_tmap(&p.tv);
     ptx::mbar_init(&bar->q_full, 1);
+    ptx::mbar_init(&bar->q_empty, 1);
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(&bar->k_full[i], 1);
       ptx::mbar_init(&bar->k_empty[i], 1);
@@ -180,52 +236,63 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
     ptx::mbar_init(&bar->pv_done, 1);
     ptx::mbar_init(&bar->v_land, 1);
     ptx::mbar_init(&bar->o_full, 1);
+    ptx::mbar_init(&bar->o_empty, 8);
+    for (int i = 0; i < kItems; ++i) {
+      ptx::mbar_init(&bar->item_full[i], 1);
+      ptx::mbar_init(&bar->item_empty[i], kReaders);
+    }
     ptx::mbar_init(&bar->drain, 1);
     bar->abort_flag = 0;
-    bar->marked[0] = 0;
+    bar->marked = -1;
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
     ptx::tmem_alloc(&bar->tmem_base, 512);
     ptx::tmem_relinquish();
   }
-  after_previous();  // the plan, and whatever the inputs come from
-  int64_t total = 0;
-  if (threadIdx.x == 0) {
-    total = (int64_t)p.plan->pairs * 2 * p.H;
-    next_item(p, total, blockIdx.x, &bar->items[0]);
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  after_previous();  // the plan, and whatever the inputs come from
 
-  int e = 0;           // key tiles before the current item's
-  int passes = 0;      // Q tiles and outputs, likewise
-  uint32_t lands = 0;  // V tiles looked over
-  for (int i = 0, again = 0;;) {
-    const Item it = bar->items[i & 1];
-    if (it.h < 0) break;
-    const int n = it.n;
-    if (warp == 0) {
-      // ---------------------------------------------------------- items, Q and K
-      const uint64_t keep = ptx::l2_policy_evict_last(), once = ptx::l2_policy_evict_first();
-      const int h_kv = it.h / p.group;
-      bool ok = true;
-      if (n > 0 && lane == 0) {
-        ptx::mbar_arrive_expect_tx(&bar->q_full, kQBytes);
-        if (debug_check(p.err, it.q_row >= 0 && it.q_row < p.T && it.h < p.H, kSiteLoad)) {
-#pragma unroll
-          for (int c = 0; c < kD / 64; ++c)
-            ptx::tma_load_3d_hint(sq + c * kQChunk, &p.tq[0], &bar->q_full, c * 64, it.h, it.q_row, once);
-        }
+  if (warp == 3) {
+    if (lane == 0) schedule(p, bar, abort_flag);
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ Q and K
+    const uint64_t keep = ptx::l2_policy_evict_last(), once = ptx::l2_policy_evict_first();
+    auto wait_all = [&](uint64_t* b, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, p.timeout_ns, abort_flag));
+    };
+    bool ok = true;
+    uint32_t g = 0, tiles = 0;  // pieces of K, Q tiles
+    for (int i = 0; ok; ++i) {
+      const Item* it = take_item(p, bar, i, abort_flag);
+      if (!it) {
+        ok = false;
+        break;
       }
+      const int n = it->n, h = it->h, q_row = it->q_row, k_row = it->k_row + it->lo * kTile;
+      drop_item(bar, i);
+      if (h == kEnd) break;
+      if (n == 0) continue;  // (kDrain too)
+      const int h_kv = h / p.group;
+      ok = debug_check(p.err, q_row >= 0 && q_row < p.T && h < p.H, kSiteLoad) && wait_all(&bar->q_empty, (tiles & 1) ^ 1);
+      ++tiles;
+      if (ok && lane == 0) {
+        ptx::mbar_arrive_expect_tx(&bar->q_full, kQBytes);
+#pragma unroll
+        for (int c = 0; c < kD / 64; ++c)
+          ptx::tma_load_3d_hint(sq + c * kQChunk, &p.tq[0], &bar->q_full, c * 64, h, q_row, once);
+      }
+      __syncwarp();
       for (int t = 0; ok && t < n; ++t) {
-        const int row = it.k_row + (it.lo + t) * kTile;
-        if (!debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad)) ok = false;
-        for (int c = 0; ok && c < kPieces; ++c) {
-          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
-          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->k_empty[slot], ((g / kRing) & 1) ^ 1, p.timeout_ns, abort_flag))) {
+        const int row = k_row + t * kTile;
+        ok = debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad);
+        for (int c = 0; ok && c < kPieces; ++c, ++g) {
+          const uint32_t slot = g % kRing;
+          if (!wait_all(&bar->k_empty[slot], ((g / kRing) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -237,23 +304,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           __syncwarp();
         }
       }
-      if (!ok && lane == 0) fail(p, bar, kErrProducer);
-      if (lane == 0 && !again) {
-        next_item(p, total, (int64_t)gridDim.x + atomicAdd(&p.plan->next, 1), &bar->items[(i + 1) & 1]);
-        bar->marked[(i + 1) % 3] = 0;
+    }
+    if (!ok && lane == 0) fail(p, bar, kErrProducer);
+    __syncwarp();
+    let_copies_land(abort_flag);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ V
+    const uint64_t keep = ptx::l2_policy_evict_last();
+    bool ok = true;
+    uint32_t g = 0, lands = 0;  // pieces, those looked over
+    for (int i = 0; ok; ++i) {
+      const Item* ring = take_item(p, bar, i, abort_flag);
+      if (!ring) {
+        ok = false;
+        break;
       }
-      __syncwarp();
-    } else if (warp == 2) {
-      // ---------------------------------------------------------- V
-      const uint64_t keep = ptx::l2_policy_evict_last();
+      const Item it = *ring;
+      drop_item(bar, i);
+      if (it.h == kEnd) break;
       const int h_kv = it.h / p.group;
-      bool ok = true;
-      for (int t = 0; ok && t < n; ++t) {
+      for (int t = 0; ok && t < it.n; ++t) {
         const int kt = it.lo + t, row = it.k_row + kt * kTile;
-        if (!debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad)) ok = false;
-        const bool look = again && it.partial(kt);
-        for (int c = 0; ok && c < kPieces; ++c) {
-          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+        ok = debug_check(p.err, row >= 0 && row < p.T_k, kSiteLoad);
+        const bool look = it.again && it.partial(kt);
+        for (int c = 0; ok && c < kPieces; ++c, ++g) {
+          const uint32_t slot = g % kRing;
           if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_empty[slot], ((g / kRing) & 1) ^ 1, p.timeout_ns, abort_flag))) {
             ok = false;
             break;
@@ -263,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           if (lane == 0) {
             ptx::mbar_arrive_expect_tx(landing, kPiece);
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i)
-              ptx::tma_load_3d_hint(piece + i * kVChunk, &p.tv, landing, i * 64, h_kv, row + c * kVRows, keep);
+            for (int j = 0; j < kD / 64; ++j)
+              ptx::tma_load_3d_hint(piece + j * kVChunk, &p.tv, landing, j * 64, h_kv, row + c * kVRows, keep);
           }
           __syncwarp();
           if (look) {
@@ -278,51 +353,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           }
         }
       }
-      if (!ok && lane == 0) fail(p, bar, kErrProducer);
-      __syncwarp();
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- products
-      auto wait_all = [&](uint64_t* b, uint32_t parity) {
-        return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, p.timeout_ns, abort_flag));
-      };
-      const uint32_t q4 = ptx::smem_addr(sq) >> 4;
-      const uint32_t k4 = ptx::smem_addr(sk) >> 4;
-      const uint32_t v4 = ptx::smem_addr(sv) >> 4;
-      constexpr uint32_t hi128 = ptx::smem_desc_hi(1024, ptx::kSw128);
-      constexpr uint32_t lbo_k = 1u << 16;  // unused for swizzled K-major operands
-      constexpr uint32_t lbo_v = (uint32_t)(kVChunk >> 4) << 16;  // V's atoms of 64 columns lie a chunk apart
-      constexpr uint32_t idesc_qk = ptx::idesc_bf16(128, kTile, 0);
-      constexpr uint32_t idesc_pv = ptx::idesc_bf16(128, kD, 1);
-      bool ok = true, issued = false;
-      auto issue_s = [&](int t) {  // S = Q K^T, piece after piece as they land
-        const int sb = (e + t) & 1;
-        for (int c = 0; c < kPieces; ++c) {
-          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
-          if (!wait_all(&bar->k_full[slot], (g / kRing) & 1)) return false;
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
+    }
+    if (!ok && lane == 0) fail(p, bar, kErrProducer);
+    __syncwarp();
+    let_copies_land(abort_flag);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    auto wait_all = [&](uint64_t* b, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, p.timeout_ns, abort_flag));
+    };
+    const uint32_t q4 = ptx::smem_addr(sq) >> 4;
+    const uint32_t k4 = ptx::smem_addr(sk) >> 4;
+    const uint32_t v4 = ptx::smem_addr(sv) >> 4;
+    constexpr uint32_t hi128 = ptx::smem_desc_hi(1024, ptx::kSw128);
+    constexpr uint32_t lbo_k = 1u << 16;  // unused for swizzled K-major operands
+    constexpr uint32_t lbo_v = (uint32_t)(kVChunk >> 4) << 16;  // V's atoms of 64 columns lie a chunk apart
+    constexpr uint32_t idesc_qk = ptx::idesc_bf16(128, kTile, 0);
+    constexpr uint32_t idesc_pv = ptx::idesc_bf16(128, kD, 1);
+    bool ok = true, issued = false;
+    uint32_t e = 0, passes = 0;  // tiles, items with keys before the current one
+    auto issue_s = [&](uint32_t g) {  // S = Q K^T, piece after piece as they land
+      for (int c = 0; c < kPieces; ++c) {
+        const uint32_t piece = g * kPieces + c, slot = piece % kRing;
+        if (!wait_all(&bar->k_full[slot], (piece / kRing) & 1)) return false;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t qo = (uint32_t)((c * kQChunk + k * 32) >> 4) + lbo_k;
-              const uint32_t ko = (uint32_t)((slot * kPiece + k * 32) >> 4) + lbo_k;
-              ptx::mma_ss(tmem + sb * kTile, dsc(q4 + qo, hi128), dsc(k4 + ko, hi128), idesc_qk, (c > 0 || k > 0) ? 1u : 0u);
-            }
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t qo = (uint32_t)((c * kQChunk + k * 32) >> 4) + lbo_k;
+            const uint32_t ko = (uint32_t)((slot * kPiece + k * 32) >> 4) + lbo_k;
+            ptx::mma_ss(tmem + (g & 1) * kTile, dsc(q4 + qo, hi128), dsc(k4 + ko, hi128), idesc_qk, (c > 0 || k > 0) ? 1u : 0u);
           }
-          __syncwarp();
-          ptx::mma_commit_elect(&bar->k_empty[slot]);
-          issued = true;
         }
-        ptx::mma_commit_elect(&bar->s_full[sb]);
-        return true;
-      };
-      if (n > 0) ok = wait_all(&bar->q_full, passes & 1);
-      for (int t = 0; ok && t < 2 && t < n; ++t) ok = issue_s(t);
-      for (int t = 0; ok && t < n; ++t) {
+        __syncwarp();
+        ptx::mma_commit_elect(&bar->k_empty[slot]);
+        issued = true;
+      }
+      ptx::mma_commit_elect(&bar->s_full[g & 1]);
+      return true;
+    };
+    for (int i = 0; ok; ++i) {
+      const Item* it = take_item(p, bar, i, abort_flag);
+      if (!it) {
+        ok = false;
+        break;
+      }
+      const int h = it->h, n = it->n;
+      drop_item(bar, i);
+      if (h == kEnd) break;
+      if (n == 0) continue;  // (kDrain too)
+      ok = wait_all(&bar->q_full, passes & 1);
+      for (int t = 0; ok && t < 2 && t < n; ++t) ok = issue_s(e + t);
+      if (ok && n <= 2) ptx::mma_commit_elect(&bar->q_empty);
+      // the last item's output read: O may be overwritten
+      ok = ok && wait_all(&bar->o_empty, (passes & 1) ^ 1);
+      for (int t = 0; ok && t < n; ++t, ++e) {
         // P there: O += P V, piece after piece, then the next scores over P
-        const int sb = (e + t) & 1;
-        ok = wait_all(&bar->p_full[sb], ((e + t) >> 1) & 1);
+        const int sb = e & 1;
+        ok = wait_all(&bar->p_full[sb], (e >> 1) & 1);
         for (int c = 0; ok && c < kPieces; ++c) {
-          const uint32_t g = (uint32_t)(e + t) * kPieces + c, slot = g % kRing;
+          const uint32_t g = e * kPieces + c, slot = g % kRing;
           if (!wait_all(&bar->v_full[slot], (g / kRing) & 1)) {
             ok = false;
             break;
@@ -343,25 +433,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         }
         if (!ok) break;
         ptx::mma_commit_elect(&bar->pv_done);
-        if (t + 2 < n) ok = issue_s(t + 2);
-      }
-      if (ok && n > 0) ptx::mma_commit_elect(&bar->o_full);
-      if (!ok) {
-        if (lane == 0) fail(p, bar, kErrMma);
-        if (issued) {
-          // wait (bounded) for the MMAs already issued before tensor memory is freed
-          ptx::mma_commit_elect(&bar->drain);
-          ptx::mbar_wait_time_only(&bar->drain, 0, p.timeout_ns);
+        if (t + 2 < n) {
+          ok = issue_s(e + 2);
+          if (ok && t + 3 == n) ptx::mma_commit_elect(&bar->q_empty);  // the item's last
         }
       }
-    } else {
-      // ---------------------------------------------------------- softmax and output
-      const int half = (warp - 3) >> 2;
-      const int quarter = warp & 3;  // tensor-memory lane quarter this warp may access
-      const int row = quarter * 32 + lane;
-      const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-      const uint32_t o_tmem = tmem + lane_off + 256;
-      const float sl2 = p.scale_log2;
+      if (ok) ptx::mma_commit_elect(&bar->o_full);
+      ++passes;
+    }
+    if (!ok) {
+      if (lane == 0) fail(p, bar, kErrMma);
+      if (issued) {
+        // wait (bounded) for the MMAs already issued before tensor memory is freed
+        ptx::mma_commit_elect(&bar->drain);
+        ptx::mbar_wait_time_only(&bar->drain, 0, p.timeout_ns);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int half = (warp - 4) >> 2;
+    const int quarter = warp & 3;  // tensor-memory lane quarter this warp may access
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_off + 256;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int e = 0;            // tiles before the item's
+    uint32_t passes = 0;  // items with keys before it
+    for (int i = 0;; ++i) {
+      const Item* ring = take_item(p, bar, i, abort_flag);
+      if (pair_any(quarter, !ring)) {
+        ok = false;
+        break;
+      }
+      const Item it = *ring;
+      if (it.h < 0) {
+        drop_item(bar, i);
+        if (it.h == kEnd) break;
+        continue;
+      }
+      const int n = it.n;
+      const bool again = it.again;
       const bool valid = row < it.rows;
       int lo = 0, hi = it.keys - 1;  // keys this row sees
       if (p.causal) {
@@ -369,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         if (p.window) lo = max(0, it.pos + row - p.window + 1);
       }
       if (!valid) hi = -1;
-      bool ok = true;
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain; both halves have the same
       float l = 0.f;        // running sum of exp2(x - m) of this half's keys
       for (int t = 0; t < n; ++t) {
@@ -441,76 +552,76 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar->p_full[sb]);
       }
-      if (ok && n > 0) {
+      if (!ok) break;
+      if (n > 0) {
         const bool got = ptx::mbar_wait(&bar->o_full, passes & 1, p.timeout_ns, abort_flag);
         ok = __all_sync(0xffffffffu, got);
+        ++passes;
         ptx::tc_fence_after();
-      }
-      if (!ok && lane == 0) fail(p, bar, kErrSoftmax);
-      bar->half[half][row] = l;
-      pair_any(quarter, false);
-      if (ok) {
+        bar->half[half][row] = l;
+        if (pair_any(quarter, !ok)) {
+          ok = false;
+          break;
+        }
         l = bar->half[0][row] + bar->half[1][row];
-        const float b2 = p.sink ? __ldg(p.sink + it.h) * kLog2e : -INFINITY;
-        const float M = fmaxf(m, b2);
-        const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
-        const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
-        const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
-        const float o_scale = z == 0.f ? 0.f : em / z;
-        const int64_t q_row = (int64_t)it.q_row + row;
-        if (valid && p.lse && half == 0) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
-        // a row's output that is not finite may be a hidden key's values' doing
-        const bool part = n > 0 && (it.partial(it.lo) || it.partial(it.lo + n - 1)) && !again;
-        float2 sum = make_float2(0.f, 0.f);
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (q_row * p.H + it.h) * kD;
-        const uint64_t o_policy = ptx::l2_policy_evict_first();
+      }
+      e += n;
+      const float b2 = p.sink ? __ldg(p.sink + it.h) * kLog2e : -INFINITY;
+      const float M = fmaxf(m, b2);
+      const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
+      const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
+      const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
+      const float o_scale = z == 0.f ? 0.f : em / z;
+      const int64_t q_row = (int64_t)it.q_row + row;
+      if (valid && p.lse && half == 0) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
+      // a row's output that is not finite may be a hidden key's values' doing
+      const bool part = n > 0 && (it.partial(it.lo) || it.partial(it.lo + n - 1)) && !again;
+      float2 sum = make_float2(0.f, 0.f);
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + (q_row * p.H + it.h) * kD;
+      const uint64_t o_policy = ptx::l2_policy_evict_first();
 #pragma unroll 1
-        for (int c0 = half * (kD / 2); c0 < (half + 1) * (kD / 2); c0 += 16) {
-          float ov[16];
-          if (n > 0) {
-            ptx::tmem_ld16(o_tmem + c0, ov);
-            ptx::tmem_wait_ld();
+      for (int c0 = half * (kD / 2); c0 < (half + 1) * (kD / 2); c0 += 16) {
+        float ov[16];
+        if (n > 0) {
+          ptx::tmem_ld16(o_tmem + c0, ov);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) ov[k] *= o_scale;
+          for (int k = 0; k < 16; ++k) ov[k] *= o_scale;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) ov[k] = 0.f;
+        }
+        if (part) {  // (a sum is finite only if its terms are)
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) sum = ptx::fadd2(sum, make_float2(ov[k], ov[k + 1]));
+        }
+        if (valid) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pk[k] = ptx::pack_bf16x2(ov[2 * k], ov[2 * k + 1]);
+          if (p.wide) {
+            st_global_32(dst + c0, pk, o_policy);
           } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) ov[k] = 0.f;
-          }
-          if (part) {  // (a sum is finite only if its terms are)
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) sum = ptx::fadd2(sum, make_float2(ov[k], ov[k + 1]));
-          }
-          if (valid) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) pk[k] = ptx::pack_bf16x2(ov[2 * k], ov[2 * k + 1]);
-            if (p.wide) {
-              st_global_32(dst + c0, pk, o_policy);
-            } else {
-              uint4* to = reinterpret_cast<uint4*>(dst + c0);
-              ptx::st_global_v4_hint(to, make_uint4(pk[0], pk[1], pk[2], pk[3]), o_policy);
-              ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
-            }
+            uint4* to = reinterpret_cast<uint4*>(dst + c0);
+            ptx::st_global_v4_hint(to, make_uint4(pk[0], pk[1], pk[2], pk[3]), o_policy);
+            ptx::st_global_v4_hint(to + 1, make_uint4(pk[4], pk[5], pk[6], pk[7]), o_policy);
           }
         }
-        if (part && valid && !(fabsf(sum.x + sum.y) < INFINITY)) *reinterpret_cast<volatile int*>(&bar->marked[i % 3]) = 1;
-        if (again) add_odd_values(p, it, row, half * (kD / 2), lo, hi);
-        ptx::tc_fence_before();  // (O is read: the next item's first product may overwrite it)
       }
+      if (n > 0) {  // O is read: the next item's first product may overwrite it
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar->o_empty);
+      }
+      if (__any_sync(0xffffffffu, part && valid && !(fabsf(sum.x + sum.y) < INFINITY)) && lane == 0 &&
+          atomicExch(&const_cast<Item*>(ring)->marked, 1) == 0)
+        p.marked[it.id] = atomicExch(&bar->marked, it.id);
+      if (again) add_odd_values(p, it, row, half * (kD / 2), lo, hi);
+      drop_item(bar, i);
     }
-    const int stop = __syncthreads_or(*abort_flag);
-    ptx::tc_fence_after();
-    if (stop) break;
-    e += n;
-    passes += n > 0 ? 1 : 0;
-    if (!again && bar->marked[i % 3]) {
-      again = 1;
-    } else {
-      again = 0;
-      ++i;
-    }
+    if (!ok && lane == 0) fail(p, bar, kErrSoftmax);
   }
-  if (threadIdx.x == 0) let_copies_land(abort_flag);
+
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {

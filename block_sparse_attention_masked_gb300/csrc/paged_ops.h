@@ -93,7 +93,7 @@ struct PackedParams {
   int64_t v_token, v_head;
   const int32_t *cu_q, *cu_k;    // [B + 1]
   PackedPlan* plan;
-  int* marked;                   // [max_pairs * H] of a CTA's marked items, the one marked before it
+  int* marked;                   // [2 max_pairs * H] of a CTA's marked items, the one marked before it
   uint32_t* err;
   unsigned long long timeout_ns;
   int B, T, T_k, H, H_kv, group;

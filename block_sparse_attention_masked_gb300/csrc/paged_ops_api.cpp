@@ -200,7 +200,8 @@ int check_paged(int B, int H, int H_kv, int table_pages, int page, int d, int dt
 size_t packed_plan_bytes(int64_t T, int64_t B) {
   return round256(sizeof(PackedPlan) + (size_t)packed_pairs(T, B) * sizeof(PackedPair));
 }
-size_t packed_bytes(int64_t T, int64_t B, int64_t H) { return packed_plan_bytes(T, B) + (size_t)(packed_pairs(T, B) * H) * 4; }
+// (heads of 256: two items a pair and head)
+size_t packed_bytes(int64_t T, int64_t B, int64_t H) { return packed_plan_bytes(T, B) + (size_t)(packed_pairs(T, B) * H) * 8; }
 
 int check_packed(int B, int T, int H) {
   if (B < 1 || H < 1 || T < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: B, H must be >= 1 and T >= 0");
