@@ -30,8 +30,8 @@
 // in time and gives up by raising a CTA-wide abort flag and a device error bit.
 //
 // Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads of 128, 349 us = 1,576
-// (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads, 306-317 us =
-// 1,200-1,240, the same tokens as 64 prompts of 256 89 us = 389, 12 images of 1 to 3,038 patches, 16 heads of 80,
+// (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads, 306-318 us =
+// 1,195-1,240, the same tokens as 64 prompts of 256 92 us = 376, 12 images of 1 to 3,038 patches, 16 heads of 80,
 // 186 us = 929.  Long lists run at the forward's own rate; an item costs 2.5 to 5 us beside its
 // tiles (its first S, its last P V and its output, which only the other query tile's work hides).
 // Tried without gain: the output staged in shared memory (d = 80 and 64 2% slower), O read from tensor memory 32 or
@@ -715,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       it->whole(p, s, &whole_lo, &whole_hi);
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain
       float l = 0.f;        // running sum of exp2(x - m)
+      float lr = 0.f;       // of these as P V takes them, where there are few
+      const bool few = few_keys(p, last - first + 1);
       for (int kt = first < 0 ? last + 1 : first; kt <= last; ++kt) {
         const bool got = ptx::mbar_wait(&bar->s_full[s], count & 1, p.timeout_ns, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
@@ -754,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
             rescale_o<D>(o_tmem, alpha);
             if (need_rescale) {
               l *= alpha;
+              lr *= alpha;
               m = m_new;
             }
           }
@@ -761,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         }
         l += ts;
         ptx::tmem_wait_st();
+        if (few) lr += rounded_sum<64>(s_tmem);
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar->p_full[s]);
       }
@@ -772,8 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       const float M = fmaxf(m, b2);
       const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
       const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
-      const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
-      const float o_scale = z == 0.f ? 0.f : em / z;
+      const float zs = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref), z = l * em + zs;
+      const float o_scale = z == 0.f ? 0.f : em / (few ? lr * em + zs : z);
       const int64_t q_row = (int64_t)it->q_row + 128 * s + row;
       if (valid && p.lse) p.lse[(int64_t)h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
       if (has_o) {

@@ -21,9 +21,9 @@
 // gives up by raising a CTA-wide abort flag and a device error bit; the two warps of a
 // pair, which meet at barriers, give up together.
 //
-// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 700 us = 1,571,
-// eight prompts of 1 to 3,352 tokens, 32 heads, 595 us = 1,277, 16 of 1,024 not causal 398 us =
-// 1,381, 64 of 256 150 us = 459.  Key tiles of 64, as in attention_sp.cu, took 882 us for the
+// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 700-725 us = 1,517-1,571,
+// eight prompts of 1 to 3,352 tokens, 32 heads, 595-607 us = 1,251-1,277, 16 of 1,024 not causal
+// 398-405 us = 1,357-1,381, 64 of 256 150-155 us = 444-459.  Key tiles of 64, as in attention_sp.cu, took 882 us for the
 // first: a product of 64 columns takes as long as one of 128.  Items that begin when the last
 // one is written took 677, 617, 444 and 191.  The next item's first scores before the last P V
 // of this one gained nothing: they wait for its Q.
@@ -483,6 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
       if (!valid) hi = -1;
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain; both halves have the same
       float l = 0.f;        // running sum of exp2(x - m) of this half's keys
+      float lr = 0.f;       // of these as P V takes them, where there are few
+      const bool few = few_keys(p, n);
       for (int t = 0; t < n; ++t) {
         const int g = e + t, sb = g & 1, kt = it.lo + t;
         const uint32_t s_tmem = tmem + lane_off + sb * kTile + half * 64;
@@ -538,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
             if (ok) rescale_o<kD>(o_tmem, need_rescale ? ptx::ex2(m - m_new) : 1.f, half * (kD / 2), (half + 1) * (kD / 2));
             if (need_rescale) {
               l *= ptx::ex2(m - m_new);
+              lr *= ptx::ex2(m - m_new);
               m = m_new;
             }
           }
@@ -549,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         }
         l += ts;
         ptx::tmem_wait_st();
+        if (few) lr += rounded_sum<32>(s_tmem);
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar->p_full[sb]);
       }
@@ -564,14 +568,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           break;
         }
         l = bar->half[0][row] + bar->half[1][row];
+        if (few) {
+          pair_any(quarter, false);  // (l is read)
+          bar->half[half][row] = lr;
+          pair_any(quarter, false);
+          lr = bar->half[0][row] + bar->half[1][row];
+        }
       }
       e += n;
       const float b2 = p.sink ? __ldg(p.sink + it.h) * kLog2e : -INFINITY;
       const float M = fmaxf(m, b2);
       const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
       const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
-      const float z = l * em + (b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref));
-      const float o_scale = z == 0.f ? 0.f : em / z;
+      const float zs = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref), z = l * em + zs;
+      const float o_scale = z == 0.f ? 0.f : em / (few ? lr * em + zs : z);
       const int64_t q_row = (int64_t)it.q_row + row;
       if (valid && p.lse && half == 0) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
       // a row's output that is not finite may be a hidden key's values' doing

@@ -4,8 +4,11 @@ implementation in 64 bits written here, and of a serving step's operators togeth
 Tolerances, derived before the first run; u = 2^-8 is bf16's half step relative to
 the value, e = 2^-24 fp32's.  o = sum p v / sum p: weights rounded to bf16 (u each),
 the output rounded once (u): |do| <= u |o| + (u + 2 t + 2^-13) A with A = sum p |v| /
-sum p, t = d e max_j sum_c |q_c k_jc| scale the error of a score, which moves a weight
-and the sum by as much, and 2^-13 for exponentials and sums.  lse: t + 2^-19 (1 + |lse|).
+sum p.  Where the sum of the rounded weights p (1 + c_j), |c_j| <= u, divides (rows of few
+keys), o is off by sum p c_j (v_j - o) / sum p, and sum p |v_j - o| / sum p <= A + |o|: u |o|
+more, and u^2 (A + |o|), which 2^-13 A holds.
+t = d e max_j sum_c |q_c k_jc| scale is the error of a score, which moves a weight and the
+sum by as much; 2^-13 for exponentials and sums.  lse: t + 2^-19 (1 + |lse|).
 """
 
 import math
@@ -77,7 +80,7 @@ def ref_sequence(q, k, v, causal, window, sink, scale):
     o, a = w @ v, w @ v.abs()
     lse = torch.where(z > 0, ref + torch.log(z), torch.full_like(z, -INF))
     t = (q.abs() @ k.abs().T).amax(dim=1) * scale * d * E if m else torch.zeros_like(z)
-    return o, lse, U * o.abs() + (U + 2 * t + 2.0 ** -13)[:, None] * a, t + 2.0 ** -19 * (1 + lse.abs().nan_to_num(posinf=0))
+    return o, lse, 2 * U * o.abs() + (U + 2 * t + 2.0 ** -13)[:, None] * a, t + 2.0 ** -19 * (1 + lse.abs().nan_to_num(posinf=0))
 
 
 def check(o, lse, q, k, v, cq, ck, causal, window, sink, scale, tag=""):
@@ -279,6 +282,19 @@ def test_packed_order_of_sequences_does_not_matter():
     rows = torch.cat([torch.arange(cq[b], cq[b + 1]) for b in order]).cuda()
     b, lb = mattn.attention_packed(q[rows], k[rows], v[rows], _i32(_cu([nq[i] for i in order])))
     assert torch.equal(a[rows], b) and torch.equal(la[:, rows], lb)
+
+
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
+def test_packed_one_key(d):
+    """A row that sees one key: its value, bit for bit."""
+    n = [1, 300, 2, 129]
+    cq = _cu(n)
+    q, k, v = inputs(cq[-1], cq[-1], 4, 2, d, 8, q_scale=3.0)
+    o, _ = mattn.attention_packed(q, k, v, _i32(cq), window=1)
+    assert torch.equal(o, v.repeat_interleave(2, dim=1))
+    o, _ = mattn.attention_packed(q, k, v, _i32(cq))
+    for c in cq[:-1]:
+        assert torch.equal(o[c], v[c].repeat_interleave(2, dim=0))
 
 
 def test_packed_agrees_with_attention():
