@@ -199,8 +199,8 @@ struct State8 {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[nt][mt][j] = (A == 4 ? (acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][A - 2][j] + acc[nt][A - 1][j])
-                                 : acc[nt][0][j] + acc[nt][1][j]) * qs[nt][j & 1];
+          s[nt][mt][j] = A == 4 ? (acc[nt][0][j] + acc[nt][1][j]) + (acc[nt][A - 2][j] + acc[nt][A - 1][j])
+                                : acc[nt][0][j] + acc[nt][1][j];
     }
     // the rows' powers, from the lane that loaded them
     float kp[T::kRows], vp[T::kRows];
@@ -221,7 +221,8 @@ struct State8 {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) s[nt][mt][2 * r + e] = there ? s[nt][mt][2 * r + e] * k2 : -INFINITY;
+          for (int e = 0; e < 2; ++e)  // (the powers first: either alone may take a product out of fp32's range)
+            s[nt][mt][2 * r + e] = there ? s[nt][mt][2 * r + e] * (qs[nt][e] * k2) : -INFINITY;
         ve[mt][r] = there ? ve[mt][r] : 0.f;
       }
     float mx[NT][2], my[NT][2];

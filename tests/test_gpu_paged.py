@@ -553,3 +553,15 @@ def test_decode_paged_waits_run_out(d, e4m3, B):
         ws.fill_(fill)
         for a, b in zip(run(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [4, 12])
+def test_decode_paged_large_queries_small_keys(H, d):
+    """Powers whose product is ordinary, the query's alone near the end of fp32's range."""
+    c = Cache(2, 1, d, 16, 9, True, seed=21)
+    c.ke[:] = torch.randint(1, 4, c.ke.shape, generator=_gen(1), device="cuda", dtype=torch.uint8)
+    q = _randn(_gen(2), 2, H, d, scale=2.0 ** 121)
+    c.freeze()
+    o, lse = mattn.decode_paged(q, c.k, c.v, c.table, _i32([144, 77]), **c.kw())
+    check_decode(o, lse, q, c, [list(range(144)), list(range(77))], None, d ** -0.5)
