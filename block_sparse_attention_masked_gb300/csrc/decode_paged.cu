@@ -353,13 +353,14 @@ struct State8 {
         const int head = nt * 8 + (lane & 3) * 2 + e;
         if (head >= G) continue;
         if (lane < 4) *reinterpret_cast<float2*>(to_ml + head * 2) = make_float2(m[nt][e], z);
-        const float f = m[nt][e] == -INFINITY ? 1.f : ptx::ex2(mo[nt][e] - 14.f - m[nt][e]);
+        // times 2^(mo - 14 - m), its root twice: mo - m lies in [-127, 127], and ex2 gives zeros below 2^-126
+        const float f = m[nt][e] == -INFINITY ? 1.f : ptx::ex2(0.5f * (mo[nt][e] - 14.f - m[nt][e]));
         float* dst = to_o + head * D + rot(lane >> 2) * (D == 64 ? 8 : 16);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2) {
           float* to = dst + (D == 64 ? 2 * i : (i >> 3) * 128 + 2 * (i & 7));
-          *reinterpret_cast<float4*>(to) = make_float4(o[nt][i][e] * f, o[nt][i][e + 2] * f, o[nt][i + 1][e] * f,
-                                                       o[nt][i + 1][e + 2] * f);
+          *reinterpret_cast<float4*>(to) = make_float4(o[nt][i][e] * f * f, o[nt][i][e + 2] * f * f,
+                                                       o[nt][i + 1][e] * f * f, o[nt][i + 1][e + 2] * f * f);
         }
       }
   }

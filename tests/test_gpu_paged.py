@@ -565,3 +565,22 @@ def test_decode_paged_large_queries_small_keys(H, d):
     c.freeze()
     o, lse = mattn.decode_paged(q, c.k, c.v, c.table, _i32([144, 77]), **c.kw())
     check_decode(o, lse, q, c, [list(range(144)), list(range(77))], None, d ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("B", [2, 90])
+def test_decode_paged_small_values(B, d):
+    """Values down to fp32's least powers, in clusters (2 sequences) and in equal shares: none is flushed on the way."""
+    H, Hkv = 12, 2
+    c = Cache(B, Hkv, d, 16, 9, True, seed=22)
+    c.ve[:] = torch.randint(8, 12, c.ve.shape, generator=_gen(1), device="cuda", dtype=torch.uint8)
+    q = _randn(_gen(2), B, H, d)
+    lens = [144 - b for b in range(B)]
+    c.freeze()
+    o, lse = mattn.decode_paged(q, c.k, c.v, c.table, _i32(lens), **c.kw())
+    qd, got = q.double().cpu(), o.double().cpu()
+    for b in (0, B - 1):
+        for h in range(H):
+            keys, values = c.rows(b, h // (H // Hkv), range(lens[b]))
+            r, _, tol, _ = ref_decode(qd[b, h], keys, values, None, d ** -0.5, True)
+            assert bool((r.abs().max() > 2.0 ** -119) and ((got[b, h] - r).abs() <= tol).all()), (b, h)
