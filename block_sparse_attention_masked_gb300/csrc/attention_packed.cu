@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain
       float l = 0.f;        // running sum of exp2(x - m)
       float lr = 0.f;       // of these as P V takes them, where there are few
-      const bool few = few_keys(p, last - first + 1);
+      const bool some_few = few_keys(p, p.causal ? min(keys - 1, pos - row) : keys - 1);  // (the first row sees least)
       for (int kt = first < 0 ? last + 1 : first; kt <= last; ++kt) {
         const bool got = ptx::mbar_wait(&bar->s_full[s], count & 1, p.timeout_ns, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
         }
         l += ts;
         ptx::tmem_wait_st();
-        if (few) lr += rounded_sum<64>(s_tmem);
+        if (some_few) lr += rounded_sum<64>(s_tmem);
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar->p_full[s]);
       }
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
       const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
       const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
       const float zs = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref), z = l * em + zs;
-      const float o_scale = z == 0.f ? 0.f : em / (few ? lr * em + zs : z);
+      const float o_scale = z == 0.f ? 0.f : em / (few_keys(p, hi) ? lr * em + zs : z);
       const int64_t q_row = (int64_t)it->q_row + 128 * s + row;
       if (valid && p.lse) p.lse[(int64_t)h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
       if (has_o) {

@@ -60,10 +60,13 @@ __device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
 // such errors add up to the output's own rounding or less; over few, where outputs are largest,
 // they are kept out of it as far as they are common to a row's weights (all of it for one
 // key): the output is divided by the sum of the rounded weights.  The LSE takes that of the
-// weights as they were.  So rows of one key tile, or of a window of 64 keys at most: eight
-// prompts of 700 tokens in all 0.0020 off the 64-bit form where the other sum left 0.0023, in 11.2 us for 10.8.
-__device__ __forceinline__ bool few_keys(const PackedParams& p, int tiles) {
-  return tiles == 1 || (p.window && p.window <= 64);
+// weights as they were.  So the rows whose last key is among their sequence's first 128, or whose
+// window is of 64 keys at most: a row's own keys decide, so that a chunk's rows get the bits of the
+// whole prompt's.  (Windows of 65 to 128 keys too took 10% more: 4 prompts of 4,096 with 8 heads of
+// 128 34.4 us for 31.1.)  Eight prompts of 700 tokens in all 0.0020 off the 64-bit form where the
+// other sum left 0.0023, in 11.2 us for 10.8.
+__device__ __forceinline__ bool few_keys(const PackedParams& p, int hi) {  // hi: the row's last key
+  return hi < 128 || (p.window && p.window <= 64);
 }
 // This thread's sum of the rounded weights in N columns (pairs) of tensor memory.
 template <int N>

@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
       float m = -INFINITY;  // running (stale) max of scaled scores, log2 domain; both halves have the same
       float l = 0.f;        // running sum of exp2(x - m) of this half's keys
       float lr = 0.f;       // of these as P V takes them, where there are few
-      const bool few = few_keys(p, n);
+      const bool some_few = few_keys(p, p.causal ? min(it.keys - 1, it.pos) : it.keys - 1);  // (the first row sees least)
       for (int t = 0; t < n; ++t) {
         const int g = e + t, sb = g & 1, kt = it.lo + t;
         const uint32_t s_tmem = tmem + lane_off + sb * kTile + half * 64;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
         }
         l += ts;
         ptx::tmem_wait_st();
-        if (few) lr += rounded_sum<32>(s_tmem);
+        if (some_few) lr += rounded_sum<32>(s_tmem);
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar->p_full[sb]);
       }
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
           break;
         }
         l = bar->half[0][row] + bar->half[1][row];
-        if (few) {
+        if (some_few) {
           pair_any(quarter, false);  // (l is read)
           bar->half[half][row] = lr;
           pair_any(quarter, false);
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
       const float ref = M == -INFINITY ? 0.f : M;  // (no key and no sink: l = 0; scores that are NaN: l is)
       const float em = m == -INFINITY ? 1.f : ptx::ex2(m - ref);
       const float zs = b2 == -INFINITY ? 0.f : ptx::ex2(b2 - ref), z = l * em + zs;
-      const float o_scale = z == 0.f ? 0.f : em / (few ? lr * em + zs : z);
+      const float o_scale = z == 0.f ? 0.f : em / (few_keys(p, hi) ? lr * em + zs : z);
       const int64_t q_row = (int64_t)it.q_row + row;
       if (valid && p.lse && half == 0) p.lse[(int64_t)it.h * p.T + q_row] = z == 0.f ? -INFINITY : (ref + ptx::lg2(z)) * kLn2;
       // a row's output that is not finite may be a hidden key's values' doing

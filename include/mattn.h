@@ -619,7 +619,9 @@ int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int pa
  *   d in {64, 80, 96, 128, 256}; H a multiple of H_kv; T, T_k <= 2^30; H * (T / 256 + B) < 2^31.
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Weights
  * meet the values in bf16 as in mattn_fwd; sums, statistics and the LSE are fp32.  Rows
- * that see few keys are divided by the sum of the rounded weights.
+ * whose last key is among their sequence's first 128, or whose window is of 64 keys at
+ * most, are divided by the sum of the rounded weights.  A row's result comes from its query
+ * and its keys alone, to the bit: a prompt's rows in chunks are those of the whole prompt.
  * What a query does not see (other sequences, later keys) has no part in its result,
  * infinities and NaN among it.
  */

@@ -366,3 +366,34 @@ def test_packed_waits_run_out(d):
         ws.fill_(fill)
         for a, b in zip(run(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
+@pytest.mark.parametrize("window", [None, 20, 64, 100, 128, 200])
+def test_packed_row_of_a_prompt_in_chunks(window, d):
+    """A row's bits come from its own keys alone: a prompt whole, and its rows from any one on as a chunk."""
+    n = 400
+    q, k, v = inputs(n, n, 4, 2, d, 15)
+    o, lse = mattn.attention_packed(q, k, v, _i32([0, n]), window=window)
+    for at, end in ((1, n), (37, n), (100, n), (127, 300), (128, n), (200, 201), (255, 390), (300, n)):
+        a, l = mattn.attention_packed(q[at:end], k[:end], v[:end], _i32([0, end - at]), _i32([0, end]), window=window)
+        assert torch.equal(a, o[at:end]) and torch.equal(l, lse[:, at:end]), at
+
+
+@pytest.mark.parametrize("d", [64, 80, 96, 128, 256])
+@pytest.mark.parametrize("causal,window", [(True, None), (False, None), (True, 65), (True, 300)])
+def test_packed_rounding_of_rows_of_many_keys(causal, window, d):
+    """A row whose last key lies behind its sequence's first 128 divides by the sum of the weights as they were: one u |o|
+    less than the bound of the other rows."""
+    nq, nk = [700, 129, 260, 40], [700, 300, 260, 41]
+    cq, ck = _cu(nq), _cu(nk)
+    q, k, v = inputs(cq[-1], ck[-1], 4, 2, d, 17)
+    o, lse = mattn.attention_packed(q, k, v, _i32(cq), _i32(ck), causal=causal, window=window)
+    check(o, lse, q, k, v, cq, ck, causal, window, None, d ** -0.5)
+    for b, (n, m) in enumerate(zip(nq, nk)):
+        first = max(0, 128 - (m - n)) if causal else (0 if m > 128 else n)  # the first row that sees key 128 or later
+        i, j = slice(cq[b] + first, cq[b + 1]), slice(ck[b], ck[b + 1])
+        for h in range(4):
+            r, _, tol, _ = ref_sequence(q[cq[b] : cq[b + 1], h].double(), k[j, h // 2].double(), v[j, h // 2].double(), causal, window,
+                                        None, d ** -0.5)
+            assert bool(((o[i, h].double() - r[first:]).abs() <= (tol - U * r.abs())[first:]).all()), (b, h)
