@@ -17,9 +17,10 @@
 //
 // Roles (384 threads): warp 0 Q and K; warp 1 tensor memory and the products; warp 2 V;
 // warp 3 the items; warps 4..11 softmax and output: warps w and w + 4 the same 32 rows, half
-// of a tile's keys and of the output's columns each.  Every wait is bounded in time and
-// gives up by raising a CTA-wide abort flag and a device error bit; the two warps of a
-// pair, which meet at barriers, give up together.
+// of a tile's keys and of the output's columns each.  Every wait is bounded in time (the
+// scheduler's: in time without a tile's progress) and gives up by raising a CTA-wide abort
+// flag and a device error bit; the two warps of a pair, which meet at barriers, give up
+// together.
 //
 // Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads, 700-725 us = 1,517-1,571,
 // eight prompts of 1 to 3,352 tokens, 32 heads, 595-607 us = 1,251-1,277, 16 of 1,024 not causal
@@ -97,6 +98,7 @@ struct Bar {
   uint32_t tmem_base;
   int abort_flag;
   int marked;                // the CTA's last marked item, from which PackedParams::marked leads to the others; -1: none
+  uint32_t tiles;            // K tiles whose copies are under way, of all items
   Item items[kItems];
   uint32_t redo[2][4];       // rows of each half and 32 rows whose tile is done again
   float half[2][kTile];      // a row's maximum over half a tile, at last half its sum
@@ -109,6 +111,19 @@ __device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t b
   atomicOr(p.err, bit);
 }
 
+// The scheduler's wait for a ring slot.  It takes as long as an item, whatever its keys take, so
+// it gives up after timeout_ns without a K tile more (every other wait is one for a tile's work).
+__device__ __forceinline__ bool slot_wait(const PackedParams& p, Bar* bar, uint64_t* b, uint32_t parity,
+                                          volatile int* abort_flag) {
+  volatile uint32_t* tiles = &bar->tiles;
+  for (uint32_t seen = *tiles;;) {
+    if (ptx::mbar_wait_backoff(b, parity, p.timeout_ns, abort_flag, 200)) return true;
+    const uint32_t now = *tiles;
+    if (now == seen || *abort_flag) return false;
+    seen = now;
+  }
+}
+
 // The items, in order (one thread).
 __device__ __forceinline__ void schedule(const PackedParams& p, Bar* bar, volatile int* abort_flag) {
   const int total = p.plan->pairs * 2 * p.H;
@@ -116,7 +131,7 @@ __device__ __forceinline__ void schedule(const PackedParams& p, Bar* bar, volati
   for (int i = 0, again = 0;; ++i) {
     const int slot = i % kItems;
     const uint32_t phase = (i / kItems) & 1;
-    if (!ptx::mbar_wait_backoff(&bar->item_empty[slot], phase ^ 1, p.timeout_ns, abort_flag, 200)) break;
+    if (!slot_wait(p, bar, &bar->item_empty[slot], phase ^ 1, abort_flag)) break;
     Item& it = bar->items[slot];
     if (!again) {
       for (; id < total; id = (int)gridDim.x + atomicAdd(&p.plan->next, 1)) {
@@ -132,7 +147,7 @@ __device__ __forceinline__ void schedule(const PackedParams& p, Bar* bar, volati
       // every item so far written: then the marked ones
       it.say(kDrain);
       ptx::mbar_arrive(&bar->item_full[slot]);
-      if (!ptx::mbar_wait_backoff(&bar->item_empty[slot], phase, p.timeout_ns, abort_flag, 200)) break;
+      if (!slot_wait(p, bar, &bar->item_empty[slot], phase, abort_flag)) break;
       again = 1;
       id = *reinterpret_cast<volatile int*>(&bar->marked);
       continue;
@@ -244,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
     ptx::mbar_init(&bar->drain, 1);
     bar->abort_flag = 0;
     bar->marked = -1;
+    bar->tiles = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
@@ -297,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_256_kernel(const
             break;
           }
           if (lane == 0) {
+            if (c == 0) *reinterpret_cast<volatile uint32_t*>(&bar->tiles) = g / kPieces + 1;
             ptx::mbar_arrive_expect_tx(&bar->k_full[slot], kPiece);
             if (!(p.selftest == 1 && g == 0))
               ptx::tma_load_3d_hint(sk + slot * kPiece, &p.tk[0], &bar->k_full[slot], c * 64, h_kv, row, keep);

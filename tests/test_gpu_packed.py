@@ -397,3 +397,21 @@ def test_packed_rounding_of_rows_of_many_keys(causal, window, d):
             r, _, tol, _ = ref_sequence(q[cq[b] : cq[b + 1], h].double(), k[j, h // 2].double(), v[j, h // 2].double(), causal, window,
                                         None, d ** -0.5)
             assert bool(((o[i, h].double() - r[first:]).abs() <= (tol - U * r.abs())[first:]).all()), (b, h)
+
+
+def test_packed_256_items_longer_than_the_wait_limit():
+    """The limit is one for a wait without progress: items of thousands of key tiles, several a CTA, run through."""
+    n, m, H = 2560, 1 << 20, 32
+    q, k, v = inputs(n, m, H, 1, 256, 16)
+    call = lambda: mattn.attention_packed(q, k, v, _i32([0, n]), _i32([0, m]), causal=False)  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    mattn.set_wait_timeout_ns(4_000_000)  # 4 ms; an item takes about 13
+    try:
+        got = call()
+        torch.cuda.synchronize()
+        rc, word = mattn.device_status()
+    finally:
+        mattn.set_wait_timeout_ns(0)
+    assert rc == 0, hex(word)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
