@@ -94,7 +94,7 @@ inline void place_rows(DecodeRowsParams* p, const RowsLayout& r, char* ws) {
 // A buffer's bytes [lo, hi); hi wraps for no buffer that can exist.
 struct Extent {
   uintptr_t lo, hi;
-  bool meets(const Extent& x) const { return lo < x.hi && x.lo < hi; }
+  bool meets(const Extent& x) const { return lo < x.hi && x.lo < hi && lo < hi && x.lo < x.hi; }
 };
 inline Extent extent_of(const void* p, uint64_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);

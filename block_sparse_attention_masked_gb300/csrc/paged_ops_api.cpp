@@ -45,6 +45,67 @@ bool rows_apart(const int64_t (&stride)[3], const int64_t (&size)[3], int64_t ro
   return true;
 }
 
+// Rows in memory: rows of `row` bytes at base + sum i_j stride_j, 0 <= i_j < size_j (in bytes;
+// the rows of one do not overlap: rows_apart).
+struct RowSet {
+  const void* base;
+  int64_t stride[3], size[3], row;
+  Extent extent() const {
+    uint64_t end = row;
+    for (int j = 0; j < 3; ++j) end += (uint64_t)(size[j] - 1) * stride[j];
+    return extent_of(base, size[0] ? end : 0);
+  }
+};
+
+// Whether -lb < at + sum n_j stride_j < la for some |n_j| < size_j, j from i on: the largest
+// stride left takes the sum to within itself of 0, as those below it span less, or it does not.
+bool rows_meet(int64_t at, const int64_t* stride, const int64_t* size, int i, int n, int64_t la, int64_t lb) {
+  if (i == n) return at > -lb && at < la;
+  const int64_t s = stride[i], f = -(at >= 0 ? (at + s - 1) / s : -(-at / s));  // floor(-at / s)
+  for (int64_t x = f; x <= f + 1; ++x)
+    if (x > -size[i] && x < size[i] && rows_meet(at + x * s, stride, size, i + 1, n, la, lb)) return true;
+  return false;
+}
+
+// Whether two sets share no byte.  Sets whose extents meet may be interleaved (k and v of one
+// pool, codes beside their exponents): with the same strides, or page by page with the same
+// stride from one page to the next.  Other ways are not told apart from an overlap.
+bool apart(const RowSet& a, const RowSet& b) {
+  if (!a.extent().meets(b.extent())) return true;
+  const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base));
+  int64_t stride[3], size[3];
+  int n = 0;
+  bool same = true;
+  for (int j = 0; j < 3; ++j) {
+    same = same && a.size[j] == b.size[j] && (a.size[j] == 1 || a.stride[j] == b.stride[j]);
+    if (a.size[j] == 1) continue;
+    int i = n++;  // (largest stride first)
+    for (; i > 0 && stride[i - 1] < a.stride[j]; --i) {
+      stride[i] = stride[i - 1];
+      size[i] = size[i - 1];
+    }
+    stride[i] = a.stride[j];
+    size[i] = a.size[j];
+  }
+  if (same) return !rows_meet(at, stride, size, 0, n, a.row, b.row);
+  const int64_t page = a.stride[0];
+  if (a.size[0] == 1 || a.size[0] != b.size[0] || page != b.stride[0]) return false;
+  auto span = [](const RowSet& x) { return (x.size[1] - 1) * x.stride[1] + (x.size[2] - 1) * x.stride[2] + x.row; };
+  const int64_t r = (at % page + page) % page;
+  return r >= span(a) && r + span(b) <= page;
+}
+
+// The same of the rows of k and v (or of their exponents), whose pages of one number must be
+// apart.  A page of one number may be another's of the other tensor, in one pool from whose
+// numbers the table gives each sequence its own (k in the even ones, v a page behind): sets a
+// whole number of pages apart.
+bool pages_apart(const RowSet& a, const RowSet& b) {
+  RowSet x = a, y = b;
+  x.size[0] = y.size[0] = 1;
+  const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base));
+  return apart(x, y) && ((a.stride[0] == b.stride[0] && at % a.stride[0] == 0) || apart(a, b));
+}
+
 int check_cache(const char* what, const mattn_paged_cache* c, int B, int H_kv, int d) {
   if (!c) return report_error(MATTN_ERR_INVALID_ARG, "%s: the cache is NULL", what);
   if (B < 1 || H_kv < 1) return report_error(MATTN_ERR_INVALID_ARG, "%s: B and H_kv must be >= 1", what);
@@ -82,14 +143,16 @@ int check_cache(const char* what, const mattn_paged_cache* c, int B, int H_kv, i
   return MATTN_OK;
 }
 
-// Lowest and one past the highest byte of rows with these strides.
-Extent pages_extent(const mattn_paged_cache* c, int i, int H_kv, int d) {
-  const int es = c->dtype == MATTN_E4M3 ? 1 : 2;
-  Extent x;
-  x.lo = reinterpret_cast<uintptr_t>(i ? c->v : c->k);
-  x.hi = x.lo + ((uint64_t)(c->n_pages - 1) * c->page_stride[i] + (uint64_t)(H_kv - 1) * c->head_stride[i] +
-                 (uint64_t)(c->page - 1) * c->row_stride[i] + d) * es;
-  return x;
+// The rows of k's (0) and v's (1) pages, and of their exponents (2, 3; none in bf16).
+RowSet cache_rows(const mattn_paged_cache* c, int i, int H_kv, int d) {
+  const int64_t es = i > 1 || c->dtype == MATTN_E4M3 ? 1 : 2;
+  const int t = i & 1;
+  if (i > 1 && c->dtype != MATTN_E4M3) return {nullptr, {0, 0, 0}, {0, 0, 0}, 0};
+  if (i > 1)
+    return {t ? c->v_exponents : c->k_exponents, {c->exp_page_stride[t], c->exp_head_stride[t], c->exp_row_stride[t]},
+            {c->n_pages, H_kv, c->page}, 1};
+  return {t ? c->v : c->k, {c->page_stride[t] * es, c->head_stride[t] * es, c->row_stride[t] * es}, {c->n_pages, H_kv, c->page},
+          d * es};
 }
 
 int fill_rows(const char* what, const void* k, const void* v, const int64_t* token_stride, const int64_t* head_stride,
@@ -133,14 +196,27 @@ int fill_rows(const char* what, const void* k, const void* v, const int64_t* tok
     p->exp_row[i] = c->exp_row_stride[i];
   }
   // rows are read and written in no order.  (Interleaved views, as k and v of one
-  // projection or of one pool, share an extent without sharing a byte: the two
+  // projection or of one pool, share an extent without sharing a byte: the
   // tensors of a side may; whole sides may not.)
+  const Extent small[3] = {extent_of(c->page_table, (uint64_t)B * c->table_pages * 4), extent_of(cu, ((uint64_t)B + 1) * 4),
+                           extent_of(starts, (uint64_t)B * 4)};
+  RowSet of[4], to[2];
+  for (int j = 0; j < 4; ++j) of[j] = cache_rows(c, j, H_kv, d);
+  for (int i = 0; i < 2; ++i) to[i] = {rows[i], {token_stride[i] * 2, head_stride[i] * 2, 0}, {T, H_kv, 1}, d * 2};
   for (int i = 0; i < 2 && T > 0; ++i)
-    for (int j = 0; j < 2; ++j)
-      if (at[i].meets(pages_extent(c, j, H_kv, d)))
-        return report_error(MATTN_ERR_INVALID_ARG, "%s: the rows overlap the cache", what);
-  if ((reads && T > 0 && rows[0] == rows[1]) || (!reads && (pages[0] == pages[1] || (exps[0] && exps[0] == exps[1]))))
-    return report_error(MATTN_ERR_INVALID_ARG, "%s: k and v are written to one place", what);
+    for (int j = 0; j < 4; ++j)
+      if (at[i].meets(of[j].extent())) return report_error(MATTN_ERR_INVALID_ARG, "%s: the rows overlap the cache", what);
+  for (const Extent& x : small) {
+    for (int i = 0; i < 4 && T > 0; ++i)
+      if (reads ? i < 2 && at[i].meets(x) : of[i].extent().meets(x))
+        return report_error(MATTN_ERR_INVALID_ARG, "%s: an output overlaps the page table, cu_seqlens or starts", what);
+  }
+  if (reads && T > 0 && !apart(to[0], to[1]))
+    return report_error(MATTN_ERR_INVALID_ARG, "%s: k and v overlap", what);
+  for (int i = 0; i < (c->dtype == MATTN_E4M3 ? 4 : 2) && !reads && T > 0; ++i)
+    for (int j = 0; j < i; ++j)
+      if (i - j == 1 && i % 2 ? !pages_apart(of[j], of[i]) : !apart(of[j], of[i]))
+        return report_error(MATTN_ERR_INVALID_ARG, "%s: two of the cache's tensors overlap", what);
   p->table = c->page_table;
   p->cu = cu;
   p->starts = starts;
@@ -266,14 +342,15 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   if ((rc = check_small("decode_paged", lse, seq_lens, sink))) return rc;
   if ((rc = check_scale("decode_paged", softmax_scale))) return rc;
   const bool e8 = cache->dtype == MATTN_E4M3;
-  const Extent ins[3] = {extent_of(q, (uint64_t)B * H * d * 2), pages_extent(cache, 0, H_kv, d), pages_extent(cache, 1, H_kv, d)};
+  const int warps = decode_share_warps(tiles, d);
+  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * warps, d);
+  if ((rc = check_workspace("decode_paged", workspace, workspace_bytes, lay.all()))) return rc;
+  const Extent ins[3] = {extent_of(q, (uint64_t)B * H * d * 2), cache_rows(cache, 0, H_kv, d).extent(),
+                         cache_rows(cache, 1, H_kv, d).extent()};
   const Extent to = extent_of(o, (uint64_t)B * H * d * 2), to_lse = extent_of(lse, (uint64_t)B * H * 4);
   for (const Extent& x : ins)
     if (to.meets(x) || to_lse.meets(x) || to.meets(to_lse))
       return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: an output overlaps q, the cache or the other output");
-  const int warps = decode_share_warps(tiles, d);
-  const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * warps, d);
-  if ((rc = check_workspace("decode_paged", workspace, workspace_bytes, lay.all()))) return rc;
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   DecodePagedParams p;

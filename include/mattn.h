@@ -559,7 +559,10 @@ typedef struct {
  *               multiples of 8 and >= 0
  *   cu_seqlens  DEVICE int32 [B + 1], ascending, or NULL (T = B: one token each)
  *   starts      DEVICE int32 [B] or NULL (0)
- *   d in {64, 128, 256}; T * H_kv < 2^31.  The cache must not overlap k and v.
+ *   d in {64, 128, 256}; T * H_kv < 2^31.  The cache's tensors must not overlap k and v, the
+ *   page table, the offsets or each other (rows that interleave with those of the same
+ *   strides, or page by page, do not).  k's and v's pages may be those of one pool a whole
+ *   number of pages apart, whose numbers the table deals out.
  */
 int mattn_cache_write(const void* k, const void* v, const int64_t token_stride[2], const int64_t head_stride[2],
                       const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,
@@ -570,7 +573,8 @@ int mattn_cache_write(const void* k, const void* v, const int64_t token_stride[2
  * cu_seqlens_{b+1} - 1 of k and v get positions starts_b, starts_b + 1, .. of
  * sequence b, rounded to bf16.  Positions outside the table or without a page give
  * zeros; rows of no sequence are left as they are.  The arguments are
- * mattn_cache_write's (token and head strides > 0).
+ * mattn_cache_write's (token and head strides > 0); k and v must not overlap each other, the
+ * cache, the page table or the offsets.
  */
 int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int64_t head_stride[2],
                      const mattn_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* starts, int B, int T,

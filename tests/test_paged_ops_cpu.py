@@ -292,3 +292,90 @@ def test_attention_packed_accepts(L):
     assert _packed(L, T_k=0, k=None, v=None, cu_k=MB) in ok
     assert f(0, 100, 8, ctypes.byref(n)) == -1 and f(3, -1, 8, ctypes.byref(n)) == -1 and f(3, 100, 8, None) == -1
     assert f(1, 1 << 30, 1024, ctypes.byref(n)) == -2
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cache_tensors_that_overlap(L, e4m3):
+    """What a call writes overlaps neither itself nor what it reads: k and v a few bytes or a row apart, codes and
+    exponents, tables and offsets, outputs a row apart.  Interleaved ones share an extent and no byte."""
+    ok = (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)
+    es = 1 if e4m3 else 2
+    k, page = 256 * MB, 2 * 16 * 128 * es  # bytes of a page
+    for off in (16, 128 * es, 16 * 128 * es, page // 2, page + 16, 3 * page - 128 * es, 9 * page + 16, -16, -page - 16):
+        assert _write(L, _cache(e4m3, v=k + off)) == -1, off
+        assert L.mattn_last_error()
+    assert _write(L, _cache(e4m3, v=k + 10 * page)) in ok and _write(L, _cache(e4m3, v=k - 10 * page)) in ok
+    # one pool: its even pages k's, v's a page behind, by the table; k and v of a page, a head or a row side by side
+    assert _write(L, _cache(e4m3, v=k + page)) in ok
+    wide = dict(page_stride=(8192, 8192))
+    assert _write(L, _cache(e4m3, v=k + page, **wide)) in ok and _write(L, _cache(e4m3, v=k + 3 * page, **wide)) in ok
+    assert _write(L, _cache(e4m3, v=k + page - 16, **wide)) == -1 and _write(L, _cache(e4m3, v=k + page + 16, **wide)) == -1
+    assert _write(L, _cache(e4m3, v=k + 16 * 128 * es, head_stride=(4096, 4096), **wide)) in ok
+    rows = dict(row_stride=(256, 256), head_stride=(4096, 4096), **wide)
+    assert _write(L, _cache(e4m3, v=k + 128 * es, **rows)) in ok and _write(L, _cache(e4m3, v=k + 64 * es, **rows)) == -1
+    # heads apart by more than their pages: a page's v a head of k's behind
+    apart = dict(page_stride=(2048, 2048), head_stride=(20480, 20480))
+    assert _write(L, _cache(e4m3, v=k + 20480 * es, **apart)) == -1 and _write(L, _cache(e4m3, v=k + 2048 * es, **apart)) in ok
+    # different layouts in one place
+    assert _write(L, _cache(e4m3, v=k + 32, head_stride=(2048, 128), row_stride=(128, 256))) == -1
+    table, size = 900 * MB, 3 * 4 * 4
+    for kw in (dict(page_table=k + 64), dict(page_table=k - size + 4), dict(page_table=512 * MB + 10 * page - 4)):
+        assert _write(L, _cache(e4m3, **kw)) == -1 and _write(L, _cache(e4m3, **kw), read=True) in ok, kw
+    for kw in (dict(cu=k + 4), dict(starts=512 * MB), dict(cu=k - 12)):
+        assert _write(L, _cache(e4m3), **kw) == -1 and _write(L, _cache(e4m3), read=True, **kw) in ok, kw
+    assert _write(L, _cache(e4m3, page_table=k - size), cu=k + 10 * page, starts=512 * MB - 12) in ok
+    # outputs of a read: 3 tokens of 2 heads of 128, 512 bytes each
+    for off in (16, 256, 512, 1024, 1280, -16, -512):
+        assert _write(L, _cache(e4m3), k=MB, v=MB + off, read=True) == -1, off
+    assert _write(L, _cache(e4m3), k=MB, v=MB + 3 * 512, read=True) in ok
+    assert _write(L, _cache(e4m3), k=MB, v=MB + 512, token=(512, 512), read=True) in ok
+    assert _write(L, _cache(e4m3), k=MB, v=MB + 256, token=(512, 512), head=(256, 256), read=True) in ok
+    assert _write(L, _cache(e4m3), k=MB, v=MB + 128, token=(512, 512), head=(256, 256), read=True) == -1
+    for kw in (dict(cu=MB + 4), dict(cu=MB - 12), dict(starts=100 * MB + 1532)):
+        assert _write(L, _cache(e4m3), read=True, **kw) == -1 and _write(L, _cache(e4m3), **kw) in ok, kw
+    assert _write(L, _cache(e4m3, page_table=100 * MB), read=True) == -1
+    if not e4m3:
+        return
+    # exponents: over the rows, the codes, each other; in one pool with the codes, page by page or row by row
+    for kw in (dict(k_exponents=MB), dict(v_exponents=100 * MB + 1500), dict(k_exponents=k + 100), dict(v_exponents=k + 100),
+               dict(k_exponents=512 * MB - 100), dict(v_exponents=768 * MB + 8), dict(v_exponents=768 * MB + 16),
+               dict(v_exponents=768 * MB + 31), dict(page_table=768 * MB + 8)):
+        assert _write(L, _cache(True, **kw)) == -1, kw
+    assert _write(L, _cache(True, k_exponents=MB), read=True) == -1 and _write(L, _cache(True, page_table=768 * MB + 8), read=True) in ok
+    assert _write(L, _cache(True, v_exponents=768 * MB + 32)) in ok  # (a whole page)
+    pool = dict(page_stride=(12288, 12288), exp_page_stride=(12288, 12288), v=k + 4096)
+    assert _write(L, _cache(True, k_exponents=k + 8192, v_exponents=k + 8224, **pool)) in ok
+    assert _write(L, _cache(True, k_exponents=k + 8191, v_exponents=k + 8224, **pool)) == -1
+    assert _write(L, _cache(True, k_exponents=k + 8192, v_exponents=k + 12288 - 31, **pool)) == -1
+    beside = dict(row_stride=(144, 144), head_stride=(2304, 2304), page_stride=(4608, 4608), exp_row_stride=(144, 144),
+                  exp_head_stride=(2304, 2304), exp_page_stride=(4608, 4608), v=512 * MB)
+    assert _write(L, _cache(True, k_exponents=k + 128, v_exponents=512 * MB + 143, **beside)) in ok
+    assert _write(L, _cache(True, k_exponents=k + 127, v_exponents=512 * MB + 143, **beside)) == -1
+
+
+def test_cache_tensors_that_overlap_by_enumeration(L):
+    """k's and v's pages at offsets and strides of many kinds: refused exactly where rows of theirs share bytes, but for
+    pools a whole number of pages apart, whose pages of one number are apart."""
+    import random
+
+    r = random.Random(1)
+    seen = {True: 0, False: 0}
+    for _ in range(1500):
+        n, H, page, d = r.choice((1, 2, 3)), r.choice((1, 2, 3)), 16, 64
+        size, order = (n, H, page), r.sample(range(3), 3)
+        stride, end = [0, 0, 0], d
+        for i in order:  # (each dimension steps over those below it, and some room)
+            stride[i] = end + 8 * r.choice((0, 0, 8, 64, end // 8))
+            end = stride[i] * (size[i] - 1) + end
+        off = r.choice((8 * r.randint(-end // 8 - 8, end // 8 + 8), r.choice((-1, 1)) * r.choice(stride), d, -d, 2 * stride[0],
+                        stride[0] + stride[1]))
+        row = lambda p, h, x: p * stride[0] + h * stride[1] + x * stride[2]  # noqa: E731
+        spots = [[(p, row(p, h, x)) for p in range(n) for h in range(H) for x in range(page)] for _ in range(2)]
+        hit = [(p, q) for p, a in spots[0] for q, b in spots[1] if abs(a - b - off) < d]
+        bad = any(p == q for p, q in hit) or (bool(hit) and off % stride[0] != 0)
+        c = _cache(n_pages=n, H_kv=H, d=d, v=256 * MB + 2 * off, page_stride=(stride[0],) * 2, head_stride=(stride[1],) * 2,
+                   row_stride=(stride[2],) * 2)
+        got = _write(L, c, H_kv=H, d=d, token=(H * d,) * 2, head=(d, d))
+        assert (got == -1) == bad and (bad or got in (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)), (size, stride, off, got, hit[:3])
+        seen[bad] += 1
+    assert min(seen.values()) > 300
