@@ -100,5 +100,16 @@ inline Extent extent_of(const void* p, uint64_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return {lo, lo + (p ? bytes : 0)};
 }
+// Whether one of `outs` meets one of `ins` or another of `outs`.
+template <int N, int M>
+bool any_meet(const Extent (&ins)[N], const Extent (&outs)[M]) {
+  for (int i = 0; i < M; ++i) {
+    for (const Extent& x : ins)
+      if (outs[i].meets(x)) return true;
+    for (int j = 0; j < i; ++j)
+      if (outs[i].meets(outs[j])) return true;
+  }
+  return false;
+}
 
 }  // namespace mattn

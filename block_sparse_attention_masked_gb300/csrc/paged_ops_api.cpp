@@ -345,12 +345,14 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   const int warps = decode_share_warps(tiles, d);
   const RowsLayout lay = rows_layout((int64_t)B * H_kv, H / H_kv, kPlanSms * warps, d);
   if ((rc = check_workspace("decode_paged", workspace, workspace_bytes, lay.all()))) return rc;
-  const Extent ins[3] = {extent_of(q, (uint64_t)B * H * d * 2), cache_rows(cache, 0, H_kv, d).extent(),
-                         cache_rows(cache, 1, H_kv, d).extent()};
-  const Extent to = extent_of(o, (uint64_t)B * H * d * 2), to_lse = extent_of(lse, (uint64_t)B * H * 4);
-  for (const Extent& x : ins)
-    if (to.meets(x) || to_lse.meets(x) || to.meets(to_lse))
-      return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: an output overlaps q, the cache or the other output");
+  const Extent ins[] = {extent_of(q, (uint64_t)B * H * d * 2), cache_rows(cache, 0, H_kv, d).extent(),
+                        cache_rows(cache, 1, H_kv, d).extent(), cache_rows(cache, 2, H_kv, d).extent(),
+                        cache_rows(cache, 3, H_kv, d).extent(), extent_of(cache->page_table, (uint64_t)B * cache->table_pages * 4),
+                        extent_of(seq_lens, (uint64_t)B * 4), extent_of(sink, (uint64_t)H * 4)};
+  const Extent outs[] = {extent_of(o, (uint64_t)B * H * d * 2), extent_of(lse, (uint64_t)B * H * 4),
+                         extent_of(workspace, lay.all())};
+  if (any_meet(ins, outs))
+    return report_error(MATTN_ERR_INVALID_ARG, "decode_paged: an output or the workspace overlaps an input or another output");
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   DecodePagedParams p;

@@ -589,7 +589,8 @@ int mattn_cache_read(void* k, void* v, const int64_t token_stride[2], const int6
  *               0 .. table_pages * page are clamped.  Positions without a page are
  *               no keys.  What rows hold that no query sees is not used.
  *   window      0: every key; sink_tokens >= 0, 0 without a window
- *   o and lse must not overlap q, the pages or each other.
+ *   o, lse and the workspace must not overlap an input (exponents, page table, seq_lens and
+ *   sink among them) or each other.
  *   At most 2^31 - 1 tiles of keys in all of B tables (16 keys; 32 in e4m3 or at
  *   d = 64, 64 where both; 16 in e4m3 at d = 256 with H / H_kv > 8).
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Sums,

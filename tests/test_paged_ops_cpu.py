@@ -379,3 +379,23 @@ def test_cache_tensors_that_overlap_by_enumeration(L):
         assert (got == -1) == bad and (bad or got in (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)), (size, stride, off, got, hit[:3])
         seen[bad] += 1
     assert min(seen.values()) > 300
+
+
+@pytest.mark.parametrize("why,kw", [
+    ("an output over the key exponents", {"o": 768 * MB}),
+    ("an output that ends in the value exponents", {"o": 800 * MB - 64}),
+    ("an lse over the page table", {"lse": 900 * MB + 44}),
+    ("an output over seq_lens", {"lens": 2 * MB + 6140}),
+    ("an lse over seq_lens", {"lens": 3 * MB}),
+    ("an output over the sink logits", {"sink": 2 * MB + 64}),
+    ("a workspace over the output", {"ws": 2 * MB}),
+    ("a workspace over the lse", {"ws": 3 * MB - 4096}),
+    ("a workspace over the queries", {"ws": MB}),
+    ("a workspace that ends in the keys", {"ws": 256 * MB - 65536}),
+    ("a workspace over the exponents", {"ws": 768 * MB}),
+    ("a workspace over the page table", {"ws": 900 * MB}),
+    ("a workspace over seq_lens", {"lens": 200 * MB + 1024}),
+])
+def test_decode_paged_refuses_what_overlaps(L, why, kw):
+    assert _paged(L, _cache(True), **kw) == -1, why
+    assert L.mattn_last_error()
