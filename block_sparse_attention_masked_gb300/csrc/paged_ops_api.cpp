@@ -459,15 +459,17 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
                           "attention_packed: strides must be positive multiples of 16 bytes below 2^40");
   }
   // (items are read and written in no order, some twice)
-  const void* from[3] = {q, k, v};
-  const Extent to = extent_of(o, (uint64_t)T * H * d * 2), to_lse = extent_of(lse, (uint64_t)T * H * 4);
-  for (int i = 0; i < 3; ++i) {
-    const int64_t rows = i ? T_k : T, heads = i ? H_kv : H;
-    const Extent x = extent_of(from[i], rows > 0 ? ((uint64_t)(rows - 1) * ts[i] + (uint64_t)(heads - 1) * hs[i] + d) * 2 : 0);
-    if (to.meets(x) || to_lse.meets(x) || to.meets(to_lse))
-      return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: an output overlaps an input or the other output");
-  }
   if ((rc = check_workspace("attention_packed", workspace, workspace_bytes, packed_bytes(T, B, H)))) return rc;
+  auto rows_of = [&](const void* x, int64_t rows, int heads, int i) {
+    return extent_of(x, rows > 0 ? ((uint64_t)(rows - 1) * ts[i] + (uint64_t)(heads - 1) * hs[i] + d) * 2 : 0);
+  };
+  const Extent ins[] = {rows_of(q, T, H, 0), rows_of(k, T_k, H_kv, 1), rows_of(v, T_k, H_kv, 2),
+                        extent_of(cu_seqlens_q, ((uint64_t)B + 1) * 4), extent_of(cu_seqlens_k, ((uint64_t)B + 1) * 4),
+                        extent_of(sink, (uint64_t)H * 4)};
+  const Extent outs[] = {extent_of(o, (uint64_t)T * H * d * 2), extent_of(lse, (uint64_t)T * H * 4),
+                         extent_of(workspace, packed_bytes(T, B, H))};
+  if (any_meet(ins, outs))
+    return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: an output or the workspace overlaps an input or another output");
   uint32_t* err = nullptr;
   if ((rc = device_error_word(stream, &err))) return rc;
   if (T == 0) return MATTN_OK;

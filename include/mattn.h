@@ -614,8 +614,8 @@ int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int pa
  *   q, k, v    DEVICE bf16: element (t, h, c) at t * token_stride + h * head_stride +
  *              c ([0] q, [1] k, [2] v), 16-byte aligned, strides positive multiples
  *              of 8 (of a dimension of one entry: any)
- *   o          DEVICE bf16 [T][H][d];  lse  DEVICE fp32 [H][T] or NULL; neither overlaps
- *              q, k, v or the other
+ *   o          DEVICE bf16 [T][H][d];  lse  DEVICE fp32 [H][T] or NULL; o, lse and the
+ *              workspace overlap no input and not each other
  *   cu_seqlens_q, cu_seqlens_k  DEVICE int32 [B + 1], ascending, inside 0..T and
  *              0..T_k (values outside are clamped); cu_seqlens_k NULL: cu_seqlens_q
  *              (T_k = T).  Rows of no sequence are not used, and o and lse left as

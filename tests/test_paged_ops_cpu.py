@@ -399,3 +399,21 @@ def test_cache_tensors_that_overlap_by_enumeration(L):
 def test_decode_paged_refuses_what_overlaps(L, why, kw):
     assert _paged(L, _cache(True), **kw) == -1, why
     assert L.mattn_last_error()
+
+
+@pytest.mark.parametrize("why,kw", [
+    ("an output over cu_seqlens", {"cu": 4 * MB + 8}),
+    ("an output over cu_seqlens_k", {"cu_k": 4 * MB + 100 * 2048 - 4}),
+    ("an lse over cu_seqlens", {"lse": 5 * MB - 3196}),
+    ("an output over the sink logits", {"sink": 4 * MB + 64}),
+    ("an lse over the sink logits", {"lse": 6 * MB, "sink": 6 * MB + 3196}),
+    ("a workspace over the queries", {"ws": MB}),
+    ("a workspace over the values", {"ws": 3 * MB + 256}),
+    ("a workspace over the output", {"ws": 4 * MB + 4096}),
+    ("a workspace over the lse", {"lse": 256 * MB + 64}),
+    ("a workspace over cu_seqlens", {"cu": 256 * MB}),
+    ("a workspace over the sink logits", {"sink": 256 * MB + 4}),
+])
+def test_attention_packed_refuses_what_overlaps(L, why, kw):
+    assert _packed(L, **kw) == -1, why
+    assert L.mattn_last_error()
