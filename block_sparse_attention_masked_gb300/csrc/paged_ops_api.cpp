@@ -434,6 +434,8 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
     return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: H = %d is not a multiple of H_kv = %d", H, H_kv);
   if (d != 64 && d != 80 && d != 96 && d != 128 && d != 256)
     return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: head dim %d (64, 80, 96, 128, 256)", d);
+  if (d == 256 && 2 * (int64_t)H * (T / 256 + (int64_t)B) > INT32_MAX)  // (an item is a query tile there, not a pair)
+    return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: H * (T / 256 + B) exceeds 2^30 - 1 at d = 256");
   if (dtype != MATTN_BF16) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed takes bf16");
   if (T_k < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: T_k must be >= 0");
   if (T_k > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: T_k exceeds 2^30");

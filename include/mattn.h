@@ -621,7 +621,7 @@ int mattn_decode_paged_workspace(int B, int H, int H_kv, int table_pages, int pa
  *              (T_k = T).  Rows of no sequence are not used, and o and lse left as
  *              they are there.  Sequences that share query rows: undefined.
  *   sink       DEVICE fp32 [H] sink logits or NULL;  softmax_scale  0 => 1/sqrt(d)
- *   d in {64, 80, 96, 128, 256}; H a multiple of H_kv; T, T_k <= 2^30; H * (T / 256 + B) < 2^31.
+ *   d in {64, 80, 96, 128, 256}; H a multiple of H_kv; T, T_k <= 2^30; H * (T / 256 + B) < 2^31 (2^30 at d = 256).
  * A query with no key at all gets O = 0 and LSE = -inf (or the sink logit).  Weights
  * meet the values in bf16 as in mattn_fwd; sums, statistics and the LSE are fp32.  Rows
  * whose last key is among their sequence's first 128, or whose window is of 64 keys at

@@ -417,3 +417,13 @@ def test_decode_paged_refuses_what_overlaps(L, why, kw):
 def test_attention_packed_refuses_what_overlaps(L, why, kw):
     assert _packed(L, **kw) == -1, why
     assert L.mattn_last_error()
+
+
+def test_attention_packed_refuses_2_30_items_of_256(L):
+    """At d = 256 an item is half as many rows."""
+    big = dict(T=1 << 29, T_k=1 << 29, H=512, H_kv=512, o=1 << 60, ws=1 << 62, ws_bytes=1 << 50, k=1 << 58, v=1 << 59)
+    strides = dict(token=(512 * 256,) * 3, head=(256,) * 3)
+    ok = (mattn.ERR_NO_DEVICE, mattn.ERR_CUDA)
+    assert _packed(L, d=256, **strides, **big) == -2
+    assert _packed(L, d=256, **strides, **dict(big, T=1 << 28, T_k=1 << 28)) in ok
+    assert _packed(L, d=128, **strides, **big) in ok
