@@ -100,7 +100,7 @@ struct PackedParams {
   int causal, window;            // window 0: none
   int wide;                      // o is 32-byte aligned
   int max_pairs, work_shift;
-  int direct;                    // no plan: at most kPackedDirect items a CTA, in the sequences' order
+  int direct;                    // no plan: at most kPackedDirect items a CTA, in the sequences' order (packed_direct)
   float scale_log2;
   int selftest;                  // 1: the first K tile is left out, so that the wait for it runs out
 };

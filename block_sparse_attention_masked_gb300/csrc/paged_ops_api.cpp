@@ -279,6 +279,15 @@ size_t packed_plan_bytes(int64_t T, int64_t B) {
 // (heads of 256: two items a pair and head)
 size_t packed_bytes(int64_t T, int64_t B, int64_t H) { return packed_plan_bytes(T, B) + (size_t)(packed_pairs(T, B) * H) * 8; }
 
+// Whether each CTA finds its items itself, without the plan kernel: where it has few, in up to
+// kDirectSequences sequences, which it then looks through, 32 at a time, before its first one (64
+// rows of four sequences, with empty ones behind them, us so and with the plan: 4 in all 8.2 and 11.5,
+// 128 8.9 and 11.5, 384 11.3 and 11.5, 512 12.6 and 11.5, 4,096 47.5 and 15.6).
+constexpr int kDirectSequences = 384;
+bool packed_direct(int64_t T, int64_t B, int64_t H, int d) {
+  return d != 256 && B <= kDirectSequences && packed_pairs(T, B) * H <= kPackedDirect * kPlanSms;
+}
+
 int check_packed(int B, int T, int H) {
   if (B < 1 || H < 1 || T < 0) return report_error(MATTN_ERR_INVALID_ARG, "attention_packed: B, H must be >= 1 and T >= 0");
   if (T > kMaxRows) return report_error(MATTN_ERR_UNSUPPORTED, "attention_packed: T exceeds 2^30");
@@ -507,7 +516,7 @@ int mattn_attention_packed(const void* q, const void* k, const void* v, const in
   p.window = window < kMaxRows ? window : (int)kMaxRows;
   p.max_pairs = (int)packed_pairs(T, B);
   while (((2 * ((int64_t)T_k / 128 + 1)) >> p.work_shift) >= 1024) ++p.work_shift;
-  p.direct = d != 256 && (int64_t)p.max_pairs * H <= kPackedDirect * kPlanSms ? 1 : 0;
+  p.direct = packed_direct(T, B, H, d) ? 1 : 0;
   p.scale_log2 = scale_log2(softmax_scale, d);
   p.selftest = g_wait_selftest.load();
   return launched(launch_attention_packed(p, d, stream), "attention_packed launch");
@@ -527,6 +536,9 @@ int mattn_internal_paged_plan(int B, int H, int H_kv, int table_pages, int page,
   out[2] = paged_tile(d, e8, H / H_kv);
   return MATTN_OK;
 }
+
+// Test hook (not in the public header), host only: whether attention_packed goes without its plan.
+int mattn_internal_packed_direct(int B, int T, int H, int d) { return packed_direct(T, B, H, d) ? 1 : 0; }
 
 // Test hook (not in the public header): the launches of decode_paged and
 // attention_packed until the next call leave out the first keys' copies (1), so that the

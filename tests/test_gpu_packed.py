@@ -415,3 +415,11 @@ def test_packed_256_items_longer_than_the_wait_limit():
         mattn.set_wait_timeout_ns(0)
     assert rc == 0, hex(word)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_packed_hundreds_of_sequences_without_rows():
+    """Few rows among many empty sequences, on both sides of the border between dealing items and planning them."""
+    for B in (384, 385, 3000):
+        nq = [0] * B
+        nq[0], nq[B // 2], nq[B - 1] = 40, 7, 17
+        packed_case(nq, 4, 2, 64, seed=B)

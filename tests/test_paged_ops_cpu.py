@@ -427,3 +427,11 @@ def test_attention_packed_refuses_2_30_items_of_256(L):
     assert _packed(L, d=256, **strides, **big) == -2
     assert _packed(L, d=256, **strides, **dict(big, T=1 << 28, T_k=1 << 28)) in ok
     assert _packed(L, d=128, **strides, **big) in ok
+
+
+def test_attention_packed_plan(L):
+    """No plan kernel for up to four items an SM, unless there are hundreds of sequences to look through."""
+    f = L.mattn_internal_packed_direct
+    assert f(8, 700, 16, 128) and f(1, 2048, 32, 64) and f(1, 1, 1, 80) and f(384, 64, 4, 128) and f(2, 128, 304, 128)
+    assert not f(385, 64, 4, 128) and not f(100000, 1, 1, 64)
+    assert not f(2, 128, 305, 128) and not f(8, 16384, 32, 128) and not f(8, 700, 16, 256)
