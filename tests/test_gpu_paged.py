@@ -584,3 +584,59 @@ def test_decode_paged_small_values(B, d):
             keys, values = c.rows(b, h // (H // Hkv), range(lens[b]))
             r, _, tol, _ = ref_decode(qd[b, h], keys, values, None, d ** -0.5, True)
             assert bool((r.abs().max() > 2.0 ** -119) and ((got[b, h] - r).abs() <= tol).all()), (b, h)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cache_write_of_one_token_each_by_value(e4m3, d):
+    """A decode step's write: each token's codes and powers against the definition, every other byte as it was."""
+    B, Hkv, page, slots = 37, 3, 16, 4
+    c = Cache(B, Hkv, d, page, slots, e4m3, seed=6)
+    k, v = rows_of(5, B, Hkv, d, "fused")
+    k = k * torch.exp2(torch.arange(B, device="cuda") % 40 - 20).to(k.dtype)[:, None, None]
+    at = [(7 * b) % (page * slots) for b in range(B)]
+    at[3], at[9] = page * slots, -1  # past the table, before it: left out
+    c.table[5] = -1
+    before = {x: (c.held(x), None if not e4m3 else (c.ke if x == "k" else c.ve).cpu().clone()) for x in "kv"}
+    mattn.cache_write(k, v, c.k, c.v, c.table, starts=_i32(at), **c.kw())
+    placed, _ = ref_places(c, [1] * B, at, B)
+    assert len(placed) == B - 3
+    for name, rows, exps in (("k", k, c.ke), ("v", v, c.ve)):
+        want, e_want = before[name]
+        for t, p, r in placed:
+            for h in range(Hkv):
+                x = rows[t, h].double().cpu()
+                if e4m3:
+                    codes, e = ref_codes(x)
+                    want[p, h, r], e_want[p, h, r] = codes * 2.0 ** (e - 127), e
+                else:
+                    want[p, h, r] = x
+        assert torch.equal(c.held(name), want)
+        if e4m3:
+            assert torch.equal(exps.cpu(), e_want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bad", [[5, 3, 40], [-7, 2000000000, 3], [2147483647, -2147483648, 0], [40, 40, 40], [0, 20, 40]])
+def test_cache_calls_with_sequences_that_are_none_stay_inside(bad, e4m3):
+    """What such calls write lies in their tensors: bytes around the pages, the powers and the outputs stay."""
+    T, n, Hkv, page, d = 40, 6, 2, 16, 64
+    guards = []
+
+    def guarded(shape, dtype):
+        size = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        x = torch.full((size + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+        guards.append((x[:4096], x[4096 + size :]))
+        return x[4096 : 4096 + size].view(dtype).view(shape)
+
+    kp, vp = (guarded((n, Hkv, page, d), CODES if e4m3 else torch.bfloat16) for _ in range(2))
+    ke, ve = (guarded((n, Hkv, page), torch.uint8) if e4m3 else None for _ in range(2))
+    ko, vo = (guarded((T, Hkv, d), torch.bfloat16) for _ in range(2))
+    table = _i32([[0, n - 1, 1 << 30], [n, 2, -1]])
+    k, v = rows_of(1, T, Hkv, d)
+    for starts in ([2147483647, -5], [-2147483648, 7], [40, 15], [0, 16]):
+        mattn.cache_write(k, v, kp, vp, table, _i32(bad), _i32(starts), k_exponents=ke, v_exponents=ve)
+        mattn.cache_read(kp, vp, table, _i32(bad), T, _i32(starts), k_exponents=ke, v_exponents=ve, k_out=ko, v_out=vo)
+    torch.cuda.synchronize()
+    for a, b in guards:
+        assert bool((a == 0x5A).all()) and bool((b == 0x5A).all())
