@@ -419,7 +419,10 @@ int mattn_decode_paged(const void* q, const mattn_paged_cache* cache, void* o, f
   m.lse = lse;
   m.B = B; m.H = H; m.H_kv = H_kv;
   m.states = 1 + (int)(lay.warps / ((int64_t)B * H_kv));
-  m.many = m.states >= 200 ? 1 : 0;  // (131,071 keys of 256 in four groups: 58.1 us without, 55.0 so; eight groups: no gain)
+  // (us with four in flight and with sixteen, e4m3, warm: 229 states a row, 131,071 keys of 256 57.6 and
+  // 54.5, of 128 54.9 and 51.3; 115, two sequences of 65,536 of 128 53.6 and 51.8; 58, four 91.1 and 90.5,
+  // eight of 32,768 52.1 and 51.2; 29, 51.4 and 51.2; 13, the same; 7, 103.9 and 105.2)
+  m.many = m.states >= 32 ? 1 : 0;
   return launched(launch_decode_merge(m, d, stream), "merge launch");
 }
 
