@@ -553,7 +553,7 @@ typedef struct {
  * e4m3 codes are its values times 2^(127 - e), rounded to nearest even, with the
  * least e >= 0 for which 448 * 2^(e - 127) is at least every |value|; a row with an
  * infinite or NaN value gets e = 255 and NaN codes.  Where two tokens go to one row
- * of a page, the row holds either.
+ * of a page, what the row (and its power) holds is undefined.
  *   k, v        DEVICE bf16, element (t, h, c) at t * token_stride + h *
  *               head_stride + c ([0] of k, [1] of v); 16-byte aligned, strides
  *               multiples of 8 and >= 0
