@@ -29,9 +29,9 @@
 // Roles (384 threads) and tensor memory: as attention_persist.cu; every wait is bounded
 // in time and gives up by raising a CTA-wide abort flag and a device error bit.
 //
-// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads of 128, 349 us = 1,576
-// (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads, 306-318 us =
-// 1,195-1,240, the same tokens as 64 prompts of 256 92 us = 376, 12 images of 1 to 3,038 patches, 16 heads of 80,
+// Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads of 128, 349-357 us =
+// 1,540-1,576 (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads,
+// 306-323 us = 1,175-1,240, the same tokens as 64 prompts of 256 91 us = 380, 12 images of 1 to 3,038 patches, 16 heads of 80,
 // 186 us = 929.  Long lists run at the forward's own rate; an item costs 2.5 to 5 us beside its
 // tiles (its first S, its last P V and its output, which only the other query tile's work hides).
 // Tried without gain: the output staged in shared memory (d = 80 and 64 2% slower), O read from tensor memory 32 or

@@ -30,12 +30,13 @@
 // puts the eight lanes of a load's phase into eight different 16-byte columns of the
 // swizzled tile.
 //
-// Measured: 64 sequences of 4K to 8K keys, 32 / 8 heads of 128 in e4m3 133 us = 850 MB at 6.4
+// Measured: 64 sequences of 4K to 8K keys, 32 / 8 heads of 128 in e4m3 133-138 us = 850 MB at 6.2-6.4
 // TB/s (HBM; loads without products take 133.6), 16 of 16K to 32K in bf16 245-255 us = 1.64 GB
-// at 6.4-6.7, one of 131,071, heads of 256, 54.7 us = 270 MB at 4.9 (8 to 10 us of it are the two
+// at 6.4-6.7, one of 131,071, heads of 256, 54.5-54.9 us = 270 MB at 4.9 (8 to 10 us of it are the two
 // launches, the first loads and the states).  With more than eight query heads a key/value
 // head the e4m3 step bounds it (64 sequences, 32 / 2 heads 63 us against 30 by the bytes): the
-// products of 16 heads and two exponentials a score on three warps a scheduler.  Tried without
+// products of 16 heads and two exponentials a score on three warps a scheduler, with registers
+// that do not suffice (60 bytes a thread spill at d = 64, 116 at 128, 152 at 256).  Tried without
 // gain: 64 keys a tile and six warps at d = 128 (160 us for 134), pages looked up for 32 boxes at
 // a time, a tile's boxes as one copy, exponent bytes as words, states of a CTA's warps joined in shared
 // memory where there are many (138 for 134).
