@@ -640,3 +640,44 @@ def test_cache_calls_with_sequences_that_are_none_stay_inside(bad, e4m3):
     torch.cuda.synchronize()
     for a, b in guards:
         assert bool((a == 0x5A).all()) and bool((b == 0x5A).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("pool", ["shifted", "page", "row"])
+def test_cache_pools(pool, e4m3):
+    """k and v in one pool, the odd pages v's; codes and exponents of a page or of a row side by side: as apart."""
+    if pool == "row" and not e4m3:
+        pytest.skip("bf16 rows have no exponents")
+    B, H, Hkv, d, page, slots = 3, 4, 2, 64, 16, 4
+    n, T, es = 2 * B * slots, 90, 1 if e4m3 else 2
+    dtype = CODES if e4m3 else torch.bfloat16
+    ke = ve = None
+    if pool == "shifted":
+        both = torch.zeros((n, Hkv, page, d * es), dtype=torch.uint8, device="cuda").view(dtype)
+        k, v = both[:-1], both[1:]
+        if e4m3:
+            exps = torch.zeros((n, Hkv, page), dtype=torch.uint8, device="cuda")
+            ke, ve = exps[:-1], exps[1:]
+        table = _i32([[2 * (b * slots + j) for j in range(slots)] for b in range(B)])
+    else:
+        table = _i32([[n - 1 - b * slots - j for j in range(slots)] for b in range(B)])
+        if pool == "page":
+            rows = Hkv * page * d * es
+            both = torch.zeros((n, 2 * rows + 2 * Hkv * page), dtype=torch.uint8, device="cuda")
+            k, v = (both[:, i * rows : (i + 1) * rows].view(dtype).view(n, Hkv, page, d) for i in range(2))
+            if e4m3:
+                ke, ve = (both[:, 2 * rows + i * Hkv * page : 2 * rows + (i + 1) * Hkv * page].view(n, Hkv, page) for i in range(2))
+        else:
+            both = torch.zeros((n, Hkv, page, 2 * d + 16), dtype=torch.uint8, device="cuda")
+            k, v = both[..., :d].view(dtype), both[..., d : 2 * d].view(dtype)
+            ke, ve = both[..., 2 * d], both[..., 2 * d + 1]
+    c = Cache(B, Hkv, d, page, slots, e4m3)
+    lens = [50, 7, 33]
+    x, y = rows_of(7, T, Hkv, d)
+    cu, q = _lens_to_cu(lens), _randn(_gen(8), B, H, d)
+    got = []
+    for kp, vp, t, kw in ((c.k, c.v, c.table, c.kw()), (k, v, table, dict(k_exponents=ke, v_exponents=ve))):
+        mattn.cache_write(x, y, kp, vp, t, cu, **kw)
+        got.append([*mattn.cache_read(kp, vp, t, cu, T, **kw), *mattn.decode_paged(q, kp, vp, t, _i32(lens), **kw)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
