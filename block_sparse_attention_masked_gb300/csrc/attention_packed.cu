@@ -27,7 +27,8 @@
 // tokens of eight prompts and 16% of a window of 576.)
 //
 // Roles (384 threads) and tensor memory: as attention_persist.cu; every wait is bounded
-// in time and gives up by raising a CTA-wide abort flag and a device error bit.
+// in time (those for an item: in time without a key tile's progress) and gives up by
+// raising a CTA-wide abort flag and a device error bit.
 //
 // Measured (TFLOP/s of visible pairs): one causal sequence of 16,384, 8 heads of 128, 349-357 us =
 // 1,540-1,576 (attention_fwd.cu's paired schedule 367), eight prompts of 1 to 3,352 tokens, 32 heads,
@@ -221,6 +222,7 @@ struct Bar {
   uint32_t tmem_base;
   int abort_flag;
   uint32_t mma_turn;
+  uint32_t tiles;          // K tiles whose copies are under way, of all items
   int marked;              // the CTA's last marked item, from which PackedParams::marked leads to the others; -1: none
   Item items[kItems];
   PackedPair direct[kPackedDirect];  // the CTA's items' pairs, where there is no plan
@@ -344,6 +346,7 @@ __device__ __forceinline__ void produce_items(const PackedParams& p, Bar* bar, u
         ++e;
         ++kj;
         moved = true;
+        *reinterpret_cast<volatile uint32_t*>(&bar->tiles) = (uint32_t)e;
       }
     }
     if (qi < pub - (done ? 1 : 0)) {
@@ -433,7 +436,10 @@ __device__ __forceinline__ void add_odd_values(const PackedParams& p, const Item
 
 // Waits for the CTA's item i; null if the wait gave up.
 __device__ __forceinline__ const Item* take_item(const PackedParams& p, Bar* bar, int i, volatile int* abort_flag) {
-  const bool got = ptx::mbar_wait(&bar->item_full[i % kItems], (i / kItems) & 1, p.timeout_ns, abort_flag);
+  // (the softmax of a query tile without rows is here while the other's keys pass)
+  const bool got = item_wait(&bar->tiles, abort_flag, [&] {
+    return ptx::mbar_wait(&bar->item_full[i % kItems], (i / kItems) & 1, p.timeout_ns, abort_flag);
+  });
   return __all_sync(0xffffffffu, got) ? &bar->items[i % kItems] : nullptr;
 }
 __device__ __forceinline__ void drop_item(Bar* bar, int i) {  // (one warp, after its last read)
@@ -502,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_packed_kernel(const __g
     }
     bar->abort_flag = 0;
     bar->mma_turn = 0;
+    bar->tiles = 0;
     bar->marked = -1;
     ptx::fence_barrier_init();
   }

@@ -50,6 +50,19 @@ __device__ __forceinline__ bool in_bounds(const PackedParams& p, const PackedPai
 // The 16-bit halves of x that are no infinity or NaN, and zeros for those that are.
 __device__ __forceinline__ uint32_t clean(uint32_t x) { return x & ~__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
 
+// A wait that may take as long as an item, whatever its keys take: `once` waits for up to the limit;
+// given up after a limit without a K tile more (`tiles`, which their producer counts).  Every other
+// wait is one for a tile's work.
+template <class Once>
+__device__ __forceinline__ bool item_wait(volatile uint32_t* tiles, volatile int* abort_flag, Once once) {
+  for (uint32_t seen = *tiles;;) {
+    if (once()) return true;
+    const uint32_t now = *tiles;
+    if (now == seen || *abort_flag) return false;
+    seen = now;
+  }
+}
+
 __device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
   if (!*abort_flag) return;
   const uint64_t t0 = ptx::globaltimer_ns();

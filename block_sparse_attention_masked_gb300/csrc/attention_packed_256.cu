@@ -111,17 +111,11 @@ __device__ __forceinline__ void fail(const PackedParams& p, Bar* bar, uint32_t b
   atomicOr(p.err, bit);
 }
 
-// The scheduler's wait for a ring slot.  It takes as long as an item, whatever its keys take, so
-// it gives up after timeout_ns without a K tile more (every other wait is one for a tile's work).
+// The scheduler's wait for a ring slot.
 __device__ __forceinline__ bool slot_wait(const PackedParams& p, Bar* bar, uint64_t* b, uint32_t parity,
                                           volatile int* abort_flag) {
-  volatile uint32_t* tiles = &bar->tiles;
-  for (uint32_t seen = *tiles;;) {
-    if (ptx::mbar_wait_backoff(b, parity, p.timeout_ns, abort_flag, 200)) return true;
-    const uint32_t now = *tiles;
-    if (now == seen || *abort_flag) return false;
-    seen = now;
-  }
+  return item_wait(&bar->tiles, abort_flag,
+                   [&] { return ptx::mbar_wait_backoff(b, parity, p.timeout_ns, abort_flag, 200); });
 }
 
 // The items, in order (one thread).

@@ -423,3 +423,26 @@ def test_packed_hundreds_of_sequences_without_rows():
         nq = [0] * B
         nq[0], nq[B // 2], nq[B - 1] = 40, 7, 17
         packed_case(nq, 4, 2, 64, seed=B)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_items_longer_than_the_wait_limit(causal, d):
+    """The same where an item is a pair of query tiles: the second one without rows, or both, several items a CTA."""
+    m = 1 << 20
+    for nq, H in (([100], 2), ([100] * 3, 200), ([300], 2)):
+        T = sum(nq)
+        q, k, v = inputs(T, m, H, 1, d, 18)
+        cu, cu_k = _i32(_cu(nq)), _i32([0] * len(nq) + [m])
+        call = lambda: mattn.attention_packed(q, k, v, cu, cu_k, causal=causal)  # noqa: E731
+        want = call()
+        torch.cuda.synchronize()
+        mattn.set_wait_timeout_ns(3_000_000)  # 3 ms; an item takes about 8
+        try:
+            got = call()
+            torch.cuda.synchronize()
+            rc, word = mattn.device_status()
+        finally:
+            mattn.set_wait_timeout_ns(0)
+        assert rc == 0, hex(word)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
