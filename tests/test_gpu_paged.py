@@ -681,3 +681,23 @@ def test_cache_pools(pool, e4m3):
         got.append([*mattn.cache_read(kp, vp, t, cu, T, **kw), *mattn.decode_paged(q, kp, vp, t, _i32(lens), **kw)])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("B", [2, 90])
+def test_decode_paged_large_values(B, d):
+    """Values up to 2^117, rows of zeros (the least power) among them; keys of 2^110 under queries of 2^-117."""
+    H, Hkv = 12, 2
+    c = Cache(B, Hkv, d, 16, 9, True, seed=23)
+    c.ve[:] = torch.randint(233, 236, c.ve.shape, generator=_gen(1), device="cuda", dtype=torch.uint8)
+    c.ke[:] = 231
+    zero = torch.rand(c.ve.shape, generator=_gen(3), device="cuda") < 0.2
+    c.ve[zero], Cache._bytes(c.v)[zero] = 0, 0
+    q = _randn(_gen(2), B, H, d, scale=2.0 ** -117)
+    lens = [144 - b for b in range(B)]
+    c.freeze()
+    o, lse = mattn.decode_paged(q, c.k, c.v, c.table, _i32(lens), scale=2.0 ** -4, **c.kw())
+    rows = [0, B - 1]
+    part = Cache.__new__(Cache)
+    part.__dict__.update(c.__dict__, table=c.table[rows])
+    check_decode(o[rows], lse[rows], q[rows], part, [range(lens[b]) for b in rows], None, 2.0 ** -4)
